@@ -1,4 +1,4 @@
-"""Python binding of the qgemm C ABI (include/qgemm.h): argument marshalling only.
+"""Python binding of the qgemm C ABI (include/qgemm.h, include/qgemm_attention.h): argument marshalling only.
 
 Every step of the GEMM runs in the HIP library ``libqgemm.so`` built next to this file;
 torch serves only for device memory and the current stream.  Importing this package
@@ -38,6 +38,9 @@ SCALE_GROUP_F16, SCALE_TENSOR_F32, SCALE_BLOCK16_E4M3, SCALE_GROUP_F16_LUT16 = r
 KERNEL_AUTO, KERNEL_DECODE, KERNEL_PREFILL, KERNEL_PREFILL_STREAMK, KERNEL_PREFILL_TRANSFORM = range(5)
 
 
+ATTENTION_AUTO, ATTENTION_ROWS, ATTENTION_TILES = range(3)
+
+
 class Problem(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("a_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
@@ -47,6 +50,29 @@ class Problem(ctypes.Structure):
 
 
 assert ctypes.sizeof(Problem) == 56
+
+
+class NormRope(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("max_pos", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("group_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("cache", Cache), ("total_q", ctypes.c_int64), ("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("kernel_hint", ctypes.c_int32),
+                ("reserved", ctypes.c_int32 * 2)]
+
+
+assert (ctypes.sizeof(NormRope), ctypes.sizeof(Cache), ctypes.sizeof(Attention)) == (48, 32, 80)
 
 _P = ctypes.POINTER(Problem)
 _vp = ctypes.c_void_p
@@ -63,9 +89,19 @@ _lib.qgemm_status_string.restype = ctypes.c_char_p
 _lib.qgemm_last_error.argtypes = []
 _lib.qgemm_last_error.restype = ctypes.c_char_p
 _lib.qgemm_version.restype = ctypes.c_int32
+_i64 = ctypes.c_int64
+_NRP, _CP, _AP = ctypes.POINTER(NormRope), ctypes.POINTER(Cache), ctypes.POINTER(Attention)
+_lib.qgemm_qk_norm_rope.argtypes = [_NRP, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp]
+_lib.qgemm_cache_bytes.argtypes = [_CP, ctypes.POINTER(_sz)]
+_lib.qgemm_cache_write.argtypes = [_CP, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.qgemm_cache_read.argtypes = [_CP, _vp, _vp, _i64, _vp, _vp, _vp]
+_lib.qgemm_attention_workspace_bytes.argtypes = [_AP, ctypes.POINTER(_sz)]
+_lib.qgemm_attention.argtypes = [_AP, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]
+_lib.qgemm_attention_describe.argtypes = [_AP, ctypes.c_char_p, _sz]
 NO_ALLOC_SCRATCH_BYTES = (32 << 20) + (64 << 10)    # QGEMM_NO_ALLOC_SCRATCH_BYTES of include/qgemm.h
 for _f in ("qgemm_quantize", "qgemm_pack", "qgemm_workspace_bytes", "qgemm_run", "qgemm_run_bias",
-           "qgemm_run_no_alloc", "qgemm_plan_describe"):
+           "qgemm_run_no_alloc", "qgemm_plan_describe", "qgemm_qk_norm_rope", "qgemm_cache_bytes", "qgemm_cache_write",
+           "qgemm_cache_read", "qgemm_attention_workspace_bytes", "qgemm_attention", "qgemm_attention_describe"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 lib = _lib
@@ -247,3 +283,132 @@ def status_string(st):
 
 def version():
     return int(_lib.qgemm_version())
+
+
+# ----------------------------------------------------------------------------- attention operators
+def _stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _rows(x, name, heads, dim, tokens, dtype):
+    """Token stride of a [tokens, heads, dim] (or [tokens, heads * dim]) tensor whose heads lie side by side."""
+    if x is None:
+        return 0
+    want = {DT_F16: torch.float16, DT_BF16: torch.bfloat16}.get(dtype)
+    flat = x.dim() == 2
+    if tuple(x.shape) != ((tokens, heads * dim) if flat else (tokens, heads, dim)):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {tuple(x.shape)}")
+    if x.dtype != want:
+        raise ValueError(f"{name} must be {want}, got {x.dtype}")
+    if x.stride(-1) != 1 or (not flat and heads > 1 and x.stride(1) != dim):
+        raise ValueError(f"{name}'s heads must be contiguous within a token, got strides {x.stride()}")
+    # a single token has no distance to the next; torch may report any stride for it
+    return x.stride(0) if tokens > 1 else heads * dim
+
+
+def _array(x, name, dtype, numel):
+    """A contiguous device array of at least `numel` elements."""
+    if x is not None and (x.dtype != dtype or not x.is_contiguous() or x.numel() < numel):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements, got "
+                         f"{x.dtype} {tuple(x.shape)} with strides {x.stride()}")
+    return x
+
+
+def norm_rope_problem(tokens, q_heads, kv_heads, head_dim, dtype=DT_F16, rot_dim=None, max_pos=0, interleaved=False,
+                      norm=True, eps=1e-6):
+    """Descriptor of qk_norm_rope; rot_dim defaults to the whole head, 0 turns nothing."""
+    return NormRope(tokens, q_heads, kv_heads, head_dim, head_dim if rot_dim is None else rot_dim, max_pos, dtype,
+                    int(interleaved), int(norm), eps, 0)
+
+
+def qk_norm_rope(p, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, stream=None):
+    """Enqueue the norm and rotation of the heads of q and k (qgemm_qk_norm_rope).  The tensors are
+    [tokens, heads, head_dim], each with its own token stride; outputs may be the inputs."""
+    t16 = {DT_F16: torch.float16, DT_BF16: torch.bfloat16}.get(p.dtype)
+    st = [_rows(x, n, h, p.head_dim, p.tokens, p.dtype) for x, n, h in
+          ((q, "q", p.q_heads), (k, "k", p.kv_heads), (q_out, "q_out", p.q_heads), (k_out, "k_out", p.kv_heads))]
+    _array(q_weight, "q_weight", t16, p.head_dim)
+    _array(k_weight, "k_weight", t16, p.head_dim)
+    if p.rot_dim:
+        _array(positions, "positions", torch.int32, p.tokens)
+        _array(cos_sin, "cos_sin", torch.float32, p.max_pos * p.rot_dim)
+    _check(_lib.qgemm_qk_norm_rope(ctypes.byref(p), _ptr(q), st[0], _ptr(k), st[1], _ptr(q_weight), _ptr(k_weight),
+                                   _ptr(positions), _ptr(cos_sin), _ptr(q_out), st[2], _ptr(k_out), st[3],
+                                   _stream(stream)))
+
+
+def cache(num_pages, page_size, kv_heads, head_dim, dtype=DT_F16, group_size=None):
+    """Descriptor of a 4-bit paged key/value cache; group_size defaults to the whole head."""
+    return Cache(num_pages, page_size, kv_heads, head_dim, head_dim if group_size is None else group_size, dtype, 0)
+
+
+def cache_bytes(c):
+    n = _sz(0)
+    _check(_lib.qgemm_cache_bytes(ctypes.byref(c), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_cache(c, device="cuda"):
+    """A zero-filled cache buffer (every slot reads as zeros)."""
+    return torch.zeros(cache_bytes(c), dtype=torch.uint8, device=device)
+
+
+def cache_write(c, data, k, v, slots, stream=None):
+    """Enqueue the quantization of k, v [tokens, kv_heads, head_dim] into the int64 slots."""
+    n = slots.numel()
+    _array(data, "data", torch.uint8, cache_bytes(c))
+    _array(slots, "slots", torch.int64, n)
+    ks, vs = (_rows(x, m, c.kv_heads, c.head_dim, n, c.dtype) for x, m in ((k, "k"), (v, "v")))
+    _check(_lib.qgemm_cache_write(ctypes.byref(c), _ptr(data), _ptr(k), ks, _ptr(v), vs, _ptr(slots), n, _stream(stream)))
+
+
+def cache_read(c, data, slots, k_out, v_out, stream=None):
+    """Enqueue the values of the slots into k_out, v_out [tokens, kv_heads, head_dim], contiguous."""
+    n = slots.numel()
+    t16 = {DT_F16: torch.float16, DT_BF16: torch.bfloat16}.get(c.dtype)
+    _array(data, "data", torch.uint8, cache_bytes(c))
+    _array(slots, "slots", torch.int64, n)
+    for x, m in ((k_out, "k_out"), (v_out, "v_out")):
+        _array(x, m, t16, n * c.kv_heads * c.head_dim)
+    _check(_lib.qgemm_cache_read(ctypes.byref(c), _ptr(data), _ptr(slots), n, _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def attention_problem(c, batch, total_q, q_heads, max_q_len, max_pages, causal=True, window=0, scale=None,
+                      kernel_hint=ATTENTION_AUTO):
+    """Descriptor of attention over the cache `c`; scale defaults to head_dim ** -0.5."""
+    return Attention(c, total_q, batch, q_heads, max_q_len, max_pages, int(causal), window,
+                     c.head_dim ** -0.5 if scale is None else scale, kernel_hint, (0, 0))
+
+
+def attention_workspace_bytes(p):
+    n = _sz(0)
+    _check(_lib.qgemm_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_attention_workspace(p, device="cuda"):
+    """A zero-filled workspace of the size qgemm_attention_workspace_bytes reports (or None)."""
+    n = attention_workspace_bytes(p)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def attention_describe(p):
+    """The launch qgemm_attention would make for this problem, as one line of text."""
+    buf = ctypes.create_string_buffer(512)
+    _check(_lib.qgemm_attention_describe(ctypes.byref(p), buf, 512))
+    return buf.value.decode()
+
+
+def attention(p, q, data, page_table, seq_lens, q_start, out, workspace=None, stream=None):
+    """Enqueue attention of q [total_q, q_heads, head_dim] over the cache into out (qgemm_attention)."""
+    c = p.cache
+    qs, os_ = (_rows(x, m, p.q_heads, c.head_dim, p.total_q, c.dtype) for x, m in ((q, "q"), (out, "out")))
+    _array(data, "data", torch.uint8, cache_bytes(c))
+    _array(page_table, "page_table", torch.int32, p.batch * p.max_pages)
+    _array(seq_lens, "seq_lens", torch.int32, p.batch)
+    _array(q_start, "q_start", torch.int32, p.batch + 1)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.qgemm_attention(ctypes.byref(p), _ptr(q), qs, _ptr(data), _ptr(page_table), _ptr(seq_lens), _ptr(q_start),
+                                _ptr(out), os_, _ptr(workspace), ws_bytes, _stream(stream)))

@@ -1,0 +1,151 @@
+// Host side of the attention operators: descriptor validation, cache geometry and launch planning.
+// Nothing in this file touches the GPU.
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "qgemm_attention_internal.h"
+
+namespace qgemm {
+
+static_assert(sizeof(qgemm_norm_rope_t) == 48, "qgemm_norm_rope_t layout is part of the ABI");
+static_assert(sizeof(qgemm_cache_t) == 32, "qgemm_cache_t layout is part of the ABI");
+static_assert(sizeof(qgemm_attention_t) == 80, "qgemm_attention_t layout is part of the ABI");
+
+static const int64_t kMaxTokens = int64_t(1) << 24;
+
+static qgemm_status_t check_dtype_dim(const char* what, int dtype, int head_dim) {
+  if (dtype < QGEMM_DT_F16 || dtype > QGEMM_DT_NF4)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "%s dtype value %d is not a qgemm_dtype_t", what, dtype);
+  if (dtype != QGEMM_DT_F16 && dtype != QGEMM_DT_BF16)
+    return fail(QGEMM_ERR_UNSUPPORTED, "%s dtype must be F16 or BF16, got %d", what, dtype);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(QGEMM_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256, got %d", head_dim);
+  return QGEMM_OK;
+}
+
+qgemm_status_t validate_norm_rope(const qgemm_norm_rope_t* p) {
+  if (!p) return fail(QGEMM_ERR_INVALID_ARGUMENT, "problem is NULL");
+  const qgemm_status_t st = check_dtype_dim("norm_rope", p->dtype, p->head_dim);
+  if (st != QGEMM_OK) return st;
+  if (p->tokens < 0 || p->tokens > kMaxTokens)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "tokens must be in [0, %lld], got %lld", (long long)kMaxTokens,
+                (long long)p->tokens);
+  if (p->q_heads < 0 || p->q_heads > 1024 || p->kv_heads < 0 || p->kv_heads > 1024 || p->q_heads + p->kv_heads == 0)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "q_heads and kv_heads must be in [0, 1024] and not both 0, got %d and %d",
+                p->q_heads, p->kv_heads);
+  if (p->rot_dim < 0 || p->rot_dim > p->head_dim || p->rot_dim % 8)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "rot_dim must be a multiple of 8 in [0, head_dim = %d], got %d", p->head_dim,
+                p->rot_dim);
+  if (p->rot_dim && (p->max_pos < 1 || p->max_pos > kMaxTokens))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "max_pos must be in [1, %lld], got %d", (long long)kMaxTokens, p->max_pos);
+  if ((p->interleaved | 1) != 1 || (p->norm | 1) != 1)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "interleaved and norm must be 0 or 1, got %d and %d", p->interleaved, p->norm);
+  if (p->norm && !(p->eps >= 0.0f && std::isfinite(p->eps)))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "eps must be finite and at least 0, got %g", (double)p->eps);
+  if (p->reserved) return fail(QGEMM_ERR_INVALID_ARGUMENT, "reserved must be 0, got %d", p->reserved);
+  return QGEMM_OK;
+}
+
+qgemm_status_t validate_cache(const qgemm_cache_t* c) {
+  if (!c) return fail(QGEMM_ERR_INVALID_ARGUMENT, "cache is NULL");
+  const qgemm_status_t st = check_dtype_dim("cache", c->dtype, c->head_dim);
+  if (st != QGEMM_OK) return st;
+  if (c->num_pages < 1 || c->num_pages > 0x7fffffffLL)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "num_pages must be in [1, 2^31 - 1], got %lld", (long long)c->num_pages);
+  if (c->page_size < 16 || c->page_size > 4096 || c->page_size % 16)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "page_size must be a multiple of 16 in [16, 4096], got %d", c->page_size);
+  if (c->kv_heads < 1 || c->kv_heads > 1024)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "kv_heads must be in [1, 1024], got %d", c->kv_heads);
+  const int g = c->group_size;
+  if (g != c->head_dim && g * 2 != c->head_dim && (g * 4 != c->head_dim || c->head_dim < 128))
+    return fail(QGEMM_ERR_UNSUPPORTED, "group_size must be head_dim, head_dim / 2 or (head_dim >= 128) head_dim / 4; got "
+                "group_size %d, head_dim %d", g, c->head_dim);
+  if (c->reserved) return fail(QGEMM_ERR_INVALID_ARGUMENT, "cache reserved must be 0, got %d", c->reserved);
+  return QGEMM_OK;
+}
+
+qgemm_status_t validate_attention(const qgemm_attention_t* p) {
+  if (!p) return fail(QGEMM_ERR_INVALID_ARGUMENT, "problem is NULL");
+  const qgemm_status_t st = validate_cache(&p->cache);
+  if (st != QGEMM_OK) return st;
+  if (p->total_q < 0 || p->total_q > kMaxTokens)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "total_q must be in [0, %lld], got %lld", (long long)kMaxTokens,
+                (long long)p->total_q);
+  if (p->batch < 1 || p->batch > 65535)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "batch must be in [1, 65535], got %d", p->batch);
+  if (p->q_heads < 1 || p->q_heads > 4096 || p->q_heads % p->cache.kv_heads)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "q_heads must be a positive multiple of kv_heads (%d), at most 4096; got %d",
+                p->cache.kv_heads, p->q_heads);
+  if (p->total_q && (p->max_q_len < 1 || p->max_q_len > p->total_q))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "max_q_len must be in [1, total_q = %lld], got %d", (long long)p->total_q,
+                p->max_q_len);
+  if (p->max_pages < 1 || (int64_t)p->max_pages * p->cache.page_size > (int64_t(1) << 30))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "max_pages must be positive and max_pages * page_size at most 2^30, got %d "
+                "pages of %d", p->max_pages, p->cache.page_size);
+  if ((p->causal | 1) != 1) return fail(QGEMM_ERR_INVALID_ARGUMENT, "causal must be 0 or 1, got %d", p->causal);
+  if (p->window < 0 || (p->window && !p->causal))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "window must be 0, or positive with causal = 1; got %d", p->window);
+  if (!std::isfinite(p->scale)) return fail(QGEMM_ERR_INVALID_ARGUMENT, "scale must be finite, got %g", (double)p->scale);
+  if (p->kernel_hint < QGEMM_ATTENTION_AUTO || p->kernel_hint > QGEMM_ATTENTION_TILES)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "kernel_hint must be 0 to 2, got %d", p->kernel_hint);
+  if (p->reserved[0] || p->reserved[1]) return fail(QGEMM_ERR_INVALID_ARGUMENT, "reserved must be 0");
+  return QGEMM_OK;
+}
+
+qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
+  std::memset(pl, 0, sizeof(*pl));
+  if (p->total_q == 0) return QGEMM_OK;
+  pl->groups = p->cache.head_dim / p->cache.group_size;
+  const int64_t units = p->total_q * p->q_heads;
+  if (units > 0x7fffffffLL)
+    return fail(QGEMM_ERR_UNSUPPORTED, "total_q * q_heads is %lld, more than one launch allows", (long long)units);
+  pl->kind = ATTN_ROWS;
+  pl->rows = p->q_heads / p->cache.kv_heads * p->max_q_len;
+  pl->grid = (unsigned)units;
+  return QGEMM_OK;
+}
+
+}  // namespace qgemm
+
+using namespace qgemm;
+
+extern "C" {
+
+qgemm_status_t qgemm_cache_bytes(const qgemm_cache_t* c, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(QGEMM_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  const qgemm_status_t st = validate_cache(c);
+  if (st != QGEMM_OK) return st;
+  *bytes = (size_t)c->num_pages * c->kv_heads * (size_t)block_geom(c).bytes;
+  return QGEMM_OK;
+}
+
+qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* p, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(QGEMM_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  qgemm_status_t st = validate_attention(p);
+  if (st != QGEMM_OK) return st;
+  AttnPlan pl;
+  st = make_attention_plan(p, &pl);
+  if (st != QGEMM_OK) return st;
+  *bytes = pl.ws_bytes;
+  return QGEMM_OK;
+}
+
+qgemm_status_t qgemm_attention_describe(const qgemm_attention_t* p, char* buf, size_t len) {
+  clear_error();
+  if (!buf || !len) return fail(QGEMM_ERR_INVALID_ARGUMENT, "buf is NULL or len is 0");
+  qgemm_status_t st = validate_attention(p);
+  if (st != QGEMM_OK) return st;
+  AttnPlan pl;
+  st = make_attention_plan(p, &pl);
+  if (st != QGEMM_OK) return st;
+  const int n = p->total_q == 0 ? std::snprintf(buf, len, "empty")
+                                : std::snprintf(buf, len, "rows grid=%u groups=%d", pl.grid, pl.groups);
+  if (n < 0 || (size_t)n >= len)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
+  return QGEMM_OK;
+}
+
+}  // extern "C"

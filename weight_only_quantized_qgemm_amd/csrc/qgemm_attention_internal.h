@@ -1,0 +1,43 @@
+// Internal declarations of the attention operators (include/qgemm_attention.h): what the host
+// validation and the kernel launchers share.
+#pragma once
+
+#include "../../include/qgemm_attention.h"
+#include "qgemm_internal.h"
+
+namespace qgemm {
+
+// Checks of the descriptors; the message names the field.
+qgemm_status_t validate_norm_rope(const qgemm_norm_rope_t* p);
+qgemm_status_t validate_cache(const qgemm_cache_t* c);
+qgemm_status_t validate_attention(const qgemm_attention_t* p);
+
+// Byte geometry of one block (one page of one kv head).
+struct BlockGeom {
+  int codes;      // bytes of one side's codes (= offset of the V codes)
+  int params;     // bytes of one side's parameters
+  int bytes;      // whole block
+};
+inline BlockGeom block_geom(const qgemm_cache_t* c) {
+  const int ng = c->head_dim / c->group_size;
+  BlockGeom g;
+  g.codes = c->page_size * c->head_dim / 2;
+  g.params = c->page_size * ng * 4;
+  g.bytes = 2 * (g.codes + g.params);
+  return g;
+}
+
+enum AttnKind : int { ATTN_ROWS = 1, ATTN_TILES = 2 };
+
+// Launch plan of qgemm_attention, a pure function of the descriptor.
+struct AttnPlan {
+  AttnKind kind;
+  int groups;          // NG
+  int rows;            // query rows per kv head and sequence, at most: ratio * max_q_len
+  unsigned grid;       // workgroups
+  size_t tickets_bytes;
+  size_t ws_bytes;
+};
+qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl);
+
+}  // namespace qgemm

@@ -1,0 +1,287 @@
+// qgemm_cache_write / qgemm_cache_read: the 4-bit paged key/value cache, in and out.
+//
+// Bound by memory: a 16-bit element in, half a byte and its share of two 16-bit parameters out (and
+// the other way round).  A head row of D elements is spread over D / 8 lanes, eight consecutive dims
+// (one 16-byte access and one dword of codes) each, so a wavefront holds 512 / D rows; they are
+// consecutive tokens of one kv head, whose K codes, V codes and parameters lie side by side when
+// their slots do.  A K dword goes out as it is.  V is stored by lane r = dim % 16, so the eight
+// codes of a lane belong to eight places: the row's dwords go through LDS (D / 2 bytes) and every
+// lane gathers the nibbles of its own place from there.
+#include <hip/hip_runtime.h>
+
+#include "qgemm_attention_internal.h"
+
+namespace {
+
+using namespace qgemm;
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+struct CacheArgs {
+  const uint16_t *k, *v;           // write: inputs
+  uint16_t *ko, *vo;               // read: outputs
+  uint8_t* data;
+  const long long* slots;
+  long long ks, vs;                // token strides in elements
+  long long total_slots;
+  int tokens, kv_heads, page, codes, params, block;
+};
+
+template <bool BF>
+__device__ __forceinline__ float from16(unsigned bits) {
+  if constexpr (BF) return __builtin_bit_cast(float, bits << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+template <bool BF>
+__device__ __forceinline__ unsigned to16(float v) {
+  if constexpr (BF) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// One row's place: its block, and the token's index in the page.
+struct Place {
+  uint8_t* block;
+  int t;
+  bool ok;
+};
+__device__ __forceinline__ Place place_of(const CacheArgs& a, int token, int head) {
+  Place p{nullptr, 0, false};
+  if (token >= a.tokens) return p;
+  const long long slot = a.slots[token];
+  if (slot < 0 || slot >= a.total_slots) return p;
+  const unsigned pg = (unsigned)((unsigned long long)slot / (unsigned)a.page);
+  p.t = (int)(slot - (long long)pg * a.page);
+  p.block = a.data + ((size_t)pg * a.kv_heads + head) * a.block;
+  p.ok = true;
+  return p;
+}
+
+// Quantizes the lane's eight elements within groups of G / 8 lanes: the codes as one dword and the
+// group's (scale, zero) as another.  Division and rounding are IEEE: the codes are those of the
+// header's formula in fp32.
+template <bool BF, int G>
+__device__ __forceinline__ void quantize8(u32x4 x, unsigned& codes, unsigned& par) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = from16<BF>(x[i] & 0xffffu);
+    f[2 * i + 1] = from16<BF>(x[i] >> 16);
+  }
+  float lo = f[0], hi = f[0];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bad |= !(__builtin_fabsf(f[i]) < __builtin_inff());       // fmin / fmax pass over a NaN
+    lo = __builtin_fminf(lo, f[i]);
+    hi = __builtin_fmaxf(hi, f[i]);
+  }
+  if (bad) hi = __builtin_inff();
+#pragma unroll
+  for (int m = 1; m < G / 8; m *= 2) {
+    lo = __builtin_fminf(lo, __shfl_xor(lo, m));
+    hi = __builtin_fmaxf(hi, __shfl_xor(hi, m));
+  }
+  const float span = hi - lo;
+  bad = !(span < __builtin_inff());
+  const unsigned sb = to16<BF>(span / 15.0f), zb = to16<BF>(lo);
+  const float s = from16<BF>(sb);
+  codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float c = __builtin_fminf(__builtin_fmaxf(__builtin_rintf((f[i] - lo) / s), 0.f), 15.f);
+    codes |= (s > 0.f && !bad ? (unsigned)(int)c : 0u) << (4 * i);
+  }
+  par = bad ? (BF ? 0x7fc07fc0u : 0x7e007e00u) : sb | zb << 16;
+}
+
+template <bool BF, int D, int NG>
+__global__ __launch_bounds__(256) void cache_write(CacheArgs a) {
+  constexpr int L = D / 8, R = 64 / L, U = D / 32, G = D / NG;
+  __shared__ unsigned rows[4][64];                      // a wavefront's V dwords
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane % L;
+  const int unit = blockIdx.x * 4 + wave;
+  const int head = unit % a.kv_heads;
+  const int token = unit / a.kv_heads * R + lane / L;
+  const Place p = place_of(a, token, head);
+  u32x4 kx = {0, 0, 0, 0}, vx = {0, 0, 0, 0};
+  if (p.ok) {
+    kx = *reinterpret_cast<const u32x4*>(a.k + token * a.ks + head * D + 8 * j);
+    vx = *reinterpret_cast<const u32x4*>(a.v + token * a.vs + head * D + 8 * j);
+  }
+  unsigned kc, kp, vc, vp;
+  quantize8<BF, G>(kx, kc, kp);
+  quantize8<BF, G>(vx, vc, vp);
+  rows[wave][lane] = vc;
+  __syncthreads();
+  if (!p.ok) return;
+  *reinterpret_cast<unsigned*>(p.block + p.t * (D / 2) + 4 * (U * (j & 3) + (j >> 2))) = kc;
+  const unsigned* row = rows[wave] + lane / L * L;
+  uint8_t* vb = p.block + a.codes + (p.t >> 2) * (64 * U) + (p.t & 3) * U;
+  // code of dim 16 i + r: dword 2 i + (r >> 3), nibble r & 7
+  if constexpr (D == 64) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = 2 * j + h;
+      unsigned w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w |= (row[2 * i + (r >> 3)] >> (4 * (r & 7)) & 15u) << (4 * i);
+      *reinterpret_cast<uint16_t*>(vb + r * (4 * U)) = (uint16_t)w;
+    }
+  } else {
+    const int r = D == 128 ? j : j >> 1, i0 = D == 128 ? 0 : 8 * (j & 1);
+    unsigned w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= (row[2 * (i0 + i) + (r >> 3)] >> (4 * (r & 7)) & 15u) << (4 * i);
+    *reinterpret_cast<unsigned*>(vb + r * (4 * U) + i0 / 2) = w;
+  }
+  if (j % (G / 8) == 0) {
+    const int at = (j / (G / 8) * a.page + p.t) * 4;
+    *reinterpret_cast<unsigned*>(p.block + 2 * a.codes + at) = kp;
+    *reinterpret_cast<unsigned*>(p.block + 2 * a.codes + a.params + at) = vp;
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ u32x4 values8(unsigned codes, unsigned par) {
+  const float s = from16<BF>(par & 0xffffu), z = from16<BF>(par >> 16);
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = to16<BF>(__builtin_fmaf((float)(codes >> (8 * i) & 15u), s, z)) |
+           to16<BF>(__builtin_fmaf((float)(codes >> (8 * i + 4) & 15u), s, z)) << 16;
+  return o;
+}
+
+template <bool BF, int D, int NG>
+__global__ __launch_bounds__(256) void cache_read(CacheArgs a) {
+  constexpr int L = D / 8, R = 64 / L, U = D / 32, G = D / NG;
+  __shared__ unsigned rows[4][64];                      // a wavefront's V units, by r
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane % L;
+  const int unit = blockIdx.x * 4 + wave;
+  const int head = unit % a.kv_heads;
+  const int token = unit / a.kv_heads * R + lane / L;
+  const Place p = place_of(a, token, head);
+  unsigned kc = 0, kp = 0, vp = 0;
+  // the row's V units, 16 bits (D = 64), a dword or two dwords for each r
+  uint16_t* row = reinterpret_cast<uint16_t*>(rows[wave]) + lane / L * (D / 4);
+  if (p.ok) {
+    kc = *reinterpret_cast<const unsigned*>(p.block + p.t * (D / 2) + 4 * (U * (j & 3) + (j >> 2)));
+    const int at = 2 * a.codes + (j / (G / 8) * a.page + p.t) * 4;
+    kp = *reinterpret_cast<const unsigned*>(p.block + at);
+    vp = *reinterpret_cast<const unsigned*>(p.block + at + a.params);
+    const uint8_t* vb = p.block + a.codes + (p.t >> 2) * (64 * U) + (p.t & 3) * U;
+    if constexpr (D == 64) {
+      row[2 * j] = *reinterpret_cast<const uint16_t*>(vb + 2 * j * (4 * U));
+      row[2 * j + 1] = *reinterpret_cast<const uint16_t*>(vb + (2 * j + 1) * (4 * U));
+    } else {
+      const int r = D == 128 ? j : j >> 1, i0 = D == 128 ? 0 : 8 * (j & 1);
+      *reinterpret_cast<unsigned*>(row + r * (U / 2) + i0 / 4) =
+          *reinterpret_cast<const unsigned*>(vb + r * (4 * U) + i0 / 2);
+    }
+  }
+  __syncthreads();
+  if (token >= a.tokens) return;
+  unsigned vc = 0;
+  if (p.ok) {
+    // dims 8 j + n: r = 8 (j & 1) + n, i = j >> 1
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      vc |= (unsigned)(row[(8 * (j & 1) + n) * (U / 2) + (j >> 3)] >> (4 * (j >> 1 & 3)) & 15) << (4 * n);
+  }
+  const size_t at = ((size_t)token * a.kv_heads + head) * D + 8 * j;
+  *reinterpret_cast<u32x4*>(a.ko + at) = values8<BF>(kc, kp);
+  *reinterpret_cast<u32x4*>(a.vo + at) = values8<BF>(vc, vp);
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+template <bool BF, int D, int NG>
+void launch_one(bool write, dim3 grid, hipStream_t s, const CacheArgs& a) {
+  if (write) cache_write<BF, D, NG><<<grid, dim3(256), 0, s>>>(a);
+  else cache_read<BF, D, NG><<<grid, dim3(256), 0, s>>>(a);
+}
+template <bool BF>
+void launch_type(int dim, int ng, bool write, dim3 grid, hipStream_t s, const CacheArgs& a) {
+  if (dim == 64) ng == 1 ? launch_one<BF, 64, 1>(write, grid, s, a) : launch_one<BF, 64, 2>(write, grid, s, a);
+  else if (dim == 128)
+    ng == 1 ? launch_one<BF, 128, 1>(write, grid, s, a)
+            : ng == 2 ? launch_one<BF, 128, 2>(write, grid, s, a) : launch_one<BF, 128, 4>(write, grid, s, a);
+  else
+    ng == 1 ? launch_one<BF, 256, 1>(write, grid, s, a)
+            : ng == 2 ? launch_one<BF, 256, 2>(write, grid, s, a) : launch_one<BF, 256, 4>(write, grid, s, a);
+}
+
+qgemm_status_t enqueue(const qgemm_cache_t* c, bool write, CacheArgs& a, const int64_t* slots, int64_t tokens, void* stream) {
+  const BlockGeom g = block_geom(c);
+  a.slots = reinterpret_cast<const long long*>(slots);
+  a.total_slots = c->num_pages * c->page_size;
+  a.tokens = (int)tokens;
+  a.kv_heads = c->kv_heads;
+  a.page = c->page_size;
+  a.codes = g.codes;
+  a.params = g.params;
+  a.block = g.bytes;
+  const int rows = 512 / c->head_dim;
+  const int64_t units = (tokens + rows - 1) / rows * c->kv_heads;
+  if (units > 0x7ffffff0LL)
+    return fail(QGEMM_ERR_UNSUPPORTED, "tokens * kv_heads needs %lld wavefronts, more than one launch allows", (long long)units);
+  const dim3 grid((unsigned)((units + 3) / 4));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int ng = c->head_dim / c->group_size;
+  if (c->dtype == QGEMM_DT_BF16) launch_type<true>(c->head_dim, ng, write, grid, s, a);
+  else launch_type<false>(c->head_dim, ng, write, grid, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(QGEMM_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  return QGEMM_OK;
+}
+
+qgemm_status_t check_common(const qgemm_cache_t* c, const void* data, const int64_t* slots, int64_t tokens) {
+  const qgemm_status_t st = validate_cache(c);
+  if (st != QGEMM_OK) return st;
+  if (tokens < 0 || tokens > (int64_t(1) << 24))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "tokens must be in [0, 2^24], got %lld", (long long)tokens);
+  if (tokens == 0) return QGEMM_OK;
+  if (!data) return fail(QGEMM_ERR_INVALID_ARGUMENT, "data is NULL");
+  if (!slots) return fail(QGEMM_ERR_INVALID_ARGUMENT, "slots is NULL");
+  if (!aligned(data, 16)) return fail(QGEMM_ERR_MISALIGNED, "data must be 16-byte aligned");
+  if (!aligned(slots, 8)) return fail(QGEMM_ERR_MISALIGNED, "slots must be 8-byte aligned");
+  return QGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" qgemm_status_t qgemm_cache_write(const qgemm_cache_t* c, void* data, const void* k, int64_t k_stride,
+                                            const void* v, int64_t v_stride, const int64_t* slots, int64_t tokens,
+                                            void* stream) {
+  clear_error();
+  const qgemm_status_t st = check_common(c, data, slots, tokens);
+  if (st != QGEMM_OK || tokens == 0) return st;
+  if (!k || !v) return fail(QGEMM_ERR_INVALID_ARGUMENT, "k or v is NULL");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(QGEMM_ERR_MISALIGNED, "k and v must be 16-byte aligned");
+  const int64_t row = (int64_t)c->kv_heads * c->head_dim;
+  for (int64_t s : {k_stride, v_stride})
+    if (s < row || s % 8 || s > (int64_t(1) << 31))
+      return fail(QGEMM_ERR_INVALID_ARGUMENT, "token strides must be multiples of 8 in [%lld, 2^31], got %lld",
+                  (long long)row, (long long)s);
+  CacheArgs a{};
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.ks = k_stride;
+  a.vs = v_stride;
+  a.data = static_cast<uint8_t*>(data);
+  return enqueue(c, true, a, slots, tokens, stream);
+}
+
+extern "C" qgemm_status_t qgemm_cache_read(const qgemm_cache_t* c, const void* data, const int64_t* slots, int64_t tokens,
+                                           void* k_out, void* v_out, void* stream) {
+  clear_error();
+  const qgemm_status_t st = check_common(c, data, slots, tokens);
+  if (st != QGEMM_OK || tokens == 0) return st;
+  if (!k_out || !v_out) return fail(QGEMM_ERR_INVALID_ARGUMENT, "k_out or v_out is NULL");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(QGEMM_ERR_MISALIGNED, "k_out and v_out must be 16-byte aligned");
+  CacheArgs a{};
+  a.ko = static_cast<uint16_t*>(k_out);
+  a.vo = static_cast<uint16_t*>(v_out);
+  a.data = const_cast<uint8_t*>(static_cast<const uint8_t*>(data));
+  return enqueue(c, false, a, slots, tokens, stream);
+}
