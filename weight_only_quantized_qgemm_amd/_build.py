@@ -19,9 +19,12 @@ PROBE_LIB = os.path.join(PKG, "libqgemm_probe.so")
 # Weight formats (the Format enum of csrc/qgemm_internal.h).  Each kernel source is compiled
 # once per format (-DQGEMM_FMT_UNIT), so the many kernel instances build in parallel.
 N_FORMATS = 6
-# The attention operators (include/qgemm_attention.h) build whole.
+# The attention kernels are compiled once per element type and head dim (QGEMM_ATTN_UNIT), the
+# other sources whole.
+N_ATTN_UNITS = 6
 UNITS = ([("qgemm_host.cpp", []), ("qgemm_run.hip", []), ("qgemm_attention_host.cpp", []), ("qgemm_heads.hip", []),
           ("qgemm_cache.hip", []), ("qgemm_attention.hip", [])]
+         + [("qgemm_attention_rows.hip", [f"-DQGEMM_ATTN_UNIT={u}"]) for u in range(N_ATTN_UNITS)]
          + [(k, [f"-DQGEMM_FMT_UNIT={f}"]) for k in ("qgemm_decode.hip", "qgemm_prefill.hip", "qgemm_prefill_tw.hip")
             for f in range(N_FORMATS)])
 

@@ -10,29 +10,13 @@
 // running maximum and sum of the softmax, then one dim a lane for the output.
 #include <hip/hip_runtime.h>
 
-#include "qgemm_attention_internal.h"
+#include "qgemm_attention_device.h"
 
 namespace {
 
 using namespace qgemm;
 
-struct AttnArgs {
-  const uint16_t* q;
-  const uint8_t* data;
-  const int *table, *lens, *starts;
-  uint16_t* out;
-  long long qs, os;
-  int total_q, batch, q_heads, kv_heads, ratio, max_pages, page, num_pages;
-  int codes, params, block;
-  int max_q, causal, window;
-  float scale;
-};
-
-template <bool BF>
-__device__ __forceinline__ float from16(unsigned bits) {
-  if constexpr (BF) return __builtin_bit_cast(float, bits << 16);
-  else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
-}
+using namespace attn;
 
 template <bool BF, int D, int NG>
 __global__ __launch_bounds__(64) void attention_row(AttnArgs a) {
@@ -78,7 +62,7 @@ __global__ __launch_bounds__(64) void attention_row(AttnArgs a) {
         const unsigned par = *reinterpret_cast<const unsigned*>(blk + 2 * a.codes + (g * a.page + in) * 4);
         s += from16<BF>(par & 0xffffu) * acc + from16<BF>(par >> 16) * qsum;
       }
-      s *= a.scale;
+      s *= a.scale * 0.6931471805599453f;
     }
     float mt = s;
     for (int x = 1; x < 64; x *= 2) mt = __builtin_fmaxf(mt, __shfl_xor(mt, x));
@@ -183,11 +167,26 @@ extern "C" qgemm_status_t qgemm_attention(const qgemm_attention_t* p, const void
   a.max_q = p->max_q_len;
   a.causal = p->causal;
   a.window = p->window;
-  a.scale = p->scale;
+  a.scale = p->scale * 1.4426950408889634f;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (p->cache.dtype == QGEMM_DT_BF16) launch_type<true>(p->cache.head_dim, pl.groups, dim3(pl.grid), s, a);
-  else launch_type<false>(p->cache.head_dim, pl.groups, dim3(pl.grid), s, a);
-  const hipError_t e = hipGetLastError();
+  hipError_t e;
+  if (pl.kind == ATTN_ROWS) {
+    a.units_min = pl.units_min;
+    a.tickets = static_cast<unsigned*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.tickets_bytes);
+    switch ((p->cache.dtype == QGEMM_DT_BF16 ? 3 : 0) + (p->cache.head_dim == 64 ? 0 : p->cache.head_dim == 128 ? 1 : 2)) {
+      case 0: e = launch_rows<false, 64>(pl, a, s); break;
+      case 1: e = launch_rows<false, 128>(pl, a, s); break;
+      case 2: e = launch_rows<false, 256>(pl, a, s); break;
+      case 3: e = launch_rows<true, 64>(pl, a, s); break;
+      case 4: e = launch_rows<true, 128>(pl, a, s); break;
+      default: e = launch_rows<true, 256>(pl, a, s); break;
+    }
+  } else {
+    if (p->cache.dtype == QGEMM_DT_BF16) launch_type<true>(p->cache.head_dim, pl.groups, dim3(pl.grid), s, a);
+    else launch_type<false>(p->cache.head_dim, pl.groups, dim3(pl.grid), s, a);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return fail(QGEMM_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return QGEMM_OK;
 }

@@ -12,6 +12,7 @@ static_assert(sizeof(qgemm_norm_rope_t) == 48, "qgemm_norm_rope_t layout is part
 static_assert(sizeof(qgemm_cache_t) == 32, "qgemm_cache_t layout is part of the ABI");
 static_assert(sizeof(qgemm_attention_t) == 80, "qgemm_attention_t layout is part of the ABI");
 
+static const int kCUs = 256;
 static const int64_t kMaxTokens = int64_t(1) << 24;
 
 static qgemm_status_t check_dtype_dim(const char* what, int dtype, int head_dim) {
@@ -97,11 +98,29 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   std::memset(pl, 0, sizeof(*pl));
   if (p->total_q == 0) return QGEMM_OK;
   pl->groups = p->cache.head_dim / p->cache.group_size;
+  const int64_t rows = (int64_t)(p->q_heads / p->cache.kv_heads) * p->max_q_len;
+  const int dim = p->cache.head_dim;
+  pl->rows = (int)(rows < 0x7fffffff ? rows : 0x7fffffff);
+  pl->kind = p->kernel_hint == QGEMM_ATTENTION_TILES || (p->kernel_hint == QGEMM_ATTENTION_AUTO && rows > 64) ? ATTN_TILES
+                                                                                                         : ATTN_ROWS;
+  if (pl->kind == ATTN_ROWS) {
+    pl->pack = rows <= 4 && dim < 256 ? 4 : rows <= 8 ? 2 : 1;
+    pl->col_tiles = rows > 16 && pl->groups == 1 && dim < 256 ? 2 : 1;
+    const int row_tile = 16 / pl->pack * pl->col_tiles;
+    const int64_t tokens = (int64_t)p->max_pages * p->cache.page_size;
+    const int64_t units = (tokens + 63) / 64 + 1, tiles = (rows + row_tile - 1) / row_tile;
+    if ((double)units * tiles * p->cache.kv_heads * p->batch > 2147483647.0)
+      return fail(QGEMM_ERR_UNSUPPORTED, "batch * kv_heads * tokens (%d * %d * %lld) is beyond what one launch divides",
+                  p->batch, p->cache.kv_heads, (long long)tokens);
+    pl->units_min = 4;
+    pl->grid = 2 * kCUs;
+    pl->tickets_bytes = ((size_t)pl->grid * 4 + 255) / 256 * 256;
+    pl->ws_bytes = pl->tickets_bytes + (size_t)2 * pl->grid * row_tile * (dim + 4) * 4;
+    return QGEMM_OK;
+  }
   const int64_t units = p->total_q * p->q_heads;
   if (units > 0x7fffffffLL)
     return fail(QGEMM_ERR_UNSUPPORTED, "total_q * q_heads is %lld, more than one launch allows", (long long)units);
-  pl->kind = ATTN_ROWS;
-  pl->rows = p->q_heads / p->cache.kv_heads * p->max_q_len;
   pl->grid = (unsigned)units;
   return QGEMM_OK;
 }
@@ -142,7 +161,9 @@ qgemm_status_t qgemm_attention_describe(const qgemm_attention_t* p, char* buf, s
   st = make_attention_plan(p, &pl);
   if (st != QGEMM_OK) return st;
   const int n = p->total_q == 0 ? std::snprintf(buf, len, "empty")
-                                : std::snprintf(buf, len, "rows grid=%u groups=%d", pl.grid, pl.groups);
+                : pl.kind == ATTN_ROWS ? std::snprintf(buf, len, "rows grid=%u groups=%d pack=%d col_tiles=%d", pl.grid,
+                                                       pl.groups, pl.pack, pl.col_tiles)
+                                       : std::snprintf(buf, len, "tiles grid=%u groups=%d", pl.grid, pl.groups);
   if (n < 0 || (size_t)n >= len)
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
   return QGEMM_OK;

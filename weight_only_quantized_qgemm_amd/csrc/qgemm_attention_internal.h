@@ -34,6 +34,9 @@ struct AttnPlan {
   AttnKind kind;
   int groups;          // NG
   int rows;            // query rows per kv head and sequence, at most: ratio * max_q_len
+  int pack;            // rows kernel: subtiles side by side in the 16 columns (F: 1, 2, 4)
+  int col_tiles;       // rows kernel: column tiles of 16 rows (NC: 1, 2)
+  int units_min;       // rows kernel: least units of 64 tokens per workgroup
   unsigned grid;       // workgroups
   size_t tickets_bytes;
   size_t ws_bytes;

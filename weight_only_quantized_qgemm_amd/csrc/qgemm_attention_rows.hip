@@ -1,0 +1,594 @@
+// Attention with few query rows per kv head (one token, a few drafted ones): the cache is read once,
+// tokens spread over wavefronts and workgroups.
+//
+// Bound by reading the cache: D + 8 NG bytes per token and kv head.  The work is cut into units of 64
+// tokens of one (sequence, kv head, row tile), laid end to end, and every workgroup of a fixed grid
+// takes an equal run of them, found from the lengths in device memory: the balance does not depend
+// on how the lengths differ, and the host needs none of them.  A segment that several workgroups
+// share is joined by the last of them to finish, in order (a ticket per segment; nobody waits).
+//
+// Inside a workgroup the four wavefronts take steps of 16 SUB tokens in turn, each with its own
+// running maximum, sum and output, joined through LDS.  The 16 columns of an MFMA are more than
+// most calls have query rows, so with F = 2 or 4 each column group of 16 / F holds the same rows for
+// another 16-token subtile: the softmax then works on full lanes, and its cost per token falls by F.
+#include "qgemm_attention_device.h"
+
+namespace qgemm {
+namespace attn {
+namespace {
+
+template <int D, int NG, int F>
+struct Step {                                       // one step's bytes, in registers
+  static constexpr int U = D / 32, SUB = F == 1 ? 2 : F, ST = F == 1 ? 2 : 1;
+  unsigned k[SUB][U], v[SUB][U];
+  u32x4 kp[ST][NG], vp[ST][NG];
+};
+
+template <int U>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, unsigned (&w)[U]) {
+  if constexpr (U == 2) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    w[0] = x[0];
+    w[1] = x[1];
+  } else {
+#pragma unroll
+    for (int j = 0; j < U / 4; ++j) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 16 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * j + i] = x[i];
+    }
+  }
+}
+
+template <bool BF, int D, int NG, int F, int NC>
+__global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
+  constexpr int U = D / 32, SUB = F == 1 ? 2 : F, ST = F == 1 ? 2 : 1, T = 16 * SUB;
+  constexpr int R16 = 16 / F, RT = R16 * NC;        // rows per column tile, rows per row tile
+  constexpr int TILES = D / 16, TG = TILES / NG;    // output tiles, and those of one group
+  constexpr int SG = U / NG;                        // k steps of one group
+  constexpr int kRowF = D + 4;                      // padded floats of an LDS row
+  constexpr int kSlot = RT * (D + 4);               // floats of a partial: rows, then (max, sum) pairs
+  typedef Step<D, NG, F> StepT;
+  __shared__ __align__(16) float s_o[4 * 16 * kRowF];
+  __shared__ float s_m[4 * 16], s_l[4 * 16];
+  __shared__ int s_last;
+
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int fcol = m / R16;                         // the lane's subtile of a step (F > 1)
+  const int wg = blockIdx.x;
+
+  // ---- this workgroup's run of units
+  auto units_of = [&](const Seq& s) {
+    if (!s.n) return 0;
+    return a.kv_heads * ((a.ratio * s.n + RT - 1) / RT) * max(1, (s.hi - s.lo + 63) / 64);
+  };
+  int total = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    int u = b0 + lane < a.batch ? units_of(load_seq(a, b0 + lane)) : 0;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) u += __shfl_xor(u, x);
+    total += u;
+  }
+  total = __builtin_amdgcn_readfirstlane(total);
+  if (!total) return;
+  const int G = min((int)gridDim.x, (total + a.units_min - 1) / a.units_min);
+  if (wg >= G) return;
+  const int uq = total / G, ur = total - uq * G;
+  int u0 = wg * uq + min(wg, ur);
+  const int u1 = u0 + uq + (wg < ur ? 1 : 0);
+  auto owner = [&](int u) { return u < ur * (uq + 1) ? u / (uq + 1) : ur + (u - ur * (uq + 1)) / uq; };
+  // the sequence that holds unit u0
+  int b = 0, before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    int u = b0 + lane < a.batch ? units_of(load_seq(a, b0 + lane)) : 0;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+      const int y = __shfl_up(u, x);
+      if (lane >= x) u += y;
+    }
+    const unsigned long long past = __ballot(before + u > u0);      // the first lane whose end lies past u0
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      b = b0 + l;
+      before += l ? __builtin_amdgcn_readlane(u, l - 1) : 0;
+      break;
+    }
+    before += __builtin_amdgcn_readlane(u, 63);
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
+  before = __builtin_amdgcn_readfirstlane(before);
+
+  while (u0 < u1) {
+    Seq s = load_seq(a, b);
+    const int ub = units_of(s);
+    if (u0 >= before + ub) {                        // next sequence (some hold nothing)
+      before += ub;
+      ++b;
+      continue;
+    }
+    const int nu = max(1, (s.hi - s.lo + 63) / 64);
+    const int seg = (u0 - before) / nu, first = before + seg * nu;   // segment, its first unit
+    const int take = min(first + nu - u0, u1 - u0);
+    const int rt = seg / a.kv_heads, kvh = seg - rt * a.kv_heads;
+    const int ts = s.lo + 64 * (u0 - first), te = min(s.hi, ts + 64 * take);
+
+    // ---- queries: rows rt RT + nc R16 + m % R16, row = query * ratio + head within the group
+    u32x4 qf[F == 1 ? 1 : F][U][NC];
+    float qz[NC][NG];
+    int see_lo[NC], see_hi[NC];
+    float kq;
+    const int rows = a.ratio * s.n;
+    {
+      u32x4 raw[NC][U];
+      float top = 0.f;
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        const int row = rt * RT + nc * R16 + m % R16;
+        const bool on = row < rows;
+        const int i = on ? row / a.ratio : 0, h = row - i * a.ratio;
+        const int pos = s.len - s.n + i;
+        see_hi[nc] = a.causal ? min(pos + 1, s.len) : s.len;
+        see_lo[nc] = a.window ? pos - a.window + 1 : 0;
+        const uint16_t* src = a.q + (long long)(s.start + i) * a.qs + (kvh * a.ratio + h) * D + 8 * g;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          raw[nc][j] = on ? *reinterpret_cast<const u32x4*>(src + 32 * j) : u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const float x = __builtin_fabsf(from16<BF>(raw[nc][j][e] >> (16 * o) & 0xffffu));
+              top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
+            }
+        }
+      }
+#pragma unroll
+      for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+      // top = f 2^e, f in [1/2, 1)
+      const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
+      kq = __builtin_ldexpf(a.scale, 24 - 14 + e);
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = gr * SG; j < (gr + 1) * SG; ++j) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              x[k] = from16<BF>(raw[nc][j][k / 2] >> (16 * (k & 1)) & 0xffffu);
+              sum += x[k];
+            }
+            u32x4 f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int sh = 14 - e - ((k & 1) ? 4 : 0);
+              f[k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
+            }
+            if constexpr (F == 1) {
+              qf[0][j][nc] = f;
+            } else {
+#pragma unroll
+              for (int ff = 0; ff < F; ++ff) qf[ff][j][nc] = fcol == ff ? f : u32x4{0, 0, 0, 0};
+            }
+          }
+          sum += __shfl_xor(sum, 16);
+          sum += __shfl_xor(sum, 32);
+          qz[nc][gr] = sum * a.scale;
+        }
+    }
+    // tokens that every row sees
+    const int last = min(rows - 1, rt * RT + RT - 1);
+    const int all_hi = a.causal ? min(s.len, s.len - s.n + rt * RT / a.ratio + 1) : s.len;
+    const int all_lo = a.window ? s.len - s.n + last / a.ratio - a.window + 1 : 0;
+
+    // ---- the wavefront's steps: token ts + T (wave + 4 j)
+    float mx[NC], l[NC], zs[NC][NG], ps[NC][NG];
+    f32x4 o[NC][TILES];
+    // a row's value scales are divided by 2^sig (inv = 2^-sig), a bound of those it has seen
+    int sig[NC];
+    float inv[NC];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      mx[nc] = kStart;
+      l[nc] = 0.f;
+      sig[nc] = -126;
+      inv[nc] = 0x1p126f;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) zs[nc][gr] = ps[nc][gr] = 0.f;
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int steps = te > ts ? (te - ts + T - 1) / T : 0;
+    const int mine = steps > wave ? (steps - wave + 3) / 4 : 0;
+    constexpr int PER = 64 / SUB;                   // steps whose pages one register holds
+    const uint8_t* blk = nullptr;
+    int in = 0;
+    auto pages = [&](int j0) {                      // lane x: subtile x % SUB of step j0 + x / SUB
+      int t = ts + T * (wave + 4 * (j0 + lane / SUB)) + 16 * (lane % SUB);
+      t = min(t, (te - 1) & ~15);                   // past the end: the last subtile again (masked)
+      const int p = t / a.page;
+      int pg = a.table[(long long)b * a.max_pages + p];
+      if ((unsigned)pg >= (unsigned)a.num_pages) pg = 0;
+      in = t - p * a.page;
+      blk = a.data + ((long long)pg * a.kv_heads + kvh) * a.block;
+    };
+    auto fetch = [&](int j, StepT& st) {
+      const int x0 = j % PER * SUB;
+#pragma unroll
+      for (int f = 0; f < SUB; ++f) {
+        const unsigned long long bits = reinterpret_cast<unsigned long long>(blk);
+        const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)bits, x0 + f);
+        const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(bits >> 32), x0 + f);
+        const uint8_t* p = reinterpret_cast<const uint8_t*>((unsigned long long)hi << 32 | lo);
+        const int at = __builtin_amdgcn_readlane(in, x0 + f);
+        load_dwords<U>(p + (at * (D / 2) + (m * (D / 2) + 4 * U * g)), st.k[f]);
+        load_dwords<U>(p + a.codes + (at * (D / 2) + lane * (4 * U)), st.v[f]);
+      }
+#pragma unroll
+      for (int x = 0; x < ST; ++x) {
+        const int src = x0 + (F == 1 ? x : fcol);
+        const unsigned long long bits = reinterpret_cast<unsigned long long>(blk);
+        const unsigned lo = __shfl((int)(unsigned)bits, src), hi = __shfl((int)(unsigned)(bits >> 32), src);
+        const uint8_t* p = reinterpret_cast<const uint8_t*>((unsigned long long)hi << 32 | lo) + 2 * a.codes +
+                           4 * (__shfl(in, src) + 4 * g);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          st.kp[x][gr] = *reinterpret_cast<const u32x4*>(p + 4 * gr * a.page);
+          st.vp[x][gr] = *reinterpret_cast<const u32x4*>(p + a.params + 4 * gr * a.page);
+        }
+      }
+    };
+    auto compute = [&](int j, const StepT& st) {
+      const int t0 = ts + T * (wave + 4 * j);
+      // S^T
+      f32x4 acc[NC][ST][NG];
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int x = 0; x < ST; ++x)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) acc[nc][x][gr] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int f = 0; f < SUB; ++f)
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const u32x4 kf = codes8(st.k[f][i]);
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            f32x4& c = acc[nc][F == 1 ? f : 0][i / SG];
+            c = mfma(kf, qf[F == 1 ? 0 : f][i][nc], c);
+          }
+        }
+      const bool edge = t0 + T > min(all_hi, te) || t0 < all_lo;
+      // scores in bits relative to the running maximum
+      float u[NC][ST][4];
+      auto score = [&](bool base) {
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float v = base ? -mx[nc] : 0.f;
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) {
+                const unsigned w = st.kp[x][gr][r];
+                v = __builtin_fmaf(par_zero<BF>(w), qz[nc][gr], v);
+                v = __builtin_fmaf(par_scale<BF>(w) * kq, acc[nc][x][gr][r], v);
+              }
+              u[nc][x][r] = v;
+            }
+      };
+      unsigned seen[NC];                            // bit 4 x + r, set in edge steps only
+      auto mask = [&]() {
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (!(seen[nc] >> (4 * x + r) & 1)) u[nc][x][r] = -__builtin_inff();
+      };
+      float vs[ST][NG][4], vm[ST][NG][4];           // scale, zero + 8 scale
+#pragma unroll
+      for (int x = 0; x < ST; ++x)
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const unsigned w = st.vp[x][gr][r];
+            vs[x][gr][r] = par_scale<BF>(w);
+            vm[x][gr][r] = __builtin_fmaf(vs[x][gr][r], 8.f, par_zero<BF>(w));
+          }
+      if (edge) {
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          seen[nc] = 0;
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int t = t0 + 16 * (F == 1 ? x : fcol) + 4 * g + r;
+              if (t >= see_lo[nc] && t < see_hi[nc] && t < te) seen[nc] |= 1u << (4 * x + r);
+            }
+        }
+      }
+      // the largest value scale that each row sees
+      float big[NC];
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        big[nc] = 0.f;
+#pragma unroll
+        for (int x = 0; x < ST; ++x)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float v = __builtin_fabsf(vs[x][gr][r]);
+              big[nc] = __builtin_fmaxf(big[nc], edge && !(seen[nc] >> (4 * x + r) & 1) ? 0.f : v);
+            }
+      }
+      score(true);
+      if (edge) mask();
+      bool move = false;
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        float high = u[nc][0][0];
+#pragma unroll
+        for (int x = 0; x < ST; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, u[nc][x][r]);
+        move |= high > kSlack || big[nc] * inv[nc] > kScaleSlack;
+      }
+      if (__any(move)) {
+        // move the running maxima and value scales that need it, rescale what is summed so far
+        score(false);
+        if (edge) mask();
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          float top = kStart;
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) top = __builtin_fmaxf(top, u[nc][x][r]);
+          top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+          // a row's maximum moves for its own scores only: its result does not depend on its neighbours
+          const float nm = top > mx[nc] + kSlack ? top : mx[nc];
+          float smax = big[nc];
+          smax = __builtin_fmaxf(smax, __shfl_xor(smax, 16));
+          smax = __builtin_fmaxf(smax, __shfl_xor(smax, 32));
+          const int ns = smax * inv[nc] > kScaleSlack ? __builtin_amdgcn_frexp_expf(smax) : sig[nc];
+          const float al = exp2_fast(mx[nc] - nm), ab = __builtin_ldexpf(al, sig[nc] - ns);
+          mx[nc] = nm;
+          sig[nc] = ns;
+          inv[nc] = __builtin_ldexpf(1.f, -ns);
+          l[nc] *= al;
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            zs[nc][gr] *= al;
+            ps[nc][gr] *= ab;
+          }
+#pragma unroll
+          for (int i = 0; i < TILES; ++i) o[nc][i] *= ab;
+        }
+        score(true);
+        if (edge) mask();
+      }
+      // weights
+      unsigned pk[NC][ST][NG][2];
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int x = 0; x < ST; ++x) {
+          float p[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            p[r] = exp2_fast(u[nc][x][r]);
+            l[nc] += p[r];
+          }
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            float w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float sc = vs[x][gr][r] * inv[nc], md = vm[x][gr][r];
+              if (edge && !(seen[nc] >> (4 * x + r) & 1)) sc = md = 0.f;
+              w[r] = p[r] * sc;
+              zs[nc][gr] = __builtin_fmaf(p[r], md, zs[nc][gr]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // rounded to 11 bits, and summed as rounded: the codes' middle is taken out exactly
+              const unsigned v = pack_f16(w[2 * h], w[2 * h + 1]);
+              ps[nc][gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), f16x2{(_Float16)1.f, (_Float16)1.f},
+                                                  ps[nc][gr], false);
+              pk[nc][x][gr][h] = v;
+            }
+          }
+        }
+      // O^T += V^T P^T, two subtiles at a time
+#pragma unroll
+      for (int pr = 0; pr < SUB / 2; ++pr) {
+        u32x4 bp[NC][NG];
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if constexpr (F == 1) {
+                bp[nc][gr][h] = pk[nc][0][gr][h];
+                bp[nc][gr][2 + h] = pk[nc][ST - 1][gr][h];
+              } else {
+                bp[nc][gr][h] = fcol == 2 * pr ? pk[nc][0][gr][h] : 0u;
+                bp[nc][gr][2 + h] = fcol == 2 * pr + 1 ? pk[nc][0][gr][h] : 0u;
+              }
+            }
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+          u32x4 vf;
+          unsigned x0, x1, y0, y1;
+          v_pairs<U>(st.v[2 * pr], i, x0, x1);
+          v_pairs<U>(st.v[2 * pr + 1], i, y0, y1);
+          vf = u32x4{x0, x1, y0, y1};
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[nc][i / TG], o[nc][i]);
+        }
+      }
+    };
+    if (mine) {
+      StepT sa, sb;
+      pages(0);
+      fetch(0, sa);
+      for (int j = 0; j < mine; j += 2) {
+        // PER is even, so only the step after an odd one can need new pages
+        if (j + 1 < mine) fetch(j + 1, sb);
+        compute(j, sa);
+        if (j + 2 < mine) {
+          if ((j + 2) % PER == 0) pages(j + 2);
+          fetch(j + 2, sa);
+        }
+        if (j + 1 < mine) compute(j + 1, sb);
+      }
+    }
+
+    // ---- join: the wavefront's sums over its lanes, the columns and wavefronts through LDS
+    const bool whole = take == nu;
+    float* slot = a.partials + (size_t)(2 * wg + (first < u0 ? 0 : 1)) * kSlot;
+    const __amdgpu_buffer_rsrc_t mydst = buffer_of(slot, kSlot * 4);
+    auto write_out = [&](int row, int d, f32x4 v, float sum) {
+      const int gi = rt * RT + row;
+      if (gi >= rows) return;
+      const int i = gi / a.ratio, h = gi - i * a.ratio;
+      const float r = sum == 0.f ? 0.f : 1.0f / sum;
+      // a sum of 0: nothing was seen, and every partial output is 0 as well
+      u32x2 w{pack2<BF>(v[0] * r, v[1] * r), pack2<BF>(v[2] * r, v[3] * r)};
+      *reinterpret_cast<u32x2*>(a.out + (long long)(s.start + i) * a.os + (kvh * a.ratio + h) * D + d) = w;
+    };
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      const float back = __builtin_ldexpf(1.f, sig[nc]);
+      float sl = l[nc], sz[NG], sp[NG];
+      sl += __shfl_xor(sl, 16);
+      sl += __shfl_xor(sl, 32);
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        sz[gr] = zs[nc][gr];
+        sp[gr] = ps[nc][gr];
+        sz[gr] += __shfl_xor(sz[gr], 16);
+        sp[gr] += __shfl_xor(sp[gr], 16);
+        sz[gr] += __shfl_xor(sz[gr], 32);
+        sp[gr] += __shfl_xor(sp[gr], 32);
+      }
+      __syncthreads();                              // the previous column tile (or segment) is done with LDS
+      if (g == 0) {
+        s_m[wave * 16 + m] = mx[nc];
+        s_l[wave * 16 + m] = sl;
+      }
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        const float up = (i & 1) ? 0x1p20f : 0x1p24f;
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[r] = __builtin_fmaf(__builtin_fmaf(o[nc][i][r], up, -8.f * sp[i / TG]), back, sz[i / TG]);
+        *reinterpret_cast<f32x4*>(&s_o[(wave * 16 + m) * kRowF + 16 * i + 4 * g]) = v;
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < R16 * (D / 4); e += 256) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        float top = kStart;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int f = 0; f < F; ++f) top = __builtin_fmaxf(top, s_m[w * 16 + f * R16 + row]);
+        float sum = 0.f;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            const int c = w * 16 + f * R16 + row;
+            const float sc = exp2_fast(s_m[c] - top);
+            sum = __builtin_fmaf(s_l[c], sc, sum);
+            v += *reinterpret_cast<const f32x4*>(&s_o[c * kRowF + d]) * sc;
+          }
+        if (whole) {
+          write_out(nc * R16 + row, d, v, sum);
+        } else {
+          store4(mydst, ((nc * R16 + row) * D + d) * 4, v);
+          if (d == 0) store4(mydst, (RT * D + 4 * (nc * R16 + row)) * 4, f32x4{top, sum, 0.f, 0.f});
+        }
+      }
+    }
+    if (!whole) {
+      const int w0 = owner(first), w1 = owner(first + nu - 1);
+      __builtin_amdgcn_s_waitcnt(0);                // this thread's partial stores are complete
+      __syncthreads();
+      if (threadIdx.x == 0)
+        s_last = __hip_atomic_fetch_add(a.tickets + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 (unsigned)(w1 - w0);
+      __syncthreads();
+      if (s_last) {
+        for (int e = threadIdx.x; e < RT * (D / 4); e += 256) {
+          const int row = e / (D / 4), d = e % (D / 4) * 4;
+          float top = kStart, sum = 0.f;
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+          for (int w = w0; w <= w1; ++w) {
+            // a segment's first piece is the tail of its workgroup's run, the others are heads of theirs
+            float* from = a.partials + (size_t)(2 * w + (w == w0 ? 1 : 0)) * kSlot;
+            const __amdgpu_buffer_rsrc_t src = buffer_of(from, kSlot * 4);
+            const f32x4 ml = load4(src, (RT * D + 4 * row) * 4);
+            const f32x4 x = load4(src, (row * D + d) * 4);
+            const float nm = __builtin_fmaxf(top, ml[0]);
+            const float old = exp2_fast(top - nm), sc = exp2_fast(ml[0] - nm);
+            top = nm;
+            sum = sum * old + ml[1] * sc;
+            v = v * old + x * sc;
+          }
+          write_out(row, d, v, sum);
+        }
+        if (threadIdx.x == 0) __hip_atomic_store(a.tickets + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+    }
+    u0 += take;
+  }
+}
+
+template <bool BF, int D, int NG>
+hipError_t launch_groups(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
+  const dim3 grid(pl.grid), block(256);
+  if (pl.pack == 4) {
+    if constexpr (D < 256) attention_rows<BF, D, NG, 4, 1><<<grid, block, 0, s>>>(a);
+  } else if (pl.pack == 2) {
+    attention_rows<BF, D, NG, 2, 1><<<grid, block, 0, s>>>(a);
+  } else if (pl.col_tiles == 1) {
+    attention_rows<BF, D, NG, 1, 1><<<grid, block, 0, s>>>(a);
+  } else {
+    if constexpr (D < 256 && NG == 1) attention_rows<BF, D, NG, 1, 2><<<grid, block, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+template <bool BF, int D>
+hipError_t launch_rows(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
+  if (pl.groups == 1) return launch_groups<BF, D, 1>(pl, a, s);
+  if (pl.groups == 2) return launch_groups<BF, D, 2>(pl, a, s);
+  if constexpr (D > 64) return launch_groups<BF, D, 4>(pl, a, s);
+  return hipErrorInvalidValue;
+}
+
+#ifndef QGEMM_ATTN_UNIT
+#error "compiled once per element type and head dim: QGEMM_ATTN_UNIT = 3 * bf16 + (0, 1, 2 for head dim 64, 128, 256)"
+#endif
+template hipError_t launch_rows<(QGEMM_ATTN_UNIT >= 3), (64 << (QGEMM_ATTN_UNIT % 3))>(const AttnPlan&, const AttnArgs&,
+                                                                                    hipStream_t);
+
+}  // namespace attn
+}  // namespace qgemm
