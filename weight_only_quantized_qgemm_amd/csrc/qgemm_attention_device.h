@@ -146,6 +146,8 @@ __device__ __forceinline__ f32x4 load4(__amdgpu_buffer_rsrc_t r, int at) {
 // Launchers of one element type and head dim; each kernel source instantiates these per object.
 template <bool BF, int D>
 hipError_t launch_rows(const AttnPlan& pl, const AttnArgs& a, hipStream_t s);
+template <bool BF, int D>
+hipError_t launch_tiles(const AttnPlan& pl, const AttnArgs& a, hipStream_t s);
 
 }  // namespace attn
 }  // namespace qgemm

@@ -118,10 +118,27 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
     pl->ws_bytes = pl->tickets_bytes + (size_t)2 * pl->grid * row_tile * (dim + 4) * 4;
     return QGEMM_OK;
   }
-  const int64_t units = p->total_q * p->q_heads;
-  if (units > 0x7fffffffLL)
-    return fail(QGEMM_ERR_UNSUPPORTED, "total_q * q_heads is %lld, more than one launch allows", (long long)units);
-  pl->grid = (unsigned)units;
+  const TileShape shape = tile_shape(dim, pl->groups);
+  pl->tile = tile_rows(shape);
+  // row tiles: every sequence may end in a partly filled one
+  const int64_t ratio = p->q_heads / p->cache.kv_heads, per_seq = (rows + pl->tile - 1) / pl->tile;
+  int64_t entries = p->batch + ratio * p->total_q / pl->tile;
+  if (entries > per_seq * p->batch) entries = per_seq * p->batch;
+  const int64_t tiles = entries * p->cache.kv_heads;
+  // A row tile's tokens are split over workgroups while there are fewer of them than the chip holds,
+  // but not below 4 steps each.
+  const int64_t steps = ((int64_t)p->max_pages * p->cache.page_size + 63) / 64;
+  int64_t splits = 1;
+  while (tiles * splits * 2 <= 2 * kCUs && splits * 2 * 4 <= steps) splits *= 2;
+  if (tiles * splits > 0x7fffffffLL)
+    return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows",
+                (long long)(tiles * splits));
+  pl->splits = (int)splits;
+  pl->grid = (unsigned)(tiles * splits);
+  if (splits > 1) {
+    pl->tickets_bytes = ((size_t)tiles * 4 + 255) / 256 * 256;
+    pl->ws_bytes = pl->tickets_bytes + (size_t)tiles * splits * ((size_t)pl->tile * dim + (size_t)shape.cols * shape.waves * 256) * 4;
+  }
   return QGEMM_OK;
 }
 
@@ -163,7 +180,8 @@ qgemm_status_t qgemm_attention_describe(const qgemm_attention_t* p, char* buf, s
   const int n = p->total_q == 0 ? std::snprintf(buf, len, "empty")
                 : pl.kind == ATTN_ROWS ? std::snprintf(buf, len, "rows grid=%u groups=%d pack=%d col_tiles=%d", pl.grid,
                                                        pl.groups, pl.pack, pl.col_tiles)
-                                       : std::snprintf(buf, len, "tiles grid=%u groups=%d", pl.grid, pl.groups);
+                                       : std::snprintf(buf, len, "tiles grid=%u groups=%d rows=%d splits=%d", pl.grid,
+                                                       pl.groups, pl.tile, pl.splits);
   if (n < 0 || (size_t)n >= len)
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
   return QGEMM_OK;

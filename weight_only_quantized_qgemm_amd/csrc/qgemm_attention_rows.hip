@@ -11,6 +11,8 @@
 // running maximum, sum and output, joined through LDS.  The 16 columns of an MFMA are more than
 // most calls have query rows, so with F = 2 or 4 each column group of 16 / F holds the same rows for
 // another 16-token subtile: the softmax then works on full lanes, and its cost per token falls by F.
+#include <type_traits>
+
 #include "qgemm_attention_device.h"
 
 namespace qgemm {
@@ -185,14 +187,15 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
 
     // ---- the wavefront's steps: token ts + T (wave + 4 j)
     float mx[NC], l[NC], zs[NC][NG], ps[NC][NG];
+    bool fresh[NC];                                 // the row has seen no token: mx is not set
     f32x4 o[NC][TILES];
     // a row's value scales are divided by 2^sig (inv = 2^-sig), a bound of those it has seen
     int sig[NC];
     float inv[NC];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      mx[nc] = kStart;
-      l[nc] = 0.f;
+      mx[nc] = l[nc] = 0.f;
+      fresh[nc] = true;
       sig[nc] = -126;
       inv[nc] = 0x1p126f;
 #pragma unroll
@@ -240,69 +243,38 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
         }
       }
     };
-    auto compute = [&](int j, const StepT& st) {
-      const int t0 = ts + T * (wave + 4 * j);
-      // S^T
-      f32x4 acc[NC][ST][NG];
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-        for (int x = 0; x < ST; ++x)
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) acc[nc][x][gr] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int f = 0; f < SUB; ++f)
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const u32x4 kf = codes8(st.k[f][i]);
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) {
-            f32x4& c = acc[nc][F == 1 ? f : 0][i / SG];
-            c = mfma(kf, qf[F == 1 ? 0 : f][i][nc], c);
-          }
-        }
-      const bool edge = t0 + T > min(all_hi, te) || t0 < all_lo;
-      // scores in bits relative to the running maximum
+    auto step = [&](auto edge_c, int t0, const StepT& st) {
+      constexpr bool kEdge = decltype(edge_c)::value;
+      // S^T, then scores in bits less the row's running maximum
       float u[NC][ST][4];
-      auto score = [&](bool base) {
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int x = 0; x < ST; ++x)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float v = base ? -mx[nc] : 0.f;
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) {
-                const unsigned w = st.kp[x][gr][r];
-                v = __builtin_fmaf(par_zero<BF>(w), qz[nc][gr], v);
-                v = __builtin_fmaf(par_scale<BF>(w) * kq, acc[nc][x][gr][r], v);
-              }
-              u[nc][x][r] = v;
-            }
-      };
-      unsigned seen[NC];                            // bit 4 x + r, set in edge steps only
-      auto mask = [&]() {
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int x = 0; x < ST; ++x)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (!(seen[nc] >> (4 * x + r) & 1)) u[nc][x][r] = -__builtin_inff();
-      };
-      float vs[ST][NG][4], vm[ST][NG][4];           // scale, zero + 8 scale
 #pragma unroll
       for (int x = 0; x < ST; ++x)
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
+        for (int gr = 0; gr < NG; ++gr) {
+          f32x4 acc[NC];
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) acc[nc] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int f = F == 1 ? x : 0; f < (F == 1 ? x + 1 : SUB); ++f)
+#pragma unroll
+            for (int i = gr * SG; i < (gr + 1) * SG; ++i) {
+              const u32x4 kf = codes8(st.k[f][i]);
+#pragma unroll
+              for (int nc = 0; nc < NC; ++nc) acc[nc] = mfma(kf, qf[F == 1 ? 0 : f][i][nc], acc[nc]);
+            }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const unsigned w = st.vp[x][gr][r];
-            vs[x][gr][r] = par_scale<BF>(w);
-            vm[x][gr][r] = __builtin_fmaf(vs[x][gr][r], 8.f, par_zero<BF>(w));
+            const unsigned w = st.kp[x][gr][r];
+            const float sc = par_scale<BF>(w) * kq, z = par_zero<BF>(w);
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) {
+              const float v = __builtin_fmaf(z, qz[nc][gr], gr ? u[nc][x][r] : -mx[nc]);
+              u[nc][x][r] = __builtin_fmaf(sc, acc[nc][r], v);
+            }
           }
-      if (edge) {
+        }
+      unsigned seen[NC];                            // bit 4 x + r
+      if constexpr (kEdge) {
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
           seen[nc] = 0;
@@ -312,57 +284,50 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
             for (int r = 0; r < 4; ++r) {
               const int t = t0 + 16 * (F == 1 ? x : fcol) + 4 * g + r;
               if (t >= see_lo[nc] && t < see_hi[nc] && t < te) seen[nc] |= 1u << (4 * x + r);
+              else u[nc][x][r] = -__builtin_inff();
             }
         }
       }
-      // the largest value scale that each row sees
-      float big[NC];
+      bool move = false;
+      float big[NC];                                // the largest value scale that each row sees
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) {
+        float high = u[nc][0][0];
         big[nc] = 0.f;
 #pragma unroll
         for (int x = 0; x < ST; ++x)
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
+          for (int r = 0; r < 4; ++r) {
+            high = __builtin_fmaxf(high, u[nc][x][r]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float v = __builtin_fabsf(vs[x][gr][r]);
-              big[nc] = __builtin_fmaxf(big[nc], edge && !(seen[nc] >> (4 * x + r) & 1) ? 0.f : v);
+            for (int gr = 0; gr < NG; ++gr) {
+              const float v = __builtin_fabsf(par_scale<BF>(st.vp[x][gr][r]));
+              big[nc] = __builtin_fmaxf(big[nc], !kEdge || (seen[nc] >> (4 * x + r) & 1) ? v : 0.f);
             }
-      }
-      score(true);
-      if (edge) mask();
-      bool move = false;
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        float high = u[nc][0][0];
-#pragma unroll
-        for (int x = 0; x < ST; ++x)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, u[nc][x][r]);
-        move |= high > kSlack || big[nc] * inv[nc] > kScaleSlack;
+          }
+        move |= high > (fresh[nc] ? -3e38f : kSlack) || big[nc] * inv[nc] > kScaleSlack;
       }
       if (__any(move)) {
-        // move the running maxima and value scales that need it, rescale what is summed so far
-        score(false);
-        if (edge) mask();
+        // set or move the running maxima and value scales that need it, rescale what is summed so far
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
-          float top = kStart;
+          float top = -3e38f, smax = big[nc];
 #pragma unroll
           for (int x = 0; x < ST; ++x)
 #pragma unroll
             for (int r = 0; r < 4; ++r) top = __builtin_fmaxf(top, u[nc][x][r]);
-          top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+#pragma unroll
+          for (int x = 16; x < 64; x *= 2) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, x));
+            smax = __builtin_fmaxf(smax, __shfl_xor(smax, x));
+          }
           // a row's maximum moves for its own scores only: its result does not depend on its neighbours
-          const float nm = top > mx[nc] + kSlack ? top : mx[nc];
-          float smax = big[nc];
-          smax = __builtin_fmaxf(smax, __shfl_xor(smax, 16));
-          smax = __builtin_fmaxf(smax, __shfl_xor(smax, 32));
+          const bool go = top > (fresh[nc] ? -3e38f : kSlack);
+          const float by = go ? top : 0.f, al = fresh[nc] ? 1.f : exp2_fast(-by);
           const int ns = smax * inv[nc] > kScaleSlack ? __builtin_amdgcn_frexp_expf(smax) : sig[nc];
-          const float al = exp2_fast(mx[nc] - nm), ab = __builtin_ldexpf(al, sig[nc] - ns);
-          mx[nc] = nm;
+          const float ab = __builtin_ldexpf(al, sig[nc] - ns);
+          fresh[nc] = fresh[nc] && !go;
+          mx[nc] += by;
           sig[nc] = ns;
           inv[nc] = __builtin_ldexpf(1.f, -ns);
           l[nc] *= al;
@@ -373,31 +338,41 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
           }
 #pragma unroll
           for (int i = 0; i < TILES; ++i) o[nc][i] *= ab;
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[nc][x][r] -= by;
         }
-        score(true);
-        if (edge) mask();
       }
-      // weights
-      unsigned pk[NC][ST][NG][2];
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-        for (int x = 0; x < ST; ++x) {
-          float p[4];
+        for (int x = 0; x < ST; ++x)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            p[r] = exp2_fast(u[nc][x][r]);
-            l[nc] += p[r];
+            u[nc][x][r] = exp2_fast(u[nc][x][r]);
+            l[nc] += u[nc][x][r];
           }
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
+      for (int gr = 0; gr < NG; ++gr) {
+        unsigned pk[NC][ST][2];
+#pragma unroll
+        for (int x = 0; x < ST; ++x) {
+          float sc[4], md[4];                       // scale, zero + 8 scale
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const unsigned w = st.vp[x][gr][r];
+            sc[r] = par_scale<BF>(w);
+            md[r] = __builtin_fmaf(sc[r], 8.f, par_zero<BF>(w));
+          }
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
             float w[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              float sc = vs[x][gr][r] * inv[nc], md = vm[x][gr][r];
-              if (edge && !(seen[nc] >> (4 * x + r) & 1)) sc = md = 0.f;
-              w[r] = p[r] * sc;
-              zs[nc][gr] = __builtin_fmaf(p[r], md, zs[nc][gr]);
+              const bool on = !kEdge || (seen[nc] >> (4 * x + r) & 1);
+              w[r] = on ? u[nc][x][r] * (sc[r] * inv[nc]) : 0.f;
+              zs[nc][gr] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][gr]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -405,39 +380,42 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
               const unsigned v = pack_f16(w[2 * h], w[2 * h + 1]);
               ps[nc][gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), f16x2{(_Float16)1.f, (_Float16)1.f},
                                                   ps[nc][gr], false);
-              pk[nc][x][gr][h] = v;
+              pk[nc][x][h] = v;
             }
           }
         }
-      // O^T += V^T P^T, two subtiles at a time
+        // O^T += V^T P^T, two subtiles at a time
 #pragma unroll
-      for (int pr = 0; pr < SUB / 2; ++pr) {
-        u32x4 bp[NC][NG];
+        for (int pr = 0; pr < SUB / 2; ++pr) {
+          u32x4 bp[NC];
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
+          for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if constexpr (F == 1) {
-                bp[nc][gr][h] = pk[nc][0][gr][h];
-                bp[nc][gr][2 + h] = pk[nc][ST - 1][gr][h];
+                bp[nc][h] = pk[nc][0][h];
+                bp[nc][2 + h] = pk[nc][ST - 1][h];
               } else {
-                bp[nc][gr][h] = fcol == 2 * pr ? pk[nc][0][gr][h] : 0u;
-                bp[nc][gr][2 + h] = fcol == 2 * pr + 1 ? pk[nc][0][gr][h] : 0u;
+                bp[nc][h] = fcol == 2 * pr ? pk[nc][0][h] : 0u;
+                bp[nc][2 + h] = fcol == 2 * pr + 1 ? pk[nc][0][h] : 0u;
               }
             }
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-          u32x4 vf;
-          unsigned x0, x1, y0, y1;
-          v_pairs<U>(st.v[2 * pr], i, x0, x1);
-          v_pairs<U>(st.v[2 * pr + 1], i, y0, y1);
-          vf = u32x4{x0, x1, y0, y1};
+          for (int i = gr * TG; i < (gr + 1) * TG; ++i) {
+            unsigned x0, x1, y0, y1;
+            v_pairs<U>(st.v[2 * pr], i, x0, x1);
+            v_pairs<U>(st.v[2 * pr + 1], i, y0, y1);
 #pragma unroll
-          for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[nc][i / TG], o[nc][i]);
+            for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(u32x4{x0, x1, y0, y1}, bp[nc], o[nc][i]);
+          }
         }
       }
+    };
+    auto compute = [&](int j, const StepT& st) {
+      const int t0 = ts + T * (wave + 4 * j);
+      // tokens that every row sees need no mask: the common case, kept free of selects
+      if (t0 + T > min(all_hi, te) || t0 < all_lo) step(std::true_type{}, t0, st);
+      else step(std::false_type{}, t0, st);
     };
     if (mine) {
       StepT sa, sb;
@@ -485,7 +463,7 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
       }
       __syncthreads();                              // the previous column tile (or segment) is done with LDS
       if (g == 0) {
-        s_m[wave * 16 + m] = mx[nc];
+        s_m[wave * 16 + m] = fresh[nc] ? kStart : mx[nc];
         s_l[wave * 16 + m] = sl;
       }
 #pragma unroll

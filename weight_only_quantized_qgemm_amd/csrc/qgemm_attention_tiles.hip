@@ -1,0 +1,554 @@
+// Attention with many query rows per kv head (prompts, chunks of prompts): query rows over the
+// wavefronts, the cache's tokens shared by a workgroup through LDS.
+//
+// Bound by arithmetic: 4 D operations per visible (row, token) pair on the matrix cores, beside about
+// ten vector operations per pair for the softmax, which is what takes longer.  A workgroup holds
+// BM = 16 NC NW query rows of one kv head (row = query * ratio + head, so the heads of a group share
+// the tokens' codes) and walks 64 tokens at a time.  The wavefronts turn the packed codes of the
+// next 64 tokens into MFMA operands once, in LDS (two buffers, one barrier per step), while the
+// current ones are read by all.  O^T, the running maxima and the sums stay in registers.
+//
+// The reference mx of a row bounds score + log2(value scale), in bits, of the tokens it has seen:
+// w = 2^(score - mx) * scale then fits fp16 whatever the scales are, at no cost per token, and
+// 2^-mx drops out with the sum.  Scales beyond 2^+-60 (bf16 only) are first brought near 1 by a power
+// of two common to the 64 tokens (tau), which O carries.
+#include <type_traits>
+
+#include "qgemm_attention_device.h"
+
+namespace qgemm {
+namespace attn {
+namespace {
+
+constexpr int kStep = 64;                           // tokens per step
+// scores may exceed their reference by this many bits less the exponent of the step's largest scale
+constexpr int kRoom = 14, kRoomMax = 60;
+
+template <bool BF, int D, int NG, int NC, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
+  constexpr int U = D / 32, TILES = D / 16, TG = TILES / NG, SG = U / NG;
+  constexpr int BM = 16 * NC * NW, NT = 64 * NW;
+  constexpr int KB = kStep * D * 2, PB = 4 * NG * 4 * 16 * 4;      // bytes of K (and of V) operands, of parameters
+  constexpr int kSlot = BM * D + NC * NT * 4;       // floats of a partial
+  __shared__ __align__(16) uint8_t s_k[2][KB], s_v[2][KB];
+  __shared__ __align__(16) float s_p[2][PB / 4];    // [subtile][group][K scale, K zero, V scale, V middle][16]
+  __shared__ int s_exp[2][2];                       // tau and the largest exponent after it
+  __shared__ float s_top[NW];
+  __shared__ int s_last;
+
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+
+  // ---- which rows: workgroups with the same kv head sit on the same XCD while heads divide by 8; the
+  // row tiles are walked from the last, which sees most
+  const int kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+  const int split = rest % a.splits;
+  int entry = rest / a.splits;
+  int total = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    int u = b0 + lane < a.batch ? (a.ratio * load_seq(a, b0 + lane).n + BM - 1) / BM : 0;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) u += __shfl_xor(u, x);
+    total += u;
+  }
+  total = __builtin_amdgcn_readfirstlane(total);
+  if (entry >= total) return;
+  entry = total - 1 - entry;
+  int b = 0, before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    int u = b0 + lane < a.batch ? (a.ratio * load_seq(a, b0 + lane).n + BM - 1) / BM : 0;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+      const int y = __shfl_up(u, x);
+      if (lane >= x) u += y;
+    }
+    const unsigned long long past = __ballot(before + u > entry);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      b = b0 + l;
+      before += l ? __builtin_amdgcn_readlane(u, l - 1) : 0;
+      break;
+    }
+    before += __builtin_amdgcn_readlane(u, 63);
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
+  before = __builtin_amdgcn_readfirstlane(before);
+  const Seq s = load_seq(a, b);
+  const int rows = a.ratio * s.n, row0 = (entry - before) * BM;
+  const int past = s.len - s.n;                     // position of query 0
+  const int row_end = min(rows, row0 + BM);
+  const int hi = a.causal ? min(s.len, max(past + (row_end - 1) / a.ratio + 1, 0)) : s.len;
+  const int lo = min(a.window ? max(past + row0 / a.ratio - a.window + 1, 0) & ~15 : 0, hi & ~15);
+  const int all_steps = (hi - lo + kStep - 1) / kStep;
+  const int per = max(1, (all_steps + a.splits - 1) / a.splits);
+  const int active = max(1, (all_steps + per - 1) / per);
+  if (split >= active) return;
+  const int ts = lo + kStep * per * split, te = min(hi, ts + kStep * per);
+  const int steps = te > ts ? (te - ts + kStep - 1) / kStep : 0;
+
+  // ---- filling: wavefront w prepares K and (or) V operands of a 16-token subtile, the first two also
+  // the parameters
+  constexpr bool kBoth = NW == 4;
+  const int fsub = wave & 3;
+  const bool fk = kBoth || wave < 4, fv = kBoth || wave >= 4;
+  unsigned rk[U], rv[U], rp[NG];
+  bool rp_on = false;
+  auto block_of = [&](int t, int& in) {             // t at most te - 1
+    const int p = t / a.page;
+    int pg = a.table[(long long)b * a.max_pages + p];
+    if ((unsigned)pg >= (unsigned)a.num_pages) pg = 0;
+    in = t - p * a.page;
+    return a.data + ((long long)pg * a.kv_heads + kvh) * a.block;
+  };
+  auto load_dwords = [&](const uint8_t* p, unsigned(&w)[U]) {
+    if constexpr (U == 2) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+      w[0] = x[0];
+      w[1] = x[1];
+    } else {
+#pragma unroll
+      for (int j = 0; j < U / 4; ++j) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(p + 16 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * j + i] = x[i];
+      }
+    }
+  };
+  auto fetch = [&](int step) {
+    const int t0 = ts + kStep * step;
+    int in;
+    const int tsub = __builtin_amdgcn_readfirstlane(min(t0 + 16 * fsub, (te - 1) & ~15));   // past the end: any subtile, masked
+    const uint8_t* blk = block_of(tsub, in);
+    if (fk) load_dwords(blk + (in * (D / 2) + (m * (D / 2) + 4 * U * g)), rk);
+    if (fv) load_dwords(blk + a.codes + (in * (D / 2) + lane * (4 * U)), rv);
+    if (wave < 2) {                                 // wavefront 0: K parameters, 1: V parameters; a token a lane
+      const int t = t0 + lane;
+      rp_on = t < te;
+      const uint8_t* pb = block_of(min(t, te - 1), in) + 2 * a.codes + wave * a.params;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) rp[gr] = *reinterpret_cast<const unsigned*>(pb + 4 * (gr * a.page + in));
+    }
+  };
+  float kq = 0.f;                                   // set below, before the first store
+  auto store = [&](int buf) {
+    if (fk) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) *reinterpret_cast<u32x4*>(&s_k[buf][((fsub * U + i) * 64 + lane) * 16]) = codes8(rk[i]);
+    }
+    if (fv) {
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        u32x2 v;
+        unsigned x, y;
+        v_pairs<U>(rv, i, x, y);
+        v = u32x2{x, y};
+        *reinterpret_cast<u32x2*>(&s_v[buf][(((fsub >> 1) * TILES + i) * 64 + lane) * 16 + (fsub & 1) * 8]) = v;
+      }
+    }
+    if (wave < 2) {
+      float sc[NG], z[NG];
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        sc[gr] = par_scale<BF>(rp[gr]);
+        z[gr] = par_zero<BF>(rp[gr]);
+      }
+      if (wave == 0) {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
+      } else {
+        float big = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          if (!rp_on) sc[gr] = z[gr] = 0.f;         // no token: its bits must not multiply
+          z[gr] = __builtin_fmaf(sc[gr], 8.f, z[gr]);
+          big = __builtin_fmaxf(big, __builtin_fabsf(sc[gr]));
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) big = __builtin_fmaxf(big, __shfl_xor(big, x));
+        int e = big > 0.f ? __builtin_amdgcn_frexp_expf(big) : -kRoomMax;
+        const int tau = e > kRoomMax ? 64 : e < -kRoomMax ? -64 : 0;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) sc[gr] = __builtin_ldexpf(sc[gr], -tau);
+        if (lane == 0) {
+          s_exp[buf][0] = tau;
+          s_exp[buf][1] = e - tau;
+        }
+      }
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        float* p = &s_p[buf][(((lane >> 4) * NG + gr) * 4 + 2 * wave) * 16 + (lane & 15)];
+        p[0] = sc[gr];
+        p[16] = z[gr];
+      }
+    }
+  };
+
+  // ---- queries
+  u32x4 qf[U][NC];
+  float qz[NC][NG];
+  int see_lo[NC], see_hi[NC];
+  {
+    u32x4 raw[NC][U];
+    float top = 0.f;
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      const int row = row0 + (wave * NC + nc) * 16 + m;
+      const bool on = row < rows;
+      const int i = on ? row / a.ratio : 0, h = row - i * a.ratio;
+      const int pos = past + i;
+      see_hi[nc] = a.causal ? min(pos + 1, s.len) : s.len;
+      see_lo[nc] = a.window ? pos - a.window + 1 : 0;
+      const uint16_t* src = a.q + (long long)(s.start + i) * a.qs + (kvh * a.ratio + h) * D + 8 * g;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        raw[nc][j] = on ? *reinterpret_cast<const u32x4*>(src + 32 * j) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const float x = __builtin_fabsf(from16<BF>(raw[nc][j][e] >> (16 * o) & 0xffffu));
+            top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
+          }
+      }
+    }
+    if (steps) fetch(0);
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+    if (lane == 0) s_top[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = __builtin_fmaxf(top, s_top[w]);
+    const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
+    kq = __builtin_ldexpf(a.scale, 24 - 14 + e);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = gr * SG; j < (gr + 1) * SG; ++j) {
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[k] = from16<BF>(raw[nc][j][k / 2] >> (16 * (k & 1)) & 0xffffu);
+            sum += x[k];
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int sh = 14 - e - ((k & 1) ? 4 : 0);
+            qf[j][nc][k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
+          }
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        qz[nc][gr] = sum * a.scale;
+      }
+  }
+  // tokens that the wavefront's rows all see, and those that any of them sees
+  const int first = row0 + wave * 16 * NC, last = min(rows - 1, first + 16 * NC - 1);
+  const bool idle = first >= rows;
+  const int all_hi = a.causal ? min(s.len, past + first / a.ratio + 1) : s.len;
+  const int all_lo = a.window ? past + last / a.ratio - a.window + 1 : 0;
+  const int any_hi = idle ? 0 : a.causal ? min(s.len, past + last / a.ratio + 1) : s.len;
+  const int any_lo = a.window ? past + first / a.ratio - a.window + 1 : 0;
+
+  float mx[NC], l[NC], zs[NC][NG], ps[NC][NG];
+  bool fresh[NC];                                   // the row has seen no token: mx is not set
+  f32x4 o[NC][TILES];
+  int tau = -1024;
+#pragma unroll
+  for (int nc = 0; nc < NC; ++nc) {
+    mx[nc] = l[nc] = 0.f;
+    fresh[nc] = true;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) zs[nc][gr] = ps[nc][gr] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // 32 tokens: scores, softmax step, products with V
+  auto half = [&](auto edge_c, int buf, int pr, int tp, float room, float tf) {
+    constexpr bool kEdge = decltype(edge_c)::value;
+    auto par = [&](int x, int gr, int c) {
+      return *reinterpret_cast<const f32x4*>(&s_p[buf][(((2 * pr + x) * NG + gr) * 4 + c) * 16 + 4 * g]);
+    };
+    float u[NC][2][4];                              // scores in bits less the row's reference
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        f32x4 acc[NC];
+#pragma unroll
+        for (int i = gr * SG; i < (gr + 1) * SG; ++i) {
+          const u32x4 kf = *reinterpret_cast<const u32x4*>(&s_k[buf][(((2 * pr + x) * U + i) * 64 + lane) * 16]);
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+            acc[nc] = mfma(kf, qf[i][nc], i == gr * SG ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[nc]);
+        }
+        const f32x4 sc = par(x, gr, 0), z = par(x, gr, 1);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float v = __builtin_fmaf(z[r], qz[nc][gr], gr ? u[nc][x][r] : -mx[nc]);
+            u[nc][x][r] = __builtin_fmaf(sc[r], acc[nc][r], v);
+          }
+      }
+    unsigned seen[NC];
+    if constexpr (kEdge) {
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        seen[nc] = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = tp + 16 * x + 4 * g + r;
+            if (t >= see_lo[nc] && t < see_hi[nc] && t < te) seen[nc] |= 1u << (4 * x + r);
+            else u[nc][x][r] = -__builtin_inff();
+          }
+      }
+    }
+    bool move = false;
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      float high = u[nc][0][0];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, u[nc][x][r]);
+      move |= high > (fresh[nc] ? -3e38f : room);
+    }
+    if (__any(move)) {
+      // set or move the references that need it, rescale what is summed so far
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        float top = -3e38f, want = -3e38f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          f32x4 sm = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            const f32x4 v = par(x, gr, 2) * tf;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sm[r] = __builtin_fmaxf(sm[r], __builtin_fabsf(v[r]));
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float ls = sm[r] > 0.f ? (float)__builtin_amdgcn_frexp_expf(sm[r]) : -(float)kRoomMax;
+            top = __builtin_fmaxf(top, u[nc][x][r]);
+            want = __builtin_fmaxf(want, u[nc][x][r] + __builtin_fmaxf(ls, -(float)kRoomMax));
+          }
+        }
+#pragma unroll
+        for (int x = 16; x < 64; x *= 2) {
+          top = __builtin_fmaxf(top, __shfl_xor(top, x));
+          want = __builtin_fmaxf(want, __shfl_xor(want, x));
+        }
+        // a row's reference moves for its own scores only: its result does not depend on its neighbours
+        const bool go = top > (fresh[nc] ? -3e38f : room);
+        const float by = go ? (fresh[nc] ? want : __builtin_fmaxf(want, 0.f)) : 0.f;
+        const float al = fresh[nc] ? 1.f : exp2_fast(-by);
+        fresh[nc] = fresh[nc] && !go;
+        mx[nc] += by;
+        l[nc] *= al;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          zs[nc][gr] *= al;
+          ps[nc][gr] *= al;
+        }
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) o[nc][i] *= al;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) u[nc][x][r] -= by;
+      }
+    }
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          u[nc][x][r] = exp2_fast(u[nc][x][r]);
+          l[nc] += u[nc][x][r];
+        }
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      u32x4 bp[NC];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        f32x4 sc = par(x, gr, 2);
+        const f32x4 md = par(x, gr, 3);
+        if (tf != 1.f) sc *= tf;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          float w[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const bool on = !kEdge || (seen[nc] >> (4 * x + r) & 1);
+            w[r] = on ? u[nc][x][r] * sc[r] : 0.f;
+            zs[nc][gr] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][gr]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // rounded to 11 bits, and summed as rounded: the codes' middle is taken out exactly
+            const unsigned v = pack_f16(w[2 * h], w[2 * h + 1]);
+            ps[nc][gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), f16x2{(_Float16)1.f, (_Float16)1.f},
+                                                ps[nc][gr], false);
+            bp[nc][2 * x + h] = v;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = gr * TG; i < (gr + 1) * TG; ++i) {
+        const u32x4 vf = *reinterpret_cast<const u32x4*>(&s_v[buf][((pr * TILES + i) * 64 + lane) * 16]);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[nc], o[nc][i]);
+      }
+    }
+  };
+
+  auto compute = [&](int step, int buf) {
+    const int t0 = ts + kStep * step;
+    if (t0 >= any_hi || t0 + kStep <= any_lo) return;
+    const int etau = __builtin_amdgcn_readfirstlane(s_exp[buf][0]);
+    const float room = (float)min(kRoomMax, kRoom - __builtin_amdgcn_readfirstlane(s_exp[buf][1]));
+    float tf = 1.f;                                 // the step's values in units of O's tau
+    if (etau != tau) {
+      if (etau > tau) {
+        const float f = __builtin_ldexpf(1.f, tau - etau);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) ps[nc][gr] *= f;
+#pragma unroll
+          for (int i = 0; i < TILES; ++i) o[nc][i] *= f;
+        }
+        tau = etau;
+      } else {
+        tf = __builtin_ldexpf(1.f, etau - tau);
+      }
+    }
+#pragma unroll 1
+    for (int pr = 0; pr < 2; ++pr) {
+      const int tp = t0 + 32 * pr;
+      // tokens that every row sees need no mask: the common case, kept free of selects
+      if (tp + 32 > min(all_hi, te) || tp < all_lo) half(std::true_type{}, buf, pr, tp, room, tf);
+      else half(std::false_type{}, buf, pr, tp, room, tf);
+    }
+  };
+
+  if (steps) {
+    store(0);
+    if (steps > 1) fetch(1);
+    for (int j = 0; j < steps; ++j) {
+      __syncthreads();                              // step j's operands are in LDS, step j - 1's are read
+      if (j + 1 < steps) {
+        store((j + 1) & 1);
+        if (j + 2 < steps) fetch(j + 2);
+      }
+      compute(j, j & 1);
+    }
+  }
+
+  // ---- results: lane sums, then out, or a partial for the last split to join
+#pragma unroll
+  for (int nc = 0; nc < NC; ++nc) {
+    l[nc] += __shfl_xor(l[nc], 16);
+    l[nc] += __shfl_xor(l[nc], 32);
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      float sz = zs[nc][gr], sp = ps[nc][gr];
+      sz += __shfl_xor(sz, 16);
+      sp += __shfl_xor(sp, 16);
+      sz += __shfl_xor(sz, 32);
+      sp += __shfl_xor(sp, 32);
+      zs[nc][gr] = sz;
+      ps[nc][gr] = sp;
+    }
+    const float back = tau == -1024 ? 0.f : __builtin_ldexpf(1.f, tau);
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      const float up = (i & 1) ? 0x1p20f : 0x1p24f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        o[nc][i][r] = __builtin_fmaf(__builtin_fmaf(o[nc][i][r], up, -8.f * ps[nc][i / TG]), back, zs[nc][i / TG]);
+    }
+  }
+  if (active > 1) {
+    const int tile = entry * a.kv_heads + kvh;
+    float* base = a.partials + (size_t)tile * a.splits * kSlot;
+    {
+      const __amdgpu_buffer_rsrc_t dst = buffer_of(base + (size_t)split * kSlot, kSlot * 4);
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) store4(dst, ((nc * TILES + i) * NT + threadIdx.x) * 16, o[nc][i]);
+        store4(dst, (BM * D + (nc * NT + threadIdx.x) * 4) * 4, f32x4{fresh[nc] ? kStart : mx[nc], l[nc], 0.f, 0.f});
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0)
+      s_last = __hip_atomic_fetch_add(a.tickets + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(active - 1);
+    __syncthreads();
+    if (!s_last) return;
+    if (threadIdx.x == 0) __hip_atomic_store(a.tickets + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      float top = kStart, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < active; ++x) {
+        const __amdgpu_buffer_rsrc_t src = buffer_of(base + (size_t)x * kSlot, kSlot * 4);
+        const f32x4 ml = load4(src, (BM * D + (nc * NT + threadIdx.x) * 4) * 4);
+        const float nm = __builtin_fmaxf(top, ml[0]);
+        const float old = exp2_fast(top - nm), sc = exp2_fast(ml[0] - nm);
+        top = nm;
+        sum = sum * old + ml[1] * sc;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) o[nc][i] = o[nc][i] * old + load4(src, ((nc * TILES + i) * NT + threadIdx.x) * 16) * sc;
+      }
+      l[nc] = sum;
+    }
+  }
+#pragma unroll
+  for (int nc = 0; nc < NC; ++nc) {
+    const int row = row0 + (wave * NC + nc) * 16 + m;
+    if (row >= rows) continue;
+    const int i = row / a.ratio, h = row - i * a.ratio;
+    const float r = l[nc] == 0.f ? 0.f : 1.0f / l[nc];
+    uint16_t* dst = a.out + (long long)(s.start + i) * a.os + (kvh * a.ratio + h) * D + 4 * g;
+#pragma unroll
+    for (int x = 0; x < TILES; ++x)
+      *reinterpret_cast<u32x2*>(dst + 16 * x) =
+          u32x2{pack2<BF>(o[nc][x][0] * r, o[nc][x][1] * r), pack2<BF>(o[nc][x][2] * r, o[nc][x][3] * r)};
+  }
+}
+
+template <bool BF, int D, int NG>
+hipError_t launch_groups(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
+  constexpr TileShape t = tile_shape(D, NG);
+  attention_tiles<BF, D, NG, t.cols, t.waves><<<dim3(pl.grid), dim3(64 * t.waves), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+template <bool BF, int D>
+hipError_t launch_tiles(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
+  if (pl.groups == 1) return launch_groups<BF, D, 1>(pl, a, s);
+  if (pl.groups == 2) return launch_groups<BF, D, 2>(pl, a, s);
+  if constexpr (D > 64) return launch_groups<BF, D, 4>(pl, a, s);
+  return hipErrorInvalidValue;
+}
+
+#ifndef QGEMM_ATTN_UNIT
+#error "compiled once per element type and head dim: QGEMM_ATTN_UNIT = 3 * bf16 + (0, 1, 2 for head dim 64, 128, 256)"
+#endif
+template hipError_t launch_tiles<(QGEMM_ATTN_UNIT >= 3), (64 << (QGEMM_ATTN_UNIT % 3))>(const AttnPlan&, const AttnArgs&,
+                                                                                     hipStream_t);
+
+}  // namespace attn
+}  // namespace qgemm
