@@ -64,6 +64,11 @@ extern "C" qgemm_status_t qgemm_attention(const qgemm_attention_t* p, const void
   a.ratio = p->q_heads / p->cache.kv_heads;
   a.max_pages = p->max_pages;
   a.page = p->cache.page_size;
+  // t / page by a multiplication: with 2^s <= page < 2^(s + 1) and mul = floor(2^(31 + s) / page) + 1, the
+  // product exceeds t 2^(31 + s) / page by at most t, which is below 2^(31 + s) / page while t < 2^30.
+  const unsigned log2_page = 31 - (unsigned)__builtin_clz((unsigned)p->cache.page_size);
+  a.page_shift = log2_page - 1;
+  a.page_mul = (unsigned)((uint64_t(1) << (31 + log2_page)) / (unsigned)p->cache.page_size + 1);
   a.num_pages = (int)p->cache.num_pages;
   a.codes = g.codes;
   a.params = g.params;

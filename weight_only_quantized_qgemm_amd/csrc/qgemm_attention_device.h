@@ -40,6 +40,7 @@ struct AttnArgs {
   long long qs, os;                // token strides in elements
   int total_q, batch, q_heads, kv_heads, ratio, max_pages, page, num_pages;
   int codes, params, block;        // bytes of one side's codes, of its parameters, of a block
+  unsigned page_mul, page_shift;   // t / page = (t * page_mul) >> (32 + page_shift) for t < 2^30
   int max_q, causal, window;
   int units_min;                   // rows kernel: least units of 64 tokens a workgroup takes
   int splits;                      // tiles kernel: workgroups per row tile
@@ -111,6 +112,17 @@ __device__ __forceinline__ void v_pairs(const unsigned (&w)[U], int i, unsigned&
   const unsigned m = (i & 1) ? kHigh : kLow;
   p01 = ((i & 2) ? a >> 8 : a) & m;
   p23 = ((i & 2) ? b >> 8 : b) & m;
+}
+
+// The same pair, c 2^-24 (even tile) or c 2^-20, as the whole numbers c - 8.
+__device__ __forceinline__ unsigned centre(unsigned pair, bool high) {
+  const f16x2 v = __builtin_bit_cast(f16x2, pair | (high ? 0x54005400u : 0x64006400u));      // 64 + c or 1024 + c
+  const _Float16 off = high ? (_Float16)72.f : (_Float16)1032.f;
+  return __builtin_bit_cast(unsigned, v - f16x2{off, off});
+}
+
+__device__ __forceinline__ int page_of(const AttnArgs& a, int t) {
+  return (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift);
 }
 
 // Sequence b's geometry from device memory, every value bounded.

@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
     auto pages = [&](int j0) {                      // lane x: subtile x % SUB of step j0 + x / SUB
       int t = ts + T * (wave + 4 * (j0 + lane / SUB)) + 16 * (lane % SUB);
       t = min(t, (te - 1) & ~15);                   // past the end: the last subtile again (masked)
-      const int p = t / a.page;
+      const int p = page_of(a, t);
       int pg = a.table[(long long)b * a.max_pages + p];
       if ((unsigned)pg >= (unsigned)a.num_pages) pg = 0;
       in = t - p * a.page;

@@ -5,8 +5,10 @@
 // ten vector operations per pair for the softmax, which is what takes longer.  A workgroup holds
 // BM = 16 NC NW query rows of one kv head (row = query * ratio + head, so the heads of a group share
 // the tokens' codes) and walks 64 tokens at a time.  The wavefronts turn the packed codes of the
-// next 64 tokens into MFMA operands once, in LDS (two buffers, one barrier per step), while the
-// current ones are read by all.  O^T, the running maxima and the sums stay in registers.
+// next 64 tokens into MFMA operands once, in LDS, while the
+// current ones are read by all (K in two buffers, V in three, one barrier per step).  O^T, the running
+// maxima and the sums stay in registers.  The products of the next 32 tokens' keys are issued beside
+// the softmax of the current 32, so that the matrix cores and the vector units work at once.
 //
 // The reference mx of a row bounds score + log2(value scale), in bits, of the tokens it has seen:
 // w = 2^(score - mx) * scale then fits fp16 whatever the scales are, at no cost per token, and
@@ -20,7 +22,6 @@ namespace qgemm {
 namespace attn {
 namespace {
 
-constexpr int kStep = 64;                           // tokens per step
 // scores may exceed their reference by this many bits less the exponent of the step's largest scale
 constexpr int kRoom = 14, kRoomMax = 60;
 
@@ -28,11 +29,13 @@ template <bool BF, int D, int NG, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   constexpr int U = D / 32, TILES = D / 16, TG = TILES / NG, SG = U / NG;
   constexpr int BM = 16 * NC * NW, NT = 64 * NW;
-  constexpr int KB = kStep * D * 2, PB = 4 * NG * 4 * 16 * 4;      // bytes of K (and of V) operands, of parameters
+  constexpr int kHalves = D == 256 ? 1 : 2, kStep = 32 * kHalves;  // 32-token halves and tokens of a step
+  constexpr int SUBS = 2 * kHalves;                 // 16-token subtiles of a step
+  constexpr int KB = kStep * D * 2, PB = SUBS * NG * 4 * 16 * 4;   // bytes of K (and of V) operands, of parameters
   constexpr int kSlot = BM * D + NC * NT * 4;       // floats of a partial
-  __shared__ __align__(16) uint8_t s_k[2][KB], s_v[2][KB];
-  __shared__ __align__(16) float s_p[2][PB / 4];    // [subtile][group][K scale, K zero, V scale, V middle][16]
-  __shared__ int s_exp[2][2];                       // tau and the largest exponent after it
+  __shared__ __align__(16) uint8_t s_k[2][KB], s_v[3][KB];
+  __shared__ __align__(16) float s_p[3][PB / 4];    // [subtile][group][K scale, K zero, V scale, V middle][16]
+  __shared__ int s_exp[3][4];                       // tau, the largest exponent after it, any parameter not finite
   __shared__ float s_top[NW];
   __shared__ int s_last;
 
@@ -85,15 +88,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int ts = lo + kStep * per * split, te = min(hi, ts + kStep * per);
   const int steps = te > ts ? (te - ts + kStep - 1) / kStep : 0;
 
-  // ---- filling: wavefront w prepares K and (or) V operands of a 16-token subtile, the first two also
-  // the parameters
-  constexpr bool kBoth = NW == 4;
-  const int fsub = wave & 3;
-  const bool fk = kBoth || wave < 4, fv = kBoth || wave >= 4;
+  // ---- filling: each wavefront prepares the K or V operands of 16-token subtiles, wavefront 0 also the K
+  // and wavefront 1 the V parameters
+  constexpr bool kBoth = NW == SUBS;                // as many wavefronts as subtiles: K and V each
+  const int fsub = wave % SUBS;
+  const bool fk = kBoth || wave < SUBS, fv = kBoth || (wave >= SUBS && wave < 2 * SUBS);
   unsigned rk[U], rv[U], rp[NG];
   bool rp_on = false;
   auto block_of = [&](int t, int& in) {             // t at most te - 1
-    const int p = t / a.page;
+    const int p = page_of(a, t);
     int pg = a.table[(long long)b * a.max_pages + p];
     if ((unsigned)pg >= (unsigned)a.num_pages) pg = 0;
     in = t - p * a.page;
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     if (fk) load_dwords(blk + (in * (D / 2) + (m * (D / 2) + 4 * U * g)), rk);
     if (fv) load_dwords(blk + a.codes + (in * (D / 2) + lane * (4 * U)), rv);
     if (wave < 2) {                                 // wavefront 0: K parameters, 1: V parameters; a token a lane
-      const int t = t0 + lane;
+      const int t = t0 + lane % kStep;
       rp_on = t < te;
       const uint8_t* pb = block_of(min(t, te - 1), in) + 2 * a.codes + wave * a.params;
 #pragma unroll
@@ -129,19 +132,19 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     }
   };
   float kq = 0.f;                                   // set below, before the first store
-  auto store = [&](int buf) {
+  auto store = [&](int step) {
+    const int kb = step & 1, vb = step % 3;
     if (fk) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) *reinterpret_cast<u32x4*>(&s_k[buf][((fsub * U + i) * 64 + lane) * 16]) = codes8(rk[i]);
+      for (int i = 0; i < U; ++i) *reinterpret_cast<u32x4*>(&s_k[kb][((fsub * U + i) * 64 + lane) * 16]) = codes8(rk[i]);
     }
     if (fv) {
 #pragma unroll
       for (int i = 0; i < TILES; ++i) {
-        u32x2 v;
         unsigned x, y;
         v_pairs<U>(rv, i, x, y);
-        v = u32x2{x, y};
-        *reinterpret_cast<u32x2*>(&s_v[buf][(((fsub >> 1) * TILES + i) * 64 + lane) * 16 + (fsub & 1) * 8]) = v;
+        *reinterpret_cast<u32x2*>(&s_v[vb][(((fsub >> 1) * TILES + i) * 64 + lane) * 16 + (fsub & 1) * 8]) =
+            u32x2{centre(x, i & 1), centre(y, i & 1)};
       }
     }
     if (wave < 2) {
@@ -156,12 +159,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
       } else {
         float big = 0.f;
+        bool odd = false;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           if (!rp_on) sc[gr] = z[gr] = 0.f;         // no token: its bits must not multiply
           z[gr] = __builtin_fmaf(sc[gr], 8.f, z[gr]);
           big = __builtin_fmaxf(big, __builtin_fabsf(sc[gr]));
+          odd |= !(__builtin_fabsf(sc[gr]) + __builtin_fabsf(z[gr]) < __builtin_inff());
         }
+        odd = __any(odd);
 #pragma unroll
         for (int x = 1; x < 64; x *= 2) big = __builtin_fmaxf(big, __shfl_xor(big, x));
         int e = big > 0.f ? __builtin_amdgcn_frexp_expf(big) : -kRoomMax;
@@ -169,15 +175,18 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) sc[gr] = __builtin_ldexpf(sc[gr], -tau);
         if (lane == 0) {
-          s_exp[buf][0] = tau;
-          s_exp[buf][1] = e - tau;
+          s_exp[vb][0] = tau;
+          s_exp[vb][1] = e - tau;
+          s_exp[vb][2] = odd;
         }
       }
+      if (lane < kStep) {
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        float* p = &s_p[buf][(((lane >> 4) * NG + gr) * 4 + 2 * wave) * 16 + (lane & 15)];
-        p[0] = sc[gr];
-        p[16] = z[gr];
+        for (int gr = 0; gr < NG; ++gr) {
+          float* p = &s_p[vb][(((lane >> 4) * NG + gr) * 4 + 2 * wave) * 16 + (lane & 15)];
+          p[0] = sc[gr];
+          p[16] = z[gr];
+        }
       }
     }
   };
@@ -243,15 +252,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         qz[nc][gr] = sum * a.scale;
       }
   }
-  // tokens that the wavefront's rows all see, and those that any of them sees
+  // tokens that the wavefront's rows all see
   const int first = row0 + wave * 16 * NC, last = min(rows - 1, first + 16 * NC - 1);
   const bool idle = first >= rows;
   const int all_hi = a.causal ? min(s.len, past + first / a.ratio + 1) : s.len;
   const int all_lo = a.window ? past + last / a.ratio - a.window + 1 : 0;
-  const int any_hi = idle ? 0 : a.causal ? min(s.len, past + last / a.ratio + 1) : s.len;
-  const int any_lo = a.window ? past + first / a.ratio - a.window + 1 : 0;
 
-  float mx[NC], l[NC], zs[NC][NG], ps[NC][NG];
+  float mx[NC], l[NC], zs[NC][NG];
   bool fresh[NC];                                   // the row has seen no token: mx is not set
   f32x4 o[NC][TILES];
   int tau = -1024;
@@ -260,53 +267,118 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     mx[nc] = l[nc] = 0.f;
     fresh[nc] = true;
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) zs[nc][gr] = ps[nc][gr] = 0.f;
+    for (int gr = 0; gr < NG; ++gr) zs[nc][gr] = 0.f;
 #pragma unroll
     for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // 32 tokens: scores, softmax step, products with V
-  auto half = [&](auto edge_c, int buf, int pr, int tp, float room, float tf) {
-    constexpr bool kEdge = decltype(edge_c)::value;
-    auto par = [&](int x, int gr, int c) {
-      return *reinterpret_cast<const f32x4*>(&s_p[buf][(((2 * pr + x) * NG + gr) * 4 + c) * 16 + 4 * g]);
-    };
-    float u[NC][2][4];                              // scores in bits less the row's reference
+  auto par = [&](int vb, int pr, int x, int gr, int c) {
+    return *reinterpret_cast<const f32x4*>(&s_p[vb][(((2 * pr + x) * NG + gr) * 4 + c) * 16 + 4 * g]);
+  };
+  typedef f32x4 Acc[2][NG][NC];
+  // the products of one half's keys with the rows
+  auto products = [&](int step, int pr, Acc& acc) {
+    const uint8_t* src = s_k[step & 1];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const u32x4 kf = *reinterpret_cast<const u32x4*>(src + (((2 * pr + x) * U + i) * 64 + lane) * 16);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          f32x4& c = acc[x][i / SG][nc];
+          c = mfma(kf, qf[i][nc], i % SG == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : c);
+        }
+      }
+  };
+  float u[NC][2][4];                                // scores in bits less the row's reference, of the half that comes next
+  auto score = [&](int step, int pr, const Acc& acc) {
+    const int vb = step % 3;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        f32x4 acc[NC];
-#pragma unroll
-        for (int i = gr * SG; i < (gr + 1) * SG; ++i) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(&s_k[buf][(((2 * pr + x) * U + i) * 64 + lane) * 16]);
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-            acc[nc] = mfma(kf, qf[i][nc], i == gr * SG ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[nc]);
-        }
-        const f32x4 sc = par(x, gr, 0), z = par(x, gr, 1);
+        const f32x4 sc = par(vb, pr, x, gr, 0), z = par(vb, pr, x, gr, 1);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float v = __builtin_fmaf(z[r], qz[nc][gr], gr ? u[nc][x][r] : -mx[nc]);
-            u[nc][x][r] = __builtin_fmaf(sc[r], acc[nc][r], v);
+            u[nc][x][r] = __builtin_fmaf(sc[r], acc[x][gr][nc][r], v);
           }
       }
-    unsigned seen[NC];
-    if constexpr (kEdge) {
+  };
+  // A half's weights, as B operands, while the next half's products with K run beside them (into
+  // buffers that exist even after the last half: its scores are not used).  kMask: a weight of 0 must
+  // not meet a parameter that is not finite, and the step's values may be in units below O's.
+  unsigned seen[NC];
+  typedef u32x4 Weights[NG][NC];
+  auto weights = [&](auto mask_c, int step, int pr, int nstep, int npr, float tf, Acc& acc, Weights& bp) {
+    constexpr bool kMask = decltype(mask_c)::value;
+    const int vb = step % 3;
+    products(nstep, npr, acc);
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        seen[nc] = 0;
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          u[nc][x][r] = exp2_fast(u[nc][x][r]);
+          l[nc] += u[nc][x][r];
+        }
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        f32x4 sc = par(vb, pr, x, gr, 2);
+        const f32x4 md = par(vb, pr, x, gr, 3);
+        if constexpr (kMask) sc *= tf;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          float w[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const bool on = !kMask || (seen[nc] >> (4 * x + r) & 1);
+            w[r] = on ? u[nc][x][r] * sc[r] : 0.f;
+            zs[nc][gr] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][gr]);
+          }
+          // rounded to 11 bits
+          bp[gr][nc][2 * x] = pack_f16(w[0], w[1]);
+          bp[gr][nc][2 * x + 1] = pack_f16(w[2], w[3]);
+        }
+      }
+  };
+  // One half, whose scores u holds.
+  auto compute = [&](int step, int pr, int nstep, int npr) {
+    const int tp = ts + kStep * step + 32 * pr, vb = step % 3;
+    const int etau = __builtin_amdgcn_readfirstlane(s_exp[vb][0]);
+    const float room = (float)min(kRoomMax, kRoom - __builtin_amdgcn_readfirstlane(s_exp[vb][1]));
+    float tf = 1.f;                                 // the step's values in units of O's tau
+    if (etau > tau) {
+      const float f = __builtin_ldexpf(1.f, tau - etau);
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) o[nc][i] *= f;
+      tau = etau;
+    } else {
+      tf = __builtin_ldexpf(1.f, etau - tau);
+    }
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) seen[nc] = 255;
+    if (tp + 32 > min(all_hi, te) || tp < all_lo || idle) {            // not every row sees every token
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int t = tp + 16 * x + 4 * g + r;
-            if (t >= see_lo[nc] && t < see_hi[nc] && t < te) seen[nc] |= 1u << (4 * x + r);
-            else u[nc][x][r] = -__builtin_inff();
+            if (!(t >= see_lo[nc] && t < see_hi[nc] && t < te)) {
+              seen[nc] &= ~(1u << (4 * x + r));
+              u[nc][x][r] = -__builtin_inff();
+            }
           }
-      }
     }
     bool move = false;
 #pragma unroll
@@ -328,7 +400,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           f32x4 sm = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            const f32x4 v = par(x, gr, 2) * tf;
+            const f32x4 v = par(vb, pr, x, gr, 2) * tf;
 #pragma unroll
             for (int r = 0; r < 4; ++r) sm[r] = __builtin_fmaxf(sm[r], __builtin_fabsf(v[r]));
           }
@@ -352,10 +424,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         mx[nc] += by;
         l[nc] *= al;
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          zs[nc][gr] *= al;
-          ps[nc][gr] *= al;
-        }
+        for (int gr = 0; gr < NG; ++gr) zs[nc][gr] *= al;
 #pragma unroll
         for (int i = 0; i < TILES; ++i) o[nc][i] *= al;
 #pragma unroll
@@ -364,91 +433,41 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           for (int r = 0; r < 4; ++r) u[nc][x][r] -= by;
       }
     }
+    Acc acc;
+    Weights bp;
+    if (tf != 1.f || __builtin_amdgcn_readfirstlane(s_exp[vb][2])) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
+    else weights(std::false_type{}, step, pr, nstep, npr, tf, acc, bp);
 #pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
+    for (int i = 0; i < TILES; ++i) {
+      const u32x4 vf = *reinterpret_cast<const u32x4*>(&s_v[vb][((pr * TILES + i) * 64 + lane) * 16]);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          u[nc][x][r] = exp2_fast(u[nc][x][r]);
-          l[nc] += u[nc][x][r];
-        }
-#pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-      u32x4 bp[NC];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        f32x4 sc = par(x, gr, 2);
-        const f32x4 md = par(x, gr, 3);
-        if (tf != 1.f) sc *= tf;
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          float w[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const bool on = !kEdge || (seen[nc] >> (4 * x + r) & 1);
-            w[r] = on ? u[nc][x][r] * sc[r] : 0.f;
-            zs[nc][gr] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][gr]);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // rounded to 11 bits, and summed as rounded: the codes' middle is taken out exactly
-            const unsigned v = pack_f16(w[2 * h], w[2 * h + 1]);
-            ps[nc][gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), f16x2{(_Float16)1.f, (_Float16)1.f},
-                                                ps[nc][gr], false);
-            bp[nc][2 * x + h] = v;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = gr * TG; i < (gr + 1) * TG; ++i) {
-        const u32x4 vf = *reinterpret_cast<const u32x4*>(&s_v[buf][((pr * TILES + i) * 64 + lane) * 16]);
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[nc], o[nc][i]);
-      }
+      for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[i / TG][nc], o[nc][i]);
     }
+    score(nstep, npr, acc);
   };
 
-  auto compute = [&](int step, int buf) {
-    const int t0 = ts + kStep * step;
-    if (t0 >= any_hi || t0 + kStep <= any_lo) return;
-    const int etau = __builtin_amdgcn_readfirstlane(s_exp[buf][0]);
-    const float room = (float)min(kRoomMax, kRoom - __builtin_amdgcn_readfirstlane(s_exp[buf][1]));
-    float tf = 1.f;                                 // the step's values in units of O's tau
-    if (etau != tau) {
-      if (etau > tau) {
-        const float f = __builtin_ldexpf(1.f, tau - etau);
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) ps[nc][gr] *= f;
-#pragma unroll
-          for (int i = 0; i < TILES; ++i) o[nc][i] *= f;
-        }
-        tau = etau;
-      } else {
-        tf = __builtin_ldexpf(1.f, etau - tau);
-      }
-    }
-#pragma unroll 1
-    for (int pr = 0; pr < 2; ++pr) {
-      const int tp = t0 + 32 * pr;
-      // tokens that every row sees need no mask: the common case, kept free of selects
-      if (tp + 32 > min(all_hi, te) || tp < all_lo) half(std::true_type{}, buf, pr, tp, room, tf);
-      else half(std::false_type{}, buf, pr, tp, room, tf);
-    }
-  };
-
+  // Step j + 1 is stored after every wavefront has passed the barrier of step j, so its K buffer (of step
+  // j - 1, whose products were taken before that barrier) and its V buffer (of step j - 2) are free.
   if (steps) {
     store(0);
     if (steps > 1) fetch(1);
+    __syncthreads();
+    {
+      Acc acc;
+      products(0, 0, acc);
+      score(0, 0, acc);
+    }
     for (int j = 0; j < steps; ++j) {
-      __syncthreads();                              // step j's operands are in LDS, step j - 1's are read
       if (j + 1 < steps) {
-        store((j + 1) & 1);
+        store(j + 1);
         if (j + 2 < steps) fetch(j + 2);
       }
-      compute(j, j & 1);
+#pragma unroll 1
+      for (int pr = 0; pr < kHalves; ++pr) {
+        const bool end = pr == kHalves - 1;
+        if (end) __syncthreads();                   // step j + 1's operands are in LDS
+        compute(j, pr, j + end, end ? 0 : 1);
+      }
     }
   }
 
@@ -459,22 +478,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     l[nc] += __shfl_xor(l[nc], 32);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-      float sz = zs[nc][gr], sp = ps[nc][gr];
-      sz += __shfl_xor(sz, 16);
-      sp += __shfl_xor(sp, 16);
-      sz += __shfl_xor(sz, 32);
-      sp += __shfl_xor(sp, 32);
-      zs[nc][gr] = sz;
-      ps[nc][gr] = sp;
+      zs[nc][gr] += __shfl_xor(zs[nc][gr], 16);
+      zs[nc][gr] += __shfl_xor(zs[nc][gr], 32);
     }
     const float back = tau == -1024 ? 0.f : __builtin_ldexpf(1.f, tau);
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) {
-      const float up = (i & 1) ? 0x1p20f : 0x1p24f;
+    for (int i = 0; i < TILES; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        o[nc][i][r] = __builtin_fmaf(__builtin_fmaf(o[nc][i][r], up, -8.f * ps[nc][i / TG]), back, zs[nc][i / TG]);
-    }
+      for (int r = 0; r < 4; ++r) o[nc][i][r] = __builtin_fmaf(o[nc][i][r], back, zs[nc][i / TG]);
   }
   if (active > 1) {
     const int tile = entry * a.kv_heads + kvh;
