@@ -95,11 +95,21 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const bool fk = kBoth || wave < SUBS, fv = kBoth || (wave >= SUBS && wave < 2 * SUBS);
   unsigned rk[U], rv[U], rp[NG];
   bool rp_on = false;
-  auto block_of = [&](int t, int& in) {             // t at most te - 1
-    const int p = page_of(a, t);
-    int pg = a.table[(long long)b * a.max_pages + p];
+  // Page ids are loaded one step before their blocks' addresses are needed: the subtile's (uniform), and
+  // for the parameters the lane's token's.
+  const int* row_of = a.table + (long long)b * a.max_pages;
+  int pg_sub = 0, pg_tok = 0;
+  auto sub_at = [&](int step) {                     // past the end: any subtile, masked
+    return __builtin_amdgcn_readfirstlane(min(ts + kStep * step + 16 * fsub, (te - 1) & ~15));
+  };
+  auto tok_at = [&](int step) { return min(ts + kStep * step + lane % kStep, te - 1); };
+  auto fetch_pages = [&](int step) {
+    pg_sub = row_of[page_of(a, sub_at(step))];
+    if (wave < 2) pg_tok = row_of[page_of(a, tok_at(step))];
+  };
+  auto block_of = [&](int t, int pg, int& in) {
+    in = t - page_of(a, t) * a.page;
     if ((unsigned)pg >= (unsigned)a.num_pages) pg = 0;
-    in = t - p * a.page;
     return a.data + ((long long)pg * a.kv_heads + kvh) * a.block;
   };
   auto load_dwords = [&](const uint8_t* p, unsigned(&w)[U]) {
@@ -117,19 +127,17 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     }
   };
   auto fetch = [&](int step) {
-    const int t0 = ts + kStep * step;
     int in;
-    const int tsub = __builtin_amdgcn_readfirstlane(min(t0 + 16 * fsub, (te - 1) & ~15));   // past the end: any subtile, masked
-    const uint8_t* blk = block_of(tsub, in);
+    const uint8_t* blk = block_of(sub_at(step), pg_sub, in);
     if (fk) load_dwords(blk + (in * (D / 2) + (m * (D / 2) + 4 * U * g)), rk);
     if (fv) load_dwords(blk + a.codes + (in * (D / 2) + lane * (4 * U)), rv);
     if (wave < 2) {                                 // wavefront 0: K parameters, 1: V parameters; a token a lane
-      const int t = t0 + lane % kStep;
-      rp_on = t < te;
-      const uint8_t* pb = block_of(min(t, te - 1), in) + 2 * a.codes + wave * a.params;
+      rp_on = ts + kStep * step + lane % kStep < te;
+      const uint8_t* pb = block_of(tok_at(step), pg_tok, in) + 2 * a.codes + wave * a.params;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) rp[gr] = *reinterpret_cast<const unsigned*>(pb + 4 * (gr * a.page + in));
     }
+    fetch_pages(step + 1);
   };
   float kq = 0.f;                                   // set below, before the first store
   auto store = [&](int step) {
@@ -219,7 +227,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           }
       }
     }
-    if (steps) fetch(0);
+    if (steps) {
+      fetch_pages(0);
+      fetch(0);
+    }
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
     if (lane == 0) s_top[wave] = top;
@@ -462,7 +473,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         store(j + 1);
         if (j + 2 < steps) fetch(j + 2);
       }
-#pragma unroll 1
+#pragma unroll
       for (int pr = 0; pr < kHalves; ++pr) {
         const bool end = pr == kHalves - 1;
         if (end) __syncthreads();                   // step j + 1's operands are in LDS
