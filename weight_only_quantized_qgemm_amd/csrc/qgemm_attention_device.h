@@ -92,6 +92,11 @@ __device__ constexpr int kSlotDim[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
+// A row of 16 lanes turned by DPP control word C (row_ror n: 0x120 + n).
+template <int C>
+__device__ __forceinline__ unsigned dpp(unsigned x) {
+  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, C, 0xf, 0xf, false);
+}
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // V codes of one 16-token subtile, as loaded (lane r = l & 15, tokens 4 (l >> 4) .. + 3), for tile i:

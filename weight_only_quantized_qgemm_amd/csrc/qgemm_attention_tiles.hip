@@ -12,8 +12,8 @@
 //
 // The reference mx of a row bounds score + log2(value scale), in bits, of the tokens it has seen:
 // w = 2^(score - mx) * scale then fits fp16 whatever the scales are, at no cost per token, and
-// 2^-mx drops out with the sum.  Scales beyond 2^+-60 (bf16 only) are first brought near 1 by a power
-// of two common to the 64 tokens (tau), which O carries.
+// 2^-mx drops out with the sum.  mx follows scales down to 2^-60; scales beyond 2^60 (bf16 only) put
+// O into units of 2^64, and ones below 2^-60 put it into units of 2^-64.
 #include <type_traits>
 
 #include "qgemm_attention_device.h"
@@ -35,7 +35,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   constexpr int kSlot = BM * D + NC * NT * 4;       // floats of a partial
   __shared__ __align__(16) uint8_t s_k[2][KB], s_v[3][KB];
   __shared__ __align__(16) float s_p[3][PB / 4];    // [subtile][group][K scale, K zero, V scale, V middle][16]
-  __shared__ int s_exp[3][4];                       // tau, the largest exponent after it, any parameter not finite
+  __shared__ __align__(16) unsigned s_big[3][4];    // per subtile: the largest finite |V scale|, as its bits
+  __shared__ int s_odd[3];                          // any V parameter that is not finite
   __shared__ float s_top[NW];
   __shared__ int s_last;
 
@@ -93,6 +94,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   constexpr bool kBoth = NW == SUBS;                // as many wavefronts as subtiles: K and V each
   const int fsub = wave % SUBS;
   const bool fk = kBoth || wave < SUBS, fv = kBoth || (wave >= SUBS && wave < 2 * SUBS);
+  constexpr int kPar = NW >= 2 * SUBS + 2 ? 2 * SUBS : 0;           // the wavefronts that prepare parameters: K's, V's
+  const bool fp = wave == kPar || wave == kPar + 1, fpv = wave == kPar + 1;
   unsigned rk[U], rv[U], rp[NG];
   bool rp_on = false;
   // Page ids are loaded one step before their blocks' addresses are needed: the subtile's (uniform), and
@@ -105,7 +108,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   auto tok_at = [&](int step) { return min(ts + kStep * step + lane % kStep, te - 1); };
   auto fetch_pages = [&](int step) {
     pg_sub = row_of[page_of(a, sub_at(step))];
-    if (wave < 2) pg_tok = row_of[page_of(a, tok_at(step))];
+    if (fp) pg_tok = row_of[page_of(a, tok_at(step))];
   };
   auto block_of = [&](int t, int pg, int& in) {
     in = t - page_of(a, t) * a.page;
@@ -131,9 +134,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     const uint8_t* blk = block_of(sub_at(step), pg_sub, in);
     if (fk) load_dwords(blk + (in * (D / 2) + (m * (D / 2) + 4 * U * g)), rk);
     if (fv) load_dwords(blk + a.codes + (in * (D / 2) + lane * (4 * U)), rv);
-    if (wave < 2) {                                 // wavefront 0: K parameters, 1: V parameters; a token a lane
+    if (fp) {                                       // a token a lane
       rp_on = ts + kStep * step + lane % kStep < te;
-      const uint8_t* pb = block_of(tok_at(step), pg_tok, in) + 2 * a.codes + wave * a.params;
+      const uint8_t* pb = block_of(tok_at(step), pg_tok, in) + 2 * a.codes + (fpv ? a.params : 0);
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) rp[gr] = *reinterpret_cast<const unsigned*>(pb + 4 * (gr * a.page + in));
     }
@@ -155,43 +158,40 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
             u32x2{centre(x, i & 1), centre(y, i & 1)};
       }
     }
-    if (wave < 2) {
+    if (fp) {
       float sc[NG], z[NG];
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         sc[gr] = par_scale<BF>(rp[gr]);
         z[gr] = par_zero<BF>(rp[gr]);
       }
-      if (wave == 0) {
+      if (!fpv) {
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
       } else {
-        float big = 0.f;
+        unsigned big = 0;                           // magnitudes compare as their bits do
         bool odd = false;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           if (!rp_on) sc[gr] = z[gr] = 0.f;         // no token: its bits must not multiply
           z[gr] = __builtin_fmaf(sc[gr], 8.f, z[gr]);
-          big = __builtin_fmaxf(big, __builtin_fabsf(sc[gr]));
-          odd |= !(__builtin_fabsf(sc[gr]) + __builtin_fabsf(z[gr]) < __builtin_inff());
+          const unsigned sb = __builtin_bit_cast(unsigned, __builtin_fabsf(sc[gr]));
+          const bool fine = __builtin_fabsf(z[gr]) < __builtin_inff();
+          big = max(big, fine ? sb : 0u);
+          odd |= !fine;
         }
         odd = __any(odd);
-#pragma unroll
-        for (int x = 1; x < 64; x *= 2) big = __builtin_fmaxf(big, __shfl_xor(big, x));
-        int e = big > 0.f ? __builtin_amdgcn_frexp_expf(big) : -kRoomMax;
-        const int tau = e > kRoomMax ? 64 : e < -kRoomMax ? -64 : 0;
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) sc[gr] = __builtin_ldexpf(sc[gr], -tau);
-        if (lane == 0) {
-          s_exp[vb][0] = tau;
-          s_exp[vb][1] = e - tau;
-          s_exp[vb][2] = odd;
-        }
+        big = max(big, dpp<0x128>(big));            // row_ror 8, 4, 2, 1: over the subtile's 16 lanes
+        big = max(big, dpp<0x124>(big));
+        big = max(big, dpp<0x122>(big));
+        big = max(big, dpp<0x121>(big));
+        if ((lane & 15) == 0) s_big[vb][lane >> 4] = big;
+        if (lane == 0) s_odd[vb] = odd;
       }
       if (lane < kStep) {
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          float* p = &s_p[vb][(((lane >> 4) * NG + gr) * 4 + 2 * wave) * 16 + (lane & 15)];
+          float* p = &s_p[vb][(((lane >> 4) * NG + gr) * 4 + (fpv ? 2 : 0)) * 16 + (lane & 15)];
           p[0] = sc[gr];
           p[16] = z[gr];
         }
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   float mx[NC], l[NC], zs[NC][NG];
   bool fresh[NC];                                   // the row has seen no token: mx is not set
   f32x4 o[NC][TILES];
-  int tau = -1024;
+  int tau = -64;                                    // O is in units of 2^tau
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
     mx[nc] = l[nc] = 0.f;
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   };
   // A half's weights, as B operands, while the next half's products with K run beside them (into
   // buffers that exist even after the last half: its scores are not used).  kMask: a weight of 0 must
-  // not meet a parameter that is not finite, and the step's values may be in units below O's.
+  // not meet a parameter that is not finite, and O's unit is not 1.
   unsigned seen[NC];
   typedef u32x4 Weights[NG][NC];
   auto weights = [&](auto mask_c, int step, int pr, int nstep, int npr, float tf, Acc& acc, Weights& bp) {
@@ -362,19 +362,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // One half, whose scores u holds.
   auto compute = [&](int step, int pr, int nstep, int npr) {
     const int tp = ts + kStep * step + 32 * pr, vb = step % 3;
-    const int etau = __builtin_amdgcn_readfirstlane(s_exp[vb][0]);
-    const float room = (float)min(kRoomMax, kRoom - __builtin_amdgcn_readfirstlane(s_exp[vb][1]));
-    float tf = 1.f;                                 // the step's values in units of O's tau
-    if (etau > tau) {
-      const float f = __builtin_ldexpf(1.f, tau - etau);
+    const u32x2 bb = *reinterpret_cast<const u32x2*>(&s_big[vb][2 * pr]);
+    const unsigned big = __builtin_amdgcn_readfirstlane(max(bb[0], bb[1]));
+    const bool odd = __builtin_amdgcn_readfirstlane(s_odd[vb]);
+    const int e = big ? (int)(big >> 23) - 126 : -kRoomMax;            // scales are below 2^e
+    const int unit = e > kRoomMax ? 64 : e < -kRoomMax ? -64 : 0;
+    if (unit > tau) {                               // O only ever goes to larger units
+      const float f = __builtin_ldexpf(1.f, tau - unit);
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
         for (int i = 0; i < TILES; ++i) o[nc][i] *= f;
-      tau = etau;
-    } else {
-      tf = __builtin_ldexpf(1.f, etau - tau);
+      tau = unit;
     }
+    const float tf = __builtin_ldexpf(1.f, -tau), room = (float)min(kRoomMax, kRoom - (e - tau));
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) seen[nc] = 255;
     if (tp + 32 > min(all_hi, te) || tp < all_lo || idle) {            // not every row sees every token
@@ -446,7 +447,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     }
     Acc acc;
     Weights bp;
-    if (tf != 1.f || __builtin_amdgcn_readfirstlane(s_exp[vb][2])) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
+    if (tau || odd) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
     else weights(std::false_type{}, step, pr, nstep, npr, tf, acc, bp);
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
@@ -492,7 +493,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       zs[nc][gr] += __shfl_xor(zs[nc][gr], 16);
       zs[nc][gr] += __shfl_xor(zs[nc][gr], 32);
     }
-    const float back = tau == -1024 ? 0.f : __builtin_ldexpf(1.f, tau);
+    const float back = __builtin_ldexpf(1.f, tau);
 #pragma unroll
     for (int i = 0; i < TILES; ++i)
 #pragma unroll
