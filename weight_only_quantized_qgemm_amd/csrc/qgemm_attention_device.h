@@ -42,7 +42,9 @@ struct AttnArgs {
   int codes, params, block;        // bytes of one side's codes, of its parameters, of a block
   unsigned page_mul, page_shift;   // t / page = (t * page_mul) >> (32 + page_shift) for t < 2^30
   int max_q, causal, window;
-  int units_min;                   // rows kernel: least units of 64 tokens a workgroup takes
+  // rows kernel, units of 64 tokens per piece: piece_most while a workgroup's share is at most piece_small
+  // units, piece_some while it is at most piece_most, else 1
+  int piece_small, piece_some, piece_most;
   int splits;                      // tiles kernel: workgroups per row tile
   float scale;                     // the caller's scale * log2(e)
   unsigned* tickets;
@@ -128,6 +130,22 @@ __device__ __forceinline__ unsigned centre(unsigned pair, bool high) {
 
 __device__ __forceinline__ int page_of(const AttnArgs& a, int t) {
   return (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift);
+}
+
+// Sum over the wavefront, and the sum up to and including each lane.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) {
+    const int y = __shfl_up(v, x);
+    if (lane >= x) v += y;
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) v += __shfl_xor(v, x);
+  return __builtin_amdgcn_readfirstlane(v);
 }
 
 // Sequence b's geometry from device memory, every value bounded.

@@ -31,15 +31,17 @@ enum AttnKind : int { ATTN_ROWS = 1, ATTN_TILES = 2 };
 
 // Tiles kernel: column tiles of 16 query rows per wavefront and wavefronts per workgroup.
 struct TileShape { int cols, waves; };
-#ifndef QGEMM_TILE_64
-#define QGEMM_TILE_64 3, 8
-#define QGEMM_TILE_128 2, 8
-#define QGEMM_TILE_256 2, 4
-#endif
 constexpr TileShape tile_shape(int dim, int groups) {
-  return dim == 64 ? TileShape{QGEMM_TILE_64} : dim == 128 ? TileShape{QGEMM_TILE_128} : TileShape{QGEMM_TILE_256};
+  return dim == 256 && groups == 4 ? TileShape{2, 4} : dim == 256 || groups == 4 ? TileShape{1, 8} : TileShape{2, 8};
 }
 constexpr int tile_rows(TileShape t) { return 16 * t.cols * t.waves; }
+
+// Rows kernel: units of 64 tokens per piece (see AttnArgs).
+#ifndef QGEMM_PIECES
+#define QGEMM_PIECES 2, 8, 16
+#endif
+struct Pieces { int small, some, most; };
+constexpr Pieces kPieces{QGEMM_PIECES};
 
 // Launch plan of qgemm_attention, a pure function of the descriptor.
 struct AttnPlan {
@@ -47,8 +49,6 @@ struct AttnPlan {
   int groups;          // NG
   int rows;            // query rows per kv head and sequence, at most: ratio * max_q_len
   int pack;            // rows kernel: subtiles side by side in the 16 columns (F: 1, 2, 4)
-  int col_tiles;       // rows kernel: column tiles of 16 rows (NC: 1, 2)
-  int units_min;       // rows kernel: least units of 64 tokens per workgroup
   int tile, splits;    // tiles kernel: query rows per workgroup, workgroups per row tile
   unsigned grid;       // workgroups
   size_t tickets_bytes;

@@ -42,10 +42,10 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, unsigned (&w)[U]) 
   }
 }
 
-template <bool BF, int D, int NG, int F, int NC>
-__global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
+template <bool BF, int D, int NG, int F>
+__global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
   constexpr int U = D / 32, SUB = F == 1 ? 2 : F, ST = F == 1 ? 2 : 1, T = 16 * SUB;
-  constexpr int R16 = 16 / F, RT = R16 * NC;        // rows per column tile, rows per row tile
+  constexpr int RT = 16 / F;                        // rows per row tile
   constexpr int TILES = D / 16, TG = TILES / NG;    // output tiles, and those of one group
   constexpr int SG = U / NG;                        // k steps of one group
   constexpr int kRowF = D + 4;                      // padded floats of an LDS row
@@ -56,43 +56,52 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
   __shared__ int s_last;
 
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int fcol = m / R16;                         // the lane's subtile of a step (F > 1)
+  const int fcol = m / RT;                          // the lane's subtile of a step (F > 1)
   const int wg = blockIdx.x;
 
-  // ---- this workgroup's run of units
-  auto units_of = [&](const Seq& s) {
-    if (!s.n) return 0;
-    return a.kv_heads * ((a.ratio * s.n + RT - 1) / RT) * max(1, (s.hi - s.lo + 63) / 64);
-  };
+  // ---- this workgroup's run of units.  Short work is cut coarsely (`piece` units of 64 tokens, so that
+  // few segments are split and a workgroup has one piece), long work finely (equal runs).
+  auto tiles_of = [&](const Seq& s) { return a.kv_heads * ((a.ratio * s.n + RT - 1) / RT); };
+  auto units_of = [&](const Seq& s) { return max(1, (s.hi - s.lo + 63) / 64); };
+  Seq mine_seq = lane < a.batch ? load_seq(a, lane) : Seq{0, 0, 0, 0, 0};      // the first 64 stay at hand
   int total = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int u = b0 + lane < a.batch ? units_of(load_seq(a, b0 + lane)) : 0;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) u += __shfl_xor(u, x);
-    total += u;
+    const Seq x = b0 == 0 ? mine_seq : b0 + lane < a.batch ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
+    total += wave_sum(tiles_of(x) * units_of(x));
   }
-  total = __builtin_amdgcn_readfirstlane(total);
   if (!total) return;
-  const int G = min((int)gridDim.x, (total + a.units_min - 1) / a.units_min);
+  const int grid = (int)gridDim.x;
+  const int piece = total <= grid * a.piece_small ? a.piece_most : total <= grid * a.piece_most ? a.piece_some : 1;
+  auto pieces_of = [&](const Seq& s) { return (units_of(s) + piece - 1) / piece; };
+  if (piece > 1) {
+    total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+      const Seq x = b0 == 0 ? mine_seq : b0 + lane < a.batch ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
+      total += wave_sum(tiles_of(x) * pieces_of(x));
+    }
+  }
+  const int G = min(grid, total);
   if (wg >= G) return;
   const int uq = total / G, ur = total - uq * G;
   int u0 = wg * uq + min(wg, ur);
   const int u1 = u0 + uq + (wg < ur ? 1 : 0);
   auto owner = [&](int u) { return u < ur * (uq + 1) ? u / (uq + 1) : ur + (u - ur * (uq + 1)) / uq; };
-  // the sequence that holds unit u0
+  // the sequence that holds piece u0
   int b = 0, before = 0;
+  Seq s;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int u = b0 + lane < a.batch ? units_of(load_seq(a, b0 + lane)) : 0;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-      const int y = __shfl_up(u, x);
-      if (lane >= x) u += y;
-    }
+    const Seq x = b0 == 0 ? mine_seq : b0 + lane < a.batch ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
+    const int u = wave_scan(tiles_of(x) * pieces_of(x));
     const unsigned long long past = __ballot(before + u > u0);      // the first lane whose end lies past u0
     if (past) {
       const int l = __builtin_ctzll(past);
       b = b0 + l;
       before += l ? __builtin_amdgcn_readlane(u, l - 1) : 0;
+      s.start = __builtin_amdgcn_readlane(x.start, l);
+      s.n = __builtin_amdgcn_readlane(x.n, l);
+      s.len = __builtin_amdgcn_readlane(x.len, l);
+      s.lo = __builtin_amdgcn_readlane(x.lo, l);
+      s.hi = __builtin_amdgcn_readlane(x.hi, l);
       break;
     }
     before += __builtin_amdgcn_readlane(u, 63);
@@ -101,108 +110,18 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
   before = __builtin_amdgcn_readfirstlane(before);
 
   while (u0 < u1) {
-    Seq s = load_seq(a, b);
-    const int ub = units_of(s);
+    const int nu = pieces_of(s), ub = tiles_of(s) * nu;
     if (u0 >= before + ub) {                        // next sequence (some hold nothing)
       before += ub;
-      ++b;
+      s = load_seq(a, ++b);
       continue;
     }
-    const int nu = max(1, (s.hi - s.lo + 63) / 64);
-    const int seg = (u0 - before) / nu, first = before + seg * nu;   // segment, its first unit
+    const int seg = (u0 - before) / nu, first = before + seg * nu;   // segment, its first piece
     const int take = min(first + nu - u0, u1 - u0);
     const int rt = seg / a.kv_heads, kvh = seg - rt * a.kv_heads;
-    const int ts = s.lo + 64 * (u0 - first), te = min(s.hi, ts + 64 * take);
-
-    // ---- queries: rows rt RT + nc R16 + m % R16, row = query * ratio + head within the group
-    u32x4 qf[F == 1 ? 1 : F][U][NC];
-    float qz[NC][NG];
-    int see_lo[NC], see_hi[NC];
-    float kq;
-    const int rows = a.ratio * s.n;
-    {
-      u32x4 raw[NC][U];
-      float top = 0.f;
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int row = rt * RT + nc * R16 + m % R16;
-        const bool on = row < rows;
-        const int i = on ? row / a.ratio : 0, h = row - i * a.ratio;
-        const int pos = s.len - s.n + i;
-        see_hi[nc] = a.causal ? min(pos + 1, s.len) : s.len;
-        see_lo[nc] = a.window ? pos - a.window + 1 : 0;
-        const uint16_t* src = a.q + (long long)(s.start + i) * a.qs + (kvh * a.ratio + h) * D + 8 * g;
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          raw[nc][j] = on ? *reinterpret_cast<const u32x4*>(src + 32 * j) : u32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const float x = __builtin_fabsf(from16<BF>(raw[nc][j][e] >> (16 * o) & 0xffffu));
-              top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
-            }
-        }
-      }
-#pragma unroll
-      for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
-      // top = f 2^e, f in [1/2, 1)
-      const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
-      kq = __builtin_ldexpf(a.scale, 24 - 14 + e);
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          float sum = 0.f;
-#pragma unroll
-          for (int j = gr * SG; j < (gr + 1) * SG; ++j) {
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              x[k] = from16<BF>(raw[nc][j][k / 2] >> (16 * (k & 1)) & 0xffffu);
-              sum += x[k];
-            }
-            u32x4 f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int sh = 14 - e - ((k & 1) ? 4 : 0);
-              f[k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
-            }
-            if constexpr (F == 1) {
-              qf[0][j][nc] = f;
-            } else {
-#pragma unroll
-              for (int ff = 0; ff < F; ++ff) qf[ff][j][nc] = fcol == ff ? f : u32x4{0, 0, 0, 0};
-            }
-          }
-          sum += __shfl_xor(sum, 16);
-          sum += __shfl_xor(sum, 32);
-          qz[nc][gr] = sum * a.scale;
-        }
-    }
-    // tokens that every row sees
-    const int last = min(rows - 1, rt * RT + RT - 1);
-    const int all_hi = a.causal ? min(s.len, s.len - s.n + rt * RT / a.ratio + 1) : s.len;
-    const int all_lo = a.window ? s.len - s.n + last / a.ratio - a.window + 1 : 0;
+    const int ts = s.lo + 64 * piece * (u0 - first), te = min(s.hi, ts + 64 * piece * take);
 
     // ---- the wavefront's steps: token ts + T (wave + 4 j)
-    float mx[NC], l[NC], zs[NC][NG], ps[NC][NG];
-    bool fresh[NC];                                 // the row has seen no token: mx is not set
-    f32x4 o[NC][TILES];
-    // a row's value scales are divided by 2^sig (inv = 2^-sig), a bound of those it has seen
-    int sig[NC];
-    float inv[NC];
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      mx[nc] = l[nc] = 0.f;
-      fresh[nc] = true;
-      sig[nc] = -126;
-      inv[nc] = 0x1p126f;
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) zs[nc][gr] = ps[nc][gr] = 0.f;
-#pragma unroll
-      for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
     const int steps = te > ts ? (te - ts + T - 1) / T : 0;
     const int mine = steps > wave ? (steps - wave + 3) / 4 : 0;
     constexpr int PER = 64 / SUB;                   // steps whose pages one register holds
@@ -243,194 +162,217 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
         }
       }
     };
-    auto step = [&](auto edge_c, int t0, const StepT& st) {
-      constexpr bool kEdge = decltype(edge_c)::value;
+    StepT sa, sb;
+    if (mine) pages(0);
+    // ---- queries: column m holds row rt RT + m % RT, row = query * ratio + head within the group
+    const int rows = a.ratio * s.n;
+    u32x4 qf[U];
+    float qz[NG], kq;
+    int see_lo, see_hi;                             // tokens the lane's row sees
+    {
+      const int row = rt * RT + m % RT;
+      const bool on = row < rows;
+      const int i = on ? row / a.ratio : 0, h = row - i * a.ratio;
+      const int pos = s.len - s.n + i;
+      see_hi = a.causal ? min(pos + 1, s.len) : s.len;
+      see_lo = a.window ? pos - a.window + 1 : 0;
+      const uint16_t* src = a.q + (long long)(s.start + i) * a.qs + (kvh * a.ratio + (on ? h : 0)) * D + 8 * g;
+      u32x4 raw[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) raw[j] = on ? *reinterpret_cast<const u32x4*>(src + 32 * j) : u32x4{0, 0, 0, 0};
+      if (mine) fetch(0, sa);                       // beside the queries' reduction and conversion
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const float x = __builtin_fabsf(from16<BF>(raw[j][e] >> (16 * o) & 0xffffu));
+            top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
+          }
+#pragma unroll
+      for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+      // top = f 2^e, f in [1/2, 1)
+      const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
+      kq = __builtin_ldexpf(a.scale, 24 - 14 + e);
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = gr * SG; j < (gr + 1) * SG; ++j) {
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[k] = from16<BF>(raw[j][k / 2] >> (16 * (k & 1)) & 0xffffu);
+            sum += x[k];
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int sh = 14 - e - ((k & 1) ? 4 : 0);
+            qf[j][k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
+          }
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        qz[gr] = sum * a.scale;
+      }
+    }
+    // tokens that every row sees
+    const int last = min(rows - 1, rt * RT + RT - 1);
+    const int all_hi = a.causal ? min(s.len, s.len - s.n + rt * RT / a.ratio + 1) : s.len;
+    const int all_lo = a.window ? s.len - s.n + last / a.ratio - a.window + 1 : 0;
+
+    float mx = 0.f, l = 0.f, zs[NG], ps[NG];
+    bool fresh = true;                              // the row has seen no token: mx is not set
+    f32x4 o[TILES];
+    // the row's value scales are divided by 2^sig (inv = 2^-sig), a bound of those it has seen
+    int sig = -126;
+    float inv = 0x1p126f;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) zs[gr] = ps[gr] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto compute = [&](int j, StepT& st) {
+      const int t0 = ts + T * (wave + 4 * j);
       // S^T, then scores in bits less the row's running maximum
-      float u[NC][ST][4];
+      float u[ST][4];
 #pragma unroll
       for (int x = 0; x < ST; ++x)
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          f32x4 acc[NC];
+          f32x4 acc;
 #pragma unroll
-          for (int nc = 0; nc < NC; ++nc) acc[nc] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int f = F == 1 ? x : 0; f < (F == 1 ? x + 1 : SUB); ++f) {
+            f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int f = F == 1 ? x : 0; f < (F == 1 ? x + 1 : SUB); ++f)
+            for (int i = gr * SG; i < (gr + 1) * SG; ++i) c = mfma(codes8(st.k[f][i]), qf[i], c);
+            // with F > 1 a lane keeps the subtile of its column group
 #pragma unroll
-            for (int i = gr * SG; i < (gr + 1) * SG; ++i) {
-              const u32x4 kf = codes8(st.k[f][i]);
-#pragma unroll
-              for (int nc = 0; nc < NC; ++nc) acc[nc] = mfma(kf, qf[F == 1 ? 0 : f][i][nc], acc[nc]);
-            }
+            for (int r = 0; r < 4; ++r) acc[r] = F == 1 || f == 0 || fcol == f ? c[r] : acc[r];
+          }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const unsigned w = st.kp[x][gr][r];
-            const float sc = par_scale<BF>(w) * kq, z = par_zero<BF>(w);
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc) {
-              const float v = __builtin_fmaf(z, qz[nc][gr], gr ? u[nc][x][r] : -mx[nc]);
-              u[nc][x][r] = __builtin_fmaf(sc, acc[nc][r], v);
-            }
+            const float v = __builtin_fmaf(par_zero<BF>(w), qz[gr], gr ? u[x][r] : -mx);
+            u[x][r] = __builtin_fmaf(par_scale<BF>(w) * kq, acc[r], v);
           }
         }
-      unsigned seen[NC];                            // bit 4 x + r
-      if constexpr (kEdge) {
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          seen[nc] = 0;
-#pragma unroll
-          for (int x = 0; x < ST; ++x)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int t = t0 + 16 * (F == 1 ? x : fcol) + 4 * g + r;
-              if (t >= see_lo[nc] && t < see_hi[nc] && t < te) seen[nc] |= 1u << (4 * x + r);
-              else u[nc][x][r] = -__builtin_inff();
-            }
-        }
-      }
-      bool move = false;
-      float big[NC];                                // the largest value scale that each row sees
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        float high = u[nc][0][0];
-        big[nc] = 0.f;
+      if (t0 + T > min(all_hi, te) || t0 < all_lo) {
+        // a token that the lane's row does not see: weight 0, and its parameters (any bits) are put away
 #pragma unroll
         for (int x = 0; x < ST; ++x)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            high = __builtin_fmaxf(high, u[nc][x][r]);
+            const int t = t0 + 16 * (F == 1 ? x : fcol) + 4 * g + r;
+            if (!(t >= see_lo && t < see_hi && t < te)) {
+              u[x][r] = -__builtin_inff();
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              const float v = __builtin_fabsf(par_scale<BF>(st.vp[x][gr][r]));
-              big[nc] = __builtin_fmaxf(big[nc], !kEdge || (seen[nc] >> (4 * x + r) & 1) ? v : 0.f);
+              for (int gr = 0; gr < NG; ++gr) st.vp[x][gr][r] = 0u;
             }
           }
-        move |= high > (fresh[nc] ? -3e38f : kSlack) || big[nc] * inv[nc] > kScaleSlack;
       }
-      if (__any(move)) {
+      float high = u[0][0], big = 0.f;              // and the largest value scale that the row sees here
+#pragma unroll
+      for (int x = 0; x < ST; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          high = __builtin_fmaxf(high, u[x][r]);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) big = __builtin_fmaxf(big, __builtin_fabsf(par_scale<BF>(st.vp[x][gr][r])));
+        }
+      if (__any(high > (fresh ? -3e38f : kSlack) || big * inv > kScaleSlack)) {
         // set or move the running maxima and value scales that need it, rescale what is summed so far
+        float top = high, smax = big;
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          float top = -3e38f, smax = big[nc];
-#pragma unroll
-          for (int x = 0; x < ST; ++x)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) top = __builtin_fmaxf(top, u[nc][x][r]);
-#pragma unroll
-          for (int x = 16; x < 64; x *= 2) {
-            top = __builtin_fmaxf(top, __shfl_xor(top, x));
-            smax = __builtin_fmaxf(smax, __shfl_xor(smax, x));
-          }
-          // a row's maximum moves for its own scores only: its result does not depend on its neighbours
-          const bool go = top > (fresh[nc] ? -3e38f : kSlack);
-          const float by = go ? top : 0.f, al = fresh[nc] ? 1.f : exp2_fast(-by);
-          const int ns = smax * inv[nc] > kScaleSlack ? __builtin_amdgcn_frexp_expf(smax) : sig[nc];
-          const float ab = __builtin_ldexpf(al, sig[nc] - ns);
-          fresh[nc] = fresh[nc] && !go;
-          mx[nc] += by;
-          sig[nc] = ns;
-          inv[nc] = __builtin_ldexpf(1.f, -ns);
-          l[nc] *= al;
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            zs[nc][gr] *= al;
-            ps[nc][gr] *= ab;
-          }
-#pragma unroll
-          for (int i = 0; i < TILES; ++i) o[nc][i] *= ab;
-#pragma unroll
-          for (int x = 0; x < ST; ++x)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u[nc][x][r] -= by;
+        for (int x = 16; x < 64; x *= 2) {
+          top = __builtin_fmaxf(top, __shfl_xor(top, x));
+          smax = __builtin_fmaxf(smax, __shfl_xor(smax, x));
         }
-      }
+        // a row's maximum moves for its own scores only: its result does not depend on its neighbours
+        const bool go = top > (fresh ? -3e38f : kSlack);
+        const float by = go ? top : 0.f, al = fresh ? 1.f : exp2_fast(-by);
+        const int ns = smax * inv > kScaleSlack ? __builtin_amdgcn_frexp_expf(smax) : sig;
+        const float ab = __builtin_ldexpf(al, sig - ns);
+        fresh = fresh && !go;
+        mx += by;
+        sig = ns;
+        inv = __builtin_ldexpf(1.f, -ns);
+        l *= al;
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc)
+        for (int gr = 0; gr < NG; ++gr) {
+          zs[gr] *= al;
+          ps[gr] *= ab;
+        }
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) o[i] *= ab;
 #pragma unroll
         for (int x = 0; x < ST; ++x)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            u[nc][x][r] = exp2_fast(u[nc][x][r]);
-            l[nc] += u[nc][x][r];
-          }
+          for (int r = 0; r < 4; ++r) u[x][r] -= by;
+      }
+#pragma unroll
+      for (int x = 0; x < ST; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          u[x][r] = exp2_fast(u[x][r]);
+          l += u[x][r];
+        }
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        unsigned pk[NC][ST][2];
+        unsigned pk[ST][2];
 #pragma unroll
         for (int x = 0; x < ST; ++x) {
-          float sc[4], md[4];                       // scale, zero + 8 scale
+          float w[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const unsigned w = st.vp[x][gr][r];
-            sc[r] = par_scale<BF>(w);
-            md[r] = __builtin_fmaf(sc[r], 8.f, par_zero<BF>(w));
+            const unsigned v = st.vp[x][gr][r];
+            const float sc = par_scale<BF>(v);
+            w[r] = u[x][r] * (sc * inv);
+            zs[gr] = __builtin_fmaf(u[x][r], __builtin_fmaf(sc, 8.f, par_zero<BF>(v)), zs[gr]);
           }
 #pragma unroll
-          for (int nc = 0; nc < NC; ++nc) {
-            float w[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const bool on = !kEdge || (seen[nc] >> (4 * x + r) & 1);
-              w[r] = on ? u[nc][x][r] * (sc[r] * inv[nc]) : 0.f;
-              zs[nc][gr] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][gr]);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // rounded to 11 bits, and summed as rounded: the codes' middle is taken out exactly
-              const unsigned v = pack_f16(w[2 * h], w[2 * h + 1]);
-              ps[nc][gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, v), f16x2{(_Float16)1.f, (_Float16)1.f},
-                                                  ps[nc][gr], false);
-              pk[nc][x][h] = v;
-            }
+          for (int h = 0; h < 2; ++h) {
+            // rounded to 11 bits, and summed as rounded: the codes' middle is taken out exactly
+            pk[x][h] = pack_f16(w[2 * h], w[2 * h + 1]);
+            ps[gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pk[x][h]), f16x2{(_Float16)1.f, (_Float16)1.f},
+                                            ps[gr], false);
           }
         }
         // O^T += V^T P^T, two subtiles at a time
 #pragma unroll
         for (int pr = 0; pr < SUB / 2; ++pr) {
-          u32x4 bp[NC];
+          u32x4 bp;
 #pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if constexpr (F == 1) {
-                bp[nc][h] = pk[nc][0][h];
-                bp[nc][2 + h] = pk[nc][ST - 1][h];
-              } else {
-                bp[nc][h] = fcol == 2 * pr ? pk[nc][0][h] : 0u;
-                bp[nc][2 + h] = fcol == 2 * pr + 1 ? pk[nc][0][h] : 0u;
-              }
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (F == 1) {
+              bp[h] = pk[0][h];
+              bp[2 + h] = pk[ST - 1][h];
+            } else {
+              bp[h] = fcol == 2 * pr ? pk[0][h] : 0u;
+              bp[2 + h] = fcol == 2 * pr + 1 ? pk[0][h] : 0u;
             }
+          }
 #pragma unroll
           for (int i = gr * TG; i < (gr + 1) * TG; ++i) {
             unsigned x0, x1, y0, y1;
             v_pairs<U>(st.v[2 * pr], i, x0, x1);
             v_pairs<U>(st.v[2 * pr + 1], i, y0, y1);
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(u32x4{x0, x1, y0, y1}, bp[nc], o[nc][i]);
+            o[i] = mfma(u32x4{x0, x1, y0, y1}, bp, o[i]);
           }
         }
       }
     };
-    auto compute = [&](int j, const StepT& st) {
-      const int t0 = ts + T * (wave + 4 * j);
-      // tokens that every row sees need no mask: the common case, kept free of selects
-      if (t0 + T > min(all_hi, te) || t0 < all_lo) step(std::true_type{}, t0, st);
-      else step(std::false_type{}, t0, st);
-    };
-    if (mine) {
-      StepT sa, sb;
-      pages(0);
-      fetch(0, sa);
-      for (int j = 0; j < mine; j += 2) {
-        // PER is even, so only the step after an odd one can need new pages
-        if (j + 1 < mine) fetch(j + 1, sb);
-        compute(j, sa);
-        if (j + 2 < mine) {
-          if ((j + 2) % PER == 0) pages(j + 2);
-          fetch(j + 2, sa);
-        }
-        if (j + 1 < mine) compute(j + 1, sb);
+    for (int j = 0; j < mine; j += 2) {
+      // PER is even, so only the step after an odd one can need new pages
+      if (j + 1 < mine) fetch(j + 1, sb);
+      compute(j, sa);
+      if (j + 2 < mine) {
+        if ((j + 2) % PER == 0) pages(j + 2);
+        fetch(j + 2, sa);
       }
+      if (j + 1 < mine) compute(j + 1, sb);
     }
 
     // ---- join: the wavefront's sums over its lanes, the columns and wavefronts through LDS
@@ -441,65 +383,58 @@ __global__ __launch_bounds__(256) void attention_rows(AttnArgs a) {
       const int gi = rt * RT + row;
       if (gi >= rows) return;
       const int i = gi / a.ratio, h = gi - i * a.ratio;
-      const float r = sum == 0.f ? 0.f : 1.0f / sum;
-      // a sum of 0: nothing was seen, and every partial output is 0 as well
-      u32x2 w{pack2<BF>(v[0] * r, v[1] * r), pack2<BF>(v[2] * r, v[3] * r)};
-      *reinterpret_cast<u32x2*>(a.out + (long long)(s.start + i) * a.os + (kvh * a.ratio + h) * D + d) = w;
+      const float r = sum == 0.f ? 0.f : 1.0f / sum;                 // 0: nothing was seen, v is 0 as well
+      *reinterpret_cast<u32x2*>(a.out + (long long)(s.start + i) * a.os + (kvh * a.ratio + h) * D + d) =
+          u32x2{pack2<BF>(v[0] * r, v[1] * r), pack2<BF>(v[2] * r, v[3] * r)};
     };
+    const float back = __builtin_ldexpf(1.f, sig);
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
 #pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      const float back = __builtin_ldexpf(1.f, sig[nc]);
-      float sl = l[nc], sz[NG], sp[NG];
-      sl += __shfl_xor(sl, 16);
-      sl += __shfl_xor(sl, 32);
+    for (int gr = 0; gr < NG; ++gr) {
+      zs[gr] += __shfl_xor(zs[gr], 16);
+      ps[gr] += __shfl_xor(ps[gr], 16);
+      zs[gr] += __shfl_xor(zs[gr], 32);
+      ps[gr] += __shfl_xor(ps[gr], 32);
+    }
+    __syncthreads();                                // the previous segment is done with LDS
+    if (g == 0) {
+      s_m[wave * 16 + m] = fresh ? kStart : mx;
+      s_l[wave * 16 + m] = l;
+    }
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        sz[gr] = zs[nc][gr];
-        sp[gr] = ps[nc][gr];
-        sz[gr] += __shfl_xor(sz[gr], 16);
-        sp[gr] += __shfl_xor(sp[gr], 16);
-        sz[gr] += __shfl_xor(sz[gr], 32);
-        sp[gr] += __shfl_xor(sp[gr], 32);
-      }
-      __syncthreads();                              // the previous column tile (or segment) is done with LDS
-      if (g == 0) {
-        s_m[wave * 16 + m] = fresh[nc] ? kStart : mx[nc];
-        s_l[wave * 16 + m] = sl;
-      }
+    for (int i = 0; i < TILES; ++i) {
+      const float up = (i & 1) ? 0x1p20f : 0x1p24f;
+      f32x4 v;
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) {
-        const float up = (i & 1) ? 0x1p20f : 0x1p24f;
-        f32x4 v;
+      for (int r = 0; r < 4; ++r)
+        v[r] = __builtin_fmaf(__builtin_fmaf(o[i][r], up, -8.f * ps[i / TG]), back, zs[i / TG]);
+      *reinterpret_cast<f32x4*>(&s_o[(wave * 16 + m) * kRowF + 16 * i + 4 * g]) = v;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < RT * (D / 4); e += 256) {
+      const int row = e / (D / 4), d = e % (D / 4) * 4;
+      float top = kStart;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[r] = __builtin_fmaf(__builtin_fmaf(o[nc][i][r], up, -8.f * sp[i / TG]), back, sz[i / TG]);
-        *reinterpret_cast<f32x4*>(&s_o[(wave * 16 + m) * kRowF + 16 * i + 4 * g]) = v;
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < R16 * (D / 4); e += 256) {
-        const int row = e / (D / 4), d = e % (D / 4) * 4;
-        float top = kStart;
+      for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int f = 0; f < F; ++f) top = __builtin_fmaxf(top, s_m[w * 16 + f * RT + row]);
+      float sum = 0.f;
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int f = 0; f < F; ++f) top = __builtin_fmaxf(top, s_m[w * 16 + f * R16 + row]);
-        float sum = 0.f;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-#pragma unroll
-          for (int f = 0; f < F; ++f) {
-            const int c = w * 16 + f * R16 + row;
-            const float sc = exp2_fast(s_m[c] - top);
-            sum = __builtin_fmaf(s_l[c], sc, sum);
-            v += *reinterpret_cast<const f32x4*>(&s_o[c * kRowF + d]) * sc;
-          }
-        if (whole) {
-          write_out(nc * R16 + row, d, v, sum);
-        } else {
-          store4(mydst, ((nc * R16 + row) * D + d) * 4, v);
-          if (d == 0) store4(mydst, (RT * D + 4 * (nc * R16 + row)) * 4, f32x4{top, sum, 0.f, 0.f});
+        for (int f = 0; f < F; ++f) {
+          const int c = w * 16 + f * RT + row;
+          const float sc = exp2_fast(s_m[c] - top);
+          sum = __builtin_fmaf(s_l[c], sc, sum);
+          v += *reinterpret_cast<const f32x4*>(&s_o[c * kRowF + d]) * sc;
         }
+      if (whole) {
+        write_out(row, d, v, sum);
+      } else {
+        store4(mydst, (row * D + d) * 4, v);
+        if (d == 0) store4(mydst, (RT * D + 4 * row) * 4, f32x4{top, sum, 0.f, 0.f});
       }
     }
     if (!whole) {
@@ -541,13 +476,11 @@ template <bool BF, int D, int NG>
 hipError_t launch_groups(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
   const dim3 grid(pl.grid), block(256);
   if (pl.pack == 4) {
-    if constexpr (D < 256) attention_rows<BF, D, NG, 4, 1><<<grid, block, 0, s>>>(a);
+    if constexpr (D < 256) attention_rows<BF, D, NG, 4><<<grid, block, 0, s>>>(a);
   } else if (pl.pack == 2) {
-    attention_rows<BF, D, NG, 2, 1><<<grid, block, 0, s>>>(a);
-  } else if (pl.col_tiles == 1) {
-    attention_rows<BF, D, NG, 1, 1><<<grid, block, 0, s>>>(a);
+    attention_rows<BF, D, NG, 2><<<grid, block, 0, s>>>(a);
   } else {
-    if constexpr (D < 256 && NG == 1) attention_rows<BF, D, NG, 1, 2><<<grid, block, 0, s>>>(a);
+    attention_rows<BF, D, NG, 1><<<grid, block, 0, s>>>(a);
   }
   return hipGetLastError();
 }
