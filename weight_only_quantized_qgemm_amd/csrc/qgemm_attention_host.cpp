@@ -107,11 +107,15 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
     pl->pack = rows <= 4 && dim < 256 ? 4 : rows <= 8 ? 2 : 1;
     const int row_tile = 16 / pl->pack;
     const int64_t tokens = (int64_t)p->max_pages * p->cache.page_size;
-    const int64_t units = (tokens + 63) / 64 + 1, tiles = (rows + row_tile - 1) / row_tile;
+    const int64_t units = (tokens + 63) / 64 + 8, tiles = (rows + row_tile - 1) / row_tile;
     if ((double)units * tiles * p->cache.kv_heads * p->batch > 2147483647.0)
       return fail(QGEMM_ERR_UNSUPPORTED, "batch * kv_heads * tokens (%d * %d * %lld) is beyond what one launch divides",
                   p->batch, p->cache.kv_heads, (long long)tokens);
-    pl->grid = 2 * kCUs;
+#ifndef QGEMM_ONE_WAVE
+#define QGEMM_ONE_WAVE 1536
+#endif
+    pl->waves = (int64_t)p->batch * p->cache.kv_heads * tiles >= QGEMM_ONE_WAVE ? 1 : 4;
+    pl->grid = 2 * kCUs * 4 / pl->waves;
     pl->tickets_bytes = ((size_t)pl->grid * 4 + 255) / 256 * 256;
     pl->ws_bytes = pl->tickets_bytes + (size_t)2 * pl->grid * row_tile * (dim + 4) * 4;
     return QGEMM_OK;
@@ -176,7 +180,8 @@ qgemm_status_t qgemm_attention_describe(const qgemm_attention_t* p, char* buf, s
   st = make_attention_plan(p, &pl);
   if (st != QGEMM_OK) return st;
   const int n = p->total_q == 0 ? std::snprintf(buf, len, "empty")
-                : pl.kind == ATTN_ROWS ? std::snprintf(buf, len, "rows grid=%u groups=%d pack=%d", pl.grid, pl.groups, pl.pack)
+                : pl.kind == ATTN_ROWS ? std::snprintf(buf, len, "rows grid=%u groups=%d pack=%d waves=%d", pl.grid, pl.groups,
+                                                       pl.pack, pl.waves)
                                        : std::snprintf(buf, len, "tiles grid=%u groups=%d rows=%d splits=%d", pl.grid,
                                                        pl.groups, pl.tile, pl.splits);
   if (n < 0 || (size_t)n >= len)

@@ -19,6 +19,8 @@ namespace qgemm {
 namespace attn {
 namespace {
 
+constexpr int kOver = 8;
+
 template <int D, int NG, int F>
 struct Step {                                       // one step's bytes, in registers
   static constexpr int U = D / 32, SUB = F == 1 ? 2 : F, ST = F == 1 ? 2 : 1;
@@ -42,8 +44,8 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, unsigned (&w)[U]) 
   }
 }
 
-template <bool BF, int D, int NG, int F>
-__global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
+template <bool BF, int D, int NG, int F, int W>
+__global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
   constexpr int U = D / 32, SUB = F == 1 ? 2 : F, ST = F == 1 ? 2 : 1, T = 16 * SUB;
   constexpr int RT = 16 / F;                        // rows per row tile
   constexpr int TILES = D / 16, TG = TILES / NG;    // output tiles, and those of one group
@@ -51,8 +53,8 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
   constexpr int kRowF = D + 4;                      // padded floats of an LDS row
   constexpr int kSlot = RT * (D + 4);               // floats of a partial: rows, then (max, sum) pairs
   typedef Step<D, NG, F> StepT;
-  __shared__ __align__(16) float s_o[4 * 16 * kRowF];
-  __shared__ float s_m[4 * 16], s_l[4 * 16];
+  __shared__ __align__(16) float s_o[W * 16 * kRowF];
+  __shared__ float s_m[W * 16], s_l[W * 16];
   __shared__ int s_last;
 
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
@@ -72,8 +74,10 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
   if (!total) return;
   const int grid = (int)gridDim.x;
   const int piece = total <= grid * a.piece_small ? a.piece_most : total <= grid * a.piece_most ? a.piece_some : 1;
-  auto pieces_of = [&](const Seq& s) { return (units_of(s) + piece - 1) / piece; };
-  if (piece > 1) {
+  // each segment also counts for kOver units, about what its start and its end cost in long work
+  const int over = piece > 1 ? 0 : kOver;
+  auto pieces_of = [&](const Seq& s) { return (units_of(s) + piece - 1) / piece + over; };
+  {
     total = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
       const Seq x = b0 == 0 ? mine_seq : b0 + lane < a.batch ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
@@ -119,16 +123,21 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
     const int seg = (u0 - before) / nu, first = before + seg * nu;   // segment, its first piece
     const int take = min(first + nu - u0, u1 - u0);
     const int rt = seg / a.kv_heads, kvh = seg - rt * a.kv_heads;
-    const int ts = s.lo + 64 * piece * (u0 - first), te = min(s.hi, ts + 64 * piece * take);
+    const int at = max(u0 - first - over, 0), cnt = u0 + take - first - over - at;       // pieces of tokens
+    if (cnt <= 0) {                                 // the run ends before the segment's first token
+      u0 += take;
+      continue;
+    }
+    const int ts = s.lo + 64 * piece * at, te = min(s.hi, ts + 64 * piece * cnt);
 
-    // ---- the wavefront's steps: token ts + T (wave + 4 j)
+    // ---- the wavefront's steps: token ts + T (wave + W j)
     const int steps = te > ts ? (te - ts + T - 1) / T : 0;
-    const int mine = steps > wave ? (steps - wave + 3) / 4 : 0;
+    const int mine = steps > wave ? (steps - wave + W - 1) / W : 0;
     constexpr int PER = 64 / SUB;                   // steps whose pages one register holds
     const uint8_t* blk = nullptr;
     int in = 0;
     auto pages = [&](int j0) {                      // lane x: subtile x % SUB of step j0 + x / SUB
-      int t = ts + T * (wave + 4 * (j0 + lane / SUB)) + 16 * (lane % SUB);
+      int t = ts + T * (wave + W * (j0 + lane / SUB)) + 16 * (lane % SUB);
       t = min(t, (te - 1) & ~15);                   // past the end: the last subtile again (masked)
       const int p = page_of(a, t);
       int pg = a.table[(long long)b * a.max_pages + p];
@@ -235,7 +244,7 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
     for (int i = 0; i < TILES; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     auto compute = [&](int j, StepT& st) {
-      const int t0 = ts + T * (wave + 4 * j);
+      const int t0 = ts + T * (wave + W * j);
       // S^T, then scores in bits less the row's running maximum
       float u[ST][4];
 #pragma unroll
@@ -376,9 +385,11 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
     }
 
     // ---- join: the wavefront's sums over its lanes, the columns and wavefronts through LDS
-    const bool whole = take == nu;
-    float* slot = a.partials + (size_t)(2 * wg + (first < u0 ? 0 : 1)) * kSlot;
-    const __amdgpu_buffer_rsrc_t mydst = buffer_of(slot, kSlot * 4);
+    const bool whole = cnt == nu - over;
+    // byte offset of a workgroup's partial: 0 for the head of its run, 1 for its tail
+    const __amdgpu_buffer_rsrc_t parts = buffer_of(a.partials, 2 * grid * kSlot * 4);
+    auto slot_of = [&](int w, int tail) { return (2 * w + tail) * kSlot * 4; };
+    const int mydst = slot_of(wg, at ? 0 : 1);
     auto write_out = [&](int row, int d, f32x4 v, float sum) {
       const int gi = rt * RT + row;
       if (gi >= rows) return;
@@ -412,17 +423,17 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
       *reinterpret_cast<f32x4*>(&s_o[(wave * 16 + m) * kRowF + 16 * i + 4 * g]) = v;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < RT * (D / 4); e += 256) {
+    for (int e = threadIdx.x; e < RT * (D / 4); e += 64 * W) {
       const int row = e / (D / 4), d = e % (D / 4) * 4;
       float top = kStart;
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+      for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int f = 0; f < F; ++f) top = __builtin_fmaxf(top, s_m[w * 16 + f * RT + row]);
       float sum = 0.f;
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+      for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int f = 0; f < F; ++f) {
           const int c = w * 16 + f * RT + row;
@@ -433,12 +444,12 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
       if (whole) {
         write_out(row, d, v, sum);
       } else {
-        store4(mydst, (row * D + d) * 4, v);
-        if (d == 0) store4(mydst, (RT * D + 4 * row) * 4, f32x4{top, sum, 0.f, 0.f});
+        store4(parts, mydst + (row * D + d) * 4, v);
+        if (d == 0) store4(parts, mydst + (RT * D + 4 * row) * 4, f32x4{top, sum, 0.f, 0.f});
       }
     }
     if (!whole) {
-      const int w0 = owner(first), w1 = owner(first + nu - 1);
+      const int w0 = owner(first + over), w1 = owner(first + nu - 1);
       __builtin_amdgcn_s_waitcnt(0);                // this thread's partial stores are complete
       __syncthreads();
       if (threadIdx.x == 0)
@@ -446,23 +457,50 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
                  (unsigned)(w1 - w0);
       __syncthreads();
       if (s_last) {
-        for (int e = threadIdx.x; e < RT * (D / 4); e += 256) {
+        constexpr int kItems = RT * (D / 4), kTeams = kItems < 64 * W ? 64 * W / kItems : 1;
+        const int team = threadIdx.x / kItems;      // teams take every kTeams-th piece
+        for (int e = threadIdx.x % kItems; e < kItems; e += 64 * W) {
           const int row = e / (D / 4), d = e % (D / 4) * 4;
           float top = kStart, sum = 0.f;
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
-          for (int w = w0; w <= w1; ++w) {
-            // a segment's first piece is the tail of its workgroup's run, the others are heads of theirs
-            float* from = a.partials + (size_t)(2 * w + (w == w0 ? 1 : 0)) * kSlot;
-            const __amdgpu_buffer_rsrc_t src = buffer_of(from, kSlot * 4);
-            const f32x4 ml = load4(src, (RT * D + 4 * row) * 4);
-            const f32x4 x = load4(src, (row * D + d) * 4);
-            const float nm = __builtin_fmaxf(top, ml[0]);
-            const float old = exp2_fast(top - nm), sc = exp2_fast(ml[0] - nm);
+          auto add = [&](f32x4 x, float xm, float xs) {
+            const float nm = __builtin_fmaxf(top, xm);
+            const float old = exp2_fast(top - nm), sc = exp2_fast(xm - nm);
             top = nm;
-            sum = sum * old + ml[1] * sc;
+            sum = sum * old + xs * sc;
             v = v * old + x * sc;
+          };
+          for (int p0 = w0 + team; p0 <= w1; p0 += 8 * kTeams) {     // eight pieces' loads in flight
+            f32x4 ml[8], x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int w = min(p0 + k * kTeams, w1);
+              // a segment's first piece is the tail of its workgroup's run, the others are heads of theirs
+              const int from = slot_of(w, w == w0);
+              ml[k] = load4(parts, from + (RT * D + 4 * row) * 4);
+              x[k] = load4(parts, from + (row * D + d) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (p0 + k * kTeams <= w1) add(x[k], ml[k][0], ml[k][1]);
           }
-          write_out(row, d, v, sum);
+          if constexpr (kTeams > 1) {
+            __syncthreads();
+            float* mine_o = s_o + 6 * threadIdx.x;
+            mine_o[0] = top;
+            mine_o[1] = sum;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mine_o[2 + r] = v[r];
+            __syncthreads();
+            if (team == 0) {
+#pragma unroll
+              for (int t = 1; t < kTeams; ++t) {
+                const float* x = s_o + 6 * (threadIdx.x + t * kItems);
+                add(f32x4{x[2], x[3], x[4], x[5]}, x[0], x[1]);
+              }
+            }
+          }
+          if (team == 0) write_out(row, d, v, sum);
         }
         if (threadIdx.x == 0) __hip_atomic_store(a.tickets + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
@@ -472,17 +510,21 @@ __global__ __launch_bounds__(256, 2) void attention_rows(AttnArgs a) {
   }
 }
 
-template <bool BF, int D, int NG>
-hipError_t launch_groups(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
-  const dim3 grid(pl.grid), block(256);
+template <bool BF, int D, int NG, int W>
+hipError_t launch_waves(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
+  const dim3 grid(pl.grid), block(64 * W);
   if (pl.pack == 4) {
-    if constexpr (D < 256) attention_rows<BF, D, NG, 4><<<grid, block, 0, s>>>(a);
+    if constexpr (D < 256) attention_rows<BF, D, NG, 4, W><<<grid, block, 0, s>>>(a);
   } else if (pl.pack == 2) {
-    attention_rows<BF, D, NG, 2><<<grid, block, 0, s>>>(a);
+    attention_rows<BF, D, NG, 2, W><<<grid, block, 0, s>>>(a);
   } else {
-    attention_rows<BF, D, NG, 1><<<grid, block, 0, s>>>(a);
+    attention_rows<BF, D, NG, 1, W><<<grid, block, 0, s>>>(a);
   }
   return hipGetLastError();
+}
+template <bool BF, int D, int NG>
+hipError_t launch_groups(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
+  return pl.waves == 1 ? launch_waves<BF, D, NG, 1>(pl, a, s) : launch_waves<BF, D, NG, 4>(pl, a, s);
 }
 
 }  // namespace
