@@ -78,9 +78,8 @@ extern "C" qgemm_status_t qgemm_attention(const qgemm_attention_t* p, const void
   a.window = p->window;
   a.scale = p->scale * 1.4426950408889634f;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  a.piece_small = kPieces.small;
-  a.piece_some = kPieces.some;
-  a.piece_most = kPieces.most;
+  a.piece_share = kPieces.share;
+  a.piece_least = kPieces.least;
   a.splits = pl.splits;
   if (pl.ws_bytes) {
     a.tickets = static_cast<unsigned*>(workspace);

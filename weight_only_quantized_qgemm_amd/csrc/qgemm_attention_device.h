@@ -42,9 +42,9 @@ struct AttnArgs {
   int codes, params, block;        // bytes of one side's codes, of its parameters, of a block
   unsigned page_mul, page_shift;   // t / page = (t * page_mul) >> (32 + page_shift) for t < 2^30
   int max_q, causal, window;
-  // rows kernel, units of 64 tokens per piece: piece_most while a workgroup's share is at most piece_small
-  // units, piece_some while it is at most piece_most, else 1
-  int piece_small, piece_some, piece_most;
+  // rows kernel: while a workgroup's even share is at most piece_share units of 64 tokens, pieces are of
+  // twice that share and at least of piece_least units
+  int piece_share, piece_least;
   int splits;                      // tiles kernel: workgroups per row tile
   float scale;                     // the caller's scale * log2(e)
   unsigned* tickets;

@@ -36,11 +36,11 @@ constexpr TileShape tile_shape(int dim, int groups) {
 }
 constexpr int tile_rows(TileShape t) { return 16 * t.cols * t.waves; }
 
-// Rows kernel: units of 64 tokens per piece (see AttnArgs).
+// Rows kernel: how short work is cut (see AttnArgs).
 #ifndef QGEMM_PIECES
-#define QGEMM_PIECES 2, 8, 16
+#define QGEMM_PIECES 12, 4
 #endif
-struct Pieces { int small, some, most; };
+struct Pieces { int share, least; };
 constexpr Pieces kPieces{QGEMM_PIECES};
 
 // Launch plan of qgemm_attention, a pure function of the descriptor.

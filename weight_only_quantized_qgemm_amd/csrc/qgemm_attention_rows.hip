@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
   }
   if (!total) return;
   const int grid = (int)gridDim.x;
-  const int piece = total <= grid * a.piece_small ? a.piece_most : total <= grid * a.piece_most ? a.piece_some : 1;
+  const int piece = total <= grid * a.piece_share ? max(a.piece_least, (2 * total + grid - 1) / grid) : 1;
   // each segment also counts for kOver units, about what its start and its end cost in long work
   const int over = piece > 1 ? 0 : kOver;
   auto pieces_of = [&](const Seq& s) { return (units_of(s) + piece - 1) / piece + over; };
