@@ -13,6 +13,7 @@ static_assert(sizeof(qgemm_cache_t) == 32, "qgemm_cache_t layout is part of the 
 static_assert(sizeof(qgemm_attention_t) == 80, "qgemm_attention_t layout is part of the ABI");
 
 static const int kCUs = 256;
+static const int64_t kMaxSplits = 32;      // workgroups per row tile
 static const int64_t kMaxTokens = int64_t(1) << 24;
 
 static qgemm_status_t check_dtype_dim(const char* what, int dtype, int head_dim) {
@@ -127,18 +128,32 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   int64_t entries = p->batch + ratio * p->total_q / pl->tile;
   if (entries > per_seq * p->batch) entries = per_seq * p->batch;
   const int64_t tiles = entries * p->cache.kv_heads;
-  // A row tile's tokens are split over workgroups while there are fewer of them than the chip holds,
-  // but not below 4 steps each.
+  // A row tile's tokens are split over workgroups (one is resident per compute unit) where a model of the
+  // launch, in steps of 64 tokens, says that it is shorter: the longest chain, or all workgroups' steps
+  // and overheads spread over the chip plus a quarter of a chain for the uneven end.  A workgroup costs
+  // about 4 steps, a part to join 8 more and 4 for each further level.  (6 chunks of a window of 4096 with
+  // 64 heads: 679 us in one part, 776 in four; 100 queries after 16000 tokens: 145 us in 32 parts joined
+  // by one workgroup, 77 in 16 joined in pairs.)
   const int64_t steps = ((int64_t)p->max_pages * p->cache.page_size + 63) / 64;
   int64_t splits = 1;
-  while (tiles * splits * 2 <= 2 * kCUs && splits * 2 * 4 <= steps) splits *= 2;
+  double best = 0.0;
+  for (int64_t s = 1, levels = 0; s <= kMaxSplits && (s == 1 || s * 4 <= steps); ++s) {
+    while ((int64_t(1) << levels) < s) ++levels;
+    const double chain = (double)((steps + s - 1) / s), over = s > 1 ? 12.0 : 4.0;
+    const double spread = (double)tiles * s * (chain + over) / kCUs + chain / 4;
+    const double cost = (chain + over > spread ? chain + over : spread) + 4.0 * levels;
+    if (s == 1 || cost < best) {
+      splits = s;
+      best = cost;
+    }
+  }
   if (tiles * splits > 0x7fffffffLL)
     return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows",
                 (long long)(tiles * splits));
   pl->splits = (int)splits;
   pl->grid = (unsigned)(tiles * splits);
   if (splits > 1) {
-    pl->tickets_bytes = ((size_t)tiles * 4 + 255) / 256 * 256;
+    pl->tickets_bytes = ((size_t)tiles * splits * 4 + 255) / 256 * 256;
     pl->ws_bytes = pl->tickets_bytes + (size_t)tiles * splits * ((size_t)pl->tile * dim + (size_t)shape.cols * shape.waves * 256) * 4;
   }
   return QGEMM_OK;

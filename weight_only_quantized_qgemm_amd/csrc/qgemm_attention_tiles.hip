@@ -499,41 +499,47 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[nc][i][r] = __builtin_fmaf(o[nc][i][r], back, zs[nc][i / TG]);
   }
+#pragma unroll
+  for (int nc = 0; nc < NC; ++nc) mx[nc] = fresh[nc] ? kStart : mx[nc];
+  // Splits are joined in pairs, pairs of pairs and so on: at each node the second of two to arrive, its
+  // part still in registers, adds the first's from the workspace and goes on; the first leaves.  Nobody
+  // waits, and a sum of two has the same bits either way round, so the result does not depend on the order.
   if (active > 1) {
     const int tile = entry * a.kv_heads + kvh;
+    unsigned* node = a.tickets + (size_t)tile * a.splits;            // level k's nodes are side by side
     float* base = a.partials + (size_t)tile * a.splits * kSlot;
-    {
-      const __amdgpu_buffer_rsrc_t dst = buffer_of(base + (size_t)split * kSlot, kSlot * 4);
+    const __amdgpu_buffer_rsrc_t parts = buffer_of(base, a.splits * kSlot * 4);
+    for (int i = split, size = 1, left = a.splits; size < active; size *= 2, i >>= 1) {
+      left = (left + 1) / 2;                        // nodes of this level
+      if ((i ^ 1) * size < active) {                // the node has two children
+        const int mydst = i * size * kSlot * 4;
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
+        for (int nc = 0; nc < NC; ++nc) {
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) store4(dst, ((nc * TILES + i) * NT + threadIdx.x) * 16, o[nc][i]);
-        store4(dst, (BM * D + (nc * NT + threadIdx.x) * 4) * 4, f32x4{fresh[nc] ? kStart : mx[nc], l[nc], 0.f, 0.f});
+          for (int x = 0; x < TILES; ++x) store4(parts, mydst + ((nc * TILES + x) * NT + threadIdx.x) * 16, o[nc][x]);
+          store4(parts, mydst + (BM * D + (nc * NT + threadIdx.x) * 4) * 4, f32x4{mx[nc], l[nc], 0.f, 0.f});
+        }
+        __builtin_amdgcn_s_waitcnt(0);              // this thread's stores are complete
+        __syncthreads();
+        if (threadIdx.x == 0)
+          s_last = __hip_atomic_fetch_add(node + (i >> 1), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 1u;
+        __syncthreads();
+        if (!s_last) return;
+        if (threadIdx.x == 0) __hip_atomic_store(node + (i >> 1), 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int from = (i ^ 1) * size * kSlot * 4;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          const f32x4 ml = load4(parts, from + (BM * D + (nc * NT + threadIdx.x) * 4) * 4);
+          const float nm = __builtin_fmaxf(mx[nc], ml[0]);
+          const float mine = exp2_fast(mx[nc] - nm), other = exp2_fast(ml[0] - nm);
+          mx[nc] = nm;
+          l[nc] = l[nc] * mine + ml[1] * other;
+#pragma unroll
+          for (int x = 0; x < TILES; ++x)
+            o[nc][x] = o[nc][x] * mine + load4(parts, from + ((nc * TILES + x) * NT + threadIdx.x) * 16) * other;
+        }
       }
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (threadIdx.x == 0)
-      s_last = __hip_atomic_fetch_add(a.tickets + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(active - 1);
-    __syncthreads();
-    if (!s_last) return;
-    if (threadIdx.x == 0) __hip_atomic_store(a.tickets + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      float top = kStart, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int x = 0; x < active; ++x) {
-        const __amdgpu_buffer_rsrc_t src = buffer_of(base + (size_t)x * kSlot, kSlot * 4);
-        const f32x4 ml = load4(src, (BM * D + (nc * NT + threadIdx.x) * 4) * 4);
-        const float nm = __builtin_fmaxf(top, ml[0]);
-        const float old = exp2_fast(top - nm), sc = exp2_fast(ml[0] - nm);
-        top = nm;
-        sum = sum * old + ml[1] * sc;
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) o[nc][i] = o[nc][i] * old + load4(src, ((nc * TILES + i) * NT + threadIdx.x) * 16) * sc;
-      }
-      l[nc] = sum;
+      node += left;
     }
   }
 #pragma unroll
