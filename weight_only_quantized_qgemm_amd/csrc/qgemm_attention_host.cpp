@@ -13,7 +13,7 @@ static_assert(sizeof(qgemm_cache_t) == 32, "qgemm_cache_t layout is part of the 
 static_assert(sizeof(qgemm_attention_t) == 80, "qgemm_attention_t layout is part of the ABI");
 
 static const int kCUs = 256;
-static const int64_t kMaxSplits = 32;      // workgroups per row tile
+static const int kMaxSplits = 32;           // workgroups per row tile
 static const int64_t kMaxTokens = int64_t(1) << 24;
 
 static qgemm_status_t check_dtype_dim(const char* what, int dtype, int head_dim) {
@@ -99,62 +99,75 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   std::memset(pl, 0, sizeof(*pl));
   if (p->total_q == 0) return QGEMM_OK;
   pl->groups = p->cache.head_dim / p->cache.group_size;
-  const int64_t rows = (int64_t)(p->q_heads / p->cache.kv_heads) * p->max_q_len;
-  const int dim = p->cache.head_dim;
-  pl->rows = (int)(rows < 0x7fffffff ? rows : 0x7fffffff);
-  pl->kind = p->kernel_hint == QGEMM_ATTENTION_TILES || (p->kernel_hint == QGEMM_ATTENTION_AUTO && rows > 64) ? ATTN_TILES
-                                                                                                         : ATTN_ROWS;
-  if (pl->kind == ATTN_ROWS) {
-    pl->pack = rows <= 4 && dim < 256 ? 4 : rows <= 8 ? 2 : 1;
-    const int row_tile = 16 / pl->pack;
-    const int64_t tokens = (int64_t)p->max_pages * p->cache.page_size;
-    const int64_t units = (tokens + 63) / 64 + 8, tiles = (rows + row_tile - 1) / row_tile;
-    if ((double)units * tiles * p->cache.kv_heads * p->batch > 2147483647.0)
-      return fail(QGEMM_ERR_UNSUPPORTED, "batch * kv_heads * tokens (%d * %d * %lld) is beyond what one launch divides",
-                  p->batch, p->cache.kv_heads, (long long)tokens);
-#ifndef QGEMM_ONE_WAVE
-#define QGEMM_ONE_WAVE 1536
-#endif
-    pl->waves = (int64_t)p->batch * p->cache.kv_heads * tiles >= QGEMM_ONE_WAVE ? 1 : 4;
-    pl->grid = 2 * kCUs * 4 / pl->waves;
+  const int dim = p->cache.head_dim, ng = pl->groups;
+  const int64_t ratio = p->q_heads / p->cache.kv_heads, rows = ratio * p->max_q_len;
+  const int64_t tokens = (int64_t)p->max_pages * p->cache.page_size, steps = (tokens + 63) / 64;
+  // tiles of `r` query rows over all sequences, each of which may end in a partly filled one
+  auto tiles_of = [&](int64_t r) {
+    const int64_t by_total = p->batch + ratio * p->total_q / r, by_longest = (rows + r - 1) / r * p->batch;
+    return (by_total < by_longest ? by_total : by_longest) * p->cache.kv_heads;
+  };
+
+  // ---- rows kernel.  Rows per column group: as few as hold a sequence's rows of a kv head, so that more
+  // subtiles lie side by side; 16 rows of D 256 in four groups do not fit the registers.
+  pl->pack = rows <= 4 && dim < 256 ? 4 : rows <= 8 || (dim == 256 && ng == 4) ? 2 : 1;
+  const int row_tile = 16 / pl->pack;
+  const int64_t row_tiles = tiles_of(row_tile);
+  // ---- tiles kernel.  A row tile's tokens are split over workgroups (one is resident per compute unit)
+  // where a model of the launch, in steps of 64 tokens, says that it is shorter: the longest chain, or all
+  // workgroups' steps and overheads spread over the chip plus a quarter of a chain for the uneven end.
+  // (6 chunks in a window of 4096, 64 heads: 679 us in one part, 776 in four; 100 queries after 16000
+  // tokens: 145 us in 32 parts joined by one workgroup, 77 in 16 joined in pairs.)
+  const TileShape shape = tile_shape(dim, ng);
+  pl->tile = tile_rows(shape);
+  const int64_t tiles = tiles_of(pl->tile);
+  double best = 0.0;
+  pl->splits = 1;
+  for (int s = 1, levels = 0; s <= kMaxSplits && (s == 1 || (int64_t)s * 4 <= steps); ++s) {
+    while ((1 << levels) < s) ++levels;
+    const double chain = (double)((steps + s - 1) / s), join = 1.2 * levels;
+    const double latency = chain + 4.0 + (s > 1 ? 2.0 : 0.0) + join;
+    const double spread = (double)tiles * s * (chain + 4.0 + (s > 1 ? 4.5 : 0.0)) / kCUs + chain / 4 + join;
+    const double cost = latency > spread ? latency : spread;
+    if (s == 1 || cost < best) {
+      pl->splits = s;
+      best = cost;
+    }
+  }
+
+  // ---- which: microseconds that a compute unit takes for 64 tokens of 16 rows (rows kernel; of 8 rows for
+  // D 256 in four groups) and of a row tile (tiles kernel), for D 64, 128, 256 and NG 1, 2, 4, measured at
+  // 32 rows and 8008 tokens x 8, and at a prompt of 4096.
+  static const double kRowUnit[3][3] = {{0.31, 0.38, 0.38}, {0.40, 0.50, 0.77}, {1.05, 1.05, 0.90}};
+  static const double kTileStep[3][3] = {{2.45, 3.0, 3.0}, {3.1, 4.5, 3.1}, {3.7, 4.8, 8.3}};
+  const int di = dim == 64 ? 0 : dim == 128 ? 1 : 2, gi = ng == 1 ? 0 : ng == 2 ? 1 : 2;
+  const double rows_us = 10.0 + kRowUnit[di][gi] * (double)row_tiles * (double)steps / kCUs;
+  const double tiles_us = 8.0 + kTileStep[di][gi] * best;
+  const bool use_rows = p->kernel_hint == QGEMM_ATTENTION_ROWS ||
+                        (p->kernel_hint == QGEMM_ATTENTION_AUTO && (rows <= row_tile || rows_us <= tiles_us));
+  if (use_rows) {
+    pl->kind = ATTN_ROWS;
+    if (((double)steps + 8) * (double)row_tiles > 2147483647.0)
+      return fail(QGEMM_ERR_UNSUPPORTED, "%lld row tiles of up to %lld tokens are beyond what one launch divides",
+                  (long long)row_tiles, (long long)tokens);
+    // Many segments (several per resident workgroup of four wavefronts) take a wavefront each: the starts
+    // and ends of short ones overlap (500 requests of 200 tokens 64 -> 38 us, 200 of 500 42 -> 30; from
+    // 1024 segments of 1500 tokens on four are as good, and better for few long ones).
+    pl->waves = row_tiles >= 1536 ? 1 : 4;
+    pl->grid = (unsigned)(2 * kCUs * 4 / pl->waves);
     pl->tickets_bytes = ((size_t)pl->grid * 4 + 255) / 256 * 256;
     pl->ws_bytes = pl->tickets_bytes + (size_t)2 * pl->grid * row_tile * (dim + 4) * 4;
     return QGEMM_OK;
   }
-  const TileShape shape = tile_shape(dim, pl->groups);
-  pl->tile = tile_rows(shape);
-  // row tiles: every sequence may end in a partly filled one
-  const int64_t ratio = p->q_heads / p->cache.kv_heads, per_seq = (rows + pl->tile - 1) / pl->tile;
-  int64_t entries = p->batch + ratio * p->total_q / pl->tile;
-  if (entries > per_seq * p->batch) entries = per_seq * p->batch;
-  const int64_t tiles = entries * p->cache.kv_heads;
-  // A row tile's tokens are split over workgroups (one is resident per compute unit) where a model of the
-  // launch, in steps of 64 tokens, says that it is shorter: the longest chain, or all workgroups' steps
-  // and overheads spread over the chip plus a quarter of a chain for the uneven end.  A workgroup costs
-  // about 4 steps, a part to join 8 more and 4 for each further level.  (6 chunks of a window of 4096 with
-  // 64 heads: 679 us in one part, 776 in four; 100 queries after 16000 tokens: 145 us in 32 parts joined
-  // by one workgroup, 77 in 16 joined in pairs.)
-  const int64_t steps = ((int64_t)p->max_pages * p->cache.page_size + 63) / 64;
-  int64_t splits = 1;
-  double best = 0.0;
-  for (int64_t s = 1, levels = 0; s <= kMaxSplits && (s == 1 || s * 4 <= steps); ++s) {
-    while ((int64_t(1) << levels) < s) ++levels;
-    const double chain = (double)((steps + s - 1) / s), over = s > 1 ? 12.0 : 4.0;
-    const double spread = (double)tiles * s * (chain + over) / kCUs + chain / 4;
-    const double cost = (chain + over > spread ? chain + over : spread) + 4.0 * levels;
-    if (s == 1 || cost < best) {
-      splits = s;
-      best = cost;
-    }
-  }
-  if (tiles * splits > 0x7fffffffLL)
+  pl->kind = ATTN_TILES;
+  if (tiles * pl->splits > 0x7fffffffLL)
     return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows",
-                (long long)(tiles * splits));
-  pl->splits = (int)splits;
-  pl->grid = (unsigned)(tiles * splits);
-  if (splits > 1) {
-    pl->tickets_bytes = ((size_t)tiles * splits * 4 + 255) / 256 * 256;
-    pl->ws_bytes = pl->tickets_bytes + (size_t)tiles * splits * ((size_t)pl->tile * dim + (size_t)shape.cols * shape.waves * 256) * 4;
+                (long long)(tiles * pl->splits));
+  pl->grid = (unsigned)(tiles * pl->splits);
+  if (pl->splits > 1) {
+    pl->tickets_bytes = ((size_t)tiles * pl->splits * 4 + 255) / 256 * 256;
+    pl->ws_bytes = pl->tickets_bytes +
+                   (size_t)tiles * pl->splits * ((size_t)pl->tile * dim + (size_t)shape.cols * shape.waves * 256) * 4;
   }
   return QGEMM_OK;
 }

@@ -47,7 +47,6 @@ constexpr Pieces kPieces{QGEMM_PIECES};
 struct AttnPlan {
   AttnKind kind;
   int groups;          // NG
-  int rows;            // query rows per kv head and sequence, at most: ratio * max_q_len
   int pack;            // rows kernel: subtiles side by side in the 16 columns (F: 1, 2, 4)
   int waves;           // rows kernel: wavefronts per workgroup (1 or 4)
   int tile, splits;    // tiles kernel: query rows per workgroup, workgroups per row tile

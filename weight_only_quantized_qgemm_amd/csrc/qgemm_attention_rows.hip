@@ -19,11 +19,18 @@ namespace qgemm {
 namespace attn {
 namespace {
 
+// What the start and the end of a segment cost, in units of 64 tokens: counted with its tokens when long
+// work is divided (64 requests of 0..8191 tokens: 90 us with 0, 70 with 4, 64 with 8, 65 with 12).
 constexpr int kOver = 8;
 
 template <int D, int NG, int F>
 struct Step {                                       // one step's bytes, in registers
   static constexpr int U = D / 32, SUB = F == 1 ? 2 : F, ST = F == 1 ? 2 : 1;
+  // Two steps' registers are held while they fit beside the rest (256 in all, two wavefronts per SIMD);
+  // past that the next step is loaded piecewise into the registers that the current one is done with
+  // (32 requests of 4000..8190 tokens, D 128: 16 rows and NG 4 116 -> 49 us, 1 row and NG 4 135 -> 110;
+  // within the limit two steps are better: 16 rows and NG 2 37.6 -> 35.9, 8 rows and NG 1 44.6 -> 42.2).
+  static constexpr bool kTwo = 2 * SUB * U + 8 * ST * NG <= (D == 256 ? 0 : F == 4 ? 40 : 48);
   unsigned k[SUB][U], v[SUB][U];
   u32x4 kp[ST][NG], vp[ST][NG];
 };
@@ -145,33 +152,53 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       in = t - p * a.page;
       blk = a.data + ((long long)pg * a.kv_heads + kvh) * a.block;
     };
-    auto fetch = [&](int j, StepT& st) {
+    auto block_at = [&](int x, int& at) {           // subtile x of those at hand (uniform)
+      const unsigned long long bits = reinterpret_cast<unsigned long long>(blk);
+      const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)bits, x);
+      const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(bits >> 32), x);
+      at = __builtin_amdgcn_readlane(in, x);
+      return reinterpret_cast<const uint8_t*>((unsigned long long)hi << 32 | lo);
+    };
+    auto params_at = [&](int x) {                   // the lane's tokens' parameters in subtile x (by lane)
+      const unsigned long long bits = reinterpret_cast<unsigned long long>(blk);
+      const unsigned lo = __shfl((int)(unsigned)bits, x), hi = __shfl((int)(unsigned)(bits >> 32), x);
+      return reinterpret_cast<const uint8_t*>((unsigned long long)hi << 32 | lo) + 2 * a.codes + 4 * (__shfl(in, x) + 4 * g);
+    };
+    auto fetch_k = [&](int j, StepT& st) {
       const int x0 = j % PER * SUB;
 #pragma unroll
       for (int f = 0; f < SUB; ++f) {
-        const unsigned long long bits = reinterpret_cast<unsigned long long>(blk);
-        const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)bits, x0 + f);
-        const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(bits >> 32), x0 + f);
-        const uint8_t* p = reinterpret_cast<const uint8_t*>((unsigned long long)hi << 32 | lo);
-        const int at = __builtin_amdgcn_readlane(in, x0 + f);
+        int at;
+        const uint8_t* p = block_at(x0 + f, at);
         load_dwords<U>(p + (at * (D / 2) + (m * (D / 2) + 4 * U * g)), st.k[f]);
+      }
+#pragma unroll
+      for (int x = 0; x < ST; ++x) {
+        const uint8_t* p = params_at(x0 + (F == 1 ? x : fcol));
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) st.kp[x][gr] = *reinterpret_cast<const u32x4*>(p + 4 * gr * a.page);
+      }
+    };
+    auto fetch_v = [&](int j, StepT& st) {
+      const int x0 = j % PER * SUB;
+#pragma unroll
+      for (int f = 0; f < SUB; ++f) {
+        int at;
+        const uint8_t* p = block_at(x0 + f, at);
         load_dwords<U>(p + a.codes + (at * (D / 2) + lane * (4 * U)), st.v[f]);
       }
 #pragma unroll
       for (int x = 0; x < ST; ++x) {
-        const int src = x0 + (F == 1 ? x : fcol);
-        const unsigned long long bits = reinterpret_cast<unsigned long long>(blk);
-        const unsigned lo = __shfl((int)(unsigned)bits, src), hi = __shfl((int)(unsigned)(bits >> 32), src);
-        const uint8_t* p = reinterpret_cast<const uint8_t*>((unsigned long long)hi << 32 | lo) + 2 * a.codes +
-                           4 * (__shfl(in, src) + 4 * g);
+        const uint8_t* p = params_at(x0 + (F == 1 ? x : fcol)) + a.params;
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          st.kp[x][gr] = *reinterpret_cast<const u32x4*>(p + 4 * gr * a.page);
-          st.vp[x][gr] = *reinterpret_cast<const u32x4*>(p + a.params + 4 * gr * a.page);
-        }
+        for (int gr = 0; gr < NG; ++gr) st.vp[x][gr] = *reinterpret_cast<const u32x4*>(p + 4 * gr * a.page);
       }
     };
-    StepT sa, sb;
+    auto fetch = [&](int j, StepT& st) {
+      fetch_k(j, st);
+      fetch_v(j, st);
+    };
+    StepT sa;
     if (mine) pages(0);
     // ---- queries: column m holds row rt RT + m % RT, row = query * ratio + head within the group
     const int rows = a.ratio * s.n;
@@ -243,7 +270,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < TILES; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto compute = [&](int j, StepT& st) {
+    auto compute = [&](int j, StepT& st, auto scored) {
       const int t0 = ts + T * (wave + W * j);
       // S^T, then scores in bits less the row's running maximum
       float u[ST][4];
@@ -268,6 +295,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
             u[x][r] = __builtin_fmaf(par_scale<BF>(w) * kq, acc[r], v);
           }
         }
+      scored();                                     // the keys' registers are free
       if (t0 + T > min(all_hi, te) || t0 < all_lo) {
         // a token that the lane's row does not see: weight 0, and its parameters (any bits) are put away
 #pragma unroll
@@ -373,15 +401,30 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
         }
       }
     };
-    for (int j = 0; j < mine; j += 2) {
-      // PER is even, so only the step after an odd one can need new pages
-      if (j + 1 < mine) fetch(j + 1, sb);
-      compute(j, sa);
-      if (j + 2 < mine) {
-        if ((j + 2) % PER == 0) pages(j + 2);
-        fetch(j + 2, sa);
+    if constexpr (StepT::kTwo) {
+      // two steps' registers: the next step is loaded as a whole before this one is worked on
+      StepT sb;
+      for (int j = 0; j < mine; j += 2) {
+        // PER is even, so only the step after an odd one can need new pages
+        if (j + 1 < mine) fetch(j + 1, sb);
+        compute(j, sa, [] {});
+        if (j + 2 < mine) {
+          if ((j + 2) % PER == 0) pages(j + 2);
+          fetch(j + 2, sa);
+        }
+        if (j + 1 < mine) compute(j + 1, sb, [] {});
       }
-      if (j + 1 < mine) compute(j + 1, sb);
+    } else {
+      // one step's: the next keys are loaded once the scores are there, the next values at the end
+      for (int j = 0; j < mine; ++j) {
+        compute(j, sa, [&] {
+          if (j + 1 < mine) {
+            if ((j + 1) % PER == 0) pages(j + 1);
+            fetch_k(j + 1, sa);
+          }
+        });
+        if (j + 1 < mine) fetch_v(j + 1, sa);
+      }
     }
 
     // ---- join: the wavefront's sums over its lanes, the columns and wavefronts through LDS
@@ -518,7 +561,7 @@ hipError_t launch_waves(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
   } else if (pl.pack == 2) {
     attention_rows<BF, D, NG, 2, W><<<grid, block, 0, s>>>(a);
   } else {
-    attention_rows<BF, D, NG, 1, W><<<grid, block, 0, s>>>(a);
+    if constexpr (D < 256 || NG < 4) attention_rows<BF, D, NG, 1, W><<<grid, block, 0, s>>>(a);
   }
   return hipGetLastError();
 }
