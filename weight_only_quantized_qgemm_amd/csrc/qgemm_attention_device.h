@@ -132,21 +132,20 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, int t) {
   return (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift);
 }
 
-// Sum over the wavefront, and the sum up to and including each lane.
+// Sum up to and including each lane, by DPP: within rows of 16 lanes, then across them.
+template <int C, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, C, ROWS, 0xf, false);
+}
 __device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) {
-    const int y = __shfl_up(v, x);
-    if (lane >= x) v += y;
-  }
-  return v;
+  v = dpp_add<0x111, 0xf>(v);                      // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);                      // lane 15 of rows 0 and 2 to the next row
+  return dpp_add<0x143, 0xc>(v);                   // lane 31 to rows 2 and 3
 }
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) v += __shfl_xor(v, x);
-  return __builtin_amdgcn_readfirstlane(v);
-}
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
 
 // Sequence b's geometry from device memory, every value bounded.
 struct Seq {
