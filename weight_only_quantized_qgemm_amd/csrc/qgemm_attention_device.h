@@ -128,6 +128,13 @@ __device__ __forceinline__ unsigned centre(unsigned pair, bool high) {
   return __builtin_bit_cast(unsigned, v - f16x2{off, off});
 }
 
+// The same as the whole numbers c.
+__device__ __forceinline__ f16x2 whole(unsigned pair, bool high) {
+  const f16x2 v = __builtin_bit_cast(f16x2, pair | (high ? 0x54005400u : 0x64006400u));
+  const _Float16 off = high ? (_Float16)64.f : (_Float16)1024.f;
+  return v - f16x2{off, off};
+}
+
 __device__ __forceinline__ int page_of(const AttnArgs& a, int t) {
   return (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift);
 }

@@ -33,10 +33,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   constexpr int SUBS = 2 * kHalves;                 // 16-token subtiles of a step
   constexpr int KB = kStep * D * 2, PB = SUBS * NG * 4 * 16 * 4;   // bytes of K (and of V) operands, of parameters
   constexpr int kSlot = BM * D + NC * NT * 4;       // floats of a partial
+  // bf16: fp16 operands hold the values themselves, a power of two per token apart; fp16: the codes
+  constexpr bool kDeq = BF;
   __shared__ __align__(16) uint8_t s_k[2][KB], s_v[3][KB];
-  __shared__ __align__(16) float s_p[3][PB / 4];    // [subtile][group][K scale, K zero, V scale, V middle][16]
-  __shared__ __align__(16) unsigned s_big[3][4];    // per subtile: the largest finite |V scale|, as its bits
-  __shared__ int s_odd[3];                          // any V parameter that is not finite
+  // [subtile][group][K scale, K zero, V scale, V middle][16]; kDeq: one V scale per token, in group 0, and
+  // in the place of the middle 0, or NaN where the group's parameters are not finite
+  __shared__ __align__(16) float s_p[4][PB / 4];
+  __shared__ __align__(16) unsigned s_w[2][kDeq ? SUBS * NG * 16 : 4];       // kDeq: V scale, zero as fp16
+  __shared__ __align__(16) unsigned s_big[4][4];    // per subtile: the largest finite |V scale|, as its bits
+  __shared__ int s_odd[4];                          // any V parameter that is not finite
   __shared__ float s_top[NW];
   __shared__ int s_last;
 
@@ -47,24 +52,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
   const int split = rest % a.splits;
   int entry = rest / a.splits;
+  auto tiles_in = [&](int b) { return b < a.batch ? (a.ratio * load_seq(a, b).n + BM - 1) / BM : 0; };
   int total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int u = b0 + lane < a.batch ? (a.ratio * load_seq(a, b0 + lane).n + BM - 1) / BM : 0;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) u += __shfl_xor(u, x);
-    total += u;
-  }
-  total = __builtin_amdgcn_readfirstlane(total);
+  for (int b0 = 0; b0 < a.batch; b0 += 64) total += wave_sum(tiles_in(b0 + lane));
   if (entry >= total) return;
   entry = total - 1 - entry;
   int b = 0, before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int u = b0 + lane < a.batch ? (a.ratio * load_seq(a, b0 + lane).n + BM - 1) / BM : 0;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-      const int y = __shfl_up(u, x);
-      if (lane >= x) u += y;
-    }
+    const int u = wave_scan(tiles_in(b0 + lane));
     const unsigned long long past = __ballot(before + u > entry);
     if (past) {
       const int l = __builtin_ctzll(past);
@@ -89,14 +84,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int ts = lo + kStep * per * split, te = min(hi, ts + kStep * per);
   const int steps = te > ts ? (te - ts + kStep - 1) / kStep : 0;
 
-  // ---- filling: each wavefront prepares the K or V operands of 16-token subtiles, wavefront 0 also the K
-  // and wavefront 1 the V parameters
-  constexpr bool kBoth = NW == SUBS;                // as many wavefronts as subtiles: K and V each
-  const int fsub = wave % SUBS;
-  const bool fk = kBoth || wave < SUBS, fv = kBoth || (wave >= SUBS && wave < 2 * SUBS);
-  constexpr int kPar = NW >= 2 * SUBS + 2 ? 2 * SUBS : 0;           // the wavefronts that prepare parameters: K's, V's
-  const bool fp = wave == kPar || wave == kPar + 1, fpv = wave == kPar + 1;
-  unsigned rk[U], rv[U], rp[NG];
+  // ---- filling: wavefront w prepares part w / SUBS of the K and V operands of subtile w % SUBS; two
+  // wavefronts also the parameters, a token a lane, a step further ahead (the V operands need them)
+  constexpr int PARTS = NW / SUBS, KP = U / PARTS, TP = TILES / PARTS;
+  const int fsub = wave % SUBS, part = wave / SUBS;
+  const bool fp = wave < 2, fpv = wave == 1;        // K's, V's
+  unsigned rk[KP], rv[U == 2 ? 2 : 4], rp[NG];
   bool rp_on = false;
   // Page ids are loaded one step before their blocks' addresses are needed: the subtile's (uniform), and
   // for the parameters the lane's token's.
@@ -106,95 +99,156 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     return __builtin_amdgcn_readfirstlane(min(ts + kStep * step + 16 * fsub, (te - 1) & ~15));
   };
   auto tok_at = [&](int step) { return min(ts + kStep * step + lane % kStep, te - 1); };
-  auto fetch_pages = [&](int step) {
-    pg_sub = row_of[page_of(a, sub_at(step))];
-    if (fp) pg_tok = row_of[page_of(a, tok_at(step))];
-  };
   auto block_of = [&](int t, int pg, int& in) {
     in = t - page_of(a, t) * a.page;
     if ((unsigned)pg >= (unsigned)a.num_pages) pg = 0;
     return a.data + ((long long)pg * a.kv_heads + kvh) * a.block;
   };
-  auto load_dwords = [&](const uint8_t* p, unsigned(&w)[U]) {
-    if constexpr (U == 2) {
+  auto load_n = [&](const uint8_t* p, unsigned* w, auto n_c) {
+    constexpr int n = decltype(n_c)::value;
+    if constexpr (n == 1) {
+      w[0] = *reinterpret_cast<const unsigned*>(p);
+    } else if constexpr (n == 2) {
       const u32x2 x = *reinterpret_cast<const u32x2*>(p);
       w[0] = x[0];
       w[1] = x[1];
     } else {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
-      for (int j = 0; j < U / 4; ++j) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(p + 16 * j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * j + i] = x[i];
-      }
+      for (int i = 0; i < 4; ++i) w[i] = x[i];
     }
   };
+  auto fetch_pages = [&](int step) { pg_sub = row_of[page_of(a, sub_at(step))]; };
   auto fetch = [&](int step) {
     int in;
     const uint8_t* blk = block_of(sub_at(step), pg_sub, in);
-    if (fk) load_dwords(blk + (in * (D / 2) + (m * (D / 2) + 4 * U * g)), rk);
-    if (fv) load_dwords(blk + a.codes + (in * (D / 2) + lane * (4 * U)), rv);
-    if (fp) {                                       // a token a lane
-      rp_on = ts + kStep * step + lane % kStep < te;
-      const uint8_t* pb = block_of(tok_at(step), pg_tok, in) + 2 * a.codes + (fpv ? a.params : 0);
+    load_n(blk + (in * (D / 2) + (m * (D / 2) + 4 * U * g + 4 * KP * part)), rk, std::integral_constant<int, KP>{});
+    const uint8_t* vb = blk + a.codes + (in * (D / 2) + lane * (4 * U));
+    if constexpr (U <= 4) {
+      load_n(vb, rv, std::integral_constant<int, U>{});
+    } else {                                        // of each token's two dwords the one that holds the part
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) rp[gr] = *reinterpret_cast<const unsigned*>(pb + 4 * (gr * a.page + in));
+      for (int t = 0; t < 4; ++t) rv[t] = *reinterpret_cast<const unsigned*>(vb + 8 * t + 4 * (TP == 4 ? part >> 1 : part));
     }
     fetch_pages(step + 1);
+  };
+  auto fetch_par_pages = [&](int step) {
+    if (fp) pg_tok = row_of[page_of(a, tok_at(step))];
+  };
+  auto fetch_par = [&](int step) {
+    if (!fp) return;
+    int in;
+    rp_on = ts + kStep * step + lane % kStep < te;
+    const uint8_t* pb = block_of(tok_at(step), pg_tok, in) + 2 * a.codes + (fpv ? a.params : 0);
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) rp[gr] = *reinterpret_cast<const unsigned*>(pb + 4 * (gr * a.page + in));
+    fetch_par_pages(step + 1);
   };
   float kq = 0.f;                                   // set below, before the first store
   auto store = [&](int step) {
     const int kb = step & 1, vb = step % 3;
-    if (fk) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) *reinterpret_cast<u32x4*>(&s_k[kb][((fsub * U + i) * 64 + lane) * 16]) = codes8(rk[i]);
-    }
-    if (fv) {
+    for (int i = 0; i < KP; ++i)
+      *reinterpret_cast<u32x4*>(&s_k[kb][((fsub * U + part * KP + i) * 64 + lane) * 16]) = codes8(rk[i]);
+    // pairs of tokens (0, 1) and (2, 3): 16 bits each of the part's nibbles
+    constexpr int HW = TP == 8 ? 2 : 1;
+    unsigned x[HW], y[HW];
+    if constexpr (U == 2) {
+      x[0] = rv[0] >> (8 * part);
+      y[0] = rv[1] >> (8 * part);
+    } else {
 #pragma unroll
-      for (int i = 0; i < TILES; ++i) {
-        unsigned x, y;
-        v_pairs<U>(rv, i, x, y);
-        *reinterpret_cast<u32x2*>(&s_v[vb][(((fsub >> 1) * TILES + i) * 64 + lane) * 16 + (fsub & 1) * 8]) =
-            u32x2{centre(x, i & 1), centre(y, i & 1)};
+      for (int h = 0; h < HW; ++h) {
+        const unsigned sel = (HW == 2 ? h : part & 1) ? 0x07060302u : 0x05040100u;
+        x[h] = __builtin_amdgcn_perm(rv[1], rv[0], sel);
+        y[h] = __builtin_amdgcn_perm(rv[3], rv[2], sel);
       }
     }
-    if (fp) {
-      float sc[NG], z[NG];
+    constexpr int GP = TP <= TG ? 1 : TP / TG;      // groups of a part
+    const int gr0 = part * TP / TG;
+#pragma unroll
+    for (int gg = 0; gg < GP; ++gg) {
+      f16x2 s01, s23, z01, z23;
+      if constexpr (kDeq) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(&s_w[step & 1][(fsub * NG + gr0 + gg) * 16 + 4 * g]);
+        s01 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w[1], w[0], 0x05040100u));
+        z01 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w[1], w[0], 0x07060302u));
+        s23 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w[3], w[2], 0x05040100u));
+        z23 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w[3], w[2], 0x07060302u));
+      }
+#pragma unroll
+      for (int ii = gg * (TP / GP); ii < (gg + 1) * (TP / GP); ++ii) {
+        const unsigned msk = (ii & 1) ? kHigh : kLow;
+        const unsigned px = ((ii & 2) ? x[ii >> 2] >> 8 : x[ii >> 2]) & msk, py = ((ii & 2) ? y[ii >> 2] >> 8 : y[ii >> 2]) & msk;
+        u32x2 v;
+        if constexpr (kDeq) {
+          v = u32x2{__builtin_bit_cast(unsigned, __builtin_elementwise_fma(whole(px, ii & 1), s01, z01)),
+                    __builtin_bit_cast(unsigned, __builtin_elementwise_fma(whole(py, ii & 1), s23, z23))};
+        } else {
+          v = u32x2{centre(px, ii & 1), centre(py, ii & 1)};
+        }
+        *reinterpret_cast<u32x2*>(&s_v[vb][(((fsub >> 1) * TILES + part * TP + ii) * 64 + lane) * 16 + (fsub & 1) * 8]) = v;
+      }
+    }
+  };
+  auto store_par = [&](int step) {
+    if (!fp) return;
+    const int pb = step & 3;
+    float sc[NG], z[NG];
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      sc[gr] = par_scale<BF>(rp[gr]);
+      z[gr] = par_zero<BF>(rp[gr]);
+    }
+    if (!fpv) {
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
+    } else {
+      unsigned big = 0;                             // magnitudes compare as their bits do
+      bool odd = false;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        sc[gr] = par_scale<BF>(rp[gr]);
-        z[gr] = par_zero<BF>(rp[gr]);
+        if (!rp_on) sc[gr] = z[gr] = 0.f;           // no token: its bits must not multiply
+        const float mid = __builtin_fmaf(sc[gr], 8.f, z[gr]);
+        const bool fine = __builtin_fabsf(mid) < __builtin_inff();
+        odd |= !fine;
+        if constexpr (kDeq) {
+          sc[gr] = fine ? sc[gr] : 0.f;
+          z[gr] = fine ? z[gr] : __builtin_nanf("");
+          const float far = __builtin_fmaxf(__builtin_fabsf(z[gr]), 16.f * __builtin_fabsf(sc[gr]));
+          big = max(big, fine ? __builtin_bit_cast(unsigned, far) : 0u);
+        } else {
+          z[gr] = mid;
+          big = max(big, fine ? __builtin_bit_cast(unsigned, __builtin_fabsf(sc[gr])) : 0u);
+        }
       }
-      if (!fpv) {
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
-      } else {
-        unsigned big = 0;                           // magnitudes compare as their bits do
-        bool odd = false;
+      if constexpr (kDeq) {
+        // the token's unit 2^e, at most its largest value's bound; values stay below 4 of it
+        big &= 0x7f800000u;
+        const float unit = __builtin_bit_cast(float, big), back = __builtin_bit_cast(float, 0x7f000000u - big);
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          if (!rp_on) sc[gr] = z[gr] = 0.f;         // no token: its bits must not multiply
-          z[gr] = __builtin_fmaf(sc[gr], 8.f, z[gr]);
-          const unsigned sb = __builtin_bit_cast(unsigned, __builtin_fabsf(sc[gr]));
           const bool fine = __builtin_fabsf(z[gr]) < __builtin_inff();
-          big = max(big, fine ? sb : 0u);
-          odd |= !fine;
+          const unsigned w = pack_f16(sc[gr] * back, fine ? z[gr] * back : 0.f);
+          if (lane < kStep) s_w[step & 1][((lane >> 4) * NG + gr) * 16 + (lane & 15)] = w;
+          z[gr] = fine ? 0.f : __builtin_nanf("");
         }
-        odd = __any(odd);
-        big = max(big, dpp<0x128>(big));            // row_ror 8, 4, 2, 1: over the subtile's 16 lanes
-        big = max(big, dpp<0x124>(big));
-        big = max(big, dpp<0x122>(big));
-        big = max(big, dpp<0x121>(big));
-        if ((lane & 15) == 0) s_big[vb][lane >> 4] = big;
-        if (lane == 0) s_odd[vb] = odd;
+        sc[0] = unit;
       }
-      if (lane < kStep) {
+      odd = __any(odd);
+      big = max(big, dpp<0x128>(big));              // row_ror 8, 4, 2, 1: over the subtile's 16 lanes
+      big = max(big, dpp<0x124>(big));
+      big = max(big, dpp<0x122>(big));
+      big = max(big, dpp<0x121>(big));
+      if ((lane & 15) == 0) s_big[pb][lane >> 4] = big;
+      if (lane == 0) s_odd[pb] = odd;
+    }
+    if (lane < kStep) {
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          float* p = &s_p[vb][(((lane >> 4) * NG + gr) * 4 + (fpv ? 2 : 0)) * 16 + (lane & 15)];
-          p[0] = sc[gr];
-          p[16] = z[gr];
-        }
+      for (int gr = 0; gr < NG; ++gr) {
+        float* p = &s_p[pb][(((lane >> 4) * NG + gr) * 4 + (fpv ? 2 : 0)) * 16 + (lane & 15)];
+        p[0] = sc[gr];
+        p[16] = z[gr];
       }
     }
   };
@@ -229,7 +283,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     }
     if (steps) {
       fetch_pages(0);
+      fetch_par_pages(0);
       fetch(0);
+      fetch_par(0);
     }
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
@@ -283,8 +339,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  auto par = [&](int vb, int pr, int x, int gr, int c) {
-    return *reinterpret_cast<const f32x4*>(&s_p[vb][(((2 * pr + x) * NG + gr) * 4 + c) * 16 + 4 * g]);
+  auto par = [&](int step, int pr, int x, int gr, int c) {
+    return *reinterpret_cast<const f32x4*>(&s_p[step & 3][(((2 * pr + x) * NG + gr) * 4 + c) * 16 + 4 * g]);
   };
   typedef f32x4 Acc[2][NG][NC];
   // the products of one half's keys with the rows
@@ -304,12 +360,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   };
   float u[NC][2][4];                                // scores in bits less the row's reference, of the half that comes next
   auto score = [&](int step, int pr, const Acc& acc) {
-    const int vb = step % 3;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        const f32x4 sc = par(vb, pr, x, gr, 0), z = par(vb, pr, x, gr, 1);
+        const f32x4 sc = par(step, pr, x, gr, 0), z = par(step, pr, x, gr, 1);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -323,10 +378,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // buffers that exist even after the last half: its scores are not used).  kMask: a weight of 0 must
   // not meet a parameter that is not finite, and O's unit is not 1.
   unsigned seen[NC];
-  typedef u32x4 Weights[NG][NC];
+  constexpr int WG = kDeq ? 1 : NG;                 // weights of a token: one, or one per group
+  typedef u32x4 Weights[WG][NC];
   auto weights = [&](auto mask_c, int step, int pr, int nstep, int npr, float tf, Acc& acc, Weights& bp) {
     constexpr bool kMask = decltype(mask_c)::value;
-    const int vb = step % 3;
     products(nstep, npr, acc);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
@@ -338,12 +393,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           l[nc] += u[nc][x][r];
         }
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr)
+    for (int gr = 0; gr < WG; ++gr)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        f32x4 sc = par(vb, pr, x, gr, 2);
-        const f32x4 md = par(vb, pr, x, gr, 3);
+        f32x4 sc = par(step, pr, x, gr, 2);
         if constexpr (kMask) sc *= tf;
+        if constexpr (!kDeq || kMask) {
+#pragma unroll
+          for (int g2 = gr; g2 < (kDeq ? NG : gr + 1); ++g2) {
+            const f32x4 md = par(step, pr, x, g2, 3);
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const bool on = !kMask || (seen[nc] >> (4 * x + r) & 1);
+                zs[nc][g2] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][g2]);
+              }
+          }
+        }
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
           float w[4];
@@ -351,7 +418,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           for (int r = 0; r < 4; ++r) {
             const bool on = !kMask || (seen[nc] >> (4 * x + r) & 1);
             w[r] = on ? u[nc][x][r] * sc[r] : 0.f;
-            zs[nc][gr] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][gr]);
           }
           // rounded to 11 bits
           bp[gr][nc][2 * x] = pack_f16(w[0], w[1]);
@@ -362,9 +428,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // One half, whose scores u holds.
   auto compute = [&](int step, int pr, int nstep, int npr) {
     const int tp = ts + kStep * step + 32 * pr, vb = step % 3;
-    const u32x2 bb = *reinterpret_cast<const u32x2*>(&s_big[vb][2 * pr]);
+    const u32x2 bb = *reinterpret_cast<const u32x2*>(&s_big[step & 3][2 * pr]);
     const unsigned big = __builtin_amdgcn_readfirstlane(max(bb[0], bb[1]));
-    const bool odd = __builtin_amdgcn_readfirstlane(s_odd[vb]);
+    const bool odd = __builtin_amdgcn_readfirstlane(s_odd[step & 3]);
     const int e = big ? (int)(big >> 23) - 126 : -kRoomMax;            // scales are below 2^e
     const int unit = e > kRoomMax ? 64 : e < -kRoomMax ? -64 : 0;
     if (unit > tau) {                               // O only ever goes to larger units
@@ -411,8 +477,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         for (int x = 0; x < 2; ++x) {
           f32x4 sm = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            const f32x4 v = par(vb, pr, x, gr, 2) * tf;
+          for (int gr = 0; gr < WG; ++gr) {
+            const f32x4 v = par(step, pr, x, gr, 2) * tf;
 #pragma unroll
             for (int r = 0; r < 4; ++r) sm[r] = __builtin_fmaxf(sm[r], __builtin_fabsf(v[r]));
           }
@@ -453,16 +519,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     for (int i = 0; i < TILES; ++i) {
       const u32x4 vf = *reinterpret_cast<const u32x4*>(&s_v[vb][((pr * TILES + i) * 64 + lane) * 16]);
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[i / TG][nc], o[nc][i]);
+      for (int nc = 0; nc < NC; ++nc) o[nc][i] = mfma(vf, bp[kDeq ? 0 : i / TG][nc], o[nc][i]);
     }
     score(nstep, npr, acc);
   };
 
   // Step j + 1 is stored after every wavefront has passed the barrier of step j, so its K buffer (of step
-  // j - 1, whose products were taken before that barrier) and its V buffer (of step j - 2) are free.
+  // j - 1, whose products were taken before that barrier) and its V buffer (of step j - 2) are free; the
+  // parameters are stored a step earlier, into the buffer of step j - 2.
   if (steps) {
+    store_par(0);
+    if (steps > 1) fetch_par(1);
+    __syncthreads();
     store(0);
-    if (steps > 1) fetch(1);
+    if (steps > 1) {
+      fetch(1);
+      store_par(1);
+      if (steps > 2) fetch_par(2);
+    }
     __syncthreads();
     {
       Acc acc;
@@ -472,7 +546,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     for (int j = 0; j < steps; ++j) {
       if (j + 1 < steps) {
         store(j + 1);
-        if (j + 2 < steps) fetch(j + 2);
+        if (j + 2 < steps) {
+          fetch(j + 2);
+          store_par(j + 2);
+          if (j + 3 < steps) fetch_par(j + 3);
+        }
       }
 #pragma unroll
       for (int pr = 0; pr < kHalves; ++pr) {
