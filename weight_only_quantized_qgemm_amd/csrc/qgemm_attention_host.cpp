@@ -118,7 +118,7 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   // workgroups' steps and overheads spread over the chip plus a quarter of a chain for the uneven end.
   // (6 chunks in a window of 4096, 64 heads: 679 us in one part, 776 in four; 100 queries after 16000
   // tokens: 145 us in 32 parts joined by one workgroup, 77 in 16 joined in pairs.)
-  const TileShape shape = tile_shape(dim, ng);
+  const TileShape shape = tile_shape(dim, ng, p->cache.dtype == QGEMM_DT_BF16);
   pl->tile = tile_rows(shape);
   const int64_t tiles = tiles_of(pl->tile);
   double best = 0.0;

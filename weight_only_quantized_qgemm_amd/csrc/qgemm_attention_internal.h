@@ -31,8 +31,10 @@ enum AttnKind : int { ATTN_ROWS = 1, ATTN_TILES = 2 };
 
 // Tiles kernel: column tiles of 16 query rows per wavefront and wavefronts per workgroup.
 struct TileShape { int cols, waves; };
-constexpr TileShape tile_shape(int dim, int groups) {
-  return dim == 256 && groups == 4 ? TileShape{2, 4} : dim == 256 || groups == 4 ? TileShape{1, 8} : TileShape{2, 8};
+// Measured at prompts of 4096 (us): D 64 2x8 157, 3x8 233, 4x4 212; D 128 2x8 198, 1x8 277, 2x4 375, and
+// four groups 1x8 398, 2x8 752; D 256 1x8 239, 2x4 372, and four groups 1x8 451 (bf16), 592 (fp16), 2x4 507, 528.
+constexpr TileShape tile_shape(int dim, int groups, bool bf16) {
+  return dim == 256 && groups == 4 && !bf16 ? TileShape{2, 4} : dim == 256 || groups == 4 ? TileShape{1, 8} : TileShape{2, 8};
 }
 constexpr int tile_rows(TileShape t) { return 16 * t.cols * t.waves; }
 

@@ -636,7 +636,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
 
 template <bool BF, int D, int NG>
 hipError_t launch_groups(const AttnPlan& pl, const AttnArgs& a, hipStream_t s) {
-  constexpr TileShape t = tile_shape(D, NG);
+  constexpr TileShape t = tile_shape(D, NG, BF);
   attention_tiles<BF, D, NG, t.cols, t.waves><<<dim3(pl.grid), dim3(64 * t.waves), 0, s>>>(a);
   return hipGetLastError();
 }
