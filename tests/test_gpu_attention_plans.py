@@ -1,0 +1,181 @@
+"""Launches of qgemm_attention that ordinary small cases do not reach, against the 64-bit oracle:
+few queries over a context split between many workgroups (numbers of parts that are not powers of
+two among them), hundreds of requests, wavefronts that work on their own, shared pages, NaN groups,
+graph replays of a split launch, side streams of the head and cache operators."""
+import numpy as np
+import pytest
+
+from gpu_cases import say
+from oracle import attention as oa
+from test_gpu_attention import T16, _check, _run, _sequences, dt, same_bits, up
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import weight_only_quantized_qgemm_amd as lib
+    return lib
+
+
+def scale_of(dim):
+    return np.float64(np.float32(dim ** -0.5))
+
+
+# kind, query lengths, context lengths, q_heads, kv_heads, dim, group, page, causal, window, parts
+SPLIT = [
+    ("f16", [64], [1300], 2, 1, 64, 64, 16, True, 0, 4),
+    ("f16", [70], [2100], 1, 1, 128, 128, 16, True, 0, 7),
+    ("bf16", [40, 3], [3000, 900], 4, 2, 128, 32, 48, True, 0, 12),
+    ("f16", [33, 20], [1500, 20], 2, 2, 256, 64, 64, True, 0, 5),
+    ("bf16", [100], [900], 1, 1, 256, 128, 16, True, 70, 3),
+    ("bf16", [30, 30, 0], [700, 30, 500], 2, 1, 64, 32, 32, False, 0, 3),
+    ("f16", [50], [2100], 3, 1, 128, 64, 16, True, 1000, 7),              # parts outside the window
+]
+
+
+@pytest.mark.parametrize("case", range(len(SPLIT)))
+def test_split_context(q, case):
+    kind, qlens, klens, hq, hk, dim, group, page, causal, window, parts = SPLIT[case]
+    say(f"case attention split {SPLIT[case]}")
+    s = _sequences(q, kind, qlens, klens, hq, hk, dim, group, page, 100 + case, spread=1.5)
+    p = q.attention_problem(s["c"], len(klens), sum(qlens), hq, max(qlens), s["max_pages"], causal=causal, window=window,
+                            kernel_hint=q.ATTENTION_TILES)
+    assert q.attention_describe(p).endswith(f"splits={parts}")
+    out = _run(q, s, kind, hq, causal, window, hint=q.ATTENTION_TILES, extra=8)
+    _check(s, out, kind, hq, causal, window, scale_of(dim))
+
+
+@pytest.mark.parametrize("kind,heads,dim,group,hint", [
+    ("f16", (16, 8), 64, 64, 0), ("bf16", (8, 8), 128, 32, 0), ("bf16", (16, 8), 64, 32, 2), ("f16", (8, 8), 256, 64, 1)])
+def test_hundreds_of_requests(q, kind, heads, dim, group, hint):
+    # 210 requests of every length from 0 on, a query each except every seventh
+    say(f"case attention 210 requests {kind} {heads} D={dim} hint={hint}")
+    klens = [(i * 37) % 131 for i in range(210)]
+    qlens = [0 if i % 7 == 3 else 1 for i in range(210)]
+    s = _sequences(q, kind, qlens, klens, *heads, dim, group, 16, 200)
+    p = q.attention_problem(s["c"], 210, sum(qlens), heads[0], 1, s["max_pages"], kernel_hint=hint)
+    assert hint == 2 or "waves=1" in q.attention_describe(p)
+    out = _run(q, s, kind, heads[0], hint=hint)
+    _check(s, out, kind, heads[0], True, 0, scale_of(dim))
+
+
+def test_many_prompts(q):
+    say("case attention 90 prompts")
+    qlens = [(i * 29) % 41 for i in range(90)]
+    klens = [n + (i * 53) % 67 for i, n in enumerate(qlens)]
+    s = _sequences(q, "bf16", qlens, klens, 4, 1, 64, 64, 16, 201)
+    for hint in (0, 1, 2):
+        _check(s, _run(q, s, "bf16", 4, hint=hint, max_q=41), "bf16", 4, True, 0, scale_of(64))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [64, 256])
+def test_six_rows_of_the_widest_heads(q, kind, group):
+    say(f"case attention D=256 six rows {kind} group={group}")
+    s = _sequences(q, kind, [3, 2], [190, 333], 4, 2, 256, group, 16, 202)
+    _check(s, _run(q, s, kind, 4, hint=q.ATTENTION_ROWS), kind, 4, True, 0, scale_of(256))
+
+
+@pytest.mark.parametrize("hint", [1, 2])
+def test_requests_that_share_pages(q, hint):
+    # three requests over one context's pages: the same rows give the same bits
+    say(f"case attention shared pages hint={hint}")
+    s = _sequences(q, "f16", [2], [95], 8, 2, 128, 64, 32, 203)
+    alone = _run(q, s, "f16", 8, hint=hint)
+    _check(s, alone, "f16", 8, True, 0, scale_of(128))
+    three = dict(s, table=s["table"].repeat(3, 1), lens=s["lens"].repeat(3), q=np.concatenate([s["q"]] * 3), qlens=[2] * 3,
+                 klens=[95] * 3, seqs=s["seqs"] * 3, starts=torch.tensor([0, 2, 4, 6], dtype=torch.int32, device="cuda"))
+    out = _run(q, three, "f16", 8, hint=hint)
+    assert torch.equal(out[:2], out[2:4]) and torch.equal(out[:2], out[4:])
+    _check(three, out, "f16", 8, True, 0, scale_of(128))
+
+
+@pytest.mark.parametrize("hint", [1, 2])
+@pytest.mark.parametrize("kind,dim,group", [("bf16", 128, 32), ("bf16", 256, 64), ("f16", 64, 32), ("bf16", 64, 64)])
+def test_one_group_that_is_not_finite(q, kind, dim, group, hint):
+    # NaN in one group of one token's value: the dims of that group are NaN for the queries that see the
+    # token, the others (and every earlier query) keep their bits
+    say(f"case attention NaN group {kind} D={dim} G={group} hint={hint}")
+    s = _sequences(q, kind, [60], [60], 2, 1, dim, group, 16, 204)
+    clean = _run(q, s, kind, 2, hint=hint)
+    k, v = (torch.empty(1, 1, dim, dtype=T16[kind], device="cuda") for _ in "kv")
+    at = torch.tensor([int(s["table"][0, 2]) * 16 + 5], device="cuda")               # token 37
+    q.cache_read(s["c"], s["data"], at, k, v)
+    rewritten = v.clone()
+    rewritten[..., dim - group:] = float("nan")
+    q.cache_write(s["c"], s["data"], k, v, at)                                        # requantized, finite
+    base = _run(q, s, kind, 2, hint=hint)
+    assert same_bits(base[:37], clean[:37])
+    q.cache_write(s["c"], s["data"], k, rewritten, at)
+    dirty = _run(q, s, kind, 2, hint=hint)
+    assert same_bits(dirty[:37], clean[:37])
+    assert torch.isnan(dirty[37:, :, dim - group:]).all()
+    if group < dim:
+        assert torch.isfinite(dirty[37:, :, :dim - group]).all()
+
+
+def test_graph_replays_of_a_split_launch(q):
+    # the parts' tickets and partial results are ready again after every replay
+    say("case attention graph of a split launch")
+    s = _sequences(q, "bf16", [40], [1500], 4, 2, 128, 64, 16, 205)
+    p = q.attention_problem(s["c"], 1, 40, 4, 40, s["max_pages"], kernel_hint=q.ATTENTION_TILES)
+    assert "splits=1" not in q.attention_describe(p).split()
+    ws, out, qx = q.alloc_attention_workspace(p), torch.zeros(40, 4, 128, dtype=torch.bfloat16, device="cuda"), up(s["q"], "bf16")
+    table = s["table"].clamp(min=0)
+    args = (p, qx, s["data"], table, s["lens"], s["starts"])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        q.attention(*args, out, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.attention(*args, out, ws)
+    for length in (1500, 40, 777, 39, 0, 1499):
+        s["lens"].fill_(length)
+        out.fill_(9.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        eager = torch.zeros_like(out)
+        q.attention(*args, eager, q.alloc_attention_workspace(p))
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), length
+
+
+def test_head_and_cache_operators_on_side_streams(q):
+    say("case norm_rope and cache on a side stream")
+    x = torch.randn(5, 3, 128, device="cuda").half()
+    pos, table = torch.arange(5, dtype=torch.int32, device="cuda"), torch.randn(8, 128, device="cuda")
+    p = q.norm_rope_problem(5, 2, 1, 128, rot_dim=128, max_pos=8)
+    c = q.cache(2, 16, 1, 128, q.DT_F16)
+    slots = torch.tensor([3, 30, 7, 0, 19], device="cuda")
+
+    def steps(src, data, stream=None):
+        o, kv = torch.empty_like(src), [torch.empty(5, 1, 128, dtype=torch.float16, device="cuda") for _ in "kv"]
+        q.qk_norm_rope(p, src[:, :2], src[:, 2:], None, None, pos, table, o[:, :2], o[:, 2:], stream=stream)
+        q.cache_write(c, data, o[:, 2:], src[:, 2:], slots, stream=stream)
+        q.cache_read(c, data, slots, *kv, stream=stream)
+        return o, *kv
+
+    want = steps(x, q.alloc_cache(c))
+    side = torch.cuda.Stream()
+    late, data = torch.zeros_like(x), q.alloc_cache(c)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+        got = steps(late, data)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    late.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+    got = steps(late, data, stream=side)                     # named, from another current stream
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -584,13 +584,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // waits, and a sum of two has the same bits either way round, so the result does not depend on the order.
   if (active > 1) {
     const int tile = entry * a.kv_heads + kvh;
-    unsigned* node = a.tickets + (size_t)tile * a.splits;            // level k's nodes are side by side
+    unsigned* tickets = a.tickets + (size_t)tile * a.splits;
     float* base = a.partials + (size_t)tile * a.splits * kSlot;
     const __amdgpu_buffer_rsrc_t parts = buffer_of(base, a.splits * kSlot * 4);
-    for (int i = split, size = 1, left = a.splits; size < active; size *= 2, i >>= 1) {
-      left = (left + 1) / 2;                        // nodes of this level
+    for (int i = split, size = 1; size < active; size *= 2, i >>= 1) {
       if ((i ^ 1) * size < active) {                // the node has two children
         const int mydst = i * size * kSlot * 4;
+        // a node goes by the first part of its right child: that number's lowest set bit is `size`, so no
+        // other node has it, and it is below `splits`
+        unsigned* node = tickets + (i | 1) * size;
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
 #pragma unroll
@@ -600,10 +602,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         __builtin_amdgcn_s_waitcnt(0);              // this thread's stores are complete
         __syncthreads();
         if (threadIdx.x == 0)
-          s_last = __hip_atomic_fetch_add(node + (i >> 1), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 1u;
+          s_last = __hip_atomic_fetch_add(node, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 1u;
         __syncthreads();
         if (!s_last) return;
-        if (threadIdx.x == 0) __hip_atomic_store(node + (i >> 1), 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (threadIdx.x == 0) __hip_atomic_store(node, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const int from = (i ^ 1) * size * kSlot * 4;
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
@@ -617,7 +619,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
             o[nc][x] = o[nc][x] * mine + load4(parts, from + ((nc * TILES + x) * NT + threadIdx.x) * 16) * other;
         }
       }
-      node += left;
     }
   }
 #pragma unroll
