@@ -131,9 +131,9 @@ typedef struct qgemm_attention {
   int32_t reserved[2];              /* 0 */
 } qgemm_attention_t;
 
-/* qgemm_attention_workspace_bytes -- device workspace of qgemm_attention, under the contract of
- * qgemm_workspace_bytes: zero-filled once by the caller, reusable by later calls in stream order
- * with the same descriptor, never shared by calls that overlap in time. */
+/* qgemm_attention_workspace_bytes -- device workspace of qgemm_attention: zero-filled once by the
+ * caller, then reusable by later calls in stream order.  One workspace of the largest size asked for
+ * serves any descriptors; calls that overlap in time need different ones. */
 qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* problem, size_t* bytes);
 
 /*
@@ -151,7 +151,9 @@ qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* problem,
  * causal t <= its own, with window t > its own - window.  A query that sees nothing gets zeros.  Bits
  * in slots that no query sees (unwritten pages, the rest of the last page) never reach the output.
  * Scores, the softmax's maximum and sum and the output are accumulated in fp32; the weights that
- * multiply the codes are rounded to fp16 (11 bits).  Results are bitwise deterministic.
+ * multiply the codes are rounded to fp16 (11 bits); the tiles kernel over a BF16 cache also rounds the
+ * values, divided by a power of two per token, to fp16 (three bits more than BF16 holds).  Results are
+ * bitwise deterministic.
  */
 qgemm_status_t qgemm_attention(const qgemm_attention_t* problem, const void* q, int64_t q_stride, const void* data,
                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_start, void* out,

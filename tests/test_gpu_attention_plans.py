@@ -179,3 +179,65 @@ def test_head_and_cache_operators_on_side_streams(q):
     got = steps(late, data, stream=side)                     # named, from another current stream
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_one_workspace_for_every_problem(q):
+    # a zero-filled workspace of the largest size, in stream order: whatever ran before, the same bits
+    say("case attention one workspace")
+    made = [("f16", [1] * 5, [300, 1, 900, 64, 2000], 8, 2, 128, 64, 1), ("f16", [70], [2100], 1, 1, 128, 128, 2),
+            ("bf16", [1], [1800], 32, 2, 256, 256, 1), ("bf16", [33, 20], [1500, 20], 2, 2, 256, 64, 2),
+            ("f16", [1] * 40, [90] * 40, 64, 64, 64, 32, 1)]
+    calls = []
+    for i, (kind, qlens, klens, hq, hk, dim, group, hint) in enumerate(made):
+        s = _sequences(q, kind, qlens, klens, hq, hk, dim, group, 16, 300 + i)
+        p = q.attention_problem(s["c"], len(klens), sum(qlens), hq, max(qlens), s["max_pages"], kernel_hint=hint)
+        calls.append((p, up(s["q"], kind), s["data"], s["table"], s["lens"], s["starts"]))
+    want = []
+    for args in calls:
+        out = torch.zeros_like(args[1])
+        q.attention(*args, out, q.alloc_attention_workspace(args[0]))
+        want.append(out)
+    ws = torch.zeros(max(q.attention_workspace_bytes(a[0]) for a in calls), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 4, 1, 0, 3, 3, 4, 2, 0, 1):
+        out = torch.zeros_like(want[i])
+        q.attention(*calls[i], out, ws)
+        assert torch.equal(out, want[i]), i
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_cache_codes_for_every_scale(q, kind):
+    # every significand a scale can have, at sizes from the smallest subnormal to the largest, elements at
+    # and next to the ties between codes: codes and parameters are the definition's
+    say(f"case cache every scale {kind}")
+    g = np.random.default_rng([30, len(kind)])
+    bits = 10 if kind == "f16" else 7
+    sizes = [2.0 ** -24, 2.0 ** -20, 2.0 ** -15, 2.0 ** -14, 2.0 ** -13, 1.0, 2.0 ** 10] if kind == "f16" else \
+        [2.0 ** -133, 2.0 ** -126, 2.0 ** -100, 2.0 ** -61, 2.0 ** -60, 2.0 ** -59, 1.0, 2.0 ** 60, 2.0 ** 120]
+    heads, dim = 2, 128
+    for size in sizes:
+        scale = (1 + np.arange(2 ** bits) / 2 ** bits) * size
+        n = len(scale)
+        c = g.integers(0, 15, (n, heads, dim)) + 0.5 + g.choice([0, 0, 1e-3, -1e-3, 3e-2, -3e-2, 0.4], (n, heads, dim))
+        x = oa.round16(c * scale[:, None, None], kind)
+        x[:, :, 0], x[:, :, 1] = 0.0, oa.round16(15 * scale, kind)[:, None]
+        x = oa.round16(x - oa.round16(g.integers(0, 3, (n, 1, 1)) * 5 * scale[:, None, None], kind), kind)
+        assert np.isfinite(x).all()
+        c = q.cache(-(-n // 16), 16, heads, dim, dt(q, kind), group_size=64)
+        data = q.alloc_cache(c)
+        slots = torch.arange(n, device="cuda")
+        q.cache_write(c, data, up(x, kind), up(x[:, ::-1], kind), slots)
+        parts = [oa.quantize(a, 64, kind) for a in (x, x[:, ::-1])]
+        got, at = data.cpu().numpy().reshape(-1, heads, oa.block_bytes(16, dim, 64)), 0
+        for page in range(-(-n // 16)):
+            m = min(16, n - at)
+            for h in range(heads):
+                full = []
+                for codes, s, z in parts:
+                    cc, ss, zz = np.zeros((16, dim), np.uint8), np.zeros((16, 2)), np.zeros((16, 2))
+                    cc[:m], ss[:m], zz[:m] = codes[at:at + m, h], s[at:at + m, h], z[at:at + m, h]
+                    full += [cc, ss, zz]
+                want = oa.pack_block(*full, kind)
+                par = 16 * dim                                        # zeros of either sign are one value
+                assert np.array_equal(got[page, h, :par], want[:par]), (size, page, h)
+                assert np.array_equal(*(oa.from_bits16(b[par:].copy().view(np.uint16), kind) for b in (got[page, h], want)))
+            at += m

@@ -14,6 +14,9 @@ static_assert(sizeof(qgemm_attention_t) == 80, "qgemm_attention_t layout is part
 
 static const int kCUs = 256;
 static const int kMaxSplits = 32;           // workgroups per row tile
+// The workspace begins with a ticket region of one size, whatever the plan, so that partial results of one
+// problem never lie where another counts and one workspace serves them all.
+static const int kTickets = 8192;
 static const int64_t kMaxTokens = int64_t(1) << 24;
 
 static qgemm_status_t check_dtype_dim(const char* what, int dtype, int head_dim) {
@@ -123,7 +126,7 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   const int64_t tiles = tiles_of(pl->tile);
   double best = 0.0;
   pl->splits = 1;
-  for (int s = 1, levels = 0; s <= kMaxSplits && (s == 1 || (int64_t)s * 4 <= steps); ++s) {
+  for (int s = 1, levels = 0; s <= kMaxSplits && (s == 1 || ((int64_t)s * 4 <= steps && tiles * s <= kTickets)); ++s) {
     while ((1 << levels) < s) ++levels;
     const double chain = (double)((steps + s - 1) / s), join = 1.2 * levels;
     const double latency = chain + 4.0 + (s > 1 ? 2.0 : 0.0) + join;
@@ -155,7 +158,7 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
     // 1024 segments of 1500 tokens on four are as good, and better for few long ones).
     pl->waves = row_tiles >= 1536 ? 1 : 4;
     pl->grid = (unsigned)(2 * kCUs * 4 / pl->waves);
-    pl->tickets_bytes = ((size_t)pl->grid * 4 + 255) / 256 * 256;
+    pl->tickets_bytes = (size_t)kTickets * 4;         // one per workgroup, at most 2048
     pl->ws_bytes = pl->tickets_bytes + (size_t)2 * pl->grid * row_tile * (dim + 4) * 4;
     return QGEMM_OK;
   }
@@ -165,7 +168,7 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
                 (long long)(tiles * pl->splits));
   pl->grid = (unsigned)(tiles * pl->splits);
   if (pl->splits > 1) {
-    pl->tickets_bytes = ((size_t)tiles * pl->splits * 4 + 255) / 256 * 256;
+    pl->tickets_bytes = (size_t)kTickets * 4;
     pl->ws_bytes = pl->tickets_bytes +
                    (size_t)tiles * pl->splits * ((size_t)pl->tile * dim + (size_t)shape.cols * shape.waves * 256) * 4;
   }

@@ -3,10 +3,15 @@
 // Bound by memory: a 16-bit element in, half a byte and its share of two 16-bit parameters out (and
 // the other way round).  A head row of D elements is spread over D / 8 lanes, eight consecutive dims
 // (one 16-byte access and one dword of codes) each, so a wavefront holds 512 / D rows; they are
-// consecutive tokens of one kv head, whose K codes, V codes and parameters lie side by side when
-// their slots do.  A K dword goes out as it is.  V is stored by lane r = dim % 16, so the eight
-// codes of a lane belong to eight places: the row's dwords go through LDS (D / 2 bytes) and every
-// lane gathers the nibbles of its own place from there.
+// consecutive tokens of one kv head, and the workgroup's four wavefronts continue them, because their K
+// codes, V codes and parameters lie side by side when their slots do (heads side by side instead: read
+// 16.3 us against 13.6).  A K dword goes out as it is; V's codes are transposed between the row's lanes
+// in registers (through LDS, a nibble at a time: 18.8).  What cache_read writes is not read again by
+// it: its stores are non-temporal (17.6 us against 23.8 with data past the caches).
+//
+// 16383 tokens of 8 heads of 128, fp16, groups of 32, in a captured graph: write 21.9 us, read 13.6 us,
+// 5.0 TB/s in both; write 23.0 and read 15.8 us when nothing lies in the 256 MB cache.  Writing is at
+// 330 vector instructions a wavefront, about as long as its memory traffic.
 #include <hip/hip_runtime.h>
 
 #include "qgemm_attention_internal.h"
@@ -16,6 +21,10 @@ namespace {
 using namespace qgemm;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+template <int N>
+struct ic { static constexpr int value = N; };
 
 struct CacheArgs {
   const uint16_t *k, *v;           // write: inputs
@@ -24,6 +33,7 @@ struct CacheArgs {
   const long long* slots;
   long long ks, vs;                // token strides in elements
   long long total_slots;
+  double per_page;                 // 1 / page
   int tokens, kv_heads, page, codes, params, block;
 };
 
@@ -49,8 +59,11 @@ __device__ __forceinline__ Place place_of(const CacheArgs& a, int token, int hea
   if (token >= a.tokens) return p;
   const long long slot = a.slots[token];
   if (slot < 0 || slot >= a.total_slots) return p;
-  const unsigned pg = (unsigned)((unsigned long long)slot / (unsigned)a.page);
-  p.t = (int)(slot - (long long)pg * a.page);
+  // slot / page by the reciprocal in fp64, at most one off, instead of a 64-bit division
+  long long pg = (long long)((double)slot * a.per_page);
+  p.t = (int)(slot - pg * a.page);
+  if (p.t < 0) p.t += a.page, --pg;
+  if (p.t >= a.page) p.t -= a.page, ++pg;
   p.block = a.data + ((size_t)pg * a.kv_heads + head) * a.block;
   p.ok = true;
   return p;
@@ -60,7 +73,7 @@ __device__ __forceinline__ Place place_of(const CacheArgs& a, int token, int hea
 // reduce like xor 4 and xor 8 once the quads are equal.
 template <int C>
 __device__ __forceinline__ float dpp(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), C, 0xf, 0xf, false));
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), C, 0xf, 0xf, true));
 }
 template <int LANES, class F>
 __device__ __forceinline__ float reduce(float x, F f) {
@@ -74,64 +87,98 @@ __device__ __forceinline__ float reduce(float x, F f) {
 
 // Quantizes the lane's eight elements within groups of G / 8 lanes: the codes as one dword and the
 // group's (scale, zero) as another.  The codes are those of the header's formula in fp32 with IEEE
-// division: with y the rounded reciprocal of s, q = d y is within two units of d / s in the last
-// place, and q + (d - q s) y, the remainder being exact, is the rounded quotient (Markstein).  Three
-// operations an element instead of a division's dozen.  Scales so small that y or the remainder leaves the normal range divide.
+// division, by Markstein's correction: with y the rounded reciprocal of s, q = d y is within two units
+// of d / s in the last place, and q + (d - q s) y, the remainder being exact, is the rounded quotient.
+// Three operations an element instead of a division's dozen.  Scales so small that y or the remainder
+// leaves the normal range, or that fp16 holds them in fewer bits, divide and clamp.
 template <bool BF, int G>
 __device__ __forceinline__ void quantize8(u32x4 x, unsigned& codes, unsigned& par) {
   float f[8];
-  unsigned top = 0;                                   // the largest magnitude's bits: above the exponent's
-#pragma unroll                                        // last value there is an infinity or a NaN
+  u16x2 top = {0, 0};                                 // the largest magnitudes' bits: from the exponent's
+#pragma unroll                                        // last value on there is an infinity or a NaN
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = from16<BF>(x[i] & 0xffffu);
     f[2 * i + 1] = from16<BF>(x[i] >> 16);
-    top = max(top, max((x[i] & 0x7fffu) << 16, x[i] & 0x7fff0000u));
+    top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i] & 0x7fff7fffu));
   }
-  const bool odd = top >= (BF ? 0x7f800000u : 0x7c000000u);
   float lo = f[0], hi = f[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
     lo = __builtin_fminf(lo, f[i]);
     hi = __builtin_fmaxf(hi, f[i]);
   }
-  if (odd) hi = __builtin_inff();                     // fmin / fmax pass over a NaN
+  if (max(top[0], top[1]) >= (BF ? 0x7f80 : 0x7c00)) hi = __builtin_inff();      // fmin / fmax pass over a NaN
   lo = reduce<G / 8>(lo, [](float a, float b) { return __builtin_fminf(a, b); });
   hi = reduce<G / 8>(hi, [](float a, float b) { return __builtin_fmaxf(a, b); });
   const float span = hi - lo;
   const bool bad = !(span < __builtin_inff());
-  const unsigned sb = to16<BF>(span / 15.0f), zb = to16<BF>(lo);
-  const float s = from16<BF>(sb);
-  const bool tiny = s < 0x1p-60f, live = s > 0.f && !bad;
-  const float y = 1.0f / (live ? s : 1.0f);
-  // A clamped quotient plus 2^23 is 0x4B000000 + code, rounded to even; the constants add up in the
+  // the quotient of 15 by the same correction, from the rounded reciprocal
+  constexpr float kY15 = 1.0f / 15.0f;
+  const float q15 = span * kY15;
+  float s = from16<BF>(to16<BF>(__builtin_fmaf(__builtin_fmaf(-15.f, q15, span), kY15, q15)));
+  // A scale of full precision is at most 2^-9 too small: no quotient reaches 15.5, where clamping begins.
+  const bool tiny = s < (BF ? 0x1p-60f : 0x1p-14f);
+  // A quotient plus 2^23 is 0x4B000000 + code, rounded to even; the constants add up in the
   // packed sum and are taken out at the end.
   constexpr unsigned kBias = 0x4B000000u * 0x11111111u;
   unsigned sum = 0;
   if (__builtin_expect(__any(tiny), 0)) {
+    s = from16<BF>(to16<BF>(span / 15.0f));
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       sum += __builtin_bit_cast(unsigned, __builtin_amdgcn_fmed3f((f[i] - lo) / s, 0.f, 15.f) + 0x1p23f) << (4 * i);
   } else {
+    // one step from the hardware's reciprocal (one unit in the last place) gives the rounded one of a number
+    // of so few bits
+    const float y0 = __builtin_amdgcn_rcpf(s), y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.f), y0, y0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = f[i] - lo, q = d * y;
       const float v = __builtin_fmaf(__builtin_fmaf(-q, s, d), y, q);
-      sum += __builtin_bit_cast(unsigned, __builtin_amdgcn_fmed3f(v, 0.f, 15.f) + 0x1p23f) << (4 * i);
+      sum += __builtin_bit_cast(unsigned, v + 0x1p23f) << (4 * i);
     }
   }
+  const bool live = s > 0.f && !bad;
   codes = sum - kBias;                                // not live: nothing of it is used
   if (!live) codes = 0;
-  par = bad ? (BF ? 0x7fc07fc0u : 0x7e007e00u) : sb | zb << 16;
+  par = bad ? (BF ? 0x7fc07fc0u : 0x7e007e00u) : to16<BF>(s) | to16<BF>(lo) << 16;
+}
+
+// V's codes between the lanes of a row.  Lane j has the codes of dims 8 j .. + 7, that is dims 16 i + r with
+// i = j / 2 and r = 8 (j % 2) + e for its nibbles e; the layout wants r fixed and i along the nibbles.  So
+// lanes of the same parity transpose an 8 x 8 matrix of nibbles (a 4 x 4 one of bytes where D = 64), one
+// index bit at a time: the lane that differs in that bit of i hands over the half of its dword where the
+// bits of i and e differ.  Each step is its own inverse and the steps commute, so the same call takes the
+// stored order back.
+template <int M>
+__device__ __forceinline__ unsigned from_lane_xor(unsigned x) {
+  auto mov = [](unsigned v, auto c) {
+    return (unsigned)__builtin_amdgcn_mov_dpp((int)v, decltype(c)::value, 0xf, 0xf, true);
+  };
+  if constexpr (M == 2) return mov(x, ic<0x4E>{});                          // quad_perm 2 3 0 1
+  else if constexpr (M == 4) return mov(mov(x, ic<0x1B>{}), ic<0x141>{});   // reversed quad, reversed eight: xor 3, xor 7
+  else return mov(mov(x, ic<0x141>{}), ic<0x140>{});                        // reversed eight, reversed row: xor 7, xor 15
+}
+template <int D>
+__device__ __forceinline__ unsigned transpose(unsigned x, int j) {
+  const bool b0 = j & 2, b1 = j & 4, b2 = j & 8;
+  // bytes 0..3 are this lane's, 4..7 the other's
+  if constexpr (D == 64) {
+    x = __builtin_amdgcn_perm(from_lane_xor<2>(x), x, b0 ? 0x03070105u : 0x06020400u);
+    return __builtin_amdgcn_perm(from_lane_xor<4>(x), x, b1 ? 0x03020706u : 0x05040100u);
+  }
+  const unsigned p = from_lane_xor<2>(x), keep = b0 ? 0xf0f0f0f0u : 0x0f0f0f0fu;
+  x = (x & keep) | (__builtin_amdgcn_alignbit(p, p, b0 ? 4 : 28) & ~keep);
+  x = __builtin_amdgcn_perm(from_lane_xor<4>(x), x, b1 ? 0x03070105u : 0x06020400u);
+  return __builtin_amdgcn_perm(from_lane_xor<8>(x), x, b2 ? 0x03020706u : 0x05040100u);
 }
 
 template <bool BF, int D, int NG>
 __global__ __launch_bounds__(256) void cache_write(CacheArgs a) {
   constexpr int L = D / 8, R = 64 / L, U = D / 32, G = D / NG;
-  __shared__ unsigned rows[4][64];                      // a wavefront's V dwords
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane % L;
-  const int unit = blockIdx.x * 4 + wave;
-  const int head = unit % a.kv_heads;
-  const int token = unit / a.kv_heads * R + lane / L;
+  const int head = blockIdx.x % a.kv_heads;
+  const int token = (blockIdx.x / a.kv_heads * 4 + wave) * R + lane / L;
   const Place p = place_of(a, token, head);
   u32x4 kx = {0, 0, 0, 0}, vx = {0, 0, 0, 0};
   if (p.ok) {
@@ -141,28 +188,20 @@ __global__ __launch_bounds__(256) void cache_write(CacheArgs a) {
   unsigned kc, kp, vc, vp;
   quantize8<BF, G>(kx, kc, kp);
   quantize8<BF, G>(vx, vc, vp);
-  rows[wave][lane] = vc;
-  __syncthreads();
+  vc = transpose<D>(vc, j);
   if (!p.ok) return;
   *reinterpret_cast<unsigned*>(p.block + p.t * (D / 2) + 4 * (U * (j & 3) + (j >> 2))) = kc;
-  const unsigned* row = rows[wave] + lane / L * L;
   uint8_t* vb = p.block + a.codes + (p.t >> 2) * (64 * U) + (p.t & 3) * U;
-  // code of dim 16 i + r: dword 2 i + (r >> 3), nibble r & 7
+  const int i = j >> 1 & 7, e = 8 * (j & 1);
   if constexpr (D == 64) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 2 * j + h;
-      unsigned w = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w |= (row[2 * i + (r >> 3)] >> (4 * (r & 7)) & 15u) << (4 * i);
-      *reinterpret_cast<uint16_t*>(vb + r * (4 * U)) = (uint16_t)w;
-    }
+    // bytes: code of r = e + 2 i low, of the next r high
+    unsigned even = vc & 0x0f0f0f0fu, next = vc >> 4 & 0x0f0f0f0fu;
+    even = (even | even >> 4) & 0x00ff00ffu;
+    next = (next | next >> 4) & 0x00ff00ffu;
+    *reinterpret_cast<uint16_t*>(vb + (e + 2 * i) * (4 * U)) = (uint16_t)(even | even >> 8);
+    *reinterpret_cast<uint16_t*>(vb + (e + 2 * i + 1) * (4 * U)) = (uint16_t)(next | next >> 8);
   } else {
-    const int r = D == 128 ? j : j >> 1, i0 = D == 128 ? 0 : 8 * (j & 1);
-    unsigned w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= (row[2 * (i0 + i) + (r >> 3)] >> (4 * (r & 7)) & 15u) << (4 * i);
-    *reinterpret_cast<unsigned*>(vb + r * (4 * U) + i0 / 2) = w;
+    *reinterpret_cast<unsigned*>(vb + (e + i) * (4 * U) + (j >> 4) * 4) = vc;
   }
   if (j % (G / 8) == 0) {
     const int at = (j / (G / 8) * a.page + p.t) * 4;
@@ -185,42 +224,33 @@ __device__ __forceinline__ u32x4 values8(unsigned codes, unsigned par) {
 template <bool BF, int D, int NG>
 __global__ __launch_bounds__(256) void cache_read(CacheArgs a) {
   constexpr int L = D / 8, R = 64 / L, U = D / 32, G = D / NG;
-  __shared__ unsigned rows[4][64];                      // a wavefront's V units, by r
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane % L;
-  const int unit = blockIdx.x * 4 + wave;
-  const int head = unit % a.kv_heads;
-  const int token = unit / a.kv_heads * R + lane / L;
+  const int head = blockIdx.x % a.kv_heads;
+  const int token = (blockIdx.x / a.kv_heads * 4 + wave) * R + lane / L;
   const Place p = place_of(a, token, head);
-  unsigned kc = 0, kp = 0, vp = 0;
-  // the row's V units, 16 bits (D = 64), a dword or two dwords for each r
-  uint16_t* row = reinterpret_cast<uint16_t*>(rows[wave]) + lane / L * (D / 4);
+  unsigned kc = 0, vc = 0, kp = 0, vp = 0;
   if (p.ok) {
     kc = *reinterpret_cast<const unsigned*>(p.block + p.t * (D / 2) + 4 * (U * (j & 3) + (j >> 2)));
     const int at = 2 * a.codes + (j / (G / 8) * a.page + p.t) * 4;
     kp = *reinterpret_cast<const unsigned*>(p.block + at);
     vp = *reinterpret_cast<const unsigned*>(p.block + at + a.params);
     const uint8_t* vb = p.block + a.codes + (p.t >> 2) * (64 * U) + (p.t & 3) * U;
+    const int i = j >> 1 & 7, e = 8 * (j & 1);
     if constexpr (D == 64) {
-      row[2 * j] = *reinterpret_cast<const uint16_t*>(vb + 2 * j * (4 * U));
-      row[2 * j + 1] = *reinterpret_cast<const uint16_t*>(vb + (2 * j + 1) * (4 * U));
+      unsigned even = *reinterpret_cast<const uint16_t*>(vb + (e + 2 * i) * (4 * U));
+      unsigned next = *reinterpret_cast<const uint16_t*>(vb + (e + 2 * i + 1) * (4 * U));
+      even = (even | even << 8) & 0x00ff00ffu;
+      next = (next | next << 8) & 0x00ff00ffu;
+      vc = ((even | even << 4) & 0x0f0f0f0fu) | ((next | next << 4) & 0x0f0f0f0fu) << 4;
     } else {
-      const int r = D == 128 ? j : j >> 1, i0 = D == 128 ? 0 : 8 * (j & 1);
-      *reinterpret_cast<unsigned*>(row + r * (U / 2) + i0 / 4) =
-          *reinterpret_cast<const unsigned*>(vb + r * (4 * U) + i0 / 2);
+      vc = *reinterpret_cast<const unsigned*>(vb + (e + i) * (4 * U) + (j >> 4) * 4);
     }
   }
-  __syncthreads();
+  vc = transpose<D>(vc, j);
   if (token >= a.tokens) return;
-  unsigned vc = 0;
-  if (p.ok) {
-    // dims 8 j + n: r = 8 (j & 1) + n, i = j >> 1
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-      vc |= (unsigned)(row[(8 * (j & 1) + n) * (U / 2) + (j >> 3)] >> (4 * (j >> 1 & 3)) & 15) << (4 * n);
-  }
   const size_t at = ((size_t)token * a.kv_heads + head) * D + 8 * j;
-  *reinterpret_cast<u32x4*>(a.ko + at) = values8<BF>(kc, kp);
-  *reinterpret_cast<u32x4*>(a.vo + at) = values8<BF>(vc, vp);
+  __builtin_nontemporal_store(values8<BF>(kc, kp), reinterpret_cast<u32x4*>(a.ko + at));
+  __builtin_nontemporal_store(values8<BF>(vc, vp), reinterpret_cast<u32x4*>(a.vo + at));
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -248,14 +278,15 @@ qgemm_status_t enqueue(const qgemm_cache_t* c, bool write, CacheArgs& a, const i
   a.tokens = (int)tokens;
   a.kv_heads = c->kv_heads;
   a.page = c->page_size;
+  a.per_page = 1.0 / c->page_size;
   a.codes = g.codes;
   a.params = g.params;
   a.block = g.bytes;
   const int rows = 512 / c->head_dim;
-  const int64_t units = (tokens + rows - 1) / rows * c->kv_heads;
-  if (units > 0x7ffffff0LL)
-    return fail(QGEMM_ERR_UNSUPPORTED, "tokens * kv_heads needs %lld wavefronts, more than one launch allows", (long long)units);
-  const dim3 grid((unsigned)((units + 3) / 4));
+  const int64_t groups = (tokens + 4 * rows - 1) / (4 * rows) * c->kv_heads;
+  if (groups > 0x7fffffffLL)
+    return fail(QGEMM_ERR_UNSUPPORTED, "tokens * kv_heads needs %lld workgroups, more than one launch allows", (long long)groups);
+  const dim3 grid((unsigned)groups);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int ng = c->head_dim / c->group_size;
   if (c->dtype == QGEMM_DT_BF16) launch_type<true>(c->head_dim, ng, write, grid, s, a);
