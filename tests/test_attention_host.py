@@ -285,3 +285,43 @@ def test_oracle_norm_rope_by_hand():
     assert np.allclose(y, [[[-0.0, 4.0, 3.0, 0.0]]])               # pairs (0, 2), (1, 3)
     y, _ = oa.norm_rope(x, None, np.array([-1]), table, 4, True, False)
     assert np.allclose(y, [[[-4.0, 3.0, 0.0, 0.0]]])               # pairs (0, 1), (2, 3)
+
+
+# ----------------------------------------------------------------------------- the compiled calls
+def test_calls_refuse_what_is_no_descriptor():
+    import torch
+    x = torch.zeros(2, 2, 128, dtype=torch.float16)
+    s = torch.zeros(2, dtype=torch.int64)
+    for bad in (q.norm_rope_problem(2, 2, 2, 128), None, 3):
+        with pytest.raises(TypeError):
+            q.cache_write(bad, x, x, x, s)
+    with pytest.raises(TypeError, match="32 bytes"):
+        q.cache_read(q.Problem(), x, s, x, x)
+    with pytest.raises(TypeError):
+        q._calls.attention(1, 2)
+    with pytest.raises(AttributeError):
+        q.cache_write(q.cache(1, 16, 2, 128), x, [1.0], x, s)
+
+
+def test_calls_hold_no_references():
+    # refused and passed checks alike leave the reference counts as they were
+    import sys
+
+    import torch
+    x, flat = torch.zeros(2, 2, 128, dtype=torch.float16), torch.zeros(2, 256, dtype=torch.float16)
+    c, s = q.cache(1, 16, 2, 128), torch.zeros(2, dtype=torch.int64)
+    data, short = q.alloc_cache(c, "cpu"), torch.zeros(5, dtype=torch.uint8)
+    held = (x, flat, c, s, data, short, torch.float16, torch.uint8)
+
+    def calls():
+        for args in ((short, x, flat, s), (data, x[:1], x, s), (data, x.float(), x, s), (data, x, flat, s.int())):
+            with pytest.raises(ValueError):
+                q.cache_write(c, *args)
+        with pytest.raises(TypeError):                                 # past the tensors' checks
+            q.cache_write(c, data, x, flat, s, stream="none")
+
+    calls()
+    before = [sys.getrefcount(o) for o in held]
+    for _ in range(50):
+        calls()
+    assert all(abs(sys.getrefcount(o) - b) < 10 for o, b in zip(held, before))

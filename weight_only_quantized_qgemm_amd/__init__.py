@@ -30,6 +30,11 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python -m weight_only_quantized_qgemm_amd._build` (hipcc, gfx950)")
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _calls
+except ImportError as e:
+    raise ImportError("the _calls module is missing or of another Python: build it with "
+                      "`python -m weight_only_quantized_qgemm_amd._build`") from e
 
 # ----------------------------------------------------------------------------- enums
 OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE_TOO_SMALL, ERR_HIP = range(6)
@@ -286,46 +291,20 @@ def version():
 
 
 # ----------------------------------------------------------------------------- attention operators
-# The calls below are made once per layer and token, so their checks read each tensor property once.
-_T16 = {DT_F16: torch.float16, DT_BF16: torch.bfloat16}
-# the raw stream handle, without building a Stream object for it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
+# The device calls below are made once per layer and token: their tensors are checked, and the C function
+# called, in csrc/qgemm_calls.cpp.  A tensor of the wrong type, shape or strides raises ValueError.
 def _stream(stream, x):
-    """The handle of `stream`; by default that of torch's current stream on x's device."""
+    """The handle of `stream`; by default that of torch's current stream."""
     if stream is None:
-        if _raw_stream is not None and x.is_cuda:
-            return _raw_stream(x.get_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _rows(x, name, tokens, heads, dim, t16):
-    """Address and token stride of a [tokens, heads, dim] (or [tokens, heads * dim]) tensor whose heads lie
-    side by side."""
-    if x is None:
-        return None, 0
-    shape, stride = x.shape, x.stride()
-    if len(shape) == 3:
-        ok = shape == (tokens, heads, dim) and stride[2] == 1 and (stride[1] == dim or heads < 2)
-    else:
-        ok = shape == (tokens, heads * dim) and stride[1] == 1
-    if not ok or x.dtype is not t16:
-        raise ValueError(f"{name} must be {t16} [{tokens}, {heads}, {dim}] with contiguous heads, got {x.dtype} "
-                         f"{tuple(shape)} with strides {stride}")
-    # a single token has no distance to the next; torch may report any stride for it
-    return x.data_ptr(), stride[0] if tokens > 1 else heads * dim
-
-
-def _array(x, name, dtype, numel):
-    """Address of a contiguous array of at least `numel` elements."""
-    if x is None:
-        return None
-    if x.dtype is not dtype or x.numel() < numel or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements, got "
-                         f"{x.dtype} {tuple(x.shape)} with strides {x.stride()}")
-    return x.data_ptr()
+_calls.setup(*(ctypes.cast(f, _vp).value for f in (_lib.qgemm_qk_norm_rope, _lib.qgemm_cache_write, _lib.qgemm_cache_read,
+                                                   _lib.qgemm_attention)),
+             torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+             # the raw stream handle of a device, without building a Stream object for it
+             getattr(torch._C, "_cuda_getCurrentRawStream", None), _stream)
 
 
 def norm_rope_problem(tokens, q_heads, kv_heads, head_dim, dtype=DT_F16, rot_dim=None, max_pos=0, interleaved=False,
@@ -338,17 +317,7 @@ def norm_rope_problem(tokens, q_heads, kv_heads, head_dim, dtype=DT_F16, rot_dim
 def qk_norm_rope(p, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, stream=None):
     """Enqueue the norm and rotation of the heads of q and k (qgemm_qk_norm_rope).  The tensors are
     [tokens, heads, head_dim], each with its own token stride; outputs may be the inputs."""
-    t16, dim, tokens, qh, kh = _T16.get(p.dtype), p.head_dim, p.tokens, p.q_heads, p.kv_heads
-    qp, qs = _rows(q, "q", tokens, qh, dim, t16)
-    kp, ks = _rows(k, "k", tokens, kh, dim, t16)
-    qo, qos = _rows(q_out, "q_out", tokens, qh, dim, t16)
-    ko, kos = _rows(k_out, "k_out", tokens, kh, dim, t16)
-    rot = p.rot_dim
-    pos = _array(positions, "positions", torch.int32, tokens) if rot else None
-    tab = _array(cos_sin, "cos_sin", torch.float32, p.max_pos * rot) if rot else None
-    st = _lib.qgemm_qk_norm_rope(ctypes.byref(p), qp, qs, kp, ks, _array(q_weight, "q_weight", t16, dim),
-                                 _array(k_weight, "k_weight", t16, dim), pos, tab, qo, qos, ko, kos,
-                                 _stream(stream, k if q is None else q))
+    st = _calls.qk_norm_rope(p, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, stream)
     if st:
         _check(st)
 
@@ -364,13 +333,6 @@ def cache_bytes(c):
     return n.value
 
 
-def _cache_data(c, data):
-    """Address of a cache buffer of at least qgemm_cache_bytes' size (computed here: no second call)."""
-    dim, group = c.head_dim, c.group_size
-    return _array(data, "data", torch.uint8,
-                  c.num_pages * c.kv_heads * c.page_size * (dim + 8 * (dim // group if group > 0 else 0)))
-
-
 def alloc_cache(c, device="cuda"):
     """A zero-filled cache buffer (every slot reads as zeros)."""
     return torch.zeros(cache_bytes(c), dtype=torch.uint8, device=device)
@@ -378,21 +340,14 @@ def alloc_cache(c, device="cuda"):
 
 def cache_write(c, data, k, v, slots, stream=None):
     """Enqueue the quantization of k, v [tokens, kv_heads, head_dim] into the int64 slots."""
-    n, t16, heads, dim = slots.numel(), _T16.get(c.dtype), c.kv_heads, c.head_dim
-    kp, ks = _rows(k, "k", n, heads, dim, t16)
-    vp, vs = _rows(v, "v", n, heads, dim, t16)
-    st = _lib.qgemm_cache_write(ctypes.byref(c), _cache_data(c, data), kp, ks, vp, vs,
-                                _array(slots, "slots", torch.int64, n), n, _stream(stream, data))
+    st = _calls.cache_write(c, data, k, v, slots, stream)
     if st:
         _check(st)
 
 
 def cache_read(c, data, slots, k_out, v_out, stream=None):
     """Enqueue the values of the slots into k_out, v_out [tokens, kv_heads, head_dim], contiguous."""
-    n, t16 = slots.numel(), _T16.get(c.dtype)
-    size = n * c.kv_heads * c.head_dim
-    st = _lib.qgemm_cache_read(ctypes.byref(c), _cache_data(c, data), _array(slots, "slots", torch.int64, n), n,
-                               _array(k_out, "k_out", t16, size), _array(v_out, "v_out", t16, size), _stream(stream, data))
+    st = _calls.cache_read(c, data, slots, k_out, v_out, stream)
     if st:
         _check(st)
 
@@ -425,15 +380,6 @@ def attention_describe(p):
 
 def attention(p, q, data, page_table, seq_lens, q_start, out, workspace=None, stream=None):
     """Enqueue attention of q [total_q, q_heads, head_dim] over the cache into out (qgemm_attention)."""
-    c, total, heads = p.cache, p.total_q, p.q_heads
-    dim, batch, t16 = c.head_dim, p.batch, _T16.get(c.dtype)
-    qp, qs = _rows(q, "q", total, heads, dim, t16)
-    op, os_ = _rows(out, "out", total, heads, dim, t16)
-    st = _lib.qgemm_attention(ctypes.byref(p), qp, qs, _cache_data(c, data),
-                              _array(page_table, "page_table", torch.int32, batch * p.max_pages),
-                              _array(seq_lens, "seq_lens", torch.int32, batch),
-                              _array(q_start, "q_start", torch.int32, batch + 1), op, os_,
-                              None if workspace is None else workspace.data_ptr(),
-                              0 if workspace is None else workspace.nbytes, _stream(stream, q))
+    st = _calls.attention(p, q, data, page_table, seq_lens, q_start, out, workspace, stream)
     if st:
         _check(st)

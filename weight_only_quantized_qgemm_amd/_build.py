@@ -6,6 +6,7 @@ build of the host code (_build_asan.py) finds the kernel objects it links agains
 """
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +17,8 @@ OBJ_DIR = os.path.join(PKG, "_build", "obj")
 # measurement helpers for the benchmark (streaming-read kernel, host time per call): a library
 # of their own, outside the qgemm ABI
 PROBE_LIB = os.path.join(PKG, "libqgemm_probe.so")
+# Python entry points of the attention operators' device calls: host code, linked with neither of them
+CALLS_LIB = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 # Weight formats (the Format enum of csrc/qgemm_internal.h).  Each kernel source is compiled
 # once per format (-DQGEMM_FMT_UNIT), so the many kernel instances build in parallel.
 N_FORMATS = 6
@@ -51,6 +54,17 @@ def _run(cmd):
     # the host pass does not know the gfx-only target feature; that warning is noise
     lines = [l for l in (res.stdout + res.stderr).splitlines() if "packed-fp32-ops" not in l and l.strip()]
     return res.returncode, lines
+
+
+def build_calls():
+    """Compile the Python module of the attention operators' calls; returns the compiler's messages."""
+    tmp = CALLS_LIB + ".tmp"
+    rc, lines = _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+                      "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "qgemm_calls.cpp"), "-o", tmp])
+    if rc != 0:
+        raise RuntimeError("compiling qgemm_calls.cpp failed:\n" + "\n".join(lines))
+    os.replace(tmp, CALLS_LIB)
+    return lines
 
 
 def build(verbose=False):
@@ -89,6 +103,7 @@ def build(verbose=False):
         raise RuntimeError("link failed (probe library):\n" + "\n".join(lines))
     msgs += lines
     os.replace(ptmp, PROBE_LIB)
+    msgs += build_calls()
     if verbose and msgs:
         print("\n".join(msgs))
     return LIB
