@@ -241,3 +241,33 @@ def test_cache_codes_for_every_scale(q, kind):
                 assert np.array_equal(got[page, h, :par], want[:par]), (size, page, h)
                 assert np.array_equal(*(oa.from_bits16(b[par:].copy().view(np.uint16), kind) for b in (got[page, h], want)))
             at += m
+
+
+@pytest.mark.parametrize("hint", [1, 2])
+@pytest.mark.parametrize("kind,dim,group,apart", [("bf16", 128, 32, 7), ("bf16", 256, 64, 6), ("bf16", 64, 32, 20), ("f16", 128, 32, 3)])
+def test_key_groups_of_different_size(q, kind, dim, group, apart, hint):
+    # each group of keys 2^apart smaller than the one before, the queries as much larger there: every
+    # group weighs the same in the scores
+    say(f"case attention key groups apart {kind} D={dim} G={group} by 2^{apart} hint={hint}")
+    s = _sequences(q, kind, [40, 1], [150, 70], 4, 2, dim, group, 16, 206)
+    ng = dim // group
+    step = 2.0 ** (-apart * np.arange(ng))
+    for b, k in enumerate(s["klens"]):
+        (kc, ks, kz), v = s["seqs"][b]
+        s["seqs"][b] = [(kc, ks * step, kz * step), v]                # powers of two: values of the type
+        assert np.array_equal(oa.round16(ks * step, kind), ks * step) or kind == "f16"
+    # the same in the cache: the parameters' exponents
+    page, hk = 16, 2
+    u8 = s["data"].cpu().numpy().reshape(-1, hk, oa.block_bytes(page, dim, group))
+    par = u8[:, :, page * dim:page * dim + page * ng * 4].copy().view(np.uint16).reshape(-1, hk, ng, page, 2)
+    value = oa.from_bits16(par, kind) * step[:, None, None]
+    bits = np.where(np.isnan(value), par, oa.bits16(np.nan_to_num(value), kind))
+    u8[:, :, page * dim:page * dim + page * ng * 4] = bits.astype(np.uint16).reshape(*u8.shape[:2], -1).view(np.uint8)
+    if kind == "f16":                                                 # fp16 rounds the smallest of them
+        for b in range(2):
+            (kc, ks, kz), v = s["seqs"][b]
+            s["seqs"][b] = [(kc, oa.round16(ks, kind), oa.round16(kz, kind)), v]
+    s["data"] = torch.from_numpy(u8.reshape(-1)).cuda()
+    s["q"] = oa.round16(s["q"] * np.repeat(1 / step, group) * step[-1], kind)
+    scale = float(np.float32(dim ** -0.5 / step[-1]))
+    _check(s, _run(q, s, kind, 4, scale=scale, hint=hint), kind, 4, True, 0, scale)

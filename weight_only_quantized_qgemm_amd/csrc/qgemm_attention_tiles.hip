@@ -30,16 +30,26 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   constexpr int U = D / 32, TILES = D / 16, TG = TILES / NG, SG = U / NG;
   constexpr int BM = 16 * NC * NW, NT = 64 * NW;
   constexpr int kHalves = D == 256 ? 1 : 2, kStep = 32 * kHalves;  // 32-token halves and tokens of a step
+  // One body for both halves where two would spill registers (fp16, D 128 in two groups: a prompt of 4096
+  // 300 -> 275 us; elsewhere two are better, D 128 in one group 184 against 205).
+  constexpr int kBodies = !BF && D == 128 && NG == 2 ? 1 : kHalves;
   constexpr int SUBS = 2 * kHalves;                 // 16-token subtiles of a step
   constexpr int KB = kStep * D * 2, PB = SUBS * NG * 4 * 16 * 4;   // bytes of K (and of V) operands, of parameters
   constexpr int kSlot = BM * D + NC * NT * 4;       // floats of a partial
   // bf16: fp16 operands hold the values themselves, a power of two per token apart; fp16: the codes
   constexpr bool kDeq = BF;
+  // and in several groups K's operands hold (code - 8) * scale, a power of two per token apart: a 3-bit times
+  // an 8-bit number fits fp16's 11 bits (down to scales of 2^-25 of the token's largest), so one accumulator
+  // serves all groups and twice the rows fit the registers (a prompt of 4096, D 128: four groups 388 -> 234
+  // us, D 256: 447 -> 278)
+  constexpr bool kDeqK = kDeq && NG > 1;
+  constexpr int AG = kDeqK ? 1 : NG;                // accumulators of a score
   __shared__ __align__(16) uint8_t s_k[2][KB], s_v[3][KB];
   // [subtile][group][K scale, K zero, V scale, V middle][16]; kDeq: one V scale per token, in group 0, and
   // in the place of the middle 0, or NaN where the group's parameters are not finite
   __shared__ __align__(16) float s_p[4][PB / 4];
   __shared__ __align__(16) unsigned s_w[2][kDeq ? SUBS * NG * 16 : 4];       // kDeq: V scale, zero as fp16
+  __shared__ unsigned s_kw[2][kDeqK ? SUBS * NG * 16 : 4];                   // kDeqK: K scale as fp16, twice
   __shared__ __align__(16) unsigned s_big[4][4];    // per subtile: the largest finite |V scale|, as its bits
   __shared__ int s_odd[4];                          // any V parameter that is not finite
   __shared__ float s_top[NW];
@@ -148,8 +158,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   auto store = [&](int step) {
     const int kb = step & 1, vb = step % 3;
 #pragma unroll
-    for (int i = 0; i < KP; ++i)
-      *reinterpret_cast<u32x4*>(&s_k[kb][((fsub * U + part * KP + i) * 64 + lane) * 16]) = codes8(rk[i]);
+    for (int i = 0; i < KP; ++i) {
+      u32x4 c = codes8(rk[i]);
+      if constexpr (kDeqK) {
+        const f16x2 sc = __builtin_bit_cast(f16x2, s_kw[step & 1][(fsub * NG + (part * KP + i) / SG) * 16 + m]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          c[k] = __builtin_bit_cast(unsigned, __builtin_bit_cast(f16x2, centre(c[k], k & 1)) * sc);
+      }
+      *reinterpret_cast<u32x4*>(&s_k[kb][((fsub * U + part * KP + i) * 64 + lane) * 16]) = c;
+    }
     // pairs of tokens (0, 1) and (2, 3): 16 bits each of the part's nibbles
     constexpr int HW = TP == 8 ? 2 : 1;
     unsigned x[HW], y[HW];
@@ -201,8 +219,30 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       z[gr] = par_zero<BF>(rp[gr]);
     }
     if (!fpv) {
+      if constexpr (kDeqK) {
+        // the token's unit 2^e, at most its largest scale; that scale becomes 2^11 to 2^12
+        unsigned big = 0x00800000u;
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
+        for (int gr = 0; gr < NG; ++gr) {
+          z[gr] = __builtin_fmaf(sc[gr], 8.f, z[gr]);
+          if (!(__builtin_fabsf(z[gr]) < __builtin_inff())) {
+            sc[gr] = 0.f;
+            z[gr] = __builtin_nanf("");
+          }
+          big = max(big, __builtin_bit_cast(unsigned, __builtin_fabsf(sc[gr])));
+        }
+        big &= 0x7f800000u;
+        const float back = __builtin_bit_cast(float, 0x7f000000u - big);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const float w = sc[gr] * back * 2048.f;
+          if (lane < kStep) s_kw[step & 1][((lane >> 4) * NG + gr) * 16 + (lane & 15)] = pack_f16(w, w);
+        }
+        sc[0] = __builtin_bit_cast(float, big) * kq;
+      } else {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) sc[gr] *= kq;
+      }
     } else {
       unsigned big = 0;                             // magnitudes compare as their bits do
       bool odd = false;
@@ -294,7 +334,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = __builtin_fmaxf(top, s_top[w]);
     const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
-    kq = __builtin_ldexpf(a.scale, 24 - 14 + e);
+    kq = __builtin_ldexpf(a.scale, (kDeqK ? -11 : 24) - 14 + e);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -310,7 +350,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int sh = 14 - e - ((k & 1) ? 4 : 0);
+            const int sh = 14 - e - (!kDeqK && (k & 1) ? 4 : 0);
             qf[j][nc][k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
           }
         }
@@ -325,7 +365,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int all_hi = a.causal ? min(s.len, past + first / a.ratio + 1) : s.len;
   const int all_lo = a.window ? past + last / a.ratio - a.window + 1 : 0;
 
-  float mx[NC], l[NC], zs[NC][NG];
+  // zs: the sums of weight times middle; kDeq: which groups of the row have met a NaN
+  constexpr int ZG = kDeq ? 1 : NG;
+  float mx[NC], l[NC], zs[NC][ZG];
+  unsigned bad[NC];
   bool fresh[NC];                                   // the row has seen no token: mx is not set
   f32x4 o[NC][TILES];
   int tau = -64;                                    // O is in units of 2^tau
@@ -333,8 +376,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   for (int nc = 0; nc < NC; ++nc) {
     mx[nc] = l[nc] = 0.f;
     fresh[nc] = true;
+    bad[nc] = 0;
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) zs[nc][gr] = 0.f;
+    for (int gr = 0; gr < ZG; ++gr) zs[nc][gr] = 0.f;
 #pragma unroll
     for (int i = 0; i < TILES; ++i) o[nc][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
@@ -342,7 +386,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   auto par = [&](int step, int pr, int x, int gr, int c) {
     return *reinterpret_cast<const f32x4*>(&s_p[step & 3][(((2 * pr + x) * NG + gr) * 4 + c) * 16 + 4 * g]);
   };
-  typedef f32x4 Acc[2][NG][NC];
+  typedef f32x4 Acc[2][AG][NC];
   // the products of one half's keys with the rows
   auto products = [&](int step, int pr, Acc& acc) {
     const uint8_t* src = s_k[step & 1];
@@ -353,8 +397,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         const u32x4 kf = *reinterpret_cast<const u32x4*>(src + (((2 * pr + x) * U + i) * 64 + lane) * 16);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
-          f32x4& c = acc[x][i / SG][nc];
-          c = mfma(kf, qf[i][nc], i % SG == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : c);
+          constexpr int AS = U / AG;
+          f32x4& c = acc[x][i / AS][nc];
+          c = mfma(kf, qf[i][nc], i % AS == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : c);
         }
       }
   };
@@ -364,13 +409,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        const f32x4 sc = par(step, pr, x, gr, 0), z = par(step, pr, x, gr, 1);
+        const f32x4 sc = par(step, pr, x, kDeqK ? 0 : gr, 0), z = par(step, pr, x, gr, 1);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float v = __builtin_fmaf(z[r], qz[nc][gr], gr ? u[nc][x][r] : -mx[nc]);
-            u[nc][x][r] = __builtin_fmaf(sc[r], acc[x][gr][nc][r], v);
+            u[nc][x][r] = kDeqK && gr < NG - 1 ? v : __builtin_fmaf(sc[r], acc[x][kDeqK ? 0 : gr][nc][r], v);
           }
       }
   };
@@ -407,7 +452,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const bool on = !kMask || (seen[nc] >> (4 * x + r) & 1);
-                zs[nc][g2] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][g2]);
+                if constexpr (kDeq) bad[nc] |= on && md[r] != md[r] ? 1u << g2 : 0u;
+                else zs[nc][g2] = __builtin_fmaf(u[nc][x][r], on ? md[r] : 0.f, zs[nc][g2]);
               }
           }
         }
@@ -502,7 +548,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         mx[nc] += by;
         l[nc] *= al;
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) zs[nc][gr] *= al;
+        for (int gr = 0; gr < ZG; ++gr) zs[nc][gr] *= al;
 #pragma unroll
         for (int i = 0; i < TILES; ++i) o[nc][i] *= al;
 #pragma unroll
@@ -552,7 +598,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           if (j + 3 < steps) fetch_par(j + 3);
         }
       }
-#pragma unroll
+#pragma unroll kBodies
       for (int pr = 0; pr < kHalves; ++pr) {
         const bool end = pr == kHalves - 1;
         if (end) __syncthreads();                   // step j + 1's operands are in LDS
@@ -566,16 +612,23 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   for (int nc = 0; nc < NC; ++nc) {
     l[nc] += __shfl_xor(l[nc], 16);
     l[nc] += __shfl_xor(l[nc], 32);
+    if constexpr (kDeq) {
+      bad[nc] |= __shfl_xor(bad[nc], 16);
+      bad[nc] |= __shfl_xor(bad[nc], 32);
+    } else {
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-      zs[nc][gr] += __shfl_xor(zs[nc][gr], 16);
-      zs[nc][gr] += __shfl_xor(zs[nc][gr], 32);
+      for (int gr = 0; gr < NG; ++gr) {
+        zs[nc][gr] += __shfl_xor(zs[nc][gr], 16);
+        zs[nc][gr] += __shfl_xor(zs[nc][gr], 32);
+      }
     }
     const float back = __builtin_ldexpf(1.f, tau);
 #pragma unroll
-    for (int i = 0; i < TILES; ++i)
+    for (int i = 0; i < TILES; ++i) {
+      const float z = !kDeq ? zs[nc][kDeq ? 0 : i / TG] : bad[nc] >> (i / TG) & 1 ? __builtin_nanf("") : 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[nc][i][r] = __builtin_fmaf(o[nc][i][r], back, zs[nc][i / TG]);
+      for (int r = 0; r < 4; ++r) o[nc][i][r] = __builtin_fmaf(o[nc][i][r], back, z);
+    }
   }
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) mx[nc] = fresh[nc] ? kStart : mx[nc];
