@@ -99,6 +99,32 @@ template <int C>
 __device__ __forceinline__ unsigned dpp(unsigned x) {
   return (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, C, 0xf, 0xf, false);
 }
+// Reductions over a wavefront's four rows of 16 lanes, every lane holding the result: a value swapped with
+// itself between odd and even rows (then halves) leaves both partners in every lane, in registers, where an
+// exchange through LDS would wait for its round trip.
+__device__ __forceinline__ float as_float(unsigned x) { return __builtin_bit_cast(float, x); }
+template <class F>
+__device__ __forceinline__ float over_rows(float x, F f) {
+  const unsigned b = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const unsigned c = __builtin_bit_cast(unsigned, f(as_float(r[0]), as_float(r[1])));
+  const auto h = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  return f(as_float(h[0]), as_float(h[1]));
+}
+__device__ __forceinline__ float sum_rows(float x) {
+  return over_rows(x, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float max_rows(float x) {
+  return over_rows(x, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+// The largest value of the wavefront: within rows of 16 lanes by DPP, then over the rows.
+template <int C>
+__device__ __forceinline__ float dpp_max(float x) {
+  return __builtin_fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), C, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return max_rows(dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(x)))));
+}
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // V codes of one 16-token subtile, as loaded (lane r = l & 15, tokens 4 (l >> 4) .. + 3), for tile i:

@@ -199,7 +199,6 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       fetch_v(j, st);
     };
     StepT sa;
-    if (mine) pages(0);
     // ---- queries: column m holds row rt RT + m % RT, row = query * ratio + head within the group
     const int rows = a.ratio * s.n;
     u32x4 qf[U];
@@ -216,7 +215,10 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       u32x4 raw[U];
 #pragma unroll
       for (int j = 0; j < U; ++j) raw[j] = on ? *reinterpret_cast<const u32x4*>(src + 32 * j) : u32x4{0, 0, 0, 0};
-      if (mine) fetch(0, sa);                       // beside the queries' reduction and conversion
+      if (mine) {                                   // the page ids arrive with the queries
+        pages(0);
+        fetch(0, sa);                               // beside the queries' reduction and conversion
+      }
       float top = 0.f;
 #pragma unroll
       for (int j = 0; j < U; ++j)
@@ -227,8 +229,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
             const float x = __builtin_fabsf(from16<BF>(raw[j][e] >> (16 * o) & 0xffffu));
             top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
           }
-#pragma unroll
-      for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+    top = wave_max(top);
       // top = f 2^e, f in [1/2, 1)
       const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
       kq = __builtin_ldexpf(a.scale, 24 - 14 + e);
@@ -249,8 +250,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
             qf[j][k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
           }
         }
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
+        sum = sum_rows(sum);
         qz[gr] = sum * a.scale;
       }
     }
@@ -322,11 +322,8 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       if (__any(high > (fresh ? -3e38f : kSlack) || big * inv > kScaleSlack)) {
         // set or move the running maxima and value scales that need it, rescale what is summed so far
         float top = high, smax = big;
-#pragma unroll
-        for (int x = 16; x < 64; x *= 2) {
-          top = __builtin_fmaxf(top, __shfl_xor(top, x));
-          smax = __builtin_fmaxf(smax, __shfl_xor(smax, x));
-        }
+        top = max_rows(top);
+        smax = max_rows(smax);
         // a row's maximum moves for its own scores only: its result does not depend on its neighbours
         const bool go = top > (fresh ? -3e38f : kSlack);
         const float by = go ? top : 0.f, al = fresh ? 1.f : exp2_fast(-by);
@@ -442,14 +439,11 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
           u32x2{pack2<BF>(v[0] * r, v[1] * r), pack2<BF>(v[2] * r, v[3] * r)};
     };
     const float back = __builtin_ldexpf(1.f, sig);
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+    l = sum_rows(l);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-      zs[gr] += __shfl_xor(zs[gr], 16);
-      ps[gr] += __shfl_xor(ps[gr], 16);
-      zs[gr] += __shfl_xor(zs[gr], 32);
-      ps[gr] += __shfl_xor(ps[gr], 32);
+      zs[gr] = sum_rows(zs[gr]);
+      ps[gr] = sum_rows(ps[gr]);
     }
     __syncthreads();                                // the previous segment is done with LDS
     if (g == 0) {

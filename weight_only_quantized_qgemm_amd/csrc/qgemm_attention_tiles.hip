@@ -327,8 +327,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       fetch(0);
       fetch_par(0);
     }
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+    top = wave_max(top);
     if (lane == 0) s_top[wave] = top;
     __syncthreads();
 #pragma unroll
@@ -354,8 +353,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
             qf[j][nc][k] = pack_f16(__builtin_ldexpf(x[kSlotDim[2 * k]], sh), __builtin_ldexpf(x[kSlotDim[2 * k + 1]], sh));
           }
         }
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
+        sum = sum_rows(sum);
         qz[nc][gr] = sum * a.scale;
       }
   }
@@ -535,11 +533,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
             want = __builtin_fmaxf(want, u[nc][x][r] + __builtin_fmaxf(ls, -(float)kRoomMax));
           }
         }
-#pragma unroll
-        for (int x = 16; x < 64; x *= 2) {
-          top = __builtin_fmaxf(top, __shfl_xor(top, x));
-          want = __builtin_fmaxf(want, __shfl_xor(want, x));
-        }
+        top = max_rows(top);
+        want = max_rows(want);
         // a row's reference moves for its own scores only: its result does not depend on its neighbours
         const bool go = top > (fresh[nc] ? -3e38f : room);
         const float by = go ? (fresh[nc] ? want : __builtin_fmaxf(want, 0.f)) : 0.f;
@@ -610,16 +605,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // ---- results: lane sums, then out, or a partial for the last split to join
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
-    l[nc] += __shfl_xor(l[nc], 16);
-    l[nc] += __shfl_xor(l[nc], 32);
+    l[nc] = sum_rows(l[nc]);
     if constexpr (kDeq) {
       bad[nc] |= __shfl_xor(bad[nc], 16);
       bad[nc] |= __shfl_xor(bad[nc], 32);
     } else {
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        zs[nc][gr] += __shfl_xor(zs[nc][gr], 16);
-        zs[nc][gr] += __shfl_xor(zs[nc][gr], 32);
+        zs[nc][gr] = sum_rows(zs[nc][gr]);
       }
     }
     const float back = __builtin_ldexpf(1.f, tau);
