@@ -142,8 +142,8 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   // D 256 in four groups) and of a row tile (tiles kernel, fp16 and bf16), for D 64, 128, 256 and NG 1, 2, 4,
   // measured at 32 rows and 8008 tokens x 8, and at a prompt of 4096.
   static const double kRowUnit[3][3] = {{0.31, 0.38, 0.38}, {0.40, 0.50, 0.77}, {1.05, 1.05, 0.90}};
-  static const double kTileStep[2][3][3] = {{{2.35, 2.85, 2.85}, {2.95, 4.3, 3.05}, {3.6, 4.85, 8.2}},
-                                            {{2.35, 2.4, 2.4}, {2.9, 3.15, 3.7}, {3.6, 3.9, 4.4}}};
+  static const double kTileStep[2][3][3] = {{{2.35, 2.85, 2.85}, {2.95, 4.05, 3.0}, {3.6, 3.9, 8.3}},
+                                            {{2.35, 2.4, 2.4}, {2.9, 3.15, 3.5}, {3.6, 3.9, 4.4}}};
   const int di = dim == 64 ? 0 : dim == 128 ? 1 : 2, gi = ng == 1 ? 0 : ng == 2 ? 1 : 2;
   const double rows_us = 10.0 + kRowUnit[di][gi] * (double)row_tiles * (double)steps / kCUs;
   const double tiles_us = 8.0 + kTileStep[p->cache.dtype == QGEMM_DT_BF16][di][gi] * best;
