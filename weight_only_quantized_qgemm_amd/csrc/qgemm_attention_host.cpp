@@ -117,10 +117,10 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   const int row_tile = 16 / pl->pack;
   const int64_t row_tiles = tiles_of(row_tile);
   // ---- tiles kernel.  A row tile's tokens are split over workgroups (one is resident per compute unit)
-  // where a model of the launch, in steps of 64 tokens, says that it is shorter: the longest chain, or all
-  // workgroups' steps and overheads spread over the chip plus a quarter of a chain for the uneven end.
-  // (6 chunks in a window of 4096, 64 heads: 679 us in one part, 776 in four; 100 queries after 16000
-  // tokens: 145 us in 32 parts joined by one workgroup, 77 in 16 joined in pairs.)
+  // where a model of the launch, in steps of 64 tokens, says that it is shorter: the longest chain while every
+  // workgroup has a compute unit; past that also all workgroups' steps and overheads spread over the chip
+  // plus a quarter of a chain for the uneven end.  (6 chunks in a window of 4096, 64 heads: 398 us in one
+  // part, 476 in four; 100 queries after 16000 tokens, 32 heads: 740 us in one part, 198 in four, 75 in 16.)
   const TileShape shape = tile_shape(dim, ng, p->cache.dtype == QGEMM_DT_BF16);
   pl->tile = tile_rows(shape);
   const int64_t tiles = tiles_of(pl->tile);
@@ -131,7 +131,7 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
     const double chain = (double)((steps + s - 1) / s), join = 1.2 * levels;
     const double latency = chain + 4.0 + (s > 1 ? 2.0 : 0.0) + join;
     const double spread = (double)tiles * s * (chain + 4.0 + (s > 1 ? 4.5 : 0.0)) / kCUs + chain / 4 + join;
-    const double cost = latency > spread ? latency : spread;
+    const double cost = tiles * s <= kCUs || latency > spread ? latency : spread;
     if (s == 1 || cost < best) {
       pl->splits = s;
       best = cost;
