@@ -325,3 +325,34 @@ def test_calls_hold_no_references():
     for _ in range(50):
         calls()
     assert all(abs(sys.getrefcount(o) - b) < 10 for o, b in zip(held, before))
+
+
+# ----------------------------------------------------------------------------- plans
+@pytest.mark.parametrize("hint", [0, 1, 2])
+@pytest.mark.parametrize("dim,group,dtype", [(64, 32, 0), (128, 128, 0), (128, 32, 1), (256, 64, 0), (256, 256, 1)])
+def test_plans_hold_their_limits(dim, group, dtype, hint):
+    # grids, parts and workspaces over the range of calls: tickets for every workgroup that may join,
+    # partial results for all of them
+    g = np.random.default_rng([9, dim, group, dtype, hint])
+    for _ in range(200):
+        hk = int(g.choice([1, 2, 3, 8, 16]))
+        batch, max_q = int(2 ** g.uniform(0, 9)), int(2 ** g.uniform(0, 13))
+        total = int(g.integers(max_q, batch * max_q + 1))
+        c = q.cache(1 << 20, 16, hk, dim, dtype, group_size=group)
+        p = q.attention_problem(c, batch, total, hk * int(g.choice([1, 2, 5, 8])), max_q, int(2 ** g.uniform(0, 14)),
+                                causal=bool(g.random() < 0.8), kernel_hint=hint)
+        try:
+            kind, *fields = q.attention_describe(p).split()
+        except q.QgemmError as e:                                      # more units than a launch divides: only on request
+            assert hint == 1 and e.status == UNS and "row tiles" in e.detail
+            continue
+        f = {k: int(v) for k, v in (x.split("=") for x in fields)}
+        ws = q.attention_workspace_bytes(p)
+        assert f["groups"] == dim // group and (hint == 0 or kind == ("rows", "tiles")[hint - 1])
+        if kind == "rows":
+            assert f["grid"] in (512, 2048) and ws == 32768 + 2 * f["grid"] * (16 // f["pack"]) * (dim + 4) * 4
+        elif f["splits"] == 1:
+            assert ws == 0
+        else:
+            assert 2 <= f["splits"] <= 32 and f["grid"] <= 8192 and f["grid"] % f["splits"] == 0
+            assert ws == 32768 + f["grid"] * f["rows"] * (dim + 16) * 4

@@ -1,5 +1,6 @@
 // Host side of the attention operators: descriptor validation, cache geometry and launch planning.
 // Nothing in this file touches the GPU.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -126,12 +127,16 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   const int64_t tiles = tiles_of(pl->tile);
   double best = 0.0;
   pl->splits = 1;
+  // the share of the steps that a causal mask leaves: a half where the queries are the whole sequence
+  const double left = p->causal && !p->window ? 1.0 - 0.5 * std::min((double)p->max_q_len, (double)tokens) / (double)tokens : 1.0;
   for (int s = 1, levels = 0; s <= kMaxSplits && (s == 1 || ((int64_t)s * 4 <= steps && tiles * s <= kTickets)); ++s) {
     while ((1 << levels) < s) ++levels;
-    const double chain = (double)((steps + s - 1) / s), join = 1.2 * levels;
-    const double latency = chain + 4.0 + (s > 1 ? 2.0 : 0.0) + join;
-    const double spread = (double)tiles * s * (chain + 4.0 + (s > 1 ? 4.5 : 0.0)) / kCUs + chain / 4 + join;
-    const double cost = tiles * s <= kCUs || latency > spread ? latency : spread;
+    const double chain = (double)((steps + s - 1) / s), join = levels;
+    const double latency = chain + 2.0 + (s > 1 ? 1.0 : 0.0) + join;
+    const double spread = left * (double)tiles * s * (chain + 4.0 + (s > 1 ? 4.5 : 0.0)) / kCUs + chain / 4 + join;
+    // parts that have work, the last of a tile's being short: do they all start at once?
+    const bool at_once = s > 1 && std::min(1.0, left + 0.5 / s) * (double)tiles * s <= kCUs;
+    const double cost = at_once || latency > spread ? latency : spread;
     if (s == 1 || cost < best) {
       pl->splits = s;
       best = cost;

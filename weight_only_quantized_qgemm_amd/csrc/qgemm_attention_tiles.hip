@@ -92,7 +92,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int hi = a.causal ? min(s.len, max(past + (row_end - 1) / a.ratio + 1, 0)) : s.len;
   const int lo = min(a.window ? max(past + row0 / a.ratio - a.window + 1, 0) & ~15 : 0, hi & ~15);
   const int all_steps = (hi - lo + kStep - 1) / kStep;
-  const int per = max(1, (all_steps + a.splits - 1) / a.splits);
+  // Parts are as long as the sequence's longest row tile needs, tiles that see less have fewer (a prompt of
+  // 1500, 32 heads: 83 us with each tile's own length divided, 67; 700 queries after 5000 tokens 150, 128).
+  const int longest = a.window ? min(s.len, a.window + (BM - 1) / a.ratio + 17) : s.len;
+  const int per = max(1, ((longest + kStep - 1) / kStep + a.splits - 1) / a.splits);
   const int active = max(1, (all_steps + per - 1) / per);
   if (split >= active) return;
   const int ts = lo + kStep * per * split, te = min(hi, ts + kStep * per);
