@@ -152,8 +152,9 @@ qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* problem,
  * in slots that no query sees (unwritten pages, the rest of the last page) never reach the output.
  * Scores, the softmax's maximum and sum and the output are accumulated in fp32; the weights that
  * multiply the codes are rounded to fp16 (11 bits); the tiles kernel over a BF16 cache also rounds the
- * values, divided by a power of two per token, to fp16 (three bits more than BF16 holds).  Results are
- * bitwise deterministic.
+ * values, divided by a power of two per token, to fp16 (three bits more than BF16 holds), and holds keys
+ * in several groups exactly while a group's scale is at least 2^-25 of the token's largest.  Results
+ * are bitwise deterministic.
  */
 qgemm_status_t qgemm_attention(const qgemm_attention_t* problem, const void* q, int64_t q_stride, const void* data,
                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_start, void* out,

@@ -1,4 +1,4 @@
-"""Builds the HIP library (libqgemm.so) in-tree for gfx950 with hipcc.
+"""Builds the HIP library (libqgemm.so) in-tree for gfx950 with hipcc, and the Python module _calls with g++.
 
 Each source compiles to its own objects in parallel (the kernel sources once per weight format), then hipcc links the shared library.
 The objects stay in _build/obj next to this file (not committed), where the host-sanitizer

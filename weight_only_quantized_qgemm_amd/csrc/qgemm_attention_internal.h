@@ -41,11 +41,10 @@ constexpr TileShape tile_shape(int dim, int groups, bool bf16) {
 constexpr int tile_rows(TileShape t) { return 16 * t.cols * t.waves; }
 
 // Rows kernel: how short work is cut (see AttnArgs).
-#ifndef QGEMM_PIECES
-#define QGEMM_PIECES 12, 4
-#endif
 struct Pieces { int share, least; };
-constexpr Pieces kPieces{QGEMM_PIECES};
+// One request of 777 / 4000 / 32000 tokens: 10.8 / 11.3 / 17.2 us; least 16 11.5 / 14.2 / 17.4, share 6
+// 10.8 / 11.4 / 20.7.
+constexpr Pieces kPieces{12, 4};
 
 // Launch plan of qgemm_attention, a pure function of the descriptor.
 struct AttnPlan {
