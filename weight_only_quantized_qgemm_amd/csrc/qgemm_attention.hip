@@ -75,7 +75,7 @@ extern "C" qgemm_status_t qgemm_attention(const qgemm_attention_t* p, const void
   a.block = g.bytes;
   a.max_q = p->max_q_len;
   a.causal = p->causal;
-  a.window = p->window;
+  a.window = bounded_window(p->window);
   a.scale = p->scale * 1.4426950408889634f;
   hipStream_t s = static_cast<hipStream_t>(stream);
   a.piece_share = kPieces.share;

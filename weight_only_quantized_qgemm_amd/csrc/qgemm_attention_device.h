@@ -20,6 +20,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "qgemm_attention_geometry.h"
 #include "qgemm_attention_internal.h"
 
 namespace qgemm {
@@ -180,21 +181,9 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 __device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
 
-// Sequence b's geometry from device memory, every value bounded.
-struct Seq {
-  int start, n, len;               // first query row, queries, tokens
-  int lo, hi;                      // tokens any query can see: lo a multiple of 16
-};
+// Sequence b's geometry from device memory.
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
-  Seq s;
-  const int s0 = a.starts[b], s1 = a.starts[b + 1];
-  s.start = min(max(s0, 0), a.total_q);
-  s.n = min(max(min(s1, a.total_q) - s.start, 0), a.max_q);
-  s.len = min(max(a.lens[b], 0), a.max_pages * a.page);
-  s.hi = s.len;
-  s.lo = a.window ? max(s.len - s.n - a.window + 1, 0) & ~15 : 0;
-  if (s.lo > s.hi) s.lo = s.hi & ~15;
-  return s;
+  return seq_of(a.starts[b], a.starts[b + 1], a.lens[b], a.total_q, a.max_q, a.max_pages * a.page, a.window);
 }
 
 // Device-scope (sc1) accesses for partial results: they pass by the XCD's own L2, so a workgroup on

@@ -89,16 +89,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int rows = a.ratio * s.n, row0 = (entry - before) * BM;
   const int past = s.len - s.n;                     // position of query 0
   const int row_end = min(rows, row0 + BM);
-  const int hi = a.causal ? min(s.len, max(past + (row_end - 1) / a.ratio + 1, 0)) : s.len;
-  const int lo = min(a.window ? max(past + row0 / a.ratio - a.window + 1, 0) & ~15 : 0, hi & ~15);
-  const int all_steps = (hi - lo + kStep - 1) / kStep;
-  // Parts are as long as the sequence's longest row tile needs, tiles that see less have fewer (a prompt of
-  // 1500, 32 heads: 83 us with each tile's own length divided, 67; 700 queries after 5000 tokens 150, 128).
-  const int longest = a.window ? min(s.len, a.window + (BM - 1) / a.ratio + 17) : s.len;
-  const int per = max(1, ((longest + kStep - 1) / kStep + a.splits - 1) / a.splits);
-  const int active = max(1, (all_steps + per - 1) / per);
+  const Tile tile = tile_of(s, row0, row_end, BM, a.ratio, a.causal, a.window, kStep, a.splits);
+  const int active = tile.active;
   if (split >= active) return;
-  const int ts = lo + kStep * per * split, te = min(hi, ts + kStep * per);
+  const int ts = tile.lo + kStep * tile.per * split, te = min(tile.hi, ts + kStep * tile.per);
   const int steps = te > ts ? (te - ts + kStep - 1) / kStep : 0;
 
   // ---- filling: wavefront w prepares part w / SUBS of the K and V operands of subtile w % SUBS; two
@@ -644,9 +638,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // part still in registers, adds the first's from the workspace and goes on; the first leaves.  Nobody
   // waits, and a sum of two has the same bits either way round, so the result does not depend on the order.
   if (active > 1) {
-    const int tile = entry * a.kv_heads + kvh;
-    unsigned* tickets = a.tickets + (size_t)tile * a.splits;
-    float* base = a.partials + (size_t)tile * a.splits * kSlot;
+    const size_t parts_at = (size_t)(entry * a.kv_heads + kvh) * a.splits;
+    unsigned* tickets = a.tickets + parts_at;
+    float* base = a.partials + parts_at * kSlot;
     const __amdgpu_buffer_rsrc_t parts = buffer_of(base, a.splits * kSlot * 4);
     for (int i = split, size = 1; size < active; size *= 2, i >>= 1) {
       if ((i ^ 1) * size < active) {                // the node has two children
