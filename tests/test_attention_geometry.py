@@ -7,6 +7,8 @@ import subprocess
 import numpy as np
 import pytest
 
+import weight_only_quantized_qgemm_amd as q
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LARGEST = 2 ** 31 - 1
 
@@ -74,3 +76,41 @@ def test_the_largest_window_is_no_window(geometry):
         assert tile(2048, 2048, 7936, 256, 4, 1, window, 64, 1) == [0, 2048, 32, 1]
         assert tile(200, 100, 0, 256, 1, 1, window, 64, 1) == [0, 100, 2, 1]      # more queries than tokens
         assert seq(0, 200, 100, 200, 200, 1 << 20, window) == [0, 200, 100, 0, 100]
+
+
+def planned(batch, total_q, max_q, q_heads, kv_heads, dim, group, dtype, max_pages, hint):
+    """Rows of a row tile, and the row tiles per kv head that the launch and its workspace are made for."""
+    p = q.attention_problem(q.cache(64, 16, kv_heads, dim, dtype, group_size=group), batch, total_q, q_heads, max_q, max_pages,
+                            kernel_hint=hint)
+    f = dict(x.split("=") for x in q.attention_describe(p).split()[1:])
+    return int(f["rows"]), int(f["grid"]) // kv_heads // int(f["splits"])
+
+
+def test_row_tiles_of_rising_starts_fit_the_launch(geometry):
+    # whatever stands in q_start, as long as it does not decrease: no more row tiles than planned, so none's
+    # tickets or partial results lie past the workspace
+    seq, _ = geometry
+    g = np.random.default_rng(52)
+    for _ in range(1500):
+        batch, max_q = int(2 ** g.uniform(0, 6)), int(2 ** g.uniform(0, 11))
+        total = int(g.integers(max_q, batch * max_q + 1))
+        ratio, kv, dim = int(g.choice([1, 3, 4, 8])), int(g.choice([1, 2, 8])), int(g.choice([64, 128, 256]))
+        rows, tiles = planned(batch, total, max_q, ratio * kv, kv, dim, dim, int(g.integers(0, 2)), int(2 ** g.uniform(0, 10)),
+                              q.ATTENTION_TILES)
+        starts = np.sort(g.integers(-100, total + 100, batch + 1))
+        if g.random() < 0.2:
+            starts[-1] = LARGEST
+        n = [seq(int(a), int(b), 500, total, max_q, 1 << 20, 0)[1] for a, b in zip(starts, starts[1:])]
+        assert min(n) >= 0 and sum(n) <= total and sum(-(-ratio * x // rows) for x in n) <= tiles
+
+
+@pytest.mark.parametrize("starts,total,max_q", [([0, 1000, 0, 1000, 0], 1000, 1000), ([0, 900, 0, 900, 0, 900, 0, 900, 0], 1000, 900)])
+def test_decreasing_starts_are_told(geometry, starts, total, max_q):
+    # such starts count rows more than once, and more row tiles than the launch has: the kernels compute nothing
+    seq, _ = geometry
+    rows, tiles = planned(len(starts) - 1, total, max_q, 32, 8, 128, 128, q.DT_F16, 200, q.ATTENTION_TILES)
+    bounded = [max(min(b, total) - a, 0) for a, b in zip(starts, starts[1:])]
+    assert sum(-(-4 * n // rows) for n in bounded) > tiles
+    assert [seq(a, b, 500, total, max_q, 1 << 20, 0)[1] for a, b in zip(starts, starts[1:])] == \
+        [n if b >= a else -1 for n, a, b in zip(bounded, starts, starts[1:])]
+    assert seq(LARGEST, -LARGEST, 5, total, max_q, 1 << 20, 0)[1] == -1

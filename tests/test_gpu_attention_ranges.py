@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from gpu_cases import say
-from test_gpu_attention import _check, _run, _sequences
+from test_gpu_attention import _check, _run, _sequences, up
 from test_gpu_attention_plans import scale_of
 
 torch = pytest.importorskip("torch")
@@ -33,3 +33,30 @@ def test_windows_wider_than_any_context(q, case, hint):
     outs = [_run(q, s, kind, hq, True, w, hint=hint) for w in (2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30)]
     _check(s, outs[0], kind, hq, True, 0, scale_of(dim))
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("hint,total,ratio", [(1, 300, 4), (2, 300, 4), (1, 3, 2), (0, 1000, 4)])
+def test_decreasing_starts_write_nothing(q, hint, total, ratio):
+    # q_start that decreases somewhere: no output, no byte behind the workspace, and the workspace is ready
+    # for the next call
+    say(f"case attention decreasing starts hint={hint} total={total}")
+    s = _sequences(q, "f16", [total, 0, 0, 0], [1200, 0, 0, 0], 2 * ratio, 2, 64, 64, 16, 410)
+    s["table"] = s["table"][:1].repeat(4, 1)
+    s["lens"].fill_(1200)
+    p = q.attention_problem(s["c"], 4, total, 2 * ratio, total, s["max_pages"], kernel_hint=hint)
+    n = q.attention_workspace_bytes(p)
+    if total > 3 and hint == 2:
+        assert "splits=1" not in q.attention_describe(p).split()
+    guarded = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    guarded[n:] = 0x5A
+    qx = up(s["q"], "f16")
+    good = torch.full_like(qx, 7.0)
+    rising = torch.tensor([0, total, total, total, total], dtype=torch.int32, device="cuda")
+    q.attention(p, qx, s["data"], s["table"], s["lens"], rising, good, q.alloc_attention_workspace(p))
+    for starts in ([0, total, 0, total, 0], [0, total, 0, total, total], [total, 0, total, total, total], [5, 4, 4, 4, 4]):
+        out = torch.full_like(qx, 7.0)
+        q.attention(p, qx, s["data"], s["table"], s["lens"], torch.tensor(starts, dtype=torch.int32, device="cuda"), out, guarded[:n])
+        torch.cuda.synchronize()
+        assert (out == 7).all() and (guarded[n:] == 0x5A).all(), starts
+        q.attention(p, qx, s["data"], s["table"], s["lens"], rising, out, guarded[:n])
+        assert torch.equal(out, good), starts

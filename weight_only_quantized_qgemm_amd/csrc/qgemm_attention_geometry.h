@@ -18,14 +18,16 @@ constexpr int bounded_window(int window) { return lesser(window, kWindowMost); }
 
 // A sequence's geometry, every value bounded.
 struct Seq {
-  int start, n, len;               // first query row, queries, tokens
+  int start, n, len;               // first query row, queries (or -1), tokens
   int lo, hi;                      // tokens any query can see: lo a multiple of 16
 };
-// From q_start[b], q_start[b + 1] and seq_lens[b]; tokens = max_pages * page_size.
+// From q_start[b], q_start[b + 1] and seq_lens[b]; tokens = max_pages * page_size.  n is -1 where q_start decreases:
+// the rows of such starts may be counted more than once, and launches and workspaces are made for total_q of
+// them.  Of starts that never decrease the bounded ranges do not overlap.
 constexpr Seq seq_of(int s0, int s1, int len, int total_q, int max_q, int tokens, int window) {
   Seq s{};
   s.start = lesser(greater(s0, 0), total_q);
-  s.n = lesser(greater(lesser(s1, total_q) - s.start, 0), max_q);
+  s.n = s1 < s0 ? -1 : lesser(greater(lesser(s1, total_q) - s.start, 0), max_q);
   s.len = lesser(greater(len, 0), tokens);
   s.hi = s.len;
   s.lo = window ? greater(s.len - s.n - window + 1, 0) & ~15 : 0;

@@ -66,10 +66,18 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
   const int split = rest % a.splits;
   int entry = rest / a.splits;
-  auto tiles_in = [&](int b) { return b < a.batch ? (a.ratio * load_seq(a, b).n + BM - 1) / BM : 0; };
+  auto tiles_in = [&](int b) {
+    const int n = b < a.batch ? load_seq(a, b).n : 0;
+    return n < 0 ? -1 : (a.ratio * n + BM - 1) / BM;
+  };
   int total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) total += wave_sum(tiles_in(b0 + lane));
-  if (entry >= total) return;
+  bool down = false;                                // starts that decrease: nothing is computed
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const int tiles = tiles_in(b0 + lane);
+    down |= __any(tiles < 0);
+    total += wave_sum(tiles);
+  }
+  if (down || entry >= total) return;
   entry = total - 1 - entry;
   int b = 0, before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
