@@ -154,3 +154,27 @@ def attention_bound(q, w, out, ks, kz, vs, vz, kmax, group, scale, kind):
     spread = w @ vmax + np.abs(out)
     bound += 2 * np.max(np.where(w > 0, ds, 0), axis=1, keepdims=True, initial=0) * spread
     return bound + (kmax + 64) * 2.0 ** -24 * (w @ vmax)
+
+
+def attention_weight_bound(q, w, out, ks, kz, vs, vz, group, scale, kind, floor, values16=False):
+    """As attention_bound, with the weights' own range and the sums' real length.
+
+    A token's weight times a group's scale, p, multiplies a code no further than 8 from the middle; it is
+    rounded to 11 bits (half a unit: 2^-12 p), or, where it is far below the group's largest in the row, to
+    `floor` of that one, or lost.  values16: the weight multiplies the whole value, itself rounded to 11 bits.
+    A result is the sum of at most one rounding for eight tokens (32 enter a product at once, whose own
+    sum rounds up to four times) and 64 at the joins."""
+    n, D = q.shape
+    ng = D // group
+    vmax = np.repeat(15 * np.abs(vs) + np.abs(vz), group, -1)                          # [len, D]
+    size = 15 * np.abs(vs) + np.abs(vz) if values16 else 8 * np.abs(vs)                # [len, NG]
+    low = np.zeros((n, ng))
+    for i in range(n):
+        p = w[i][:, None] * size
+        low[i] = (2.0 ** -12 * (2 if values16 else 1) * p + np.minimum(p, floor * p.max(0, initial=0.0))).sum(0)
+    bound = UNIT[kind] * np.abs(out) + (2.0 ** -25 if kind == "f16" else 0.0) + np.repeat(low, group, -1)
+    amount = np.abs(q) @ np.repeat(15 * np.abs(ks) + np.abs(kz), group, -1).T * abs(scale)   # [n, len]
+    ds = (D + 16) * 2.0 ** -24 * amount + 2.0 ** -21
+    spread = w @ vmax + np.abs(out)
+    bound += 2 * np.max(np.where(w > 0, ds, 0), axis=1, keepdims=True, initial=0) * spread
+    return bound + (w.shape[1] / 8 + 64) * 2.0 ** -24 * (w @ vmax)

@@ -1,0 +1,154 @@
+"""Attention where numbers of very different size meet, against the 64-bit oracle and a bound that allows
+the formats' own rounding only: a dominating token over a long context, value groups and query heads of different
+magnitude, a huge scale of negligible weight, scores and values at the end of the type's range."""
+import numpy as np
+import pytest
+
+from gpu_cases import say
+from oracle import attention as oa
+from test_gpu_attention import T16, _run, down, dt, up
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# what is kept of a weight far below the largest of its group: fp16's 2^-25 against a largest that stands at 2^6 at
+# least, and in the tiles kernel, where the groups of a row share a reference, two bits less
+FLOOR = {1: 2.0 ** -31, 2: 2.0 ** -29}
+
+
+@pytest.fixture(scope="module")
+def q():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import weight_only_quantized_qgemm_amd as lib
+    return lib
+
+
+def store(q, kind, k, v, qx, group, page=64):
+    """One sequence: k, v [kv_heads, tokens, D] and queries [n, q_heads, D], values of the type."""
+    hk, n, dim = k.shape
+    pages = -(-n // page)
+    c = q.cache(pages, page, hk, dim, dt(q, kind), group_size=group)
+    data = q.alloc_cache(c)
+    q.cache_write(c, data, up(k.swapaxes(0, 1), kind), up(v.swapaxes(0, 1), kind), torch.arange(n, device="cuda"))
+    return dict(c=c, data=data, table=torch.arange(pages, dtype=torch.int32, device="cuda")[None], q=qx,
+                parts=[oa.quantize(x, group, kind) for x in (k, v)], group=group, max_pages=pages, qlens=[len(qx)], klens=[n],
+                lens=torch.tensor([n], dtype=torch.int32, device="cuda"),
+                starts=torch.tensor([0, len(qx)], dtype=torch.int32, device="cuda"))
+
+
+def check(s, out, kind, hint, scale):
+    got, group, worst = down(out), s["group"], 0.0
+    ratio = s["q"].shape[1] // s["c"].kv_heads
+    for h in range(s["q"].shape[1]):
+        (kc, ks, kz), (vc, vs, vz) = [[a[h // ratio] for a in part] for part in s["parts"]]
+        want, w = oa.attention(s["q"][:, h], oa.dequantize(kc, ks, kz, group), oa.dequantize(vc, vs, vz, group), s["klens"][0],
+                               True, 0, scale)
+        bound = oa.attention_weight_bound(s["q"][:, h], w, want, ks, kz, vs, vz, group, scale, kind, FLOOR[hint],
+                                          hint == 2 and kind == "bf16")
+        off = np.abs(got[:, h] - want)
+        assert np.isfinite(want).all() and np.isfinite(off).all()
+        worst = max(worst, float(np.max(off / np.maximum(bound, 1e-300))))
+        say(f"  head {h}: largest error / bound {float(np.max(off / np.maximum(bound, 1e-300))):.3f}")
+    assert worst <= 1, worst
+
+
+KINDS = pytest.mark.parametrize("kind", ["f16", "bf16"])
+
+
+@pytest.mark.parametrize("hint", [1])
+@KINDS
+@pytest.mark.parametrize("below,sink", [(17.5, 1.0), (16.0, 0.0), (17.5, 0.0)])
+def test_a_dominating_token_over_a_long_context(q, kind, below, sink, hint):
+    # 131072 tokens, all but one e^-below of the largest: together they still count
+    say(f"case attention dominating token {kind} hint={hint} e^-{below} value {sink}")
+    g = np.random.default_rng([60, hint])
+    n, dim, rows = 131072, 64, 1 if hint == 1 else 33
+    k, v = np.zeros((1, n, dim)), np.empty((1, n, dim))
+    k[0] = oa.round16(0.002 * g.standard_normal((n, 1)), kind)
+    v[0] = np.linspace(-1, 1, dim) + 0.2 * g.standard_normal((n, dim)) - 0.3
+    k[0, 100], v[0, 100] = 2.0, sink * v[0, 100]
+    qx = np.full((rows, 1, dim), 1.0)
+    s = store(q, kind, k, oa.round16(v, kind), qx, dim, 256)
+    scale = float(np.float32(below / (2 * dim)))
+    check(s, _run(q, s, kind, 1, scale=scale, hint=hint), kind, hint, scale)
+
+
+@pytest.mark.parametrize("hint", [1])
+@KINDS
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 128)])
+@pytest.mark.parametrize("at", [0, 20, 59])
+def test_a_dominating_token_without_a_value(q, kind, dim, group, at, hint):
+    # the largest score by far belongs to a token whose value is 0: the others make the result
+    say(f"case attention dominating zero value {kind} D={dim} G={group} at {at} hint={hint}")
+    g = np.random.default_rng([66, dim, group])
+    n = 60
+    k, v = oa.round16(0.1 * g.standard_normal((1, n, dim)), kind), 1000 * g.standard_normal((1, n, dim))
+    k[0, at], v[0, at] = 20.0 / dim, 0.0
+    s = store(q, kind, oa.round16(k, kind), oa.round16(v, kind), np.full((1, 2, dim), 1.0), group, 16)
+    check(s, _run(q, s, kind, 2, scale=1.0, hint=hint), kind, hint, 1.0)
+
+
+@pytest.mark.parametrize("hint", [1])
+@KINDS
+@pytest.mark.parametrize("below", [16.0, 17.5, 18.5])
+def test_a_dominating_token_in_every_row_tile(q, kind, below, hint):
+    # row tiles so many that each walks its context in one part: one token is e^below times the rest, whose sum
+    # stands in the dims where its value is 0
+    say(f"case attention dominating token, one part {kind} hint={hint} e^-{below}")
+    g = np.random.default_rng([67])
+    n, dim, hk, rows = 4096, 64, 128, 129 if hint == 2 else 1
+    odd = np.arange(dim) % 2
+    k, v = np.zeros((hk, n, dim)), np.empty((hk, n, dim))
+    v[:] = 2.0 * odd + 0.1 * g.standard_normal((1, n, dim))
+    k[:, 5], v[:, 5] = 2.0, 1.0 - odd
+    s = store(q, kind, k, oa.round16(v, kind), np.full((rows, 2 * hk, dim), 1.0), dim, 64)
+    p = q.attention_problem(s["c"], 1, rows, 2 * hk, rows, s["max_pages"], kernel_hint=hint)
+    assert hint == 1 or q.attention_describe(p).endswith("splits=1")
+    scale = float(np.float32(below / (2 * dim)))
+    out = _run(q, s, kind, 2 * hk, scale=scale, hint=hint)
+    one = dict(s, q=s["q"][:, :2], parts=[[a[:1] for a in part] for part in s["parts"]], c=q.cache(n // 64, 64, 1, dim, dt(q, kind)))
+    check(one, out[:, :2], kind, hint, scale)
+
+
+def sizes(kind, ng, order):
+    """A size for each group, 2^20 (fp16) or 2^30 (bf16) between the first and the last."""
+    top, far = (11.0, 20.0) if kind == "f16" else (0.0, 30.0)
+    e = top - np.round(far * np.arange(ng) / (ng - 1))
+    return 2.0 ** (e if order == "falling" else e[::-1])
+
+
+@pytest.mark.parametrize("hint", [1])
+@KINDS
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 64), (128, 32), (256, 128), (256, 64)])
+@pytest.mark.parametrize("order", ["falling", "rising"])
+def test_value_groups_far_apart(q, kind, dim, group, order, hint):
+    say(f"case attention value groups apart {kind} D={dim} G={group} {order} hint={hint}")
+    g = np.random.default_rng([61, dim, group])
+    n, rows = 400, 40
+    k = oa.round16(g.standard_normal((2, n, dim)), kind)
+    v = (g.standard_normal((2, n, dim)) + g.standard_normal(dim)) * np.repeat(sizes(kind, dim // group, order), group)
+    s = store(q, kind, k, oa.round16(v, kind), oa.round16(g.standard_normal((rows, 4, dim)), kind), group, 48)
+    scale = float(np.float32(dim ** -0.5))
+    check(s, _run(q, s, kind, 4, scale=scale, hint=hint), kind, hint, scale)
+
+
+@pytest.mark.parametrize("hint", [1])
+@KINDS
+@pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 32), (256, 64)])
+@pytest.mark.parametrize("at", [0, 70, 399])
+@pytest.mark.parametrize("groups", ["all", "one"])
+def test_a_huge_scale_of_negligible_weight(q, kind, dim, group, at, groups, hint):
+    # one token's values are 2^16 (fp16) or 2^40 (bf16) times the others', its weight e^-60 of theirs
+    say(f"case attention huge value, no weight {kind} D={dim} G={group} at {at} {groups} hint={hint}")
+    g = np.random.default_rng([62, dim, group])
+    n, rows = 400, 40
+    k = oa.round16(0.3 * g.standard_normal((1, n, dim)), kind)
+    v = g.standard_normal((1, n, dim))
+    qx = oa.round16(0.1 * g.standard_normal((rows, 2, dim)) + 1, kind)
+    k[0, at] = -60.0 / dim
+    k = oa.round16(k, kind)
+    v *= 0.125
+    v[0, at, :group if groups == "one" else dim] *= 2.0 ** (16 if kind == "f16" else 40)
+    s = store(q, kind, k, oa.round16(v, kind), qx, group, 16)
+    check(s, _run(q, s, kind, 2, scale=1.0, hint=hint), kind, hint, 1.0)

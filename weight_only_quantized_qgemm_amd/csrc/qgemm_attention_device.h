@@ -54,9 +54,9 @@ struct AttnArgs {
 
 constexpr unsigned kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 constexpr float kStart = -1e30f;   // running maximum before the first token
-// A running maximum is moved when a score exceeds it by this much (in bits); weights stay below
-// 2^kSlack, scaled values below 2^(kSlack + kScaleSlack): inside fp16.
-constexpr float kSlack = 8.0f, kScaleSlack = 64.0f;
+// Rows kernel: a running maximum is moved when a score exceeds it by kSlack (in bits); weights times scales
+// enter the matrix products in units that keep them below kTop, inside fp16.
+constexpr float kSlack = 8.0f, kTop = 0x1p15f;
 
 template <bool BF>
 __device__ __forceinline__ float from16(unsigned bits) {
@@ -126,6 +126,8 @@ __device__ __forceinline__ float dpp_max(float x) {
 __device__ __forceinline__ float wave_max(float x) {
   return max_rows(dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(x)))));
 }
+// The exponent of a power of two within the normal range.
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__builtin_bit_cast(unsigned, x) >> 23) - 127; }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // V codes of one 16-token subtile, as loaded (lane r = l & 15, tokens 4 (l >> 4) .. + 3), for tile i:

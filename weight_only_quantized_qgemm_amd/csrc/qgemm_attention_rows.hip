@@ -268,11 +268,15 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
     float mx = 0.f, l = 0.f, zs[NG], ps[NG];
     bool fresh = true;                              // the row has seen no token: mx is not set
     f32x4 o[TILES];
-    // the row's value scales are divided by 2^sig (inv = 2^-sig), a bound of those it has seen
-    int sig = -126;
-    float inv = 0x1p126f;
+    // The row's products of weight and value scale enter the matrix products times inv, a power of two for each
+    // group: the largest so far stands between 2^6 and kTop, whatever the scales are, whichever token has
+    // the largest score, and however the groups differ.
+    float inv[NG];
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) zs[gr] = ps[gr] = 0.f;
+    for (int gr = 0; gr < NG; ++gr) {
+      zs[gr] = ps[gr] = 0.f;
+      inv[gr] = 0x1p126f;
+    }
 #pragma unroll
     for (int i = 0; i < TILES; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -316,37 +320,31 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
             }
           }
       }
-      float high = u[0][0], big = 0.f;              // and the largest value scale that the row sees here
+      float high = u[0][0];
 #pragma unroll
       for (int x = 0; x < ST; ++x)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          high = __builtin_fmaxf(high, u[x][r]);
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) big = __builtin_fmaxf(big, __builtin_fabsf(par_scale<BF>(st.vp[x][gr][r])));
-        }
-      if (__any(high > (fresh ? -3e38f : kSlack) || big * inv > kScaleSlack)) {
-        // set or move the running maxima and value scales that need it, rescale what is summed so far
-        float top = high, smax = big;
-        top = max_rows(top);
-        smax = max_rows(smax);
+        for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, u[x][r]);
+      if (__any(high > (fresh ? -3e38f : kSlack))) {
+        // set or move the running maxima that need it, rescale what is summed so far
+        const float top = max_rows(high);
         // a row's maximum moves for its own scores only: its result does not depend on its neighbours
-        const bool go = top > (fresh ? -3e38f : kSlack);
-        const float by = go ? top : 0.f, al = fresh ? 1.f : exp2_fast(-by);
-        const int ns = smax * inv > kScaleSlack ? __builtin_amdgcn_frexp_expf(smax) : sig;
-        const float ab = __builtin_ldexpf(al, sig - ns);
+        const bool go = top > (fresh ? -3e38f : kSlack), moved = go && !fresh;
+        const float by = go ? top : 0.f, al = moved ? exp2_fast(-by) : 1.f;
         fresh = fresh && !go;
         mx += by;
-        sig = ns;
-        inv = __builtin_ldexpf(1.f, -ns);
         l *= al;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           zs[gr] *= al;
+          // the products so far became smaller by 2^by: inv takes up the whole powers of two
+          const int up = moved ? (int)__builtin_fminf(by, 126.f - (float)exponent_of(inv[gr])) : 0;
+          inv[gr] = __builtin_ldexpf(inv[gr], up);
+          const float ab = exp2_fast((float)up - (moved ? by : 0.f));
           ps[gr] *= ab;
-        }
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) o[i] *= ab;
+          for (int i = gr * TG; i < (gr + 1) * TG; ++i) o[i] *= ab;
+        }
 #pragma unroll
         for (int x = 0; x < ST; ++x)
 #pragma unroll
@@ -362,20 +360,42 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         unsigned pk[ST][2];
+        float w[ST][4], big = 0.f;
 #pragma unroll
-        for (int x = 0; x < ST; ++x) {
-          float w[4];
+        for (int x = 0; x < ST; ++x)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const unsigned v = st.vp[x][gr][r];
             const float sc = par_scale<BF>(v);
-            w[r] = u[x][r] * (sc * inv);
+            w[x][r] = u[x][r] * sc * inv[gr];
+            big = __builtin_fmaxf(big, __builtin_fabsf(w[x][r]));
             zs[gr] = __builtin_fmaf(u[x][r], __builtin_fmaf(sc, 8.f, par_zero<BF>(v)), zs[gr]);
           }
+        if (__any(big > kTop)) {                    // set or lower the unit of the rows that need it
+          big = 0.f;
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              big = __builtin_fmaxf(big, __builtin_fabsf(u[x][r] * par_scale<BF>(st.vp[x][gr][r])));
+          big = max_rows(big);
+          const int down = big * inv[gr] > kTop ? max(8 - __builtin_amdgcn_frexp_expf(big), -126) - exponent_of(inv[gr]) : 0;
+          const float by = __builtin_ldexpf(1.f, down);
+          inv[gr] = __builtin_ldexpf(inv[gr], down);
+          ps[gr] *= by;
+#pragma unroll
+          for (int i = gr * TG; i < (gr + 1) * TG; ++i) o[i] *= by;
+#pragma unroll
+          for (int x = 0; x < ST; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[x][r] = u[x][r] * par_scale<BF>(st.vp[x][gr][r]) * inv[gr];
+        }
+#pragma unroll
+        for (int x = 0; x < ST; ++x) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // rounded to 11 bits, and summed as rounded: the codes' middle is taken out exactly
-            pk[x][h] = pack_f16(w[2 * h], w[2 * h + 1]);
+            pk[x][h] = pack_f16(w[x][2 * h], w[x][2 * h + 1]);
             ps[gr] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pk[x][h]), f16x2{(_Float16)1.f, (_Float16)1.f},
                                             ps[gr], false);
           }
@@ -444,7 +464,6 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       *reinterpret_cast<u32x2*>(a.out + (long long)(s.start + i) * a.os + (kvh * a.ratio + h) * D + d) =
           u32x2{pack2<BF>(v[0] * r, v[1] * r), pack2<BF>(v[2] * r, v[3] * r)};
     };
-    const float back = __builtin_ldexpf(1.f, sig);
     l = sum_rows(l);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
@@ -462,7 +481,8 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       f32x4 v;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        v[r] = __builtin_fmaf(__builtin_fmaf(o[i][r], up, -8.f * ps[i / TG]), back, zs[i / TG]);
+        v[r] = __builtin_fmaf(__builtin_fmaf(o[i][r], up, -8.f * ps[i / TG]), __builtin_ldexpf(1.f, -exponent_of(inv[i / TG])),
+                              zs[i / TG]);
       *reinterpret_cast<f32x4*>(&s_o[(wave * 16 + m) * kRowF + 16 * i + 4 * g]) = v;
     }
     __syncthreads();
