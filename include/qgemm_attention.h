@@ -152,8 +152,8 @@ qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* problem,
  * causal t <= its own, with window t > its own - window.  A query that sees nothing gets zeros.  Bits
  * in slots that no query sees (unwritten pages, the rest of the last page) never reach the output.
  * Scores, the softmax's maximum and sum and the output are accumulated in fp32; the weights that
- * multiply the codes, each times its value scale, are rounded to fp16 (11 bits; in the rows kernel to no less than
- * 2^-31 of the largest such product of the row and group); the tiles kernel over a BF16 cache also rounds the
+ * multiply the codes, each times its value scale, are rounded to fp16 (11 bits, and to no less than 2^-31 of the
+ * largest such product: in the rows kernel of the row and group, in the tiles kernel of the row); the tiles kernel over a BF16 cache also rounds the
  * values, divided by a power of two per token, to fp16 (three bits more than BF16 holds), and holds keys
  * in several groups exactly while a group's scale is at least 2^-25 of the token's largest.  Results
  * are bitwise deterministic.

@@ -156,8 +156,9 @@ def attention_bound(q, w, out, ks, kz, vs, vz, kmax, group, scale, kind):
     return bound + (kmax + 64) * 2.0 ** -24 * (w @ vmax)
 
 
-def attention_weight_bound(q, w, out, ks, kz, vs, vz, group, scale, kind, floor, values16=False):
-    """As attention_bound, with the weights' own range and the sums' real length.
+def attention_weight_bound(q, w, v, out, ks, kz, vs, vz, group, scale, kind, floor, values16=False):
+    """As attention_bound, with the weights' own range, the sums' real length and the values' real distance from the
+    result.
 
     A token's weight times a group's scale, p, multiplies a code no further than 8 from the middle; it is
     rounded to 11 bits (half a unit: 2^-12 p), or, where it is far below the group's largest in the row, to
@@ -175,6 +176,6 @@ def attention_weight_bound(q, w, out, ks, kz, vs, vz, group, scale, kind, floor,
     bound = UNIT[kind] * np.abs(out) + (2.0 ** -25 if kind == "f16" else 0.0) + np.repeat(low, group, -1)
     amount = np.abs(q) @ np.repeat(15 * np.abs(ks) + np.abs(kz), group, -1).T * abs(scale)   # [n, len]
     ds = (D + 16) * 2.0 ** -24 * amount + 2.0 ** -21
-    spread = w @ vmax + np.abs(out)
+    spread = np.stack([w[i] @ np.abs(v - out[i]) for i in range(n)])
     bound += 2 * np.max(np.where(w > 0, ds, 0), axis=1, keepdims=True, initial=0) * spread
     return bound + (w.shape[1] / 8 + 64) * 2.0 ** -24 * (w @ vmax)

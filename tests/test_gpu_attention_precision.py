@@ -42,9 +42,9 @@ def check(s, out, kind, hint, scale):
     ratio = s["q"].shape[1] // s["c"].kv_heads
     for h in range(s["q"].shape[1]):
         (kc, ks, kz), (vc, vs, vz) = [[a[h // ratio] for a in part] for part in s["parts"]]
-        want, w = oa.attention(s["q"][:, h], oa.dequantize(kc, ks, kz, group), oa.dequantize(vc, vs, vz, group), s["klens"][0],
-                               True, 0, scale)
-        bound = oa.attention_weight_bound(s["q"][:, h], w, want, ks, kz, vs, vz, group, scale, kind, FLOOR[hint],
+        val = oa.dequantize(vc, vs, vz, group)
+        want, w = oa.attention(s["q"][:, h], oa.dequantize(kc, ks, kz, group), val, s["klens"][0], True, 0, scale)
+        bound = oa.attention_weight_bound(s["q"][:, h], w, val, want, ks, kz, vs, vz, group, scale, kind, FLOOR[hint],
                                           hint == 2 and kind == "bf16")
         off = np.abs(got[:, h] - want)
         assert np.isfinite(want).all() and np.isfinite(off).all()
@@ -54,9 +54,10 @@ def check(s, out, kind, hint, scale):
 
 
 KINDS = pytest.mark.parametrize("kind", ["f16", "bf16"])
+KERNELS = pytest.mark.parametrize("hint", [1, 2])
 
 
-@pytest.mark.parametrize("hint", [1])
+@KERNELS
 @KINDS
 @pytest.mark.parametrize("below,sink", [(17.5, 1.0), (16.0, 0.0), (17.5, 0.0)])
 def test_a_dominating_token_over_a_long_context(q, kind, below, sink, hint):
@@ -74,7 +75,7 @@ def test_a_dominating_token_over_a_long_context(q, kind, below, sink, hint):
     check(s, _run(q, s, kind, 1, scale=scale, hint=hint), kind, hint, scale)
 
 
-@pytest.mark.parametrize("hint", [1])
+@KERNELS
 @KINDS
 @pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 128)])
 @pytest.mark.parametrize("at", [0, 20, 59])
@@ -89,26 +90,28 @@ def test_a_dominating_token_without_a_value(q, kind, dim, group, at, hint):
     check(s, _run(q, s, kind, 2, scale=1.0, hint=hint), kind, hint, 1.0)
 
 
-@pytest.mark.parametrize("hint", [1])
+@KERNELS
 @KINDS
-@pytest.mark.parametrize("below", [16.0, 17.5, 18.5])
-def test_a_dominating_token_in_every_row_tile(q, kind, below, hint):
-    # row tiles so many that each walks its context in one part: one token is e^below times the rest, whose sum
-    # stands in the dims where its value is 0
+@pytest.mark.parametrize("below", [16.0, 17.5])
+def test_a_dominating_token_in_one_part(q, kind, below, hint):
+    # requests so many that a workgroup walks a whole context (they share its pages): one token is e^below times each
+    # of the 131071 others, whose sum stands in the dims where its value is 0
     say(f"case attention dominating token, one part {kind} hint={hint} e^-{below}")
     g = np.random.default_rng([67])
-    n, dim, hk, rows = 4096, 64, 128, 129 if hint == 2 else 1
+    n, dim, batch = 131072, 64, 5000
     odd = np.arange(dim) % 2
-    k, v = np.zeros((hk, n, dim)), np.empty((hk, n, dim))
-    v[:] = 2.0 * odd + 0.1 * g.standard_normal((1, n, dim))
-    k[:, 5], v[:, 5] = 2.0, 1.0 - odd
-    s = store(q, kind, k, oa.round16(v, kind), np.full((rows, 2 * hk, dim), 1.0), dim, 64)
-    p = q.attention_problem(s["c"], 1, rows, 2 * hk, rows, s["max_pages"], kernel_hint=hint)
+    k, v = np.zeros((1, n, dim)), odd + 0.05 * g.standard_normal((1, n, dim))
+    k[0, 5], v[0, 5] = 2.0, 1.0 - odd
+    s = store(q, kind, k, oa.round16(v, kind), np.full((1, 1, dim), 1.0), dim, 256)
+    many = dict(s, q=np.full((batch, 1, dim), 1.0), table=s["table"].repeat(batch, 1), lens=s["lens"].repeat(batch), qlens=[1] * batch,
+                klens=[n] * batch, starts=torch.arange(batch + 1, dtype=torch.int32, device="cuda"))
+    p = q.attention_problem(s["c"], batch, batch, 1, 1, s["max_pages"], kernel_hint=hint)
     assert hint == 1 or q.attention_describe(p).endswith("splits=1")
     scale = float(np.float32(below / (2 * dim)))
-    out = _run(q, s, kind, 2 * hk, scale=scale, hint=hint)
-    one = dict(s, q=s["q"][:, :2], parts=[[a[:1] for a in part] for part in s["parts"]], c=q.cache(n // 64, 64, 1, dim, dt(q, kind)))
-    check(one, out[:, :2], kind, hint, scale)
+    out = _run(q, many, kind, 1, scale=scale, hint=hint)
+    assert hint == 1 or torch.equal(out, out[:1].expand_as(out))
+    for i in (0, 1234, batch - 1):
+        check(s, out[i:i + 1], kind, hint, scale)
 
 
 def sizes(kind, ng, order):
@@ -133,7 +136,7 @@ def test_value_groups_far_apart(q, kind, dim, group, order, hint):
     check(s, _run(q, s, kind, 4, scale=scale, hint=hint), kind, hint, scale)
 
 
-@pytest.mark.parametrize("hint", [1])
+@KERNELS
 @KINDS
 @pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 32), (256, 64)])
 @pytest.mark.parametrize("at", [0, 70, 399])

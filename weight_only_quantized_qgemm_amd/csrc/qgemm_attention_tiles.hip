@@ -14,7 +14,7 @@
 // 8192^3 reach 1164 on the same card).  Of its cycles the matrix cores work 33% and the vector units 58%,
 // with two wavefronts on a SIMD: what is left to gain is their overlap.
 //
-// The reference mx of a row bounds score + log2(value scale), in bits, of the tokens it has seen:
+// The reference mx of a row bounds score + log2(value scale), in bits, of the tokens it has seen, less kStand:
 // w = 2^(score - mx) * scale then fits fp16 whatever the scales are, at no cost per token, and
 // 2^-mx drops out with the sum.  mx follows scales down to 2^-60; scales beyond 2^60 (bf16 only) put
 // O into units of 2^64, and ones below 2^-60 put it into units of 2^-64.
@@ -26,8 +26,13 @@ namespace qgemm {
 namespace attn {
 namespace {
 
-// scores may exceed their reference by this many bits less the exponent of the step's largest scale
-constexpr int kRoom = 14, kRoomMax = 60;
+// scores may exceed their reference by this many bits less the exponent of the step's largest scale: weights
+// stay below 2^15, inside fp16
+constexpr int kRoom = 15, kRoomMax = 60;
+// Where a reference puts the largest weight of its tokens: 2^6 to 2^7.  Weights down to 2^-20 of that keep 11 bits,
+// down to 2^-31 they count, and larger ones have eight bits before the reference moves (with seven, chunks in a window
+// take 404 us instead of 398).
+constexpr int kStand = 7;
 
 template <bool BF, int D, int NG, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
@@ -553,6 +558,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         want = max_rows(want);
         // a row's reference moves for its own scores only: its result does not depend on its neighbours
         const bool go = top > (fresh[nc] ? -3e38f : room);
+        want -= (float)kStand;
         const float by = go ? (fresh[nc] ? want : __builtin_fmaxf(want, 0.f)) : 0.f;
         const float al = fresh[nc] ? 1.f : exp2_fast(-by);
         fresh[nc] = fresh[nc] && !go;
