@@ -151,12 +151,14 @@ qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* problem,
  * Query i of n of a sequence of length L stands at position L - n + i.  It sees positions t < L, with
  * causal t <= its own, with window t > its own - window.  A query that sees nothing gets zeros.  Bits
  * in slots that no query sees (unwritten pages, the rest of the last page) never reach the output.
- * Scores, the softmax's maximum and sum and the output are accumulated in fp32; the weights that
- * multiply the codes, each times its value scale, are rounded to fp16 (11 bits, and to no less than 2^-31 of the
- * largest such product: in the rows kernel of the row and group, in the tiles kernel of the row); the tiles kernel over a BF16 cache also rounds the
- * values, divided by a power of two per token, to fp16 (three bits more than BF16 holds), and holds keys
- * in several groups exactly while a group's scale is at least 2^-25 of the token's largest.  Results
- * are bitwise deterministic.
+ * Scores, the softmax's maximum and sum and the output are accumulated in fp32.  The weights that multiply
+ * the codes, each times its value scale, are rounded to fp16: 11 bits, and no less than 2^-31 of the largest such
+ * product, in the rows kernel of the row and group, in the tiles kernel of the row, where the groups' scales
+ * count relative to their means over the first 64 tokens (32 for head_dim 256) of a workgroup's part.  The tiles
+ * kernel over a BF16 cache also rounds the values to fp16, in units of a power of two per token, groups likewise relative to
+ * their means: to 11 bits, three more than BF16 holds, down to 2^-14 of the token's largest, and to 2^-25 of it
+ * below; and it holds keys in several groups exactly while a group's scale is at least 2^-25 of the token's
+ * largest.  Results are bitwise deterministic.
  */
 qgemm_status_t qgemm_attention(const qgemm_attention_t* problem, const void* q, int64_t q_stride, const void* data,
                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_start, void* out,

@@ -12,14 +12,14 @@ void geometry_seq(int s0, int s1, int len, int total_q, int max_q, int tokens, i
   for (int i = 0; i < 5; ++i) out[i] = v[i];
 }
 
-// out: lo, hi, per, active of the row tile that begins at row0, of a sequence of n queries and len tokens
+// out: lo, hi, per, active, seen of the row tile that begins at row0, of a sequence of n queries and len tokens
 void geometry_tile(int n, int len, int row0, int BM, int ratio, int causal, int window, int step, int splits, int* out) {
   Seq s{};
   s.n = n;
   s.len = len;
   const Tile t = tile_of(s, row0, lesser(ratio * n, row0 + BM), BM, ratio, causal, bounded_window(window), step, splits);
-  const int v[4] = {t.lo, t.hi, t.per, t.active};
-  for (int i = 0; i < 4; ++i) out[i] = v[i];
+  const int v[5] = {t.lo, t.hi, t.per, t.active, t.seen};
+  for (int i = 0; i < 5; ++i) out[i] = v[i];
 }
 
 }

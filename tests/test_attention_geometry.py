@@ -25,7 +25,7 @@ def geometry(tmp_path_factory):
         f(*args, out)
         return list(out)
 
-    return (lambda *a: call(lib.geometry_seq, 5, *a)), (lambda *a: call(lib.geometry_tile, 4, *a))
+    return (lambda *a: call(lib.geometry_seq, 5, *a)), (lambda *a: call(lib.geometry_tile, 5, *a))
 
 
 def windows(g):
@@ -56,14 +56,14 @@ def test_parts_cover_each_row_tile(geometry, step):
         row0 = int(g.integers(0, -(-ratio * n // BM))) * BM
         causal = bool(g.random() < 0.8)
         window = windows(g) if causal else 0
-        lo, hi, per, active = tile(n, length, row0, BM, ratio, int(causal), window, step, splits)
+        lo, hi, per, active, seen = tile(n, length, row0, BM, ratio, int(causal), window, step, splits)
         rows = range(row0, min(ratio * n, row0 + BM))
         places = [length - n + r // ratio for r in (rows[0], rows[-1])]
         last = max(min(length, places[1] + 1), 0) if causal else length
         first = max(places[0] - window + 1, 0) if window else 0
         case = (BM, ratio, splits, n, length, row0, causal, window)
         assert hi == last and lo % 16 == 0 and 0 <= lo <= hi, case
-        assert lo <= first or first >= hi, case
+        assert seen == first and (lo <= first or first >= hi), case
         assert 1 <= active <= splits and per >= 1, case
         assert lo + per * active * step >= hi, case
         assert active == 1 or lo + per * (active - 1) * step < hi, case
@@ -73,8 +73,8 @@ def test_the_largest_window_is_no_window(geometry):
     # 2048 queries of four heads a kv head, one part: all 32 steps of the last row tile are in it
     seq, tile = geometry
     for window in (0, LARGEST - 100, LARGEST):
-        assert tile(2048, 2048, 7936, 256, 4, 1, window, 64, 1) == [0, 2048, 32, 1]
-        assert tile(200, 100, 0, 256, 1, 1, window, 64, 1) == [0, 100, 2, 1]      # more queries than tokens
+        assert tile(2048, 2048, 7936, 256, 4, 1, window, 64, 1) == [0, 2048, 32, 1, 0]
+        assert tile(200, 100, 0, 256, 1, 1, window, 64, 1) == [0, 100, 2, 1, 0]   # more queries than tokens
         assert seq(0, 200, 100, 200, 200, 1 << 20, window) == [0, 200, 100, 0, 100]
 
 

@@ -121,7 +121,7 @@ def sizes(kind, ng, order):
     return 2.0 ** (e if order == "falling" else e[::-1])
 
 
-@pytest.mark.parametrize("hint", [1])
+@KERNELS
 @KINDS
 @pytest.mark.parametrize("dim,group", [(64, 32), (128, 64), (128, 32), (256, 128), (256, 64)])
 @pytest.mark.parametrize("order", ["falling", "rising"])
@@ -155,3 +155,22 @@ def test_a_huge_scale_of_negligible_weight(q, kind, dim, group, at, groups, hint
     v[0, at, :group if groups == "one" else dim] *= 2.0 ** (16 if kind == "f16" else 40)
     s = store(q, kind, k, oa.round16(v, kind), qx, group, 16)
     check(s, _run(q, s, kind, 2, scale=1.0, hint=hint), kind, hint, 1.0)
+
+
+@KERNELS
+@KINDS
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 128)])
+def test_what_lies_before_the_window_is_not_read(q, kind, dim, group, hint):
+    # slots of the window's first page that no query sees hold anything: the same bits
+    say(f"case attention before the window {kind} D={dim} G={group} hint={hint}")
+    g = np.random.default_rng([68, dim, group])
+    n, rows, window = 150, 9, 100                                     # the first query sees tokens from 42 on
+    k, v = (oa.round16(g.standard_normal((1, n, dim)), kind) for _ in "kv")
+    outs = []
+    for size in (1.0, 2.0 ** 12, np.nan):
+        k2, v2 = k.copy(), v.copy()
+        k2[:, :42] *= size
+        v2[:, :42, :group] *= size
+        s = store(q, kind, k2, v2, oa.round16(g.standard_normal((rows, 2, dim)), kind) if not outs else s["q"], group, 16)
+        outs.append(_run(q, s, kind, 2, True, window, hint=hint))
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])

@@ -39,13 +39,15 @@ constexpr Seq seq_of(int s0, int s1, int len, int total_q, int max_q, int tokens
 // of BM rows divides them, in steps of `step` tokens.
 struct Tile {
   int lo, hi;                      // tokens: lo a multiple of 16
+  int seen;                        // the first that a row sees (or one past all)
   int per, active;                 // steps of a part, parts that have work (the first `active` workgroups)
 };
 constexpr Tile tile_of(const Seq& s, int row0, int row_end, int BM, int ratio, int causal, int window, int step, int splits) {
   Tile t{};
   const int past = s.len - s.n;    // position of query 0
   t.hi = causal ? lesser(s.len, greater(past + (row_end - 1) / ratio + 1, 0)) : s.len;
-  t.lo = lesser(window ? greater(past + row0 / ratio - window + 1, 0) & ~15 : 0, t.hi & ~15);
+  t.seen = window ? greater(past + row0 / ratio - window + 1, 0) : 0;
+  t.lo = lesser(t.seen & ~15, t.hi & ~15);
   const int all = (t.hi - t.lo + step - 1) / step;
   // Parts are as long as the sequence's longest row tile needs, tiles that see less have fewer (a prompt of
   // 1500, 32 heads: 83 us with each tile's own length divided, 67; 700 queries after 5000 tokens 150, 128).

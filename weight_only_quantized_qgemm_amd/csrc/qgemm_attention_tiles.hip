@@ -61,6 +61,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   __shared__ unsigned s_kw[2][kDeqK ? SUBS * NG * 16 : 4];                   // kDeqK: K scale as fp16, twice
   __shared__ __align__(16) unsigned s_big[4][4];    // per subtile: the largest finite |V scale|, as its bits
   __shared__ int s_odd[4];                          // any V parameter that is not finite
+  __shared__ __align__(16) float s_unit[NG];        // a power of two that V values of the group are held times
   __shared__ float s_top[NW];
   __shared__ int s_last;
 
@@ -162,7 +163,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   auto fetch_par = [&](int step) {
     if (!fp) return;
     int in;
-    rp_on = ts + kStep * step + lane % kStep < te;
+    const int t = ts + kStep * step + lane % kStep;
+    rp_on = t >= tile.seen && t < te;
     const uint8_t* pb = block_of(tok_at(step), pg_tok, in) + 2 * a.codes + (fpv ? a.params : 0);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) rp[gr] = *reinterpret_cast<const unsigned*>(pb + 4 * (gr * a.page + in));
@@ -223,6 +225,26 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       }
     }
   };
+  // Groups of dims whose values differ in size (a few channels far out, in every token) would share one
+  // reference, or in bf16 one unit of each token.  Each group's values are divided by a power of two that brings
+  // its ordinary scale, the mean exponent over the first step's tokens, down to that of the smallest group; O takes it
+  // back at the end.  A token that is far out by itself changes the mean little.
+  constexpr int kApart = 40;
+  auto set_units = [&] {
+    if (NG == 1 || !fpv) return;
+    int mean[NG], low = 255;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      const float sc = __builtin_fabsf(par_scale<BF>(rp[gr])), z = __builtin_fabsf(par_zero<BF>(rp[gr]));
+      const unsigned size = __builtin_bit_cast(unsigned, kDeq ? __builtin_fmaxf(z, 16.f * sc) : sc) >> 23;
+      const int sum = wave_sum(rp_on && size - 1u < 254u ? (int)size | 1 << 16 : 0);        // exponents, and how many
+      mean[gr] = sum ? (int)((float)(sum & 0xffff) / (float)(sum >> 16)) : -1;
+      low = min(low, sum ? mean[gr] : 255);
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) s_unit[gr] = __builtin_ldexpf(1.f, mean[gr] < 0 ? 0 : -min(mean[gr] - low, kApart));
+  };
   auto store_par = [&](int step) {
     if (!fp) return;
     const int pb = step & 3;
@@ -266,7 +288,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         const float mid = __builtin_fmaf(sc[gr], 8.f, z[gr]);
         const bool fine = __builtin_fabsf(mid) < __builtin_inff();
         odd |= !fine;
+        if constexpr (NG > 1) sc[gr] *= s_unit[gr];
         if constexpr (kDeq) {
+          if constexpr (NG > 1) z[gr] *= s_unit[gr];
           sc[gr] = fine ? sc[gr] : 0.f;
           z[gr] = fine ? z[gr] : __builtin_nanf("");
           const float far = __builtin_fmaxf(__builtin_fabsf(z[gr]), 16.f * __builtin_fabsf(sc[gr]));
@@ -592,6 +616,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   // j - 1, whose products were taken before that barrier) and its V buffer (of step j - 2) are free; the
   // parameters are stored a step earlier, into the buffer of step j - 2.
   if (steps) {
+    set_units();
     store_par(0);
     if (steps > 1) fetch_par(1);
     __syncthreads();
@@ -638,9 +663,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         zs[nc][gr] = sum_rows(zs[nc][gr]);
       }
     }
-    const float back = __builtin_ldexpf(1.f, tau);
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
+      const float back = __builtin_ldexpf(1.f, tau - (NG > 1 && steps ? exponent_of(s_unit[i / TG]) : 0));
       const float z = !kDeq ? zs[nc][kDeq ? 0 : i / TG] : bad[nc] >> (i / TG) & 1 ? __builtin_nanf("") : 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[nc][i][r] = __builtin_fmaf(o[nc][i][r], back, z);
