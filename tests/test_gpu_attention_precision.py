@@ -174,3 +174,20 @@ def test_what_lies_before_the_window_is_not_read(q, kind, dim, group, hint):
         s = store(q, kind, k2, v2, oa.round16(g.standard_normal((rows, 2, dim)), kind) if not outs else s["q"], group, 16)
         outs.append(_run(q, s, kind, 2, True, window, hint=hint))
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@KERNELS
+@pytest.mark.parametrize("size", [-1e28, -1e33, -1e37, 1e37])
+def test_scores_at_the_end_of_the_range(q, size, hint):
+    # scores far beyond 2^100 in magnitude: whatever 32 bits leave of their differences, a mean of the values with
+    # weights that sum to 1, so between the smallest and the largest
+    say(f"case attention scores of {size} hint={hint}")
+    g = np.random.default_rng([65])
+    n, dim = 90, 64
+    v = oa.round16(3 + 0.3 * g.standard_normal((1, n, dim)), "bf16")
+    qx = oa.round16(np.full((20, 2, dim), 2.0 ** 40), "bf16")
+    k = oa.round16(np.full((1, n, dim), size / 2.0 ** 46), "bf16")
+    s = store(q, "bf16", k, v, qx, dim, 16)
+    got = down(_run(q, s, "bf16", 2, scale=1.0, hint=hint))
+    val = oa.dequantize(*(a[0] for a in s["parts"][1]), dim)
+    assert np.all(got >= val.min(0) * (1 - 2.0 ** -7)) and np.all(got <= val.max(0) * (1 + 2.0 ** -7))

@@ -53,7 +53,7 @@ struct AttnArgs {
 };
 
 constexpr unsigned kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
-constexpr float kStart = -1e30f;   // running maximum before the first token
+constexpr float kStart = -0x1.fffffep127f;   // running maximum before the first token: no score is below
 // Rows kernel: a running maximum is moved when a score exceeds it by kSlack (in bits); weights times scales
 // enter the matrix products in units that keep them below kTop, inside fp16.
 constexpr float kSlack = 8.0f, kTop = 0x1p15f;

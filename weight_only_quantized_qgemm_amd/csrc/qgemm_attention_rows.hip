@@ -325,11 +325,11 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
       for (int x = 0; x < ST; ++x)
 #pragma unroll
         for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, u[x][r]);
-      if (__any(high > (fresh ? -3e38f : kSlack))) {
+      if (__any(high > (fresh ? -__builtin_inff() : kSlack))) {
         // set or move the running maxima that need it, rescale what is summed so far
         const float top = max_rows(high);
         // a row's maximum moves for its own scores only: its result does not depend on its neighbours
-        const bool go = top > (fresh ? -3e38f : kSlack), moved = go && !fresh;
+        const bool go = top > (fresh ? -__builtin_inff() : kSlack), moved = go && !fresh;
         const float by = go ? top : 0.f, al = moved ? exp2_fast(-by) : 1.f;
         fresh = fresh && !go;
         mx += by;

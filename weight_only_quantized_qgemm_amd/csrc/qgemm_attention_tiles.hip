@@ -555,13 +555,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, u[nc][x][r]);
-      move |= high > (fresh[nc] ? -3e38f : room);
+      move |= high > (fresh[nc] ? -__builtin_inff() : room);
     }
     if (__any(move)) {
       // set or move the references that need it, rescale what is summed so far
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) {
-        float top = -3e38f, want = -3e38f;
+        float top = -__builtin_inff(), want = top;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           f32x4 sm = {0.f, 0.f, 0.f, 0.f};
@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         top = max_rows(top);
         want = max_rows(want);
         // a row's reference moves for its own scores only: its result does not depend on its neighbours
-        const bool go = top > (fresh[nc] ? -3e38f : room);
+        const bool go = top > (fresh[nc] ? -__builtin_inff() : room);
         want -= (float)kStand;
         const float by = go ? (fresh[nc] ? want : __builtin_fmaxf(want, 0.f)) : 0.f;
         const float al = fresh[nc] ? 1.f : exp2_fast(-by);
