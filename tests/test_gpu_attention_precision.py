@@ -191,3 +191,15 @@ def test_scores_at_the_end_of_the_range(q, size, hint):
     got = down(_run(q, s, "bf16", 2, scale=1.0, hint=hint))
     val = oa.dequantize(*(a[0] for a in s["parts"][1]), dim)
     assert np.all(got >= val.min(0) * (1 - 2.0 ** -7)) and np.all(got <= val.max(0) * (1 + 2.0 ** -7))
+
+
+@KERNELS
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 64)])
+def test_values_at_the_end_of_the_range(q, dim, group, hint):
+    # one visible token: its value, up to the largest that bf16 holds
+    say(f"case attention largest values D={dim} G={group} hint={hint}")
+    for size in (1e38, 1.8e38, 3.3e38, -2.5e38):
+        v = oa.round16(np.full((1, 1, dim), size), "bf16")
+        s = store(q, "bf16", np.ones((1, 1, dim)), v, np.ones((1, 2, dim)), group, 16)
+        got = down(_run(q, s, "bf16", 2, hint=hint))
+        assert np.all(np.abs(got / v[0, 0] - 1) <= 2.0 ** -8), size

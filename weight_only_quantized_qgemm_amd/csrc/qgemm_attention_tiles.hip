@@ -33,6 +33,8 @@ constexpr int kRoom = 15, kRoomMax = 60;
 // down to 2^-31 they count, and larger ones have eight bits before the reference moves (with seven, chunks in a window
 // take 404 us instead of 398).
 constexpr int kStand = 7;
+// the largest unit of a token's keys or values, as bits: its reciprocal is a normal number
+constexpr unsigned kUnitMost = 0x7e800000u;
 
 template <bool BF, int D, int NG, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           }
           big = max(big, __builtin_bit_cast(unsigned, __builtin_fabsf(sc[gr])));
         }
-        big &= 0x7f800000u;
+        big = min(big & 0x7f800000u, kUnitMost);
         const float back = __builtin_bit_cast(float, 0x7f000000u - big);
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
@@ -301,8 +303,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         }
       }
       if constexpr (kDeq) {
-        // the token's unit 2^e, at most its largest value's bound; values stay below 4 of it
-        big &= 0x7f800000u;
+        // the token's unit 2^e, at most its largest value's bound; values stay below 8 of it
+        big = min(big & 0x7f800000u, kUnitMost);
         const float unit = __builtin_bit_cast(float, big), back = __builtin_bit_cast(float, 0x7f000000u - big);
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
