@@ -177,6 +177,44 @@ def test_what_lies_before_the_window_is_not_read(q, kind, dim, group, hint):
 
 
 @KERNELS
+@pytest.mark.parametrize("kind,step", [("f16", 8), ("bf16", 25)])
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 128)])
+def test_query_heads_far_apart(q, kind, step, order, dim, group, hint):
+    # four heads, each 2^step times the one before; the smallest head's scores are of ordinary size.  The same for
+    # the tokens' queries in a second call
+    for along in ("heads", "queries"):
+        say(f"case attention query {along} apart {kind} by 2^{step} order {order} D={dim} G={group} hint={hint}")
+        g = np.random.default_rng([63, dim, group])
+        n, rows = 300, 4 if along == "queries" else 20
+        base = 2.0 ** (-13 if kind == "f16" else -40)
+        size = (base * 2.0 ** (step * np.arange(4)))[::order]
+        qx = g.standard_normal((rows, 4, dim)) * (size[None, :, None] if along == "heads" else size[:, None, None])
+        k, v = (oa.round16(g.standard_normal((1, n, dim)), kind) for _ in "kv")
+        s = store(q, kind, k, v, oa.round16(qx, kind), group, 16)
+        scale = float(np.float32(dim ** -0.5 / base))
+        check(s, _run(q, s, kind, 4, scale=scale, hint=hint), kind, hint, scale)
+
+
+@KERNELS
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32)])
+def test_a_row_does_not_change_with_its_neighbours(q, dim, group, hint):
+    # the first head alone, beside ordinary heads and beside one 2^40 times as large: the same bits
+    say(f"case attention neighbours D={dim} G={group} hint={hint}")
+    g = np.random.default_rng([64, dim])
+    k, v = (oa.round16(g.standard_normal((1, 500, dim)), "bf16") for _ in "kv")
+    qx = oa.round16(g.standard_normal((20, 4, dim)), "bf16")
+    outs = []
+    for other in (1.0, 2.0 ** 40, 2.0 ** -40):
+        mixed = qx.copy()
+        mixed[:, 1:] *= other
+        mixed[::2, 1:] *= other
+        s = store(q, "bf16", k, v, mixed, group, 16)
+        outs.append(_run(q, s, "bf16", 4, scale=0.1, hint=hint)[:, 0])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@KERNELS
 @pytest.mark.parametrize("size", [-1e28, -1e33, -1e37, 1e37])
 def test_scores_at_the_end_of_the_range(q, size, hint):
     # scores far beyond 2^100 in magnitude: whatever 32 bits leave of their differences, a mean of the values with

@@ -10,8 +10,8 @@
 // Codes become fp16 operands with one AND each: a nibble in the low bits of an fp16 pattern is the
 // subnormal code * 2^-24 (bits 0..3) or code * 2^-20 (bits 4..7), which the MFMA multiplies exactly;
 // the powers of two are taken out of the fp32 result.  Both element types therefore use the fp16
-// MFMA (16x16x32).  Queries are scaled by a power of two common to the wavefront's rows, so that
-// the largest finite one lies in [2^13, 2^14): bf16 queries fit fp16 exactly down to 2^-27 of that.
+// MFMA (16x16x32).  Each query row is scaled by a power of two, so that its largest finite element lies below
+// 2^14 (in [2^13, 2^14) in the rows kernel): bf16 queries fit fp16 exactly down to 2^-27 of that.
 //
 // The scores are computed transposed, S^T = K Q^T: lane l holds query row l & 15 and tokens
 // 4 (l >> 4) .. + 3, which is the operand layout of P^T in O^T = V^T P^T (the contraction runs over
@@ -117,14 +117,6 @@ __device__ __forceinline__ float sum_rows(float x) {
 }
 __device__ __forceinline__ float max_rows(float x) {
   return over_rows(x, [](float a, float b) { return __builtin_fmaxf(a, b); });
-}
-// The largest value of the wavefront: within rows of 16 lanes by DPP, then over the rows.
-template <int C>
-__device__ __forceinline__ float dpp_max(float x) {
-  return __builtin_fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), C, 0xf, 0xf, true)));
-}
-__device__ __forceinline__ float wave_max(float x) {
-  return max_rows(dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(x)))));
 }
 // The exponent of a power of two within the normal range.
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__builtin_bit_cast(unsigned, x) >> 23) - 127; }

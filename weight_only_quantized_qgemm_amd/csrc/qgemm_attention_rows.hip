@@ -235,7 +235,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
             const float x = __builtin_fabsf(from16<BF>(raw[j][e] >> (16 * o) & 0xffffu));
             top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
           }
-    top = wave_max(top);
+      top = max_rows(top);                          // of the lane's row: its result does not depend on its neighbours
       // top = f 2^e, f in [1/2, 1)
       const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
       kq = __builtin_ldexpf(a.scale, 24 - 14 + e);

@@ -35,6 +35,9 @@ constexpr int kRoom = 15, kRoomMax = 60;
 constexpr int kStand = 7;
 // the largest unit of a token's keys or values, as bits: its reciprocal is a normal number
 constexpr unsigned kUnitMost = 0x7e800000u;
+// Query rows whose largest lies in [2^-5, 2^6): their elements keep 11 bits down to 2^-13 of the largest and
+// are rounded to 2^-24 of it at worst, which is what a 32-bit sum keeps.
+constexpr int kQueryExp = 6, kQueryBand = 10;
 
 template <bool BF, int D, int NG, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
@@ -64,7 +67,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   __shared__ __align__(16) unsigned s_big[4][4];    // per subtile: the largest finite |V scale|, as its bits
   __shared__ int s_odd[4];                          // any V parameter that is not finite
   __shared__ __align__(16) float s_unit[NG];        // a power of two that V values of the group are held times
-  __shared__ float s_top[NW];
+  __shared__ float s_fit[BM];                       // rows' factors on the products with K
   __shared__ int s_last;
 
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
@@ -337,11 +340,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   u32x4 qf[U][NC];
   float qz[NC][NG];
   int see_lo[NC], see_hi[NC];
+  // A row's queries enter the products times 2^(14 - e), a rule of the row alone: rows of ordinary size share e =
+  // kQueryExp, which is part of the keys' factor; others have their products multiplied by 2^(e - kQueryExp) in a wavefront that
+  // holds such a row.
+  bool wide = false;
   {
     u32x4 raw[NC][U];
-    float top = 0.f;
+    float top[NC];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
+      top[nc] = 0.f;
       const int row = row0 + (wave * NC + nc) * 16 + m;
       const bool on = row < rows;
       const int i = on ? row / a.ratio : 0, h = row - i * a.ratio;
@@ -357,7 +365,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             const float x = __builtin_fabsf(from16<BF>(raw[nc][j][e] >> (16 * o) & 0xffffu));
-            top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
+            top[nc] = x < __builtin_inff() ? __builtin_fmaxf(top[nc], x) : top[nc];
           }
       }
     }
@@ -367,15 +375,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       fetch(0);
       fetch_par(0);
     }
-    top = wave_max(top);
-    if (lane == 0) s_top[wave] = top;
-    __syncthreads();
+    kq = __builtin_ldexpf(a.scale, (kDeqK ? -11 : 24) - 14 + kQueryExp);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) top = __builtin_fmaxf(top, s_top[w]);
-    const int e = top > 0.f ? __builtin_amdgcn_frexp_expf(top) : 0;
-    kq = __builtin_ldexpf(a.scale, (kDeqK ? -11 : 24) - 14 + e);
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
+    for (int nc = 0; nc < NC; ++nc) {
+      // the row's largest is f 2^e, f in [1/2, 1)
+      top[nc] = max_rows(top[nc]);
+      int e = top[nc] > 0.f ? __builtin_amdgcn_frexp_expf(top[nc]) : kQueryExp;
+      if (e >= kQueryExp - kQueryBand && e < kQueryExp) e = kQueryExp;
+      wide |= e != kQueryExp;
+      if (g == 0) s_fit[(wave * NC + nc) * 16 + m] = __builtin_ldexpf(1.f, e - kQueryExp);
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         float sum = 0.f;
@@ -396,7 +404,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
         sum = sum_rows(sum);
         qz[nc][gr] = sum * a.scale;
       }
+    }
   }
+  wide = __any(wide);
   // tokens that the wavefront's rows all see
   const int first = row0 + wave * 16 * NC, last = min(rows - 1, first + 16 * NC - 1);
   const bool idle = first >= rows;
@@ -457,15 +467,27 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
           }
       }
   };
+  auto fit = [&](Acc& acc) {
+    if (!wide) return;
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      const float f = s_fit[(wave * NC + nc) * 16 + m];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int gr = 0; gr < AG; ++gr) acc[x][gr][nc] *= f;
+    }
+  };
   // A half's weights, as B operands, while the next half's products with K run beside them (into
   // buffers that exist even after the last half: its scores are not used).  kMask: a weight of 0 must
-  // not meet a parameter that is not finite, and O's unit is not 1.
+  // not meet a parameter that is not finite, or O's unit is not 1, or the products take the rows' factors.
   unsigned seen[NC];
   constexpr int WG = kDeq ? 1 : NG;                 // weights of a token: one, or one per group
   typedef u32x4 Weights[WG][NC];
   auto weights = [&](auto mask_c, int step, int pr, int nstep, int npr, float tf, Acc& acc, Weights& bp) {
     constexpr bool kMask = decltype(mask_c)::value;
     products(nstep, npr, acc);
+    if constexpr (kMask) fit(acc);
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -602,7 +624,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     }
     Acc acc;
     Weights bp;
-    if (tau || odd) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
+    if (tau || odd || wide) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
     else weights(std::false_type{}, step, pr, nstep, npr, tf, acc, bp);
     if (kSkew && pr == 0 && late) __syncthreads();
 #pragma unroll
@@ -632,6 +654,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     {
       Acc acc;
       products(0, 0, acc);
+      fit(acc);
       score(0, 0, acc);
     }
     for (int j = 0; j < steps; ++j) {
