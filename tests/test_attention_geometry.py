@@ -114,3 +114,18 @@ def test_decreasing_starts_are_told(geometry, starts, total, max_q):
     assert [seq(a, b, 500, total, max_q, 1 << 20, 0)[1] for a, b in zip(starts, starts[1:])] == \
         [n if b >= a else -1 for n, a, b in zip(bounded, starts, starts[1:])]
     assert seq(LARGEST, -LARGEST, 5, total, max_q, 1 << 20, 0)[1] == -1
+
+
+# ----------------------------------------------------------------------------- the choice of kernel
+@pytest.mark.parametrize("batch,kv_heads,pages", [(4096, 32, 1 << 16), (1024, 32, 1 << 18), (65535, 8, 1 << 15), (65535, 64, 1 << 13)])
+def test_problems_beyond_the_rows_kernel_go_to_the_tiles_kernel(batch, kv_heads, pages):
+    # one token a request over tables so wide that the rows kernel could not number all their units
+    c = q.cache(1 << 20, 16, kv_heads, 128, q.DT_BF16)
+    p = q.attention_problem(c, batch, batch, 4 * kv_heads, 1, pages)
+    assert q.attention_describe(p).startswith("tiles ") and q.attention_workspace_bytes(p) == 0
+    asked = q.attention_problem(c, batch, batch, 4 * kv_heads, 1, pages, kernel_hint=q.ATTENTION_ROWS)
+    with pytest.raises(q.QgemmError, match="row tiles") as e:
+        q.attention_describe(asked)
+    assert e.value.status == q.ERR_UNSUPPORTED
+    narrow = q.attention_problem(c, batch, batch, 4 * kv_heads, 1, pages // 64)
+    assert q.attention_describe(narrow).startswith("rows ")

@@ -60,3 +60,31 @@ def test_decreasing_starts_write_nothing(q, hint, total, ratio):
         assert (out == 7).all() and (guarded[n:] == 0x5A).all(), starts
         q.attention(p, qx, s["data"], s["table"], s["lens"], rising, out, guarded[:n])
         assert torch.equal(out, good), starts
+
+
+def test_short_contexts_in_very_wide_tables(q):
+    # one token each over tables of 4 million slots: more units than the rows kernel numbers, so the tiles kernel,
+    # against the rows kernel over a narrow table
+    say("case attention 1024 requests, tables of 2^22 slots")
+    batch, hk, dim, page, wide = 1024, 32, 64, 16, 1 << 18
+    g = torch.Generator(device="cuda").manual_seed(70)
+    c = q.cache(4, page, hk, dim, q.DT_BF16)
+    data = q.alloc_cache(c)
+    k, v = (torch.randn(64, hk, dim, generator=g, device="cuda").bfloat16() for _ in "kv")
+    q.cache_write(c, data, k, v, torch.arange(64, device="cuda"))
+    qx = torch.randn(batch, hk, dim, generator=g, device="cuda").bfloat16()
+    lens = (torch.arange(batch, device="cuda") * 7 % 65).int()
+    starts = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+    outs = []
+    for columns, kind in ((wide, "tiles"), (4, "rows")):
+        p = q.attention_problem(c, batch, batch, hk, 1, columns)
+        assert q.attention_describe(p).startswith(kind)
+        table = torch.zeros(batch, columns, dtype=torch.int32, device="cuda")
+        table[:, :4] = torch.arange(4, dtype=torch.int32, device="cuda")
+        out = torch.full_like(qx, 7.0)
+        q.attention(p, qx, data, table, lens, starts, out, q.alloc_attention_workspace(p))
+        outs.append(out.float())
+        del table
+    assert not outs[0][lens == 0].any() and not outs[1][lens == 0].any()
+    # each within a rounding to bf16 and to fp16 weights of the values' mean
+    assert (outs[0] - outs[1]).abs().max() <= 2.0 ** -8 * 2 * outs[1].abs().max() + 2.0 ** -10 * v.float().abs().max()

@@ -152,11 +152,13 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
   const int di = dim == 64 ? 0 : dim == 128 ? 1 : 2, gi = ng == 1 ? 0 : ng == 2 ? 1 : 2;
   const double rows_us = 10.0 + kRowUnit[di][gi] * (double)row_tiles * (double)steps / kCUs;
   const double tiles_us = 8.0 + kTileStep[p->cache.dtype == QGEMM_DT_BF16][di][gi] * best;
+  // the rows kernel numbers the units of all row tiles, as long as the table is wide, in 32 bits
+  const bool divides = ((double)steps + 8) * (double)row_tiles <= 2147483647.0;
   const bool use_rows = p->kernel_hint == QGEMM_ATTENTION_ROWS ||
-                        (p->kernel_hint == QGEMM_ATTENTION_AUTO && (rows <= row_tile || rows_us <= tiles_us));
+                        (p->kernel_hint == QGEMM_ATTENTION_AUTO && divides && (rows <= row_tile || rows_us <= tiles_us));
   if (use_rows) {
     pl->kind = ATTN_ROWS;
-    if (((double)steps + 8) * (double)row_tiles > 2147483647.0)
+    if (!divides)
       return fail(QGEMM_ERR_UNSUPPORTED, "%lld row tiles of up to %lld tokens are beyond what one launch divides",
                   (long long)row_tiles, (long long)tokens);
     // Many segments (several per resident workgroup of four wavefronts) take a wavefront each: the starts
