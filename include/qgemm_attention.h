@@ -24,7 +24,8 @@ extern "C" {
 /*
  * qgemm_norm_rope_t -- heads of `tokens` tokens: q [tokens][q_heads][head_dim] and
  * k [tokens][kv_heads][head_dim].
- *   tokens in [0, 2^24]; q_heads in [0, 1024], kv_heads in [0, 1024], not both 0;
+ *   tokens in [0, 2^24]; q_heads in [0, 1024], kv_heads in [0, 1024], not both 0 (more than about 2^36
+ *   elements are beyond one launch: UNSUPPORTED);
  *   head_dim 64, 128 or 256; rot_dim a multiple of 8 in [0, head_dim]; max_pos in [1, 2^24]
  *   (rows of the table; ignored for rot_dim 0); dtype F16 or BF16.
  *   norm: 1 = RMS norm of every head first, 0 = rotation only.  eps >= 0 (finite), used with norm.
@@ -95,7 +96,7 @@ qgemm_status_t qgemm_cache_bytes(const qgemm_cache_t* cache, size_t* bytes);
  *           multiple of 8, at least kv_heads * head_dim); 16-byte aligned.
  *   slots   int64 [tokens]; a slot outside the cache (e.g. -1, padding) is skipped.  Slots of one
  *           call are distinct.
- * tokens in [0, 2^24].
+ * tokens in [0, 2^24]; more than about 2^35 elements of k are beyond one launch: UNSUPPORTED.
  */
 qgemm_status_t qgemm_cache_write(const qgemm_cache_t* cache, void* data, const void* k, int64_t k_stride,
                                  const void* v, int64_t v_stride, const int64_t* slots, int64_t tokens, void* stream);

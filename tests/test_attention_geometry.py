@@ -129,3 +129,25 @@ def test_problems_beyond_the_rows_kernel_go_to_the_tiles_kernel(batch, kv_heads,
     assert e.value.status == q.ERR_UNSUPPORTED
     narrow = q.attention_problem(c, batch, batch, 4 * kv_heads, 1, pages // 64)
     assert q.attention_describe(narrow).startswith("rows ")
+
+
+# ----------------------------------------------------------------------------- launch limits
+def test_launches_of_too_many_work_items_are_refused():
+    # a launch holds less than 2^32 work-items; calls beyond that are refused by the host, not by the runtime
+    def text(status):
+        assert status == q.ERR_UNSUPPORTED, q.last_error()
+        assert "more than one launch allows" in q.last_error()
+
+    tokens, a = 1 << 24, 0x100000
+    for heads, dim in ((64, 128), (128, 64), (32, 256), (1024, 64)):
+        p = q.NormRope(tokens, heads, heads, dim, 0, 0, q.DT_F16, 0, 1, 1e-6, 0)
+        row = heads * dim
+        text(q.lib.qgemm_qk_norm_rope(ctypes.byref(p), a, row, a, row, None, None, None, None, a, row, a, row, None))
+    for heads, dim in ((16, 128), (32, 64), (8, 256), (1024, 64)):
+        c, row = q.cache(1 << 20, 16, heads, dim, q.DT_F16), heads * dim
+        text(q.lib.qgemm_cache_write(ctypes.byref(c), a, a, row, a, row, a, tokens, None))
+        text(q.lib.qgemm_cache_read(ctypes.byref(c), a, a, tokens, a, a, None))
+    for heads, dim, batch in ((512, 64, 65535), (1024, 128, 16384), (1024, 256, 65535)):
+        p = q.attention_problem(q.cache(1 << 20, 16, heads, dim, q.DT_F16), batch, batch, heads, 1, 4, kernel_hint=q.ATTENTION_TILES)
+        n = ctypes.c_size_t()
+        text(q.lib.qgemm_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(n)))

@@ -171,7 +171,7 @@ qgemm_status_t make_attention_plan(const qgemm_attention_t* p, AttnPlan* pl) {
     return QGEMM_OK;
   }
   pl->kind = ATTN_TILES;
-  if (tiles * pl->splits > 0x7fffffffLL)
+  if (!launchable(tiles * pl->splits, 64 * shape.waves))
     return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows",
                 (long long)(tiles * pl->splits));
   pl->grid = (unsigned)(tiles * pl->splits);

@@ -12,6 +12,9 @@ qgemm_status_t validate_norm_rope(const qgemm_norm_rope_t* p);
 qgemm_status_t validate_cache(const qgemm_cache_t* c);
 qgemm_status_t validate_attention(const qgemm_attention_t* p);
 
+// A launch holds less than 2^32 work-items.
+inline bool launchable(int64_t workgroups, int threads) { return workgroups <= 0xffffffffLL / threads; }
+
 // Byte geometry of one block (one page of one kv head).
 struct BlockGeom {
   int codes;      // bytes of one side's codes (= offset of the V codes)

@@ -284,7 +284,7 @@ qgemm_status_t enqueue(const qgemm_cache_t* c, bool write, CacheArgs& a, const i
   a.block = g.bytes;
   const int rows = 512 / c->head_dim;
   const int64_t groups = (tokens + 4 * rows - 1) / (4 * rows) * c->kv_heads;
-  if (groups > 0x7fffffffLL)
+  if (!launchable(groups, 256))
     return fail(QGEMM_ERR_UNSUPPORTED, "tokens * kv_heads needs %lld workgroups, more than one launch allows", (long long)groups);
   const dim3 grid((unsigned)groups);
   hipStream_t s = static_cast<hipStream_t>(stream);

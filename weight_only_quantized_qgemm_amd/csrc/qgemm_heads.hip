@@ -201,7 +201,7 @@ extern "C" qgemm_status_t qgemm_qk_norm_rope(const qgemm_norm_rope_t* p, const v
   const bool two = p->tokens * runs > 4096;
   a.chunks = two ? (runs + 1) / 2 : runs;
   const int64_t waves = p->tokens * a.chunks;
-  if (waves > 0x7ffffff0LL)
+  if (!launchable((waves + 3) / 4, 256))
     return fail(QGEMM_ERR_UNSUPPORTED, "tokens * heads needs %lld wavefronts, more than one launch allows", (long long)waves);
   const dim3 grid((unsigned)((waves + 3) / 4));
   hipStream_t s = static_cast<hipStream_t>(stream);
