@@ -13,7 +13,9 @@ Quick use::
     ... upload with torch, then q.run(p, A, wpk_dev, spk_dev, alpha_dev, out, ws)
 """
 import ctypes
+import importlib
 import os
+import threading
 
 import numpy as np
 # torch first: it loads its HIP runtime (soname libamdhip64.so.7), and the library below then
@@ -30,11 +32,6 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python -m weight_only_quantized_qgemm_amd._build` (hipcc, gfx950)")
 _lib = ctypes.CDLL(LIB_PATH)
-try:
-    from . import _calls
-except ImportError as e:
-    raise ImportError("the _calls module is missing or of another Python: build it with "
-                      "`python -m weight_only_quantized_qgemm_amd._build`") from e
 
 # ----------------------------------------------------------------------------- enums
 OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE_TOO_SMALL, ERR_HIP = range(6)
@@ -300,11 +297,30 @@ def _stream(stream, x):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-_calls.setup(*(ctypes.cast(f, _vp).value for f in (_lib.qgemm_qk_norm_rope, _lib.qgemm_cache_write, _lib.qgemm_cache_read,
-                                                   _lib.qgemm_attention)),
-             torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
-             # the raw stream handle of a device, without building a Stream object for it
-             getattr(torch._C, "_cuda_getCurrentRawStream", None), _stream)
+class _Calls:
+    """Stands for the compiled module until the first call loads it: programs that call the products only need not have it."""
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        global _calls_ready
+        with self._lock:
+            if _calls_ready is self:
+                try:
+                    module = importlib.import_module("._calls", __name__)
+                except ImportError as e:
+                    raise ImportError("the _calls module is missing or of another Python: build it with "
+                                      "`python -m weight_only_quantized_qgemm_amd._build`") from e
+                module.setup(*(ctypes.cast(f, _vp).value for f in (_lib.qgemm_qk_norm_rope, _lib.qgemm_cache_write,
+                                                                   _lib.qgemm_cache_read, _lib.qgemm_attention)),
+                             torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+                             # the raw stream handle of a device, without building a Stream object for it
+                             getattr(torch._C, "_cuda_getCurrentRawStream", None), _stream)
+                _calls_ready = module
+        return getattr(_calls_ready, name)
+
+
+# the calls go through _calls_ready, which becomes the module once it is set up (importing it binds _calls before)
+_calls = _calls_ready = _Calls()
 
 
 def norm_rope_problem(tokens, q_heads, kv_heads, head_dim, dtype=DT_F16, rot_dim=None, max_pos=0, interleaved=False,
@@ -317,7 +333,7 @@ def norm_rope_problem(tokens, q_heads, kv_heads, head_dim, dtype=DT_F16, rot_dim
 def qk_norm_rope(p, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, stream=None):
     """Enqueue the norm and rotation of the heads of q and k (qgemm_qk_norm_rope).  The tensors are
     [tokens, heads, head_dim], each with its own token stride; outputs may be the inputs."""
-    st = _calls.qk_norm_rope(p, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, stream)
+    st = _calls_ready.qk_norm_rope(p, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, stream)
     if st:
         _check(st)
 
@@ -340,14 +356,14 @@ def alloc_cache(c, device="cuda"):
 
 def cache_write(c, data, k, v, slots, stream=None):
     """Enqueue the quantization of k, v [tokens, kv_heads, head_dim] into the int64 slots."""
-    st = _calls.cache_write(c, data, k, v, slots, stream)
+    st = _calls_ready.cache_write(c, data, k, v, slots, stream)
     if st:
         _check(st)
 
 
 def cache_read(c, data, slots, k_out, v_out, stream=None):
     """Enqueue the values of the slots into k_out, v_out [tokens, kv_heads, head_dim], contiguous."""
-    st = _calls.cache_read(c, data, slots, k_out, v_out, stream)
+    st = _calls_ready.cache_read(c, data, slots, k_out, v_out, stream)
     if st:
         _check(st)
 
@@ -380,6 +396,6 @@ def attention_describe(p):
 
 def attention(p, q, data, page_table, seq_lens, q_start, out, workspace=None, stream=None):
     """Enqueue attention of q [total_q, q_heads, head_dim] over the cache into out (qgemm_attention)."""
-    st = _calls.attention(p, q, data, page_table, seq_lens, q_start, out, workspace, stream)
+    st = _calls_ready.attention(p, q, data, page_table, seq_lens, q_start, out, workspace, stream)
     if st:
         _check(st)
