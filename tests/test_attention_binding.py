@@ -5,6 +5,9 @@ import shutil
 import subprocess
 import sys
 
+import pytest
+import torch
+
 import weight_only_quantized_qgemm_amd as q
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -55,3 +58,60 @@ assert len(seen) == 8 and all("data must be" in s for s in seen), seen
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+class Elsewhere:
+    """A tensor that says it lies on another device; its memory is the host's, which the checks must keep from the library."""
+
+    def __init__(self, x, device):
+        self.x, self.device = x, device
+
+    def get_device(self):
+        return self.device
+
+    def __getattr__(self, name):
+        return getattr(self.x, name)
+
+
+def calls(at):
+    """Each call's function and its arguments by name, at(name, tensor) in place of each tensor."""
+    half, i32 = torch.float16, torch.int32
+    x, kv = torch.zeros(3, 4, 64, dtype=half), torch.zeros(3, 2, 64, dtype=half)
+    c = q.cache(4, 16, 2, 64)
+    data, slots = torch.zeros(q.cache_bytes(c), dtype=torch.uint8), torch.zeros(3, dtype=torch.int64)
+    w, lens = torch.ones(64, dtype=half), torch.zeros(2, dtype=i32)
+    p = q.attention_problem(c, 1, 3, 4, 3, 2)
+    r = q.norm_rope_problem(3, 4, 2, 64, max_pos=8)
+    found = [
+        (q.qk_norm_rope, dict(p=r), dict(q=x, k=kv, q_weight=w, k_weight=w, positions=torch.zeros(3, dtype=i32),
+                                         cos_sin=torch.zeros(8, 64), q_out=x, k_out=kv)),
+        (q.cache_write, dict(c=c), dict(data=data, k=kv, v=kv, slots=slots)),
+        (q.cache_read, dict(c=c), dict(data=data, slots=slots, k_out=kv, v_out=kv)),
+        (q.attention, dict(p=p), dict(q=x, data=data, page_table=torch.zeros(1, 2, dtype=i32), seq_lens=lens, q_start=lens, out=x,
+                                      workspace=torch.zeros(1 << 20, dtype=torch.uint8)))]
+    return [(f, dict(fixed, **{n: at(n, v) for n, v in t.items()}), list(t)) for f, fixed, t in found]
+
+
+@pytest.mark.parametrize("stream", [None, 0])
+def test_tensors_on_the_host_are_refused(stream):
+    for f, args, names in calls(lambda n, t: t):
+        with pytest.raises(ValueError, match="on the GPU"):
+            f(**args, stream=stream)
+
+
+def test_one_tensor_elsewhere_is_refused():
+    for i in range(4):
+        for odd in calls(lambda n, t: t)[i][2]:
+            for device, text in ((-1, f"{odd} must be on the GPU"), (1, "on device")):
+                f, args, _ = calls(lambda n, t: Elsewhere(t, device if n == odd else 0))[i]
+                with pytest.raises(ValueError, match=text):
+                    f(**args, stream=0)
+
+
+def test_page_tables_of_another_width_and_loose_workspaces_are_refused():
+    f, args, _ = calls(lambda n, t: Elsewhere(t, 0))[3]
+    for wide in (torch.zeros(1, 3, dtype=torch.int32), torch.zeros(2, 1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="max_pages = 2 columns"):
+            f(**dict(args, page_table=Elsewhere(wide, 0)), stream=0)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        f(**dict(args, workspace=Elsewhere(torch.zeros(2 << 20, dtype=torch.uint8)[::2], 0)), stream=0)

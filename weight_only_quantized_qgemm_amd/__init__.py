@@ -289,7 +289,8 @@ def version():
 
 # ----------------------------------------------------------------------------- attention operators
 # The device calls below are made once per layer and token: their tensors are checked, and the C function
-# called, in csrc/qgemm_calls.cpp.  A tensor of the wrong type, shape or strides raises ValueError.
+# called, in csrc/qgemm_calls.cpp.  A tensor of the wrong type, shape or strides, or that is not on the call's GPU,
+# raises ValueError.
 def _stream(stream, x):
     """The handle of `stream`; by default that of torch's current stream."""
     if stream is None:

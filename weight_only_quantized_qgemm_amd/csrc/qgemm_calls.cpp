@@ -8,6 +8,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <initializer_list>
+
 #include "../../include/qgemm_attention.h"
 
 namespace {
@@ -108,18 +110,44 @@ bool stream_of(PyObject* stream, PyObject* x, void** h) {
     if (!device) return false;
     const long index = PyLong_AsLong(device.o);
     if (index == -1 && PyErr_Occurred()) return false;
-    if (index >= 0) {
-      const Ref handle(PyObject_CallOneArg(g_raw_stream, device.o));
-      if (!handle) return false;
-      *h = PyLong_AsVoidPtr(handle.o);
-      return *h || !PyErr_Occurred();
+    if (index < 0) {
+      PyErr_SetString(PyExc_ValueError, "tensors must be on the GPU");
+      return false;
     }
+    const Ref handle(PyObject_CallOneArg(g_raw_stream, device.o));
+    if (!handle) return false;
+    *h = PyLong_AsVoidPtr(handle.o);
+    return *h || !PyErr_Occurred();
   }
   const Ref handle(PyObject_CallFunctionObjArgs(g_stream, stream, x, nullptr));
   if (!handle) return false;
   if (handle.o == Py_None) return true;
   *h = PyLong_AsVoidPtr(handle.o);
   return *h || !PyErr_Occurred();
+}
+
+// All tensors of a call lie on one GPU: an address of the host's, or of another device, would fault there.
+struct Named { const char* name; PyObject* x; };
+bool one_gpu(std::initializer_list<Named> tensors) {
+  const char* first = nullptr;
+  long long at = -1;
+  for (const Named& t : tensors) {
+    if (t.x == Py_None) continue;
+    long long index;
+    if (!call_int(t.x, n_device, &index)) return false;
+    if (index < 0) {
+      PyErr_Format(PyExc_ValueError, "%s must be on the GPU", t.name);
+      return false;
+    }
+    if (!first) {
+      first = t.name;
+      at = index;
+    } else if (index != at) {
+      PyErr_Format(PyExc_ValueError, "%s is on device %lld, %s on device %lld", t.name, index, first, at);
+      return false;
+    }
+  }
+  return true;
 }
 
 // A descriptor: the bytes of a ctypes structure, held while this lives.
@@ -175,7 +203,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      !array(a[6], "cos_sin", g_f32, (double)p->max_pos * p->rot_dim, &tab)))
     return nullptr;
   if (!array(a[3], "q_weight", t16, (double)dim, &qw) || !array(a[4], "k_weight", t16, (double)dim, &kw) ||
-      !stream_of(a[9], a[1] == Py_None ? a[2] : a[1], &st))
+      !stream_of(a[9], a[1] == Py_None ? a[2] : a[1], &st) ||
+      !one_gpu({{"q", a[1]}, {"k", a[2]}, {"q_weight", a[3]}, {"k_weight", a[4]}, {"positions", p->rot_dim ? a[5] : Py_None},
+                {"cos_sin", p->rot_dim ? a[6] : Py_None}, {"q_out", a[7]}, {"k_out", a[8]}}))
     return nullptr;
   CALL(g_rope(p.get(), q, qs, k, ks, qw, kw, static_cast<const int32_t*>(pos), static_cast<const float*>(tab), qo, qos, ko,
               kos, st));
@@ -193,7 +223,7 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!rows(a[2], "k", tokens, c->kv_heads, c->head_dim, t16, &k, &ks) ||
       !rows(a[3], "v", tokens, c->kv_heads, c->head_dim, t16, &v, &vs) ||
       !array(a[1], "data", g_u8, cache_bytes(*c.get()), &data) || !array(a[4], "slots", g_i64, (double)tokens, &slots) ||
-      !stream_of(a[5], a[1], &st))
+      !stream_of(a[5], a[1], &st) || !one_gpu({{"data", a[1]}, {"k", a[2]}, {"v", a[3]}, {"slots", a[4]}}))
     return nullptr;
   CALL(g_write(c.get(), data, k, ks, v, vs, static_cast<const int64_t*>(slots), tokens, st));
 }
@@ -208,7 +238,8 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double size = (double)tokens * c->kv_heads * c->head_dim;
   void *k, *v, *data, *slots, *st;
   if (!array(a[1], "data", g_u8, cache_bytes(*c.get()), &data) || !array(a[2], "slots", g_i64, (double)tokens, &slots) ||
-      !array(a[3], "k_out", t16, size, &k) || !array(a[4], "v_out", t16, size, &v) || !stream_of(a[5], a[1], &st))
+      !array(a[3], "k_out", t16, size, &k) || !array(a[4], "v_out", t16, size, &v) || !stream_of(a[5], a[1], &st) ||
+      !one_gpu({{"data", a[1]}, {"slots", a[2]}, {"k_out", a[3]}, {"v_out", a[4]}}))
     return nullptr;
   CALL(g_read(c.get(), data, static_cast<const int64_t*>(slots), tokens, k, v, st));
 }
@@ -228,11 +259,29 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !array(a[3], "page_table", g_i32, (double)p->batch * p->max_pages, &table) ||
       !array(a[4], "seq_lens", g_i32, p->batch, &lens) || !array(a[5], "q_start", g_i32, p->batch + 1.0, &starts))
     return nullptr;
-  if (a[7] != Py_None) {
-    const Ref bytes(PyObject_GetAttr(a[7], n_nbytes));
-    if (!bytes || !as_int(bytes.o, &ws_bytes) || !address(a[7], &ws)) return nullptr;
+  if (a[3] != Py_None) {                            // rows of another length would be read as if they were max_pages long
+    const Ref shape(PyObject_GetAttr(a[3], n_shape));
+    if (!shape) return nullptr;
+    const Py_ssize_t dims = PyTuple_Check(shape.o) ? PyTuple_GET_SIZE(shape.o) : 0;
+    long long columns = p->max_pages;
+    if (dims > 1 && !as_int(PyTuple_GET_ITEM(shape.o, dims - 1), &columns)) return nullptr;
+    if (columns != p->max_pages) {
+      PyErr_Format(PyExc_ValueError, "page_table must have max_pages = %d columns, got %lld", p->max_pages, columns);
+      return nullptr;
+    }
   }
-  if (!stream_of(a[8], a[1], &st)) return nullptr;
+  if (a[7] != Py_None) {
+    const Ref bytes(PyObject_GetAttr(a[7], n_nbytes)), whole(PyObject_CallMethodNoArgs(a[7], n_contiguous));
+    if (!bytes || !whole || !as_int(bytes.o, &ws_bytes) || !address(a[7], &ws)) return nullptr;
+    if (whole.o != Py_True) {
+      PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
+      return nullptr;
+    }
+  }
+  if (!stream_of(a[8], a[1], &st) ||
+      !one_gpu({{"q", a[1]}, {"data", a[2]}, {"page_table", a[3]}, {"seq_lens", a[4]}, {"q_start", a[5]}, {"out", a[6]},
+                {"workspace", a[7]}}))
+    return nullptr;
   CALL(g_attention(p.get(), q, qs, data, static_cast<const int32_t*>(table), static_cast<const int32_t*>(lens),
                    static_cast<const int32_t*>(starts), o, os, ws, (size_t)ws_bytes, st));
 }
