@@ -59,7 +59,6 @@ extern "C" qgemm_status_t qgemm_attention(const qgemm_attention_t* p, const void
   a.os = out_stride;
   a.total_q = (int)p->total_q;
   a.batch = p->batch;
-  a.q_heads = p->q_heads;
   a.kv_heads = p->cache.kv_heads;
   a.ratio = p->q_heads / p->cache.kv_heads;
   a.max_pages = p->max_pages;

@@ -39,7 +39,7 @@ struct AttnArgs {
   const int *table, *lens, *starts;
   uint16_t* out;
   long long qs, os;                // token strides in elements
-  int total_q, batch, q_heads, kv_heads, ratio, max_pages, page, num_pages;
+  int total_q, batch, kv_heads, ratio, max_pages, page, num_pages;
   int codes, params, block;        // bytes of one side's codes, of its parameters, of a block
   unsigned page_mul, page_shift;   // t / page = (t * page_mul) >> (32 + page_shift) for t < 2^30
   int max_q, causal, window;
