@@ -468,7 +468,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
       }
   };
   auto fit = [&](Acc& acc) {
-    if (!wide) return;
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       const float f = s_fit[(wave * NC + nc) * 16 + m];
@@ -624,7 +623,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     }
     Acc acc;
     Weights bp;
-    if (tau || odd || wide) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
+    if (__builtin_expect(tau || odd || wide, 0)) weights(std::true_type{}, step, pr, nstep, npr, tf, acc, bp);
     else weights(std::false_type{}, step, pr, nstep, npr, tf, acc, bp);
     if (kSkew && pr == 0 && late) __syncthreads();
 #pragma unroll
@@ -654,7 +653,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
     {
       Acc acc;
       products(0, 0, acc);
-      fit(acc);
+      if (wide) fit(acc);
       score(0, 0, acc);
     }
     for (int j = 0; j < steps; ++j) {
