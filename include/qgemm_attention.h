@@ -119,7 +119,8 @@ qgemm_status_t qgemm_cache_read(const qgemm_cache_t* cache, const void* data, co
  *   max_q_len in [1, total_q]: an upper bound of a sequence's query tokens; max_pages: the columns
  *   of the page table, max_pages * page_size <= 2^30;
  *   causal 0 or 1; window 0, or with causal the number of latest positions a query sees (>= 1);
- *   scale finite, the factor on q . k.
+ *   scale finite, the factor on q . k.  Queries, keys, values, scale and scale * q . k of up to 2^100 in magnitude
+ *   are covered; beyond that fp32 steps may overflow.
  *   kernel_hint QGEMM_ATTENTION_* (testing and tuning; 0 is the right choice for applications).
  * The launch depends on the descriptor only, never on lengths in device memory.
  */

@@ -34,9 +34,9 @@ enum AttnKind : int { ATTN_ROWS = 1, ATTN_TILES = 2 };
 
 // Tiles kernel: column tiles of 16 query rows per wavefront and wavefronts per workgroup.
 struct TileShape { int cols, waves; };
-// Measured at prompts of 4096 (us): D 64 2x8 147, 3x8 233, 4x4 212; D 128 2x8 183, 1x8 277, 2x4 375;
-// four groups in bf16 2x8 222, 1x8 388, in fp16 (an accumulator per group) 1x8 380, 2x8 752; D 256 1x8 229,
-// 2x4 372, and four groups in bf16 1x8 277, in fp16 1x8 592, 2x4 531.
+// Measured at prompts of 4096 (us): D 64 2x8 146, 3x8 233, 4x4 212; D 128 2x8 187, 1x8 277, 2x4 375;
+// four groups in bf16 2x8 224, 1x8 388, in fp16 (an accumulator per group) 1x8 397, 2x8 752; D 256 1x8 226,
+// 2x4 372, and four groups in bf16 1x8 278, in fp16 1x8 592, 2x4 527.
 constexpr TileShape tile_shape(int dim, int groups, bool bf16) {
   if (groups == 4 && !bf16) return dim == 256 ? TileShape{2, 4} : TileShape{1, 8};
   return dim == 256 ? TileShape{1, 8} : TileShape{2, 8};

@@ -12,9 +12,9 @@
 // most calls have query rows, so with F = 2 or 4 each column group of 16 / F holds the same rows for
 // another 16-token subtile: the softmax then works on full lanes, and its cost per token falls by F.
 //
-// 64 requests of up to 8191 tokens, 64 query and 8 kv heads of 128, bf16: 63.9 us, 4.6 TB/s; 4 requests of
+// 64 requests of up to 8191 tokens, 64 query and 8 kv heads of 128, bf16: 64.2 us, 4.6 TB/s; 4 requests of
 // 100000 to 131000 tokens in groups of 64: 105 us, 5.1 TB/s, what a large copy reaches.  One token over 777
-// takes 9.6 us: a launch (3.2), three dependent memory trips, one step and one join at about 1.3 us each.
+// takes 9.9 us: a launch (3.2), three dependent memory trips, one step and one join at about 1.3 us each.
 #include <type_traits>
 
 #include "qgemm_attention_device.h"

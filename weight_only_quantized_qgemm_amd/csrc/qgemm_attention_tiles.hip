@@ -10,8 +10,8 @@
 // maxima and the sums stay in registers.  The products of the next 32 tokens' keys are issued beside
 // the softmax of the current 32, so that the matrix cores and the vector units work at once.
 //
-// A prompt of 8192 queries of 32 heads of 128, fp16, causal: 677 us, 812 TFLOP/s (plain fp16 products of
-// 8192^3 reach 1164 on the same card).  Of its cycles the matrix cores work 33% and the vector units 58%,
+// A prompt of 8192 queries of 32 heads of 128, fp16, causal: 679 us, 810 TFLOP/s (plain fp16 products of
+// 8192^3 reach 1164 on the same card).  Of its cycles the matrix cores work 32% and the vector units 58%,
 // with two wavefronts on a SIMD: what is left to gain is their overlap.
 //
 // The reference mx of a row bounds score + log2(value scale), in bits, of the tokens it has seen, less kStand:
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   constexpr int BM = 16 * NC * NW, NT = 64 * NW;
   constexpr int kHalves = D == 256 ? 1 : 2, kStep = 32 * kHalves;  // 32-token halves and tokens of a step
   // One body for both halves where two would spill registers (fp16, D 128 in two groups: a prompt of 4096
-  // 300 -> 275 us; elsewhere two are better, D 128 in one group 184 against 205).  With the skew below 256.
+  // 300 -> 275 us; elsewhere two are better, D 128 in one group 184 against 205).  With the skew below 236.
   constexpr int kBodies = !BF && D == 128 && NG == 2 ? 1 : kHalves;
   constexpr int SUBS = 2 * kHalves;                 // 16-token subtiles of a step
   constexpr int KB = kStep * D * 2, PB = SUBS * NG * 4 * 16 * 4;   // bytes of K (and of V) operands, of parameters
