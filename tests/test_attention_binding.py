@@ -110,8 +110,15 @@ def test_one_tensor_elsewhere_is_refused():
 
 def test_page_tables_of_another_width_and_loose_workspaces_are_refused():
     f, args, _ = calls(lambda n, t: Elsewhere(t, 0))[3]
-    for wide in (torch.zeros(1, 3, dtype=torch.int32), torch.zeros(2, 1, dtype=torch.int32)):
+    # of several requests; one request's row may be longer, and a flat table is taken as it is
+    two = dict(args, p=q.attention_problem(args["p"].cache, 2, 3, 4, 3, 2), q_start=Elsewhere(torch.zeros(3, dtype=torch.int32), 0))
+    for wide in (torch.zeros(2, 3, dtype=torch.int32), torch.zeros(4, 1, dtype=torch.int32)):
         with pytest.raises(ValueError, match="max_pages = 2 columns"):
-            f(**dict(args, page_table=Elsewhere(wide, 0)), stream=0)
+            f(**dict(two, page_table=Elsewhere(wide, 0)), stream=0)
+    loose = Elsewhere(torch.zeros(2 << 20, dtype=torch.uint8)[::2], 0)
+    for taken in (dict(args, page_table=Elsewhere(torch.zeros(1, 3, dtype=torch.int32), 0)),
+                  dict(two, page_table=Elsewhere(torch.zeros(4, dtype=torch.int32), 0))):
+        with pytest.raises(ValueError, match="workspace"):               # the check after the table's
+            f(**dict(taken, workspace=loose), stream=0)
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         f(**dict(args, workspace=Elsewhere(torch.zeros(2 << 20, dtype=torch.uint8)[::2], 0)), stream=0)

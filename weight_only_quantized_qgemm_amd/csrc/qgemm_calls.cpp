@@ -259,13 +259,14 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !array(a[3], "page_table", g_i32, (double)p->batch * p->max_pages, &table) ||
       !array(a[4], "seq_lens", g_i32, p->batch, &lens) || !array(a[5], "q_start", g_i32, p->batch + 1.0, &starts))
     return nullptr;
-  if (a[3] != Py_None) {                            // rows of another length would be read as if they were max_pages long
+  if (a[3] != Py_None && p->batch > 1) {            // rows of another length would be read as if they were max_pages long
     const Ref shape(PyObject_GetAttr(a[3], n_shape));
     if (!shape) return nullptr;
-    const Py_ssize_t dims = PyTuple_Check(shape.o) ? PyTuple_GET_SIZE(shape.o) : 0;
-    long long columns = p->max_pages;
-    if (dims > 1 && !as_int(PyTuple_GET_ITEM(shape.o, dims - 1), &columns)) return nullptr;
-    if (columns != p->max_pages) {
+    long long count = 1, columns = p->max_pages;
+    if (PyTuple_Check(shape.o) && PyTuple_GET_SIZE(shape.o) == 2 &&
+        (!as_int(PyTuple_GET_ITEM(shape.o, 0), &count) || !as_int(PyTuple_GET_ITEM(shape.o, 1), &columns)))
+      return nullptr;
+    if (count > 1 && columns != p->max_pages) {
       PyErr_Format(PyExc_ValueError, "page_table must have max_pages = %d columns, got %lld", p->max_pages, columns);
       return nullptr;
     }
