@@ -148,8 +148,8 @@ qgemm_status_t qgemm_attention_workspace_bytes(const qgemm_attention_t* problem,
  *   seq_lens    int32 [batch]: tokens of the sequence in the cache, this call's included (bounded to
  *               [0, max_pages * page_size]).
  *   q_start     int32 [batch + 1]: sequence b owns query rows q_start[b] .. q_start[b + 1] - 1, at most
- *               max_q_len, none is fine; rows of no sequence keep their output.  Where q_start decreases
- *               anywhere, the call writes nothing.
+ *               max_q_len, none is fine (also where it decreases); rows of no sequence keep their output.  Where
+ *               the sequences claim more than total_q rows in all, the call writes nothing.
  * Query i of n of a sequence of length L stands at position L - n + i.  It sees positions t < L, with
  * causal t <= its own, with window t > its own - window.  A query that sees nothing gets zeros.  Bits
  * in slots that no query sees (unwritten pages, the rest of the last page) never reach the output.

@@ -12,6 +12,17 @@ void geometry_seq(int s0, int s1, int len, int total_q, int max_q, int tokens, i
   for (int i = 0; i < 5; ++i) out[i] = v[i];
 }
 
+// the rows that n sequences claim in all, summed in runs of 64
+unsigned geometry_claimed(const int* queries, int n) {
+  unsigned claimed = 0;
+  for (int i = 0; i < n; i += 64) {
+    int run = 0;
+    for (int j = i; j < n && j < i + 64; ++j) run += queries[j];
+    claimed = claim(claimed, run);
+  }
+  return claimed;
+}
+
 // out: lo, hi, per, active, seen of the row tile that begins at row0, of a sequence of n queries and len tokens
 void geometry_tile(int n, int len, int row0, int BM, int ratio, int causal, int window, int step, int splits, int* out) {
   Seq s{};

@@ -25,7 +25,8 @@ def geometry(tmp_path_factory):
         f(*args, out)
         return list(out)
 
-    return (lambda *a: call(lib.geometry_seq, 5, *a)), (lambda *a: call(lib.geometry_tile, 5, *a))
+    lib.geometry_claimed.restype = ctypes.c_uint
+    return (lambda *a: call(lib.geometry_seq, 5, *a)), (lambda *a: call(lib.geometry_tile, 5, *a)), lib.geometry_claimed
 
 
 def windows(g):
@@ -33,7 +34,7 @@ def windows(g):
 
 
 def test_sequences_see_what_their_windows_leave(geometry):
-    seq, _ = geometry
+    seq = geometry[0]
     g = np.random.default_rng(50)
     for _ in range(4000):
         n, length = (int(2 ** g.uniform(0, top)) - 1 for top in (24, 30))
@@ -48,7 +49,7 @@ def test_sequences_see_what_their_windows_leave(geometry):
 @pytest.mark.parametrize("step", [32, 64])
 def test_parts_cover_each_row_tile(geometry, step):
     # every token that a row of the tile sees lies in one of the parts, and there are no more parts than workgroups
-    _, tile = geometry
+    tile = geometry[1]
     g = np.random.default_rng([51, step])
     for _ in range(6000):
         BM, ratio, splits = int(g.choice([128, 256])), int(g.choice([1, 2, 3, 5, 8, 16, 64])), int(g.integers(1, 33))
@@ -71,7 +72,7 @@ def test_parts_cover_each_row_tile(geometry, step):
 
 def test_the_largest_window_is_no_window(geometry):
     # 2048 queries of four heads a kv head, one part: all 32 steps of the last row tile are in it
-    seq, tile = geometry
+    seq, tile, _ = geometry
     for window in (0, LARGEST - 100, LARGEST):
         assert tile(2048, 2048, 7936, 256, 4, 1, window, 64, 1) == [0, 2048, 32, 1, 0]
         assert tile(200, 100, 0, 256, 1, 1, window, 64, 1) == [0, 100, 2, 1, 0]   # more queries than tokens
@@ -86,34 +87,46 @@ def planned(batch, total_q, max_q, q_heads, kv_heads, dim, group, dtype, max_pag
     return int(f["rows"]), int(f["grid"]) // kv_heads // int(f["splits"])
 
 
-def test_row_tiles_of_rising_starts_fit_the_launch(geometry):
-    # whatever stands in q_start, as long as it does not decrease: no more row tiles than planned, so none's
-    # tickets or partial results lie past the workspace
-    seq, _ = geometry
+def claimed(geometry, n):
+    return geometry[2]((ctypes.c_int * len(n))(*n), len(n))
+
+
+def test_row_tiles_fit_the_launch_unless_too_many_rows_are_claimed(geometry):
+    # whatever stands in q_start: no more row tiles than planned, so none's tickets or partial results lie past
+    # the workspace, or more rows than total_q, where the kernels compute nothing
+    seq = geometry[0]
     g = np.random.default_rng(52)
-    for _ in range(1500):
+    over = 0
+    for case in range(3000):
         batch, max_q = int(2 ** g.uniform(0, 6)), int(2 ** g.uniform(0, 11))
         total = int(g.integers(max_q, batch * max_q + 1))
         ratio, kv, dim = int(g.choice([1, 3, 4, 8])), int(g.choice([1, 2, 8])), int(g.choice([64, 128, 256]))
         rows, tiles = planned(batch, total, max_q, ratio * kv, kv, dim, dim, int(g.integers(0, 2)), int(2 ** g.uniform(0, 10)),
                               q.ATTENTION_TILES)
-        starts = np.sort(g.integers(-100, total + 100, batch + 1))
+        starts = g.integers(-100, total + 100, batch + 1)
+        if case % 3:
+            starts = np.sort(starts)
+        if case % 3 == 1:                                             # padded with zeros
+            starts[int(g.integers(1, batch + 1)):] = 0
         if g.random() < 0.2:
             starts[-1] = LARGEST
         n = [seq(int(a), int(b), 500, total, max_q, 1 << 20, 0)[1] for a, b in zip(starts, starts[1:])]
-        assert min(n) >= 0 and sum(n) <= total and sum(-(-ratio * x // rows) for x in n) <= tiles
+        rising = bool(np.all(np.diff(starts) >= 0))
+        assert min(n) >= 0 and claimed(geometry, n) == sum(n) and (sum(n) <= total or not rising)
+        if sum(n) > total:
+            over += 1
+        else:
+            assert sum(-(-ratio * x // rows) for x in n) <= tiles
+    assert over > 100
+    # sums far past 32 bits stay above any total_q
+    assert claimed(geometry, [1 << 24] * 65535) == 1 << 30 and claimed(geometry, [1 << 24] * 64) == 1 << 30
 
 
 @pytest.mark.parametrize("starts,total,max_q", [([0, 1000, 0, 1000, 0], 1000, 1000), ([0, 900, 0, 900, 0, 900, 0, 900, 0], 1000, 900)])
-def test_decreasing_starts_are_told(geometry, starts, total, max_q):
-    # such starts count rows more than once, and more row tiles than the launch has: the kernels compute nothing
-    seq, _ = geometry
+def test_starts_that_claim_too_much_count_more_tiles_than_planned(geometry, starts, total, max_q):
+    n = [geometry[0](a, b, 500, total, max_q, 1 << 20, 0)[1] for a, b in zip(starts, starts[1:])]
     rows, tiles = planned(len(starts) - 1, total, max_q, 32, 8, 128, 128, q.DT_F16, 200, q.ATTENTION_TILES)
-    bounded = [max(min(b, total) - a, 0) for a, b in zip(starts, starts[1:])]
-    assert sum(-(-4 * n // rows) for n in bounded) > tiles
-    assert [seq(a, b, 500, total, max_q, 1 << 20, 0)[1] for a, b in zip(starts, starts[1:])] == \
-        [n if b >= a else -1 for n, a, b in zip(bounded, starts, starts[1:])]
-    assert seq(LARGEST, -LARGEST, 5, total, max_q, 1 << 20, 0)[1] == -1
+    assert sum(-(-4 * x // rows) for x in n) > tiles and claimed(geometry, n) > total
 
 
 # ----------------------------------------------------------------------------- the choice of kernel

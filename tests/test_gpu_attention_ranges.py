@@ -36,10 +36,10 @@ def test_windows_wider_than_any_context(q, case, hint):
 
 
 @pytest.mark.parametrize("hint,total,ratio", [(1, 300, 4), (2, 300, 4), (1, 3, 2), (0, 1000, 4)])
-def test_decreasing_starts_write_nothing(q, hint, total, ratio):
-    # q_start that decreases somewhere: no output, no byte behind the workspace, and the workspace is ready
-    # for the next call
-    say(f"case attention decreasing starts hint={hint} total={total}")
+def test_starts_that_claim_more_rows_than_there_are_write_nothing(q, hint, total, ratio):
+    # no output, no byte behind the workspace, and the workspace is ready for the next call; starts that decrease
+    # without that own no rows there
+    say(f"case attention starts that claim too much hint={hint} total={total}")
     s = _sequences(q, "f16", [total, 0, 0, 0], [1200, 0, 0, 0], 2 * ratio, 2, 64, 64, 16, 410)
     s["table"] = s["table"][:1].repeat(4, 1)
     s["lens"].fill_(1200)
@@ -50,16 +50,22 @@ def test_decreasing_starts_write_nothing(q, hint, total, ratio):
     guarded = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
     guarded[n:] = 0x5A
     qx = up(s["q"], "f16")
-    good = torch.full_like(qx, 7.0)
-    rising = torch.tensor([0, total, total, total, total], dtype=torch.int32, device="cuda")
-    q.attention(p, qx, s["data"], s["table"], s["lens"], rising, good, q.alloc_attention_workspace(p))
-    for starts in ([0, total, 0, total, 0], [0, total, 0, total, total], [total, 0, total, total, total], [5, 4, 4, 4, 4]):
+
+    def call(starts, ws):
         out = torch.full_like(qx, 7.0)
-        q.attention(p, qx, s["data"], s["table"], s["lens"], torch.tensor(starts, dtype=torch.int32, device="cuda"), out, guarded[:n])
+        q.attention(p, qx, s["data"], s["table"], s["lens"], torch.tensor(starts, dtype=torch.int32, device="cuda"), out, ws)
         torch.cuda.synchronize()
-        assert (out == 7).all() and (guarded[n:] == 0x5A).all(), starts
-        q.attention(p, qx, s["data"], s["table"], s["lens"], rising, out, guarded[:n])
-        assert torch.equal(out, good), starts
+        assert (guarded[n:] == 0x5A).all(), starts
+        return out
+
+    good = call([0, total, total, total, total], q.alloc_attention_workspace(p))
+    for starts in ([0, total, 0, total, 0], [0, total, 0, total, total], [0, total, 1, total, total]):
+        assert (call(starts, guarded[:n]) == 7).all(), starts
+        assert torch.equal(call([0, total, total, total, total], guarded[:n]), good), starts
+    part = call([0, 2, 2, 2, 2], guarded[:n])
+    for starts, want in (([0, total, 0, 0, 0], good), ([total, 0, total, total, total], good), ([0, 2, 1, 1, 0], part), ([0, 2, 0, 0, -5], part)):
+        assert torch.equal(call(starts, guarded[:n]), want), starts
+    assert (part[2:] == 7).all() and not (part[:2] == 7).all(-1).any()
 
 
 def test_short_contexts_in_very_wide_tables(q):

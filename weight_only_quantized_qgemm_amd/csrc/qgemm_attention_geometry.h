@@ -18,21 +18,27 @@ constexpr int bounded_window(int window) { return lesser(window, kWindowMost); }
 
 // A sequence's geometry, every value bounded.
 struct Seq {
-  int start, n, len;               // first query row, queries (or -1), tokens
+  int start, n, len;               // first query row, queries, tokens
   int lo, hi;                      // tokens any query can see: lo a multiple of 16
 };
-// From q_start[b], q_start[b + 1] and seq_lens[b]; tokens = max_pages * page_size.  n is -1 where q_start decreases:
-// the rows of such starts may be counted more than once, and launches and workspaces are made for total_q of
-// them.  Of starts that never decrease the bounded ranges do not overlap.
+// From q_start[b], q_start[b + 1] and seq_lens[b]; tokens = max_pages * page_size.
 constexpr Seq seq_of(int s0, int s1, int len, int total_q, int max_q, int tokens, int window) {
   Seq s{};
   s.start = lesser(greater(s0, 0), total_q);
-  s.n = s1 < s0 ? -1 : lesser(greater(lesser(s1, total_q) - s.start, 0), max_q);
+  s.n = lesser(greater(lesser(s1, total_q) - s.start, 0), max_q);
   s.len = lesser(greater(len, 0), tokens);
   s.hi = s.len;
   s.lo = window ? greater(s.len - s.n - window + 1, 0) & ~15 : 0;
   if (s.lo > s.hi) s.lo = s.hi & ~15;
   return s;
+}
+
+// Launches and workspaces are made for total_q query rows.  Starts that decrease and rise again may claim more,
+// and more row tiles than there are workgroups and partial results; no others do.  The claimed rows are summed
+// in runs of 64 sequences, whose sum is at most 2^30, and stop there.
+constexpr unsigned claim(unsigned claimed, int run) {
+  const unsigned sum = claimed + (unsigned)run;
+  return sum < 1u << 30 ? sum : 1u << 30;
 }
 
 // Tiles kernel: the tokens that rows row0 .. row_end - 1 see, and how a launch of `splits` workgroups per row tile

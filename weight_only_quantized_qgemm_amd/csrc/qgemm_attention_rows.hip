@@ -78,13 +78,13 @@ __global__ __launch_bounds__(64 * W, 2) void attention_rows(AttnArgs a) {
   auto units_of = [&](const Seq& s) { return max(1, (s.hi - s.lo + 63) / 64); };
   Seq mine_seq = lane < a.batch ? load_seq(a, lane) : Seq{0, 0, 0, 0, 0};      // the first 64 stay at hand
   int total = 0;
-  bool down = false;                                // starts that decrease: nothing is computed
+  unsigned claimed = 0;                             // more query rows than total_q: nothing is computed
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     const Seq x = b0 == 0 ? mine_seq : b0 + lane < a.batch ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
-    down |= __any(x.n < 0);
+    claimed = claim(claimed, wave_sum(x.n));
     total += wave_sum(tiles_of(x) * units_of(x));
   }
-  if (down || !total) return;
+  if (claimed > (unsigned)a.total_q || !total) return;
   const int grid = (int)gridDim.x;
   const int piece = total <= grid * a.piece_share ? max(a.piece_least, (2 * total + grid - 1) / grid) : 1;
   // each segment also counts for kOver units, about what its start and its end cost in long work

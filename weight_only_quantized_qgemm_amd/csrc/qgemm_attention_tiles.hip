@@ -77,22 +77,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles(AttnArgs a) {
   const int kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
   const int split = rest % a.splits;
   int entry = rest / a.splits;
-  auto tiles_in = [&](int b) {
-    const int n = b < a.batch ? load_seq(a, b).n : 0;
-    return n < 0 ? -1 : (a.ratio * n + BM - 1) / BM;
-  };
+  auto queries_in = [&](int b) { return b < a.batch ? load_seq(a, b).n : 0; };
+  auto tiles_in = [&](int n) { return (a.ratio * n + BM - 1) / BM; };
   int total = 0;
-  bool down = false;                                // starts that decrease: nothing is computed
+  unsigned claimed = 0;                             // more than total_q: nothing is computed
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const int tiles = tiles_in(b0 + lane);
-    down |= __any(tiles < 0);
-    total += wave_sum(tiles);
+    const int n = queries_in(b0 + lane);
+    claimed = claim(claimed, wave_sum(n));
+    total += wave_sum(tiles_in(n));
   }
-  if (down || entry >= total) return;
+  if (claimed > (unsigned)a.total_q || entry >= total) return;
   entry = total - 1 - entry;
   int b = 0, before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const int u = wave_scan(tiles_in(b0 + lane));
+    const int u = wave_scan(tiles_in(queries_in(b0 + lane)));
     const unsigned long long past = __ballot(before + u > entry);
     if (past) {
       const int l = __builtin_ctzll(past);
