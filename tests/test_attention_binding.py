@@ -63,8 +63,11 @@ assert len(seen) == 8 and all("data must be" in s for s in seen), seen
 class Elsewhere:
     """A tensor that says it lies on another device; its memory is the host's, which the checks must keep from the library."""
 
-    def __init__(self, x, device):
-        self.x, self.device = x, device
+    def __init__(self, x, device, pinned=False):
+        self.x, self.device, self.pinned = x, device, pinned
+
+    def is_pinned(self):
+        return self.pinned
 
     def get_device(self):
         return self.device
@@ -106,6 +109,13 @@ def test_one_tensor_elsewhere_is_refused():
                 f, args, _ = calls(lambda n, t: Elsewhere(t, device if n == odd else 0))[i]
                 with pytest.raises(ValueError, match=text):
                     f(**args, stream=0)
+
+
+def test_pinned_tensors_pass():
+    # the GPU reads them where they lie: the next wrong tensor is named
+    f, args, _ = calls(lambda n, t: Elsewhere(t, -1 if n == "seq_lens" else 0, n == "seq_lens"))[3]
+    with pytest.raises(ValueError, match="^out is on device 1, q on device 0"):
+        f(**dict(args, out=Elsewhere(args["out"].x, 1)), stream=0)
 
 
 def test_page_tables_of_another_width_and_loose_workspaces_are_refused():

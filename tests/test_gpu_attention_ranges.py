@@ -94,3 +94,14 @@ def test_short_contexts_in_very_wide_tables(q):
     assert not outs[0][lens == 0].any() and not outs[1][lens == 0].any()
     # each within a rounding to bf16 and to fp16 weights of the values' mean
     assert (outs[0] - outs[1]).abs().max() <= 2.0 ** -8 * 2 * outs[1].abs().max() + 2.0 ** -10 * v.float().abs().max()
+
+
+def test_pinned_lengths(q):
+    # small arrays in pinned memory are read by the kernels where they lie
+    say("case attention pinned lengths and starts")
+    s = _sequences(q, "f16", [1, 3], [100, 70], 4, 2, 128, 128, 16, 420)
+    want = _run(q, s, "f16", 4)
+    held = dict(s, lens=s["lens"].cpu().pin_memory(), starts=s["starts"].cpu().pin_memory())
+    assert torch.equal(_run(q, held, "f16", 4), want)
+    with pytest.raises(ValueError, match="seq_lens must be on the GPU"):
+        _run(q, dict(s, lens=s["lens"].cpu()), "f16", 4)

@@ -20,7 +20,7 @@ decltype(&qgemm_cache_read) g_read;
 decltype(&qgemm_attention) g_attention;
 PyObject *g_f16, *g_bf16, *g_f32, *g_i32, *g_i64, *g_u8;
 PyObject *g_raw_stream, *g_stream;                 // torch's query by device index, or None; the general one
-PyObject *n_shape, *n_stride, *n_dtype, *n_data_ptr, *n_numel, *n_contiguous, *n_device, *n_nbytes;
+PyObject *n_shape, *n_stride, *n_dtype, *n_data_ptr, *n_numel, *n_contiguous, *n_device, *n_nbytes, *n_pinned;
 
 // A reference that ends with its scope.
 struct Ref {
@@ -102,6 +102,13 @@ bool array(PyObject* x, const char* name, PyObject* type, double numel, void** p
   return address(x, p);
 }
 
+// Whether the GPU reads a tensor of the host where it lies.
+bool pinned(PyObject* x) {
+  const Ref r(PyObject_CallMethodNoArgs(x, n_pinned));
+  if (!r) PyErr_Clear();
+  return r.o == Py_True;
+}
+
 // The handle of `stream`; by default that of torch's current stream on x's device.
 bool stream_of(PyObject* stream, PyObject* x, void** h) {
   *h = nullptr;
@@ -110,14 +117,16 @@ bool stream_of(PyObject* stream, PyObject* x, void** h) {
     if (!device) return false;
     const long index = PyLong_AsLong(device.o);
     if (index == -1 && PyErr_Occurred()) return false;
-    if (index < 0) {
-      PyErr_SetString(PyExc_ValueError, "tensors must be on the GPU");
+    if (index >= 0) {
+      const Ref handle(PyObject_CallOneArg(g_raw_stream, device.o));
+      if (!handle) return false;
+      *h = PyLong_AsVoidPtr(handle.o);
+      return *h || !PyErr_Occurred();
+    }
+    if (!pinned(x)) {
+      PyErr_SetString(PyExc_ValueError, "tensors must be on the GPU, or pinned");
       return false;
     }
-    const Ref handle(PyObject_CallOneArg(g_raw_stream, device.o));
-    if (!handle) return false;
-    *h = PyLong_AsVoidPtr(handle.o);
-    return *h || !PyErr_Occurred();
   }
   const Ref handle(PyObject_CallFunctionObjArgs(g_stream, stream, x, nullptr));
   if (!handle) return false;
@@ -126,7 +135,8 @@ bool stream_of(PyObject* stream, PyObject* x, void** h) {
   return *h || !PyErr_Occurred();
 }
 
-// All tensors of a call lie on one GPU: an address of the host's, or of another device, would fault there.
+// All tensors of a call lie on one GPU, or in pinned memory: another address of the host's, or of another device, would
+// fault there.
 struct Named { const char* name; PyObject* x; };
 bool one_gpu(std::initializer_list<Named> tensors) {
   const char* first = nullptr;
@@ -136,7 +146,8 @@ bool one_gpu(std::initializer_list<Named> tensors) {
     long long index;
     if (!call_int(t.x, n_device, &index)) return false;
     if (index < 0) {
-      PyErr_Format(PyExc_ValueError, "%s must be on the GPU", t.name);
+      if (pinned(t.x)) continue;
+      PyErr_Format(PyExc_ValueError, "%s must be on the GPU, or pinned", t.name);
       return false;
     }
     if (!first) {
@@ -321,7 +332,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 PyMODINIT_FUNC PyInit__calls() {
   const struct { PyObject** o; const char* s; } names[] = {
       {&n_shape, "shape"}, {&n_stride, "stride"}, {&n_dtype, "dtype"}, {&n_data_ptr, "data_ptr"}, {&n_numel, "numel"},
-      {&n_contiguous, "is_contiguous"}, {&n_device, "get_device"}, {&n_nbytes, "nbytes"}};
+      {&n_contiguous, "is_contiguous"}, {&n_device, "get_device"}, {&n_nbytes, "nbytes"}, {&n_pinned, "is_pinned"}};
   for (const auto& x : names)
     if (!(*x.o = PyUnicode_InternFromString(x.s))) return nullptr;
   return PyModule_Create(&module);
