@@ -1,4 +1,4 @@
-"""Python binding of the qgemm C ABI (include/qgemm.h, include/qgemm_attention.h): argument marshalling only.
+"""Python binding of the qgemm C ABI (include/qgemm.h, qgemm_attention.h, qgemm_w8a8.h): argument marshalling only.
 
 Every step of the GEMM runs in the HIP library ``libqgemm.so`` built next to this file;
 torch serves only for device memory and the current stream.  Importing this package
@@ -41,6 +41,8 @@ KERNEL_AUTO, KERNEL_DECODE, KERNEL_PREFILL, KERNEL_PREFILL_STREAMK, KERNEL_PREFI
 
 
 ATTENTION_AUTO, ATTENTION_ROWS, ATTENTION_TILES = range(3)
+GATE_NONE, GATE_SILU, GATE_GELU_TANH = range(3)
+W8A8_AUTO, W8A8_ROWS, W8A8_TILES = range(3)
 
 
 class Problem(ctypes.Structure):
@@ -74,7 +76,20 @@ class Attention(ctypes.Structure):
                 ("reserved", ctypes.c_int32 * 2)]
 
 
+class AddNorm(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class W8A8(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("kernel_hint", ctypes.c_int32), ("split_hint", ctypes.c_int32),
+                ("tile_hint", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 assert (ctypes.sizeof(NormRope), ctypes.sizeof(Cache), ctypes.sizeof(Attention)) == (48, 32, 80)
+assert (ctypes.sizeof(AddNorm), ctypes.sizeof(W8A8)) == (32, 48)
 
 _P = ctypes.POINTER(Problem)
 _vp = ctypes.c_void_p
@@ -100,10 +115,17 @@ _lib.qgemm_cache_read.argtypes = [_CP, _vp, _vp, _i64, _vp, _vp, _vp]
 _lib.qgemm_attention_workspace_bytes.argtypes = [_AP, ctypes.POINTER(_sz)]
 _lib.qgemm_attention.argtypes = [_AP, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]
 _lib.qgemm_attention_describe.argtypes = [_AP, ctypes.c_char_p, _sz]
+_ANP, _W8P = ctypes.POINTER(AddNorm), ctypes.POINTER(W8A8)
+_lib.qgemm_add_norm.argtypes = [_ANP, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp]
+_lib.qgemm_w8a8_quantize.argtypes = [_W8P, _vp, _vp, _vp]
+_lib.qgemm_w8a8_workspace_bytes.argtypes = [_W8P, ctypes.POINTER(_sz)]
+_lib.qgemm_w8a8_run.argtypes = [_W8P, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.qgemm_w8a8_describe.argtypes = [_W8P, ctypes.c_char_p, _sz]
 NO_ALLOC_SCRATCH_BYTES = (32 << 20) + (64 << 10)    # QGEMM_NO_ALLOC_SCRATCH_BYTES of include/qgemm.h
 for _f in ("qgemm_quantize", "qgemm_pack", "qgemm_workspace_bytes", "qgemm_run", "qgemm_run_bias",
            "qgemm_run_no_alloc", "qgemm_plan_describe", "qgemm_qk_norm_rope", "qgemm_cache_bytes", "qgemm_cache_write",
-           "qgemm_cache_read", "qgemm_attention_workspace_bytes", "qgemm_attention", "qgemm_attention_describe"):
+           "qgemm_cache_read", "qgemm_attention_workspace_bytes", "qgemm_attention", "qgemm_attention_describe",
+           "qgemm_add_norm", "qgemm_w8a8_quantize", "qgemm_w8a8_workspace_bytes", "qgemm_w8a8_run", "qgemm_w8a8_describe"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 lib = _lib
@@ -288,7 +310,7 @@ def version():
 
 
 # ----------------------------------------------------------------------------- attention operators
-# The device calls below are made once per layer and token: their tensors are checked, and the C function
+# The device calls below, those of the 8-bit operators too, are made once per layer and token: their tensors are checked, and the C function
 # called, in csrc/qgemm_calls.cpp.  A tensor of the wrong type, shape or strides, or that is not on the call's GPU,
 # raises ValueError.
 def _stream(stream, x):
@@ -312,8 +334,10 @@ class _Calls:
                     raise ImportError("the _calls module is missing or of another Python: build it with "
                                       "`python -m weight_only_quantized_qgemm_amd._build`") from e
                 module.setup(*(ctypes.cast(f, _vp).value for f in (_lib.qgemm_qk_norm_rope, _lib.qgemm_cache_write,
-                                                                   _lib.qgemm_cache_read, _lib.qgemm_attention)),
+                                                                   _lib.qgemm_cache_read, _lib.qgemm_attention,
+                                                                   _lib.qgemm_add_norm, _lib.qgemm_w8a8_run)),
                              torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+                             torch.float8_e4m3fn,
                              # the raw stream handle of a device, without building a Stream object for it
                              getattr(torch._C, "_cuda_getCurrentRawStream", None), _stream)
                 _calls_ready = module
@@ -398,5 +422,64 @@ def attention_describe(p):
 def attention(p, q, data, page_table, seq_lens, q_start, out, workspace=None, stream=None):
     """Enqueue attention of q [total_q, q_heads, head_dim] over the cache into out (qgemm_attention)."""
     st = _calls_ready.attention(p, q, data, page_table, seq_lens, q_start, out, workspace, stream)
+    if st:
+        _check(st)
+
+
+# ----------------------------------------------------------------------------- 8-bit operators
+# Values in 8 bits are torch.float8_e4m3fn codes and fp32 scales: of activations [K / 128, tokens], of weights
+# [row blocks, K / 128].
+def add_norm_problem(tokens, dim, dtype=DT_F16, out_dtype=None, norm=True, eps=1e-6):
+    """Descriptor of add_norm; out_dtype is DT_FP8_E4M3 or, by default, dtype."""
+    return AddNorm(tokens, dim, dtype, dtype if out_dtype is None else out_dtype, int(norm), eps, 0)
+
+
+def add_norm(p, x, residual, weight, sum_out, y, y_scales=None, stream=None):
+    """Enqueue y = norm(x + residual) * weight and sum_out = x + residual (qgemm_add_norm).  x, residual and
+    sum_out are [tokens, dim], each with its own token stride; residual, weight and sum_out may be None."""
+    st = _calls_ready.add_norm(p, x, residual, weight, sum_out, y, y_scales, stream)
+    if st:
+        _check(st)
+
+
+def w8a8_problem(M, N, K, out_dtype=DT_BF16, gate=GATE_NONE, kernel_hint=W8A8_AUTO, split_hint=0, tile_hint=0):
+    """Descriptor of a product of 8-bit activations and weights, or with a gate of a pair of them."""
+    return W8A8(M, N, K, out_dtype, gate, kernel_hint, split_hint, tile_hint, 0)
+
+
+def w8a8_quantize(p, w):
+    """fp32 [rows, K] weights (rows = N, or 2 N with a gate) -> (codes uint8 [rows, K], scales fp32
+    [row blocks, K / 128]), host numpy.  On the GPU the codes are viewed as torch.float8_e4m3fn."""
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    parts = 1 if p.gate == GATE_NONE else 2
+    assert w.shape == (parts * p.N, p.K)
+    codes = np.empty(w.shape, np.uint8)
+    scales = np.empty((parts * -(-int(p.N) // 128), p.K // 128), np.float32)
+    _check(_lib.qgemm_w8a8_quantize(ctypes.byref(p), w.ctypes.data, codes.ctypes.data, scales.ctypes.data))
+    return codes, scales
+
+
+def w8a8_workspace_bytes(p):
+    n = _sz(0)
+    _check(_lib.qgemm_w8a8_workspace_bytes(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_w8a8_workspace(p, device="cuda"):
+    """A zero-filled workspace of the size qgemm_w8a8_workspace_bytes reports (or None)."""
+    n = w8a8_workspace_bytes(p)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def w8a8_describe(p):
+    """The launch qgemm_w8a8_run would make for this problem, as one line of text."""
+    buf = ctypes.create_string_buffer(512)
+    _check(_lib.qgemm_w8a8_describe(ctypes.byref(p), buf, 512))
+    return buf.value.decode()
+
+
+def w8a8_run(p, A, a_scales, W, w_scales, out, out_scales=None, workspace=None, stream=None):
+    """Enqueue the product, or with a gate the gated pair, of A [M, K] and W (qgemm_w8a8_run)."""
+    st = _calls_ready.w8a8_run(p, A, a_scales, W, w_scales, out, out_scales, workspace, stream)
     if st:
         _check(st)

@@ -17,7 +17,7 @@ OBJ_DIR = os.path.join(PKG, "_build", "obj")
 # measurement helpers for the benchmark (streaming-read kernel, host time per call): a library
 # of their own, outside the qgemm ABI
 PROBE_LIB = os.path.join(PKG, "libqgemm_probe.so")
-# Python entry points of the attention operators' device calls: host code, linked with neither of them
+# Python entry points of the attention and 8-bit operators' device calls: host code, linked with neither of them
 CALLS_LIB = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 # Weight formats (the Format enum of csrc/qgemm_internal.h).  Each kernel source is compiled
 # once per format (-DQGEMM_FMT_UNIT), so the many kernel instances build in parallel.
@@ -26,7 +26,8 @@ N_FORMATS = 6
 # other sources whole.
 N_ATTN_UNITS = 6
 UNITS = ([("qgemm_host.cpp", []), ("qgemm_run.hip", []), ("qgemm_attention_host.cpp", []), ("qgemm_heads.hip", []),
-          ("qgemm_cache.hip", []), ("qgemm_attention.hip", [])]
+          ("qgemm_cache.hip", []), ("qgemm_attention.hip", []), ("qgemm_w8a8_host.cpp", []), ("qgemm_w8a8.hip", []),
+          ("qgemm_add_norm.hip", []), ("qgemm_w8a8_rows.hip", []), ("qgemm_w8a8_tiles.hip", [])]
          + [(k, [f"-DQGEMM_ATTN_UNIT={u}"]) for k in ("qgemm_attention_rows.hip", "qgemm_attention_tiles.hip")
             for u in range(N_ATTN_UNITS)]
          + [(k, [f"-DQGEMM_FMT_UNIT={f}"]) for k in ("qgemm_decode.hip", "qgemm_prefill.hip", "qgemm_prefill_tw.hip")
@@ -57,7 +58,7 @@ def _run(cmd):
 
 
 def build_calls():
-    """Compile the Python module of the attention operators' calls; returns the compiler's messages."""
+    """Compile the Python module of the attention and 8-bit operators' calls; returns the compiler's messages."""
     tmp = CALLS_LIB + ".tmp"
     rc, lines = _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
                       "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "qgemm_calls.cpp"), "-o", tmp])

@@ -1,8 +1,8 @@
 """Host-sanitizer build of the library, for the CPU tests of the host code (not shipped).
 
 The host code -- validation, launch planning, the quantizer and the packer (qgemm_host.cpp,
-qgemm_attention_host.cpp) and the entry points (qgemm_run.hip, qgemm_heads.hip, qgemm_cache.hip,
-qgemm_attention.hip) -- is recompiled with AddressSanitizer and
+qgemm_attention_host.cpp, qgemm_w8a8_host.cpp) and the entry points (qgemm_run.hip, qgemm_heads.hip,
+qgemm_cache.hip, qgemm_attention.hip, qgemm_w8a8.hip, qgemm_add_norm.hip) -- is recompiled with AddressSanitizer and
 UndefinedBehaviorSanitizer on its host pass only, and linked with the kernel objects of the
 regular build (_build/obj) into _build/libqgemm_asan.so.  A process that loads it must
 preload the sanitizer runtime (tests/test_host_asan.py runs the packer and ABI tests that way).
@@ -13,7 +13,8 @@ import _build as B
 
 ASAN_LIB = os.path.join(B.PKG, "_build", "libqgemm_asan.so")
 HOST_UNITS = [("qgemm_host.cpp", []), ("qgemm_run.hip", []), ("qgemm_attention_host.cpp", []), ("qgemm_heads.hip", []),
-              ("qgemm_cache.hip", []), ("qgemm_attention.hip", [])]
+              ("qgemm_cache.hip", []), ("qgemm_attention.hip", []), ("qgemm_w8a8_host.cpp", []), ("qgemm_w8a8.hip", []),
+              ("qgemm_add_norm.hip", [])]
 # sanitizers on the host compilation only (device code is built exactly as in the library)
 HOST_SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                  "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all"]

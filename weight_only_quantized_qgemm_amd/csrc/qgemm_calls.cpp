@@ -1,4 +1,4 @@
-// Python entry points of the attention operators' device calls (module _calls): the tensors' checks and
+// Python entry points of the attention and 8-bit operators' device calls (module _calls): the tensors' checks and
 // the call of the C ABI in one C function.  The calls are made once per layer and token, and their
 // arguments are up to twelve tensors: checked in Python they kept the host busy for longer than the
 // smallest launches run (16 tokens' heads: 8.4 us a call against 4 us on the GPU).
@@ -11,6 +11,7 @@
 #include <initializer_list>
 
 #include "../../include/qgemm_attention.h"
+#include "../../include/qgemm_w8a8.h"
 
 namespace {
 
@@ -18,7 +19,9 @@ decltype(&qgemm_qk_norm_rope) g_rope;
 decltype(&qgemm_cache_write) g_write;
 decltype(&qgemm_cache_read) g_read;
 decltype(&qgemm_attention) g_attention;
-PyObject *g_f16, *g_bf16, *g_f32, *g_i32, *g_i64, *g_u8;
+decltype(&qgemm_add_norm) g_add_norm;
+decltype(&qgemm_w8a8_run) g_w8a8;
+PyObject *g_f16, *g_bf16, *g_f32, *g_i32, *g_i64, *g_u8, *g_e4m3;
 PyObject *g_raw_stream, *g_stream;                 // torch's query by device index, or None; the general one
 PyObject *n_shape, *n_stride, *n_dtype, *n_data_ptr, *n_numel, *n_contiguous, *n_device, *n_nbytes, *n_pinned;
 
@@ -78,6 +81,28 @@ bool rows(PyObject* x, const char* name, long long tokens, long long heads, long
     return false;
   }
   *stride = tokens > 1 ? s[0] : heads * dim;     // one token has no distance to the next; torch may report any
+  return address(x, p);
+}
+
+// Address of a contiguous [n0, n1] tensor.
+bool matrix(PyObject* x, const char* name, PyObject* type, long long n0, long long n1, void** p) {
+  *p = nullptr;
+  if (x == Py_None) return true;
+  const Ref shape(PyObject_GetAttr(x, n_shape)), dtype(PyObject_GetAttr(x, n_dtype));
+  if (!shape || !dtype) return false;
+  const Ref whole(PyObject_CallMethodNoArgs(x, n_contiguous));
+  if (!whole) return false;
+  long long d[2] = {-1, -1};
+  if (PyTuple_Check(shape.o) && PyTuple_GET_SIZE(shape.o) == 2)
+    for (int i = 0; i < 2; ++i)
+      if (!as_int(PyTuple_GET_ITEM(shape.o, i), d + i)) return false;
+  if (dtype.o != type || whole.o != Py_True || d[0] != n0 || d[1] != n1) {
+    const Ref plain(PySequence_Tuple(shape.o)), strides(PyObject_CallMethodNoArgs(x, n_stride));
+    if (plain && strides)
+      PyErr_Format(PyExc_ValueError, "%s must be %S [%lld, %lld], contiguous, got %S %R with strides %R", name, type, n0, n1,
+                   dtype.o, plain.o, strides.o);
+    return false;
+  }
   return address(x, p);
 }
 
@@ -255,6 +280,18 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CALL(g_read(c.get(), data, static_cast<const int64_t*>(slots), tokens, k, v, st));
 }
 
+// Address and bytes of a workspace.
+bool workspace(PyObject* x, void** p, long long* size) {
+  *p = nullptr;
+  *size = 0;
+  if (x == Py_None) return true;
+  const Ref bytes(PyObject_GetAttr(x, n_nbytes)), whole(PyObject_CallMethodNoArgs(x, n_contiguous));
+  if (!bytes || !whole || !as_int(bytes.o, size) || !address(x, p)) return false;
+  if (whole.o == Py_True) return true;
+  PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
+  return false;
+}
+
 // (p, q, data, page_table, seq_lens, q_start, out, workspace, stream)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count("attention", n, 9)) return nullptr;
@@ -282,14 +319,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return nullptr;
     }
   }
-  if (a[7] != Py_None) {
-    const Ref bytes(PyObject_GetAttr(a[7], n_nbytes)), whole(PyObject_CallMethodNoArgs(a[7], n_contiguous));
-    if (!bytes || !whole || !as_int(bytes.o, &ws_bytes) || !address(a[7], &ws)) return nullptr;
-    if (whole.o != Py_True) {
-      PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
-      return nullptr;
-    }
-  }
+  if (!workspace(a[7], &ws, &ws_bytes)) return nullptr;
   if (!stream_of(a[8], a[1], &st) ||
       !one_gpu({{"q", a[1]}, {"data", a[2]}, {"page_table", a[3]}, {"seq_lens", a[4]}, {"q_start", a[5]}, {"out", a[6]},
                 {"workspace", a[7]}}))
@@ -298,11 +328,56 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    static_cast<const int32_t*>(starts), o, os, ws, (size_t)ws_bytes, st));
 }
 
-// (addresses of the four C functions, the six dtypes, the two stream queries)
+// (p, x, residual, weight, sum_out, y, y_scales, stream)
+PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count("add_norm", n, 8)) return nullptr;
+  const Desc<qgemm_add_norm_t> p(a[0]);
+  if (!p) return nullptr;
+  PyObject* const t16 = type16(p->dtype);
+  PyObject* const out = p->out_dtype == QGEMM_DT_FP8_E4M3 ? g_e4m3 : type16(p->out_dtype);
+  const long long tokens = p->tokens, dim = p->dim;
+  void *x, *r, *w = nullptr, *sum, *y, *ys, *st;
+  int64_t xs, rs, ss;
+  if (!rows(a[1], "x", tokens, 1, dim, t16, &x, &xs) || !rows(a[2], "residual", tokens, 1, dim, t16, &r, &rs) ||
+      !rows(a[4], "sum_out", tokens, 1, dim, t16, &sum, &ss) || (p->norm && !array(a[3], "weight", t16, (double)dim, &w)) ||
+      !matrix(a[5], "y", out, tokens, dim, &y) || !matrix(a[6], "y_scales", g_f32, dim / 128, tokens, &ys) ||
+      !stream_of(a[7], a[1], &st) ||
+      !one_gpu({{"x", a[1]}, {"residual", a[2]}, {"weight", p->norm ? a[3] : Py_None}, {"sum_out", a[4]}, {"y", a[5]},
+                {"y_scales", a[6]}}))
+    return nullptr;
+  CALL(g_add_norm(p.get(), x, xs, r, rs, w, sum, ss, y, static_cast<float*>(ys), st));
+}
+
+// (p, A, a_scales, W, w_scales, out, out_scales, workspace, stream)
+PyObject* w8a8_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count("w8a8_run", n, 9)) return nullptr;
+  const Desc<qgemm_w8a8_t> p(a[0]);
+  if (!p) return nullptr;
+  const long long M = p->M, N = p->N, K = p->K, parts = p->gate != QGEMM_GATE_NONE ? 2 : 1;
+  if (M < 0 || N < 0 || K < 0 || M > 1 << 30 || N > 1 << 30 || K > 1 << 30) {   // the products below must not overflow
+    PyErr_SetString(PyExc_ValueError, "M, N and K must be in [0, 2^30]");
+    return nullptr;
+  }
+  PyObject* const out = p->out_dtype == QGEMM_DT_FP8_E4M3 ? g_e4m3 : p->out_dtype == QGEMM_DT_F32 ? g_f32 : type16(p->out_dtype);
+  void *A, *as, *W, *ws, *o, *os, *work, *st;
+  long long bytes;
+  if (!matrix(a[1], "A", g_e4m3, M, K, &A) || !matrix(a[2], "a_scales", g_f32, K / 128, M, &as) ||
+      !matrix(a[3], "W", g_e4m3, parts * N, K, &W) ||
+      !matrix(a[4], "w_scales", g_f32, parts * ((N + 127) / 128), K / 128, &ws) || !matrix(a[5], "out", out, M, N, &o) ||
+      !matrix(a[6], "out_scales", g_f32, N / 128, M, &os) || !workspace(a[7], &work, &bytes) || !stream_of(a[8], a[1], &st) ||
+      !one_gpu({{"A", a[1]}, {"a_scales", a[2]}, {"W", a[3]}, {"w_scales", a[4]}, {"out", a[5]}, {"out_scales", a[6]},
+                {"workspace", a[7]}}))
+    return nullptr;
+  CALL(g_w8a8(p.get(), A, static_cast<const float*>(as), W, static_cast<const float*>(ws), o, static_cast<float*>(os), work,
+              (size_t)bytes, st));
+}
+
+// (addresses of the six C functions, the seven dtypes, the two stream queries)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count("setup", n, 12)) return nullptr;
-  void* f[4];
-  for (int i = 0; i < 4; ++i) {
+  constexpr int F = 6, K = 9;
+  if (!count("setup", n, F + K)) return nullptr;
+  void* f[F];
+  for (int i = 0; i < F; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a function's address is 0");
@@ -313,18 +388,21 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_write = reinterpret_cast<decltype(g_write)>(f[1]);
   g_read = reinterpret_cast<decltype(g_read)>(f[2]);
   g_attention = reinterpret_cast<decltype(g_attention)>(f[3]);
-  PyObject** const kept[8] = {&g_f16, &g_bf16, &g_f32, &g_i32, &g_i64, &g_u8, &g_raw_stream, &g_stream};
-  for (int i = 0; i < 8; ++i) {
-    Py_INCREF(a[4 + i]);
+  g_add_norm = reinterpret_cast<decltype(g_add_norm)>(f[4]);
+  g_w8a8 = reinterpret_cast<decltype(g_w8a8)>(f[5]);
+  PyObject** const kept[K] = {&g_f16, &g_bf16, &g_f32, &g_i32, &g_i64, &g_u8, &g_e4m3, &g_raw_stream, &g_stream};
+  for (int i = 0; i < K; ++i) {
+    Py_INCREF(a[F + i]);
     Py_XDECREF(*kept[i]);
-    *kept[i] = a[4 + i];
+    *kept[i] = a[F + i];
   }
   Py_RETURN_NONE;
 }
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(setup),      METHOD(qk_norm_rope), METHOD(cache_write),
-                         METHOD(cache_read), METHOD(attention),    {nullptr, nullptr, 0, nullptr}};
+                         METHOD(cache_read), METHOD(attention),    METHOD(add_norm),
+                         METHOD(w8a8_run),   {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,208 @@
+// Host side of the 8-bit operators: descriptor validation, the weights' quantizer and launch planning.
+// Nothing in this file touches the GPU.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "qgemm_w8a8_internal.h"
+
+namespace qgemm {
+
+static_assert(sizeof(qgemm_add_norm_t) == 32, "qgemm_add_norm_t layout is part of the ABI");
+static_assert(sizeof(qgemm_w8a8_t) == 48, "qgemm_w8a8_t layout is part of the ABI");
+
+static const int kCUs = 256;
+static const int kMaxSplits = 32;
+static const int64_t kMaxSize = int64_t(1) << 24;
+static const int64_t kMaxK = int64_t(1) << 22;
+
+static qgemm_status_t check_dtype(const char* what, int dtype) {
+  if (dtype < QGEMM_DT_F16 || dtype > QGEMM_DT_NF4)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "%s value %d is not a qgemm_dtype_t", what, dtype);
+  return QGEMM_OK;
+}
+
+qgemm_status_t validate_add_norm(const qgemm_add_norm_t* p) {
+  if (!p) return fail(QGEMM_ERR_INVALID_ARGUMENT, "problem is NULL");
+  qgemm_status_t st = check_dtype("dtype", p->dtype);
+  if (st != QGEMM_OK || (st = check_dtype("out_dtype", p->out_dtype)) != QGEMM_OK) return st;
+  if (p->dtype != QGEMM_DT_F16 && p->dtype != QGEMM_DT_BF16)
+    return fail(QGEMM_ERR_UNSUPPORTED, "dtype must be F16 or BF16, got %d", p->dtype);
+  if (p->out_dtype != p->dtype && p->out_dtype != QGEMM_DT_FP8_E4M3)
+    return fail(QGEMM_ERR_UNSUPPORTED, "out_dtype must be dtype (%d) or FP8_E4M3, got %d", p->dtype, p->out_dtype);
+  if (p->tokens < 0 || p->tokens > kMaxSize)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "tokens must be in [0, %lld], got %lld", (long long)kMaxSize,
+                (long long)p->tokens);
+  if (p->dim < 8 || p->dim > 32768 || p->dim % 8)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "dim must be a multiple of 8 in [8, 32768], got %d", p->dim);
+  if (p->out_dtype == QGEMM_DT_FP8_E4M3 && p->dim % kBlock)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "dim must be a multiple of %d for FP8_E4M3, got %d", kBlock, p->dim);
+  if (p->norm != 0 && p->norm != 1) return fail(QGEMM_ERR_INVALID_ARGUMENT, "norm must be 0 or 1, got %d", p->norm);
+  if (p->norm && !(p->eps >= 0.0f && std::isfinite(p->eps)))
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0, got %g", (double)p->eps);
+  if (p->reserved != 0) return fail(QGEMM_ERR_INVALID_ARGUMENT, "reserved must be 0, got %d", p->reserved);
+  return QGEMM_OK;
+}
+
+qgemm_status_t validate_w8a8(const qgemm_w8a8_t* p) {
+  if (!p) return fail(QGEMM_ERR_INVALID_ARGUMENT, "problem is NULL");
+  if (p->M < 0 || p->M > kMaxSize)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "M must be in [0, %lld], got %lld", (long long)kMaxSize, (long long)p->M);
+  if (p->N < 16 || p->N > kMaxSize || p->N % 16)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "N must be a multiple of 16 in [16, %lld], got %lld", (long long)kMaxSize,
+                (long long)p->N);
+  if (p->K < kBlock || p->K > kMaxK || p->K % kBlock)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "K must be a multiple of %d in [%d, %lld], got %lld", kBlock, kBlock,
+                (long long)kMaxK, (long long)p->K);
+  if (p->gate < QGEMM_GATE_NONE || p->gate > QGEMM_GATE_GELU_TANH)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "gate must be 0, 1 or 2, got %d", p->gate);
+  qgemm_status_t st = check_dtype("out_dtype", p->out_dtype);
+  if (st != QGEMM_OK) return st;
+  if (p->out_dtype == QGEMM_DT_FP8_E4M3) {
+    if (p->gate == QGEMM_GATE_NONE)
+      return fail(QGEMM_ERR_UNSUPPORTED, "out_dtype FP8_E4M3 needs a gate (without one: F16, BF16 or F32)");
+    if (p->N % kBlock)
+      return fail(QGEMM_ERR_INVALID_ARGUMENT, "N must be a multiple of %d for out_dtype FP8_E4M3, got %lld", kBlock,
+                  (long long)p->N);
+  } else if (p->out_dtype > QGEMM_DT_F32) {
+    return fail(QGEMM_ERR_UNSUPPORTED, "out_dtype must be F16, BF16, F32 or (with a gate) FP8_E4M3, got %d", p->out_dtype);
+  }
+  if (p->kernel_hint < QGEMM_W8A8_AUTO || p->kernel_hint > QGEMM_W8A8_TILES)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "kernel_hint must be 0, 1 or 2, got %d", p->kernel_hint);
+  if (p->kernel_hint == QGEMM_W8A8_ROWS && p->M > kRowsMaxM)
+    return fail(QGEMM_ERR_UNSUPPORTED, "the rows kernel takes M <= %d, got %lld", kRowsMaxM, (long long)p->M);
+  if (p->split_hint < 0 || p->split_hint > kMaxSplits)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "split_hint must be in [0, %d], got %d", kMaxSplits, p->split_hint);
+  if (p->tile_hint != 0 && p->tile_hint != 64 && p->tile_hint != 128 && p->tile_hint != 256)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "tile_hint must be 0, 64, 128 or 256, got %d", p->tile_hint);
+  if (p->reserved != 0) return fail(QGEMM_ERR_INVALID_ARGUMENT, "reserved must be 0, got %d", p->reserved);
+  return QGEMM_OK;
+}
+
+// A launch holds less than 2^32 work-items.
+static bool launchable(int64_t workgroups) { return workgroups <= 0xffffffffLL / (64 * kW8Waves); }
+
+static qgemm_status_t finish_plan(W8Plan* pl, int64_t groups, int members_n, int splits, int KB, size_t slot_bytes) {
+  pl->kb_per_split = (KB + splits - 1) / splits;
+  pl->splits = (KB + pl->kb_per_split - 1) / pl->kb_per_split;       // none of them empty
+  pl->groups = groups;
+  pl->members = members_n * pl->splits;
+  const int64_t workgroups = groups * pl->members;
+  if (!launchable(workgroups))
+    return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows", (long long)workgroups);
+  pl->grid = (unsigned)workgroups;
+  pl->ws_bytes = pl->members > 1 ? (size_t)kW8Tickets * 4 + (size_t)workgroups * slot_bytes : 0;
+  return QGEMM_OK;
+}
+
+qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
+  *pl = W8Plan{};
+  const bool gated = p->gate != QGEMM_GATE_NONE, quantized = p->out_dtype == QGEMM_DT_FP8_E4M3;
+  const int KB = (int)(p->K / kBlock);
+  const int64_t M = std::max<int64_t>(p->M, 1);
+  const int hint = std::min(p->split_hint, KB);
+  if (p->kernel_hint == QGEMM_W8A8_ROWS || (p->kernel_hint == QGEMM_W8A8_AUTO && M <= kRowsMaxM)) {
+    pl->kind = W8_ROWS;
+    pl->tile = (int)((M + 15) / 16) * 16;
+    pl->blocks = gated ? 2 : 1;
+    const int64_t columns = p->N / 16;                               // workgroups without a split
+    const int members = quantized ? kBlock / 16 : 1;
+    const int64_t groups = columns / members;
+    int splits = hint;
+    if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, 2 * kCUs / columns), std::max(1, KB / kW8Waves));
+    splits = std::min(splits, kMaxSplits);
+    if (groups > kW8Tickets) splits = 1;
+    return finish_plan(pl, groups, members, splits, KB, (size_t)pl->blocks * pl->tile * 16 * 4);
+  }
+  pl->kind = W8_TILES;
+  const int64_t tiles_n = (p->N + (gated ? kTileRows / 2 : kTileRows) - 1) / (gated ? kTileRows / 2 : kTileRows);
+  const auto tiles_of = [&](int t) { return (M + t - 1) / t * tiles_n; };
+  pl->tile = p->tile_hint;
+  if (!pl->tile) pl->tile = tiles_of(256) >= kCUs ? 256 : tiles_of(128) >= kCUs / 2 ? 128 : 64;
+  const int64_t tiles = tiles_of(pl->tile);
+  int splits = hint;
+  if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / tiles), std::max(1, KB / 4));
+  splits = std::min(splits, kMaxSplits);
+  if (tiles > kW8Tickets) splits = 1;
+  return finish_plan(pl, tiles, 1, splits, KB, (size_t)pl->tile * kTileRows * 4);
+}
+
+// RNE to e4m3, |v| <= 448.
+static uint8_t e4m3_code(double v) {
+  const uint8_t sign = std::signbit(v) ? 0x80 : 0;
+  const double a = std::fabs(v);
+  int e;
+  std::frexp(a, &e);
+  e = std::max(e - 1, -6);                                           // exponent of the leading bit
+  const int units = (int)std::nearbyint(std::ldexp(a, 3 - e));       // of 2^(e - 3): 0 .. 16
+  if (units == 0) return 0;
+  // a sum: 16 units of one binade carry into the exponent field, fewer than 8 (e is -6) are a subnormal
+  return (uint8_t)(sign | (((e + 7) << 3) + units - 8));
+}
+
+}  // namespace qgemm
+
+using namespace qgemm;
+
+extern "C" {
+
+qgemm_status_t qgemm_w8a8_quantize(const qgemm_w8a8_t* p, const float* w, uint8_t* codes, float* scales) {
+  clear_error();
+  const qgemm_status_t st = validate_w8a8(p);
+  if (st != QGEMM_OK) return st;
+  if (!w || !codes || !scales) return fail(QGEMM_ERR_INVALID_ARGUMENT, "w, codes and scales must not be NULL");
+  const int64_t KB = p->K / kBlock, row_blocks = (p->N + kBlock - 1) / kBlock;
+  for (int part = 0; part < (p->gate != QGEMM_GATE_NONE ? 2 : 1); ++part)
+    for (int64_t rb = 0; rb < row_blocks; ++rb) {
+      const int64_t first = part * p->N + rb * kBlock, rows = std::min<int64_t>(kBlock, p->N - rb * kBlock);
+      for (int64_t kb = 0; kb < KB; ++kb) {
+        float amax = 0.0f;
+        for (int64_t r = first; r < first + rows; ++r)
+          for (int64_t k = kb * kBlock; k < (kb + 1) * kBlock; ++k) {
+            const float v = std::fabs(w[r * p->K + k]);
+            if (!std::isfinite(v)) return fail(QGEMM_ERR_INVALID_ARGUMENT, "w[%lld] is not finite", (long long)(r * p->K + k));
+            amax = std::max(amax, v);
+          }
+        const float scale = amax / 448.0f;
+        scales[(part * row_blocks + rb) * KB + kb] = scale;
+        for (int64_t r = first; r < first + rows; ++r)
+          for (int64_t k = kb * kBlock; k < (kb + 1) * kBlock; ++k) {
+            const double x = scale == 0.0f ? 0.0 : (double)w[r * p->K + k] / (double)scale;
+            codes[r * p->K + k] = e4m3_code(std::min(std::max(x, -448.0), 448.0));
+          }
+      }
+    }
+  return QGEMM_OK;
+}
+
+qgemm_status_t qgemm_w8a8_workspace_bytes(const qgemm_w8a8_t* p, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(QGEMM_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  qgemm_status_t st = validate_w8a8(p);
+  if (st != QGEMM_OK) return st;
+  W8Plan pl;
+  st = make_w8a8_plan(p, &pl);
+  if (st != QGEMM_OK) return st;
+  *bytes = p->M ? pl.ws_bytes : 0;
+  return QGEMM_OK;
+}
+
+qgemm_status_t qgemm_w8a8_describe(const qgemm_w8a8_t* p, char* buf, size_t len) {
+  clear_error();
+  if (!buf || !len) return fail(QGEMM_ERR_INVALID_ARGUMENT, "buf is NULL or len is 0");
+  qgemm_status_t st = validate_w8a8(p);
+  if (st != QGEMM_OK) return st;
+  W8Plan pl;
+  st = make_w8a8_plan(p, &pl);
+  if (st != QGEMM_OK) return st;
+  const int n = p->M == 0 ? std::snprintf(buf, len, "empty")
+                : pl.kind == W8_ROWS ? std::snprintf(buf, len, "rows grid=%u tokens=%d blocks=%d splits=%d members=%d", pl.grid,
+                                                     pl.tile, pl.blocks, pl.splits, pl.members)
+                                     : std::snprintf(buf, len, "tiles grid=%u tokens=%d splits=%d", pl.grid, pl.tile, pl.splits);
+  if (n < 0 || (size_t)n >= len)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
+  return QGEMM_OK;
+}
+
+}  // extern "C"
