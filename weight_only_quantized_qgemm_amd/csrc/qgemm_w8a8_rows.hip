@@ -4,9 +4,9 @@
 //
 // A workgroup owns one 16-row weight block (with a gate that of both projections); its wavefronts take the k
 // blocks of 128 in turn, so that together they read 1 KiB of every weight row side by side.  The weights go
-// from memory straight into the first operand of v_mfma_f32_16x16x128_f8f6f4 and the tokens' codes into the
-// second: lane l holds row (token) l & 15 and the 16-byte chunks l >> 4 and 4 + (l >> 4) of the k block, the same
-// for both, which is all that a dot product asks of its order.  The result has token l & 15 and weight rows
+// from memory straight into registers, as fp16 into the first operand of v_mfma_f32_16x16x32_f16 and the tokens'
+// codes into the second: lane l holds row (token) l & 15 and the 16-byte chunks l >> 4 and 4 + (l >> 4) of the k block,
+// the same for both, which is all that a dot product asks of its order.  The result has token l & 15 and weight rows
 // 4 (l >> 4) .. + 3 in lane l, so both scales are one factor per lane, applied to the fp32 block sum.
 //
 // The wavefronts' sums meet in LDS, in wavefront order.  Where several workgroups make one output (splits along
@@ -50,33 +50,39 @@ __global__ __launch_bounds__(64 * kW8Waves) void rows_kernel(W8Args a) {
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[u][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto operand = [](const uint8_t* p) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(p), hi = *reinterpret_cast<const i32x4*>(p + 64);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  struct Chunks { i32x4 v[2]; };
+  const auto chunks = [](const uint8_t* p) {
+    return Chunks{{*reinterpret_cast<const i32x4*>(p), *reinterpret_cast<const i32x4*>(p + 64)}};
   };
 
   for (int kb = kb0 + wave; kb < kb1; kb += NW) {
-    i32x8 w[U], x[MB];
+    Chunks w[U], x[MB];
     float sw[U], sa[MB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      w[u] = operand(wp[u] + (size_t)kb * kBlock);
+      w[u] = chunks(wp[u] + (size_t)kb * kBlock);
       sw[u] = sp[u][kb];
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      x[i] = operand(ap[i] + (size_t)kb * kBlock);
+      x[i] = chunks(ap[i] + (size_t)kb * kBlock);
       sa[i] = a.as[(size_t)kb * a.M + token[i]];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < MB; ++i) {
+      const Halves x0 = halves(x[i].v[0]), x1 = halves(x[i].v[1]);
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[u], x[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const Halves w0 = halves(w[u].v[0]), w1 = halves(w[u].v[1]);
+        f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[0], x0.v[0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[1], x0.v[1], p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[0], x1.v[0], p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[1], x1.v[1], p, 0, 0, 0);
         const float s = sa[i] * sw[u];
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[u][i][r] = __builtin_fmaf(p[r], s, acc[u][i][r]);
       }
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)

@@ -15,6 +15,8 @@
 // The weights are the first MFMA operand and the tokens the second: lane l of the result holds token l & 31, so both
 // scales of a block are one factor per lane and MFMA tile, and a step costs one fp32 FMA per 128 products beside the
 // MFMA (16 of 64 lanes' issue cycles beside 128 MFMA cycles for a 32 x 32 tile).
+#include <type_traits>
+
 #include "qgemm_w8a8_fixup.h"
 
 namespace qgemm {
@@ -42,7 +44,7 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int WM, int TM, int GATE, bool Q>
+template <int WM, int TM, int GATE, bool Q, bool FP16>
 __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   constexpr int NW = kW8Waves, WN = NW / WM, TN = kTileRows / (32 * WN), BM = 32 * WM * TM;
   constexpr bool G = GATE != QGEMM_GATE_NONE;
@@ -117,7 +119,38 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(p + coff[j][0]), hi = *reinterpret_cast<const i32x4*>(p + coff[j][1]);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  const auto compute = [&](const unsigned char* As, const unsigned char* Ws, const float (&sa)[TM], float sw0, float sw1) {
+  const auto accumulate = [&](int t, int i, f32x16 p, float s) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[t][i][r] = __builtin_fmaf(p[r], s, acc[t][i][r]);
+  };
+  // chunk 2 j + half of a row as two fp16 operands of 16 k
+  int hoff[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) hoff[j] = col * kBlock + 16 * ((2 * j + half) ^ (col & 7));
+  const auto compute16 = [&](const unsigned char* As, const unsigned char* Ws, const float (&sa)[TM], float sw0, float sw1) {
+    Halves x[TM][4];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[i][j] = halves(*reinterpret_cast<const i32x4*>(As + 32 * (wm * TM + i) * kBlock + hoff[j]));
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      f32x16 p[TM];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Halves w = halves(*reinterpret_cast<const i32x4*>(Ws + 32 * (wn * TN + t) * kBlock + hoff[j]));
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+            p[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.v[b], x[i][j].v[b], j + b ? p[i] : f32x16{}, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) accumulate(t, i, p[i], sa[i] * (G && t >= TN / 2 ? sw1 : sw0));
+    }
+  };
+  const auto compute8 = [&](const unsigned char* As, const unsigned char* Ws, const float (&sa)[TM], float sw0, float sw1) {
     i32x8 x[TM][2];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -132,11 +165,13 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
       for (int i = 0; i < TM; ++i) {
         f32x16 p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w0, x[i][0], f32x16{}, 0, 0, 0, 0, 0, 0);
         p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w1, x[i][1], p, 0, 0, 0, 0, 0, 0);
-        const float s = sa[i] * sw;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[t][i][r] = __builtin_fmaf(p[r], s, acc[t][i][r]);
+        accumulate(t, i, p, sa[i] * sw);
       }
     }
+  };
+  const auto compute = [&](const unsigned char* As, const unsigned char* Ws, const float (&sa)[TM], float sw0, float sw1) {
+    if constexpr (FP16) compute16(As, Ws, sa, sw0, sw1);
+    else compute8(As, Ws, sa, sw0, sw1);
   };
 
   float sa[2][TM], sw0[2], sw1[2];
@@ -262,14 +297,17 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
 template <int WM, int TM>
 void launch_tile(const W8Plan& pl, const W8Args& a, hipStream_t s) {
   const dim3 grid(pl.grid), block(64 * kW8Waves);
-  const bool q = a.out_dtype == QGEMM_DT_FP8_E4M3;
-  if (a.gate == QGEMM_GATE_NONE) tiles_kernel<WM, TM, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a);
-  else if (a.gate == QGEMM_GATE_SILU)
-    q ? tiles_kernel<WM, TM, QGEMM_GATE_SILU, true><<<grid, block, 0, s>>>(a)
-      : tiles_kernel<WM, TM, QGEMM_GATE_SILU, false><<<grid, block, 0, s>>>(a);
-  else
-    q ? tiles_kernel<WM, TM, QGEMM_GATE_GELU_TANH, true><<<grid, block, 0, s>>>(a)
-      : tiles_kernel<WM, TM, QGEMM_GATE_GELU_TANH, false><<<grid, block, 0, s>>>(a);
+  const auto gate = [&](auto g) {
+    constexpr int GATE = decltype(g)::value;
+    if (a.out_dtype == QGEMM_DT_F32) tiles_kernel<WM, TM, GATE, false, true><<<grid, block, 0, s>>>(a);
+    else if (a.out_dtype != QGEMM_DT_FP8_E4M3) tiles_kernel<WM, TM, GATE, false, false><<<grid, block, 0, s>>>(a);
+    else if constexpr (GATE != QGEMM_GATE_NONE) tiles_kernel<WM, TM, GATE, true, true><<<grid, block, 0, s>>>(a);
+  };
+  switch (a.gate) {
+    case QGEMM_GATE_NONE: gate(std::integral_constant<int, QGEMM_GATE_NONE>{}); break;
+    case QGEMM_GATE_SILU: gate(std::integral_constant<int, QGEMM_GATE_SILU>{}); break;
+    default: gate(std::integral_constant<int, QGEMM_GATE_GELU_TANH>{}); break;
+  }
 }
 
 }  // namespace
