@@ -94,15 +94,16 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     }
   };
 
-  // ---- scales: one per token block and lane; of the weights one per projection (a wavefront's rows of one
-  // projection lie in one block of 128)
-  unsigned token[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) token[i] = (unsigned)min(m0 + 16 * (wm * TM + i) + col, a.M - 1);
+  // ---- scales: one per token block and lane (past the last token: 0); of the weights one per projection (a
+  // wavefront's rows of one projection lie in one block of 128)
   const int c0 = n0 + wn * (G ? 8 * TN : 16 * TN);   // the wavefront's first output column
   const int rb = min(c0 / kBlock, a.row_blocks - 1);
-  const float* swp0 = a.ws + (size_t)rb * a.KB;
-  const float* swp1 = a.ws + (size_t)((G ? a.row_blocks : 0) + rb) * a.KB;
+  const auto scale_row = [&](int row) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.ws + (size_t)row * a.KB), (short)0, a.KB * 4, 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t sr0 = scale_row(rb), sr1 = scale_row((G ? a.row_blocks : 0) + rb);
+  const int first_token = 4 * (m0 + 16 * wm * TM + col);
+  const auto as_float = [](unsigned v) { return __builtin_bit_cast(float, v); };
 
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -113,92 +114,134 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   // operand chunks g and 4 + g of row `col` of a block of 16 rows
   const int off0 = col * kBlock + 16 * (g ^ (col & 7)), off1 = off0 ^ 64;
   const auto chunk = [](const unsigned char* p) { return *reinterpret_cast<const i32x4*>(p); };
-  const auto compute = [&](const unsigned char* As, const unsigned char* Ws, const float (&sa)[TM], float sw0, float sw1) {
-    const unsigned char* const ap = As + 16 * wm * TM * kBlock;
-    const unsigned char* const wp = Ws + 16 * wn * TN * kBlock;
-    // chunk c of the weights' blocks (block c / 2) is read AHEAD chunks before it multiplies, and no earlier: more would
-    // not fit the registers beside the sums
-    constexpr int AHEAD = FP16 ? 1 : 2;
-    i32x4 w[AHEAD + 2];
-    const auto read = [&](int c) {
-      if (c < 2 * TN) w[c % (AHEAD + 2)] = chunk(wp + c / 2 * 16 * kBlock + (c & 1 ? off1 : off0));
-    };
+  const int aoff = 16 * wm * TM * kBlock, woff = 16 * wn * TN * kBlock;
+  // chunk c of the weights' blocks: half c & 1 of the operand of block c / 2
+  const auto wchunk = [&](const unsigned char* Ws, int c) {
+    return chunk(Ws + woff + c / 2 * 16 * kBlock + (c & 1 ? off1 : off0));
+  };
+  const auto achunk = [&](const unsigned char* As, int i, int c) {
+    return chunk(As + aoff + i * 16 * kBlock + (c ? off1 : off0));
+  };
+  // a step's scales: sa of the tokens, times the weights' of either projection
+  float sa[TM], s0[TM], s1[TM], sw0, sw1 = 0.f;
+  const auto load_scales = [&](int kb) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
 #pragma unroll
-    for (int c = 0; c < AHEAD; ++c) read(c);
-    Halves xh[FP16 ? TM : 1][2];
-    i32x8 x8[FP16 ? 1 : TM];
+    for (int i = 0; i < TM; ++i) sa[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, first_token + 64 * i, 0, 0));
+    sw0 = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr0, 0, 4 * kb, 0));
+    if (G) sw1 = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr1, 0, 4 * kb, 0));
+  };
+  f32x4 p[TM];                                       // block sums that are not yet in acc
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const i32x4 lo = chunk(ap + i * 16 * kBlock + off0), hi = chunk(ap + i * 16 * kBlock + off1);
-      if constexpr (FP16) {
-        xh[i][0] = halves(lo);
-        xh[i][1] = halves(hi);
-      } else {
-        x8[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
+  for (int i = 0; i < TM; ++i) {
+    p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s0[i] = s1[i] = 0.f;
+  }
+  const auto accumulate = [&](int t, int i) {
+    const float s = G && t >= TN / 2 ? s1[i] : s0[i];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[t][i][r] = __builtin_fmaf(p[i][r], s, acc[t][i][r]);
+  };
+  // The scales of a step take effect once the last block of the step before is in acc.
+  const auto next_scales = [&](int i) {
+    s0[i] = sa[i] * sw0;
+    s1[i] = sa[i] * sw1;
+  };
+
+  constexpr int RING = FP16 ? 2 : 4;                 // weight chunks in registers
+  i32x4 w[RING];
+  Halves h[2];                                       // fp16: the chunk that multiplies and the next one, converted in parts
+  const auto convert = [&](int c, int e) {           // two codes of chunk c
+    const unsigned codes = (unsigned)w[c % RING][e >> 1];
+    const f16x2 v = e & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, false);
+    h[c & 1].v[e >> 2][2 * (e & 3)] = v[0];
+    h[c & 1].v[e >> 2][2 * (e & 3) + 1] = v[1];
+  };
+  i32x8 x8[FP16 ? 1 : TM];
+  Halves xh[FP16 ? TM : 1][2];
+  const auto read_x = [&](const unsigned char* As, int i) {
+    const i32x4 lo = achunk(As, i, 0), hi = achunk(As, i, 1);
+    if constexpr (FP16) {
+      xh[i][0] = halves(lo);
+      xh[i][1] = halves(hi);
+    } else {
+      x8[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
+  };
+  // One k block: its data lie in (As, Ws), x and the first weight block are in registers.  Block t - 1 enters acc between
+  // the MFMAs of block t, so that a wavefront's MFMAs and FMAs overlap (kept apart, the two wavefronts of a SIMD run in step
+  // and wait for each other).  Before the last block everything of this step has been read, and the next one's data
+  // have landed: one barrier says both, the stage just read receives the step after next, and the next step's operands are
+  // read while this one finishes.
+  const auto step = [&](unsigned char* As, unsigned char* Ws, const unsigned char* An, const unsigned char* Wn, int kb_next,
+                        int kb_load) {
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
-      __builtin_amdgcn_sched_barrier(0);
-      f32x4 p[TM];
+      const bool last = t == TN - 1;
+      if (last) {
+        __builtin_amdgcn_s_waitcnt(0);
+        barrier();
+        load_scales(kb_next);
+      }
       if constexpr (FP16) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          read(2 * t + j + AHEAD);
-          const Halves h = halves(w[(2 * t + j) % (AHEAD + 2)]);
+        for (int e = 0; e < 4 * TM; ++e) {           // (half of the block, half of the chunk, token block)
+          const int j = e / (2 * TM), b = e / TM % 2, i = e % TM;
+          __builtin_amdgcn_sched_barrier(0);
+          if (e < TM) accumulate((t + TN - 1) % TN, i);
+          if (e < TM && t == 0) next_scales(i);
+          p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[j].v[b], xh[i][j].v[b], e < TM ? f32x4{0.f, 0.f, 0.f, 0.f} : p[i], 0, 0, 0);
+          if (e % (2 * TM) == 0) w[(2 * t + j + 2) % RING] = last ? wchunk(Wn, j) : wchunk(Ws, 2 * t + j + 2);
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int c = 0; c < 4 / TM; ++c) convert(2 * t + j + 1, (e % (2 * TM)) * (4 / TM) + c);
+          if (last && e == 2 * TM - 1) load(kb_load, As, Ws);
+        }
+        if (last) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-              p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h.v[b], xh[i][j].v[b], j + b ? p[i] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          for (int i = 0; i < TM; ++i) read_x(An, i);
         }
       } else {
-        read(2 * t + AHEAD);
-        read(2 * t + AHEAD + 1);
-        const i32x8 w8 = __builtin_shufflevector(w[2 * t % (AHEAD + 2)], w[(2 * t + 1) % (AHEAD + 2)], 0, 1, 2, 3, 4, 5, 6, 7);
+        const i32x8 w8 = __builtin_shufflevector(w[2 * t % RING], w[(2 * t + 1) % RING], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          accumulate((t + TN - 1) % TN, i);
+          if (t == 0) next_scales(i);
           p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const float s = sa[i] * (G && t >= TN / 2 ? sw1 : sw0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[t][i][r] = __builtin_fmaf(p[i][r], s, acc[t][i][r]);
+          if (i < 2) w[(2 * t + 2 + i) % RING] = last ? wchunk(Wn, i) : wchunk(Ws, 2 * t + 2 + i);
+          if (last) read_x(An, i);
+          if (last && i == TM - 1) load(kb_load, As, Ws);
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  float sa[2][TM], sw0[2], sw1[2];
-  const auto load_scales = [&](int kb, int b) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) sa[b][i] = (a.as + (size_t)kb * a.M)[token[i]];
-    sw0[b] = swp0[kb];
-    sw1[b] = G ? swp1[kb] : 0.f;
-  };
-  load_scales(kb0, 0);
+  const int kl = kb1 - 1;                            // loads past the end read the last k block again, unused
   load(kb0, A0, W0);
-  // before each step: its loads have landed for every wavefront, and every wavefront is done reading the other stage
+  load_scales(kb0);
+  load(min(kb0 + 1, kl), A1, W1);
+  __builtin_amdgcn_s_waitcnt(0);
+  barrier();
+#pragma unroll
+  for (int i = 0; i < TM; ++i) read_x(A0, i);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) w[c] = wchunk(W0, c);
+  if constexpr (FP16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) convert(0, e);
+  }
   int kb = kb0;
   for (; kb + 1 < kb1; kb += 2) {
-    __builtin_amdgcn_s_waitcnt(0);
-    barrier();
-    load_scales(kb + 1, 1);
-    load(kb + 1, A1, W1);
-    compute(A0, W0, sa[0], sw0[0], sw1[0]);
-    __builtin_amdgcn_s_waitcnt(0);
-    barrier();
-    const int next = min(kb + 2, kb1 - 1);             // past the end: loaded once more, not used
-    load_scales(next, 0);
-    load(next, A0, W0);
-    compute(A1, W1, sa[1], sw0[1], sw1[1]);
+    step(A0, W0, A1, W1, kb + 1, min(kb + 2, kl));
+    step(A1, W1, A0, W0, min(kb + 2, kl), min(kb + 3, kl));
   }
-  __builtin_amdgcn_s_waitcnt(0);
-  if (kb < kb1) {
-    barrier();
-    compute(A0, W0, sa[0], sw0[0], sw1[0]);
-  }
+  if (kb < kb1) step(A0, W0, A1, W1, kl, kl);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) accumulate(TN - 1, i);
+  __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
 
   // ---- splits along K: partial tiles, summed in order by the workgroup that comes last
   if (a.splits > 1) {
