@@ -151,13 +151,13 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
 
   constexpr int RING = FP16 ? 2 : 4;                 // weight chunks in registers
   i32x4 w[RING];
-  Halves h[2];                                       // fp16: the chunk that multiplies and the next one, converted in parts
-  const auto convert = [&](int c, int e) {           // two codes of chunk c
-    const unsigned codes = (unsigned)w[c % RING][e >> 1];
+  f16x8 h[2];                                        // fp16: the halves of a chunk; one multiplies while the other is converted
+  const auto convert = [&](int c, int b, int e) {    // codes 2 e, 2 e + 1 of half b of chunk c
+    const unsigned codes = (unsigned)w[c % RING][2 * b + (e >> 1)];
     const f16x2 v = e & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, true)
                           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, false);
-    h[c & 1].v[e >> 2][2 * (e & 3)] = v[0];
-    h[c & 1].v[e >> 2][2 * (e & 3) + 1] = v[1];
+    h[b][2 * e] = v[0];
+    h[b][2 * e + 1] = v[1];
   };
   i32x8 x8[FP16 ? 1 : TM];
   Halves xh[FP16 ? TM : 1][2];
@@ -192,10 +192,11 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
           __builtin_amdgcn_sched_barrier(0);
           if (e < TM) accumulate((t + TN - 1) % TN, i);
           if (e < TM && t == 0) next_scales(i);
-          p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[j].v[b], xh[i][j].v[b], e < TM ? f32x4{0.f, 0.f, 0.f, 0.f} : p[i], 0, 0, 0);
-          if (e % (2 * TM) == 0) w[(2 * t + j + 2) % RING] = last ? wchunk(Wn, j) : wchunk(Ws, 2 * t + j + 2);
+          p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[b], xh[i][j].v[b], e < TM ? f32x4{0.f, 0.f, 0.f, 0.f} : p[i], 0, 0, 0);
+          const int c = 2 * t + j;
+          if (b == 1 && i == 0) w[c % RING] = last ? wchunk(Wn, j) : wchunk(Ws, c + 2);
 #pragma unroll
-          for (int c = 0; c < 4 / TM; ++c) convert(2 * t + j + 1, (e % (2 * TM)) * (4 / TM) + c);
+          for (int f = 0; f < 4 / TM; ++f) convert(c + b, 1 - b, i * (4 / TM) + f);
           if (last && e == 2 * TM - 1) load(kb_load, As, Ws);
         }
         if (last) {
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   for (int c = 0; c < 2; ++c) w[c] = wchunk(W0, c);
   if constexpr (FP16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) convert(0, e);
+    for (int e = 0; e < 4; ++e) convert(0, 0, e);
   }
   int kb = kb0;
   for (; kb + 1 < kb1; kb += 2) {
