@@ -44,16 +44,21 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int WM, int TM, int GATE, bool Q, bool FP16>
+template <int WM, int TM, int ST, int GATE, bool Q, bool FP16>
 __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   constexpr int NW = kW8Waves, WN = NW / WM, TN = kTileRows / (16 * WN), BM = 16 * WM * TM;
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int COLS = G ? kTileRows / 2 : kTileRows;          // output columns of a tile
   constexpr int LA = BM / (8 * NW), LW = kTileRows / (8 * NW); // loads of a wavefront per step
   static_assert(!G || TN % 2 == 0, "both projections' rows lie in one wavefront");
+  // Each stage is arrays of its own, so that the compiler can tell the one that is read from those being filled.
   __shared__ __attribute__((aligned(1024))) unsigned char A0[BM * kBlock], A1[BM * kBlock];
   __shared__ __attribute__((aligned(1024))) unsigned char W0[kTileRows * kBlock], W1[kTileRows * kBlock];
-  __shared__ int s_last;
+  __shared__ __attribute__((aligned(1024))) unsigned char A2[ST > 2 ? BM * kBlock : 16], W2[ST > 2 ? kTileRows * kBlock : 16];
+  __shared__ __attribute__((aligned(1024))) unsigned char A3[ST > 3 ? BM * kBlock : 16], W3[ST > 3 ? kTileRows * kBlock : 16];
+  static_assert(ST >= 2 && ST <= 4, "two to four stages");
+  const auto as = [&](int j) -> unsigned char* { return j == 0 ? A0 : j == 1 ? A1 : j == 2 ? A2 : A3; };
+  const auto ws = [&](int j) -> unsigned char* { return j == 0 ? W0 : j == 1 ? W1 : j == 2 ? W2 : W3; };
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -123,14 +128,25 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     return chunk(As + aoff + i * 16 * kBlock + (c ? off1 : off0));
   };
   // a step's scales: sa of the tokens, times the weights' of either projection
-  float sa[TM], s0[TM], s1[TM], sw0, sw1 = 0.f;
-  const auto load_scales = [&](int kb) {
+  // With two stages the scales of the next step are loaded as it comes near (the 256-token tile has no registers for
+  // two sets), with more together with the step's data: loads return in order, and one waited for late would wait for all.
+  constexpr int SETS = ST > 2 ? ST : 1;
+  float sa[SETS][TM], sw0[SETS], sw1[SETS], s0[TM], s1[TM];
+  const auto load_scales = [&](int kb, int j) {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, first_token + 64 * i, 0, 0));
-    sw0 = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr0, 0, 4 * kb, 0));
-    if (G) sw1 = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr1, 0, 4 * kb, 0));
+    for (int i = 0; i < TM; ++i) sa[j][i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, first_token + 64 * i, 0, 0));
+    sw0[j] = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr0, 0, 4 * kb, 0));
+    sw1[j] = G ? as_float(__builtin_amdgcn_raw_buffer_load_b32(sr1, 0, 4 * kb, 0)) : 0.f;
+  };
+  // The loads of a step stay between two barriers (both are fences to the compiler): the waits count them.
+  constexpr int LOADS = LA + LW + (SETS > 1 ? TM + (G ? 2 : 1) : 0), PEND = (ST - 2) * LOADS;
+  static_assert((ST - 1) * LOADS <= 63, "vmcnt counts at most 63");
+  constexpr auto vmcnt = [](int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); };      // and no LDS read pending
+  const auto load_step = [&](int kb, int j) {
+    if constexpr (SETS > 1) load_scales(kb, j);
+    load(kb, as(j), ws(j));
   };
   f32x4 p[TM];                                       // block sums that are not yet in acc
 #pragma unroll
@@ -144,9 +160,9 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     for (int r = 0; r < 4; ++r) acc[t][i][r] = __builtin_fmaf(p[i][r], s, acc[t][i][r]);
   };
   // The scales of a step take effect once the last block of the step before is in acc.
-  const auto next_scales = [&](int i) {
-    s0[i] = sa[i] * sw0;
-    s1[i] = sa[i] * sw1;
+  const auto next_scales = [&](int i, int j) {
+    s0[i] = sa[j % SETS][i] * sw0[j % SETS];
+    s1[i] = sa[j % SETS][i] * sw1[j % SETS];
   };
 
   constexpr int RING = FP16 ? 2 : 4;                 // weight chunks in registers
@@ -170,20 +186,22 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
       x8[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   };
-  // One k block: its data lie in (As, Ws), x and the first weight block are in registers.  Block t - 1 enters acc between
+  // One k block: its data lie in stage j, x and the first weight block are in registers.  Block t - 1 enters acc between
   // the MFMAs of block t, so that a wavefront's MFMAs and FMAs overlap (kept apart, the two wavefronts of a SIMD run in step
   // and wait for each other).  Before the last block everything of this step has been read, and the next one's data
-  // have landed: one barrier says both, the stage just read receives the step after next, and the next step's operands are
-  // read while this one finishes.
-  const auto step = [&](unsigned char* As, unsigned char* Ws, const unsigned char* An, const unsigned char* Wn, int kb_next,
-                        int kb_load) {
+  // have landed: one barrier says both, the stage just read receives the step ST further on, and the next step's operands
+  // are read while this one finishes.
+  const auto step = [&](auto stage, int kb_next, int kb_load) {
+    constexpr int J = decltype(stage)::value;
+    unsigned char* const Ws = ws(J);
+    const unsigned char *const An = as((J + 1) % ST), *const Wn = ws((J + 1) % ST);
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       const bool last = t == TN - 1;
       if (last) {
-        __builtin_amdgcn_s_waitcnt(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt(PEND));
         barrier();
-        load_scales(kb_next);
+        if constexpr (SETS == 1) load_scales(kb_next, 0);
       }
       if constexpr (FP16) {
 #pragma unroll
@@ -191,13 +209,13 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
           const int j = e / (2 * TM), b = e / TM % 2, i = e % TM;
           __builtin_amdgcn_sched_barrier(0);
           if (e < TM) accumulate((t + TN - 1) % TN, i);
-          if (e < TM && t == 0) next_scales(i);
+          if (e < TM && t == 0) next_scales(i, J);
           p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[b], xh[i][j].v[b], e < TM ? f32x4{0.f, 0.f, 0.f, 0.f} : p[i], 0, 0, 0);
           const int c = 2 * t + j;
           if (b == 1 && i == 0) w[c % RING] = last ? wchunk(Wn, j) : wchunk(Ws, c + 2);
 #pragma unroll
           for (int f = 0; f < 4 / TM; ++f) convert(c + b, 1 - b, i * (4 / TM) + f);
-          if (last && e == 2 * TM - 1) load(kb_load, As, Ws);
+          if (last && e == 2 * TM - 1) load_step(kb_load, J);
         }
         if (last) {
 #pragma unroll
@@ -209,11 +227,11 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
         for (int i = 0; i < TM; ++i) {
           __builtin_amdgcn_sched_barrier(0);
           accumulate((t + TN - 1) % TN, i);
-          if (t == 0) next_scales(i);
+          if (t == 0) next_scales(i, J);
           p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
           if (i < 2) w[(2 * t + 2 + i) % RING] = last ? wchunk(Wn, i) : wchunk(Ws, 2 * t + 2 + i);
           if (last) read_x(An, i);
-          if (last && i == TM - 1) load(kb_load, As, Ws);
+          if (last && i == TM - 1) load_step(kb_load, J);
         }
       }
     }
@@ -221,10 +239,13 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   };
 
   const int kl = kb1 - 1;                            // loads past the end read the last k block again, unused
-  load(kb0, A0, W0);
-  load_scales(kb0);
-  load(min(kb0 + 1, kl), A1, W1);
-  __builtin_amdgcn_s_waitcnt(0);
+  if constexpr (SETS == 1) load_scales(kb0, 0);
+#pragma unroll
+  for (int j = 0; j < ST; ++j) {
+    asm volatile("" ::: "memory");
+    load_step(min(kb0 + j, kl), j);
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt((ST - 1) * LOADS));
   barrier();
 #pragma unroll
   for (int i = 0; i < TM; ++i) read_x(A0, i);
@@ -235,14 +256,33 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     for (int e = 0; e < 4; ++e) convert(0, 0, e);
   }
   int kb = kb0;
-  for (; kb + 1 < kb1; kb += 2) {
-    step(A0, W0, A1, W1, kb + 1, min(kb + 2, kl));
-    step(A1, W1, A0, W0, min(kb + 2, kl), min(kb + 3, kl));
+  const auto next = [&](auto stage) {
+    step(stage, min(kb + 1, kl), min(kb + ST, kl));
+    ++kb;
+  };
+  constexpr std::integral_constant<int, 0> S0{};
+  constexpr std::integral_constant<int, 1> S1{};
+  constexpr std::integral_constant<int, (ST > 2 ? 2 : 0)> S2{};
+  constexpr std::integral_constant<int, (ST > 3 ? 3 : 0)> S3{};
+  while (kb + ST <= kb1) {
+    next(S0);
+    next(S1);
+    if constexpr (ST > 2) next(S2);
+    if constexpr (ST > 3) next(S3);
   }
-  if (kb < kb1) step(A0, W0, A1, W1, kl, kl);
+  if (kb < kb1) {
+    next(S0);
+    if constexpr (ST > 2)
+      if (kb < kb1) {
+        next(S1);
+        if constexpr (ST > 3)
+          if (kb < kb1) next(S2);
+      }
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) accumulate(TN - 1, i);
   __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
+  __syncthreads();                                   // and no wavefront reads it: what follows uses it otherwise
 
   // ---- splits along K: partial tiles, summed in order by the workgroup that comes last
   if (a.splits > 1) {
@@ -254,7 +294,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     for (int t = 0; t < TN; ++t)
 #pragma unroll
       for (int i = 0; i < TM; ++i) store_partial(part, split * SLOT + (t * TM + i) * (64 * NW * 16) + at, acc[t][i]);
-    if (!last_arrival(a.tickets + tile, a.splits, &s_last)) return;
+    if (!last_arrival(a.tickets + tile, a.splits, reinterpret_cast<int*>(W0))) return;
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
@@ -280,7 +320,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
       }
     }
   } else {
-    __shared__ unsigned top[WN][BM];                 // largest magnitude of a token in each wavefront's columns
+    auto& top = *reinterpret_cast<unsigned(*)[WN][BM]>(A0);   // largest magnitude of a token in each wavefront's columns
     unsigned m[TM];
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -314,14 +354,14 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   }
 }
 
-template <int WM, int TM>
+template <int WM, int TM, int ST>
 void launch_tile(const W8Plan& pl, const W8Args& a, hipStream_t s) {
   const dim3 grid(pl.grid), block(64 * kW8Waves);
   const auto gate = [&](auto g) {
     constexpr int GATE = decltype(g)::value;
-    if (a.out_dtype == QGEMM_DT_F32) tiles_kernel<WM, TM, GATE, false, true><<<grid, block, 0, s>>>(a);
-    else if (a.out_dtype != QGEMM_DT_FP8_E4M3) tiles_kernel<WM, TM, GATE, false, false><<<grid, block, 0, s>>>(a);
-    else if constexpr (GATE != QGEMM_GATE_NONE) tiles_kernel<WM, TM, GATE, true, true><<<grid, block, 0, s>>>(a);
+    if (a.out_dtype == QGEMM_DT_F32) tiles_kernel<WM, TM, ST, GATE, false, true><<<grid, block, 0, s>>>(a);
+    else if (a.out_dtype != QGEMM_DT_FP8_E4M3) tiles_kernel<WM, TM, ST, GATE, false, false><<<grid, block, 0, s>>>(a);
+    else if constexpr (GATE != QGEMM_GATE_NONE) tiles_kernel<WM, TM, ST, GATE, true, true><<<grid, block, 0, s>>>(a);
   };
   switch (a.gate) {
     case QGEMM_GATE_NONE: gate(std::integral_constant<int, QGEMM_GATE_NONE>{}); break;
@@ -334,9 +374,9 @@ void launch_tile(const W8Plan& pl, const W8Args& a, hipStream_t s) {
 
 hipError_t launch_tiles(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
   switch (pl.tile) {
-    case 64: launch_tile<2, 2>(pl, a, stream); break;
-    case 128: launch_tile<4, 2>(pl, a, stream); break;
-    default: launch_tile<4, 4>(pl, a, stream); break;
+    case 64: launch_tile<2, 2, 4>(pl, a, stream); break;
+    case 128: launch_tile<4, 2, 3>(pl, a, stream); break;
+    default: launch_tile<4, 4, 2>(pl, a, stream); break;
   }
   return hipGetLastError();
 }
