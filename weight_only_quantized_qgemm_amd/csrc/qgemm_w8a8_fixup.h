@@ -18,6 +18,28 @@ __device__ __forceinline__ f32x4 load_partial(__amdgpu_buffer_rsrc_t part, int o
   return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(part, offset, 0, kDeviceScope));
 }
 
+// Tile of workgroup b.  Workgroups go to the eight XCDs round-robin by number; each XCD takes a contiguous range of
+// positions, which walk the tiles in bands of four token rows, so that the tiles an XCD runs at one time share
+// tokens and weights in its L2.
+__device__ __forceinline__ void tile_of(int b, int tiles, int tiles_n, int& tm, int& tn) {
+  constexpr int kBand = 4;
+  const int x = b & 7, slot = b >> 3, q = tiles >> 3, r = tiles & 7;
+  const int at = x < r ? x * (q + 1) + slot : r * (q + 1) + (x - r) * q + slot;
+  const int tiles_m = tiles / tiles_n;
+  const int band = at / (kBand * tiles_n), first = band * kBand;
+  const int rows = min(kBand, tiles_m - first);
+  const int in = at - band * kBand * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+// Workgroup barrier without the fence of __syncthreads(), which would wait for every load still in flight.
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Called by every thread of a workgroup once its partial sums are stored; true in the workgroup that came last
 // of `members`.  It leaves the ticket at zero for the next call.
 __device__ __forceinline__ bool last_arrival(unsigned* ticket, int members, int* s_last) {
@@ -61,6 +83,84 @@ __device__ __forceinline__ void store4(const W8Args& a, size_t at, f32x4 v) {
     const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
         u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+  }
+}
+
+// The end of a workgroup's tile: lane l of a wavefront holds token m0 + 16 (i0 + i) + (l & 15) and weight rows
+// 4 (l >> 4) .. + 3 of each block acc[t][i].  `top` and `flag` are LDS that nothing else uses any more.
+//
+// Workgroups that share a tile (splits along K) leave partial tiles in the workspace, and the one that comes last
+// sums them in order.
+template <int WN, int NW, int GATE, bool Q, int TN, int TM>
+__device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM], unsigned char* top_lds, unsigned char* flag,
+                                            int tile, int split, int tn, int m0, int i0, int wn, int c0) {
+  constexpr bool G = GATE != QGEMM_GATE_NONE;
+  constexpr int BM = 16 * TM * NW / WN;
+  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+  if (a.splits > 1) {
+    constexpr int SLOT = TN * TM * 64 * NW * 16;     // bytes of a partial tile: 16 per thread and block
+    const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
+        a.partials + (size_t)tile * a.splits * (SLOT / 4), (short)0, a.splits * SLOT, 0x00020000);
+    const int at = 16 * threadIdx.x;
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int i = 0; i < TM; ++i) store_partial(part, split * SLOT + (t * TM + i) * (64 * NW * 16) + at, acc[t][i]);
+    if (!last_arrival(a.tickets + tile, a.splits, reinterpret_cast<int*>(flag))) return;
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int i = 0; i < TM; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+      for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) acc[t][i] += load_partial(part, s * SLOT + (t * TM + i) * (64 * NW * 16) + at);
+  }
+  constexpr int OT = G ? TN / 2 : TN;
+  if constexpr (!Q) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = m0 + 16 * (i0 + i) + col;
+      if (m >= a.M) continue;
+#pragma unroll
+      for (int t = 0; t < OT; ++t) {
+        const int n = c0 + 16 * t + 4 * g;
+        if (n < a.N) store4(a, (size_t)m * a.N + n, gated<GATE>(acc[t][i], acc[t + TN - OT][i]));
+      }
+    }
+  } else {
+    auto& top = *reinterpret_cast<unsigned(*)[WN][BM]>(top_lds);   // largest magnitude of a token in each wavefront's columns
+    unsigned m[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      m[i] = 0;
+#pragma unroll
+      for (int t = 0; t < OT; ++t) {
+        acc[t][i] = gated<GATE>(acc[t][i], acc[t + OT][i]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[i] = max(m[i], magnitude(acc[t][i][r]));
+      }
+      m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 16));
+      m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 32));
+      if (g == 0) top[wn][16 * (i0 + i) + col] = m[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int w = 0; w < WN; ++w) m[i] = max(m[i], top[w][16 * (i0 + i) + col]);
+      const BlockScale b = block_scale(m[i], 1.0f);
+      const int token = m0 + 16 * (i0 + i) + col;
+      if (token >= a.M) continue;
+      if (wn == 0 && g == 0) a.os[(size_t)tn * a.M + token] = b.scale;
+#pragma unroll
+      for (int t = 0; t < OT; ++t) {
+        const f32x4 v = acc[t][i];
+        *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)token * a.N + c0 + 16 * t + 4 * g) =
+            codes4(v[0] * b.to_code, v[1] * b.to_code, v[2] * b.to_code, v[3] * b.to_code);
+      }
+    }
   }
 }
 

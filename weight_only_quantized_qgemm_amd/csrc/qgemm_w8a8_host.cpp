@@ -2,6 +2,7 @@
 // Nothing in this file touches the GPU.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstdio>
 #include <cstring>
 
@@ -105,27 +106,30 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   if (p->kernel_hint == QGEMM_W8A8_ROWS || (p->kernel_hint == QGEMM_W8A8_AUTO && M <= kRowsMaxM)) {
     pl->kind = W8_ROWS;
     pl->tile = (int)((M + 15) / 16) * 16;
-    pl->blocks = gated ? 2 : 1;
-    const int64_t columns = p->N / 16;                               // workgroups without a split
-    const int members = quantized ? kBlock / 16 : 1;
-    const int64_t groups = columns / members;
+    pl->blocks = rows_blocks(pl->tile, gated);
+    const int column_blocks = gated ? pl->blocks / 2 : pl->blocks;   // of a workgroup
+    const int members = quantized ? kBlock / 16 / column_blocks : 1;
+    const int64_t columns = (p->N / 16 + column_blocks - 1) / column_blocks, groups = columns / members;
     int splits = hint;
     if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, 2 * kCUs / columns), std::max(1, KB / kW8Waves));
     splits = std::min(splits, kMaxSplits);
     if (groups > kW8Tickets) splits = 1;
     return finish_plan(pl, groups, members, splits, KB, (size_t)pl->blocks * pl->tile * 16 * 4);
   }
-  pl->kind = W8_TILES;
-  const int64_t tiles_n = (p->N + (gated ? kTileRows / 2 : kTileRows) - 1) / (gated ? kTileRows / 2 : kTileRows);
-  const auto tiles_of = [&](int t) { return (M + t - 1) / t * tiles_n; };
+  const auto tiles_n = [&](int rows) { return (p->N * (gated ? 2 : 1) + rows - 1) / rows; };
+  const auto tiles_of = [&](int t, int rows) { return (M + t - 1) / t * tiles_n(rows); };
   pl->tile = p->tile_hint;
-  if (!pl->tile) pl->tile = tiles_of(256) >= kCUs ? 256 : tiles_of(128) >= kCUs / 2 ? 128 : 64;
-  const int64_t tiles = tiles_of(pl->tile);
+  if (!pl->tile) pl->tile = tiles_of(256, kTileRows) >= kCUs ? 256 : tiles_of(128, kTileRows) >= kCUs / 2 ? 128 : 64;
+  pl->kind = getenv("STREAM") && pl->tile < 256 ? W8_STREAM : W8_TILES;
+  pl->blocks = gated || pl->kind == W8_TILES || tiles_of(pl->tile, kTileRows) >= kCUs / 2 ? 2 : 1;
+  const int rows = pl->blocks * kTileRows / 2;
+  pl->tiles_n = (int)tiles_n(rows);
+  const int64_t tiles = tiles_of(pl->tile, rows);
   int splits = hint;
   if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / tiles), std::max(1, KB / 4));
   splits = std::min(splits, kMaxSplits);
   if (tiles > kW8Tickets) splits = 1;
-  return finish_plan(pl, tiles, 1, splits, KB, (size_t)pl->tile * kTileRows * 4);
+  return finish_plan(pl, tiles, 1, splits, KB, (size_t)pl->tile * rows * 4);
 }
 
 // RNE to e4m3, |v| <= 448.
@@ -199,7 +203,8 @@ qgemm_status_t qgemm_w8a8_describe(const qgemm_w8a8_t* p, char* buf, size_t len)
   const int n = p->M == 0 ? std::snprintf(buf, len, "empty")
                 : pl.kind == W8_ROWS ? std::snprintf(buf, len, "rows grid=%u tokens=%d blocks=%d splits=%d members=%d", pl.grid,
                                                      pl.tile, pl.blocks, pl.splits, pl.members)
-                                     : std::snprintf(buf, len, "tiles grid=%u tokens=%d splits=%d", pl.grid, pl.tile, pl.splits);
+                                     : std::snprintf(buf, len, "%s grid=%u tokens=%d blocks=%d splits=%d",
+                                                     pl.kind == W8_STREAM ? "stream" : "tiles", pl.grid, pl.tile, pl.blocks, pl.splits);
   if (n < 0 || (size_t)n >= len)
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
   return QGEMM_OK;

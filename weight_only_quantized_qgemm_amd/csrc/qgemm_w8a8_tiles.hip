@@ -23,27 +23,6 @@ namespace qgemm {
 namespace w8 {
 namespace {
 
-// Tile of workgroup b.  Workgroups go to the eight XCDs round-robin by number; each XCD takes a contiguous range of
-// positions, which walk the tiles in bands of four token rows, so that the tiles an XCD runs at one time share
-// tokens and weights in its L2.
-__device__ __forceinline__ void tile_of(int b, int tiles, int tiles_n, int& tm, int& tn) {
-  constexpr int kBand = 4;
-  const int x = b & 7, slot = b >> 3, q = tiles >> 3, r = tiles & 7;
-  const int at = x < r ? x * (q + 1) + slot : r * (q + 1) + (x - r) * q + slot;
-  const int tiles_m = tiles / tiles_n;
-  const int band = at / (kBand * tiles_n), first = band * kBand;
-  const int rows = min(kBand, tiles_m - first);
-  const int in = at - band * kBand * tiles_n;
-  tm = first + in % rows;
-  tn = in / rows;
-}
-
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 template <int WM, int TM, int ST, int GATE, bool Q, bool FP16>
 __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   constexpr int NW = kW8Waves, WN = NW / WM, TN = kTileRows / (16 * WN), BM = 16 * WM * TM;
@@ -56,9 +35,11 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   __shared__ __attribute__((aligned(1024))) unsigned char W0[kTileRows * kBlock], W1[kTileRows * kBlock];
   __shared__ __attribute__((aligned(1024))) unsigned char A2[ST > 2 ? BM * kBlock : 16], W2[ST > 2 ? kTileRows * kBlock : 16];
   __shared__ __attribute__((aligned(1024))) unsigned char A3[ST > 3 ? BM * kBlock : 16], W3[ST > 3 ? kTileRows * kBlock : 16];
-  static_assert(ST >= 2 && ST <= 4, "two to four stages");
+  __shared__ float T0[NW][64], T1[NW][64], T2[ST > 2 ? NW : 1][64], T3[ST > 3 ? NW : 1][64];   // the tokens' scales
+  static_assert(ST >= 2 && ST <= 4 && TM <= 4, "two to four stages, a lane for each token of a wavefront");
   const auto as = [&](int j) -> unsigned char* { return j == 0 ? A0 : j == 1 ? A1 : j == 2 ? A2 : A3; };
   const auto ws = [&](int j) -> unsigned char* { return j == 0 ? W0 : j == 1 ? W1 : j == 2 ? W2 : W3; };
+  const auto ts = [&](int j) -> float(*)[64] { return j == 0 ? T0 : j == 1 ? T1 : j == 2 ? T2 : T3; };
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -68,8 +49,13 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   const int m0 = tm * BM, n0 = tn * COLS;
   const int kb0 = split * a.kb_per_split, kb1 = min(a.KB, kb0 + a.kb_per_split);
 
+  // What each step needs once is worked out from the lane's number anew: kept in registers, it would not fit beside the sums.
+  const auto anew = [](int l) {
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+
   // ---- loads into LDS: 1 KiB each, eight rows
-  const int drow = lane >> 3, dchunk = (lane & 7) ^ drow;
   const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.a + (size_t)m0 * a.K), (short)0, min(a.M - m0, BM) * a.K, 0x00020000);
   const int wrows = min(a.N - n0, COLS);
@@ -78,8 +64,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   const __amdgpu_buffer_rsrc_t wr1 = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.w + (size_t)(G ? a.N + n0 : n0) * a.K), (short)0, wrows * a.K, 0x00020000);
   const auto load = [&](int kb, unsigned char* As, unsigned char* Ws) {
-    int lane_off = drow * a.K + 16 * dchunk;
-    asm volatile("" : "+v"(lane_off));               // the loads' offsets are added up anew each step, not kept in registers
+    const int l = anew(lane), drow = l >> 3, lane_off = drow * a.K + 16 * ((l & 7) ^ drow);
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       const int r = 8 * (NW * i + wave);             // first row of the load
@@ -99,16 +84,12 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     }
   };
 
-  // ---- scales: one per token block and lane (past the last token: 0); of the weights one per projection (a
+  // ---- scales: of the tokens through LDS, one load a step and wavefront for its 16 TM tokens (a load instruction
+  // costs the same however little it carries; past the last token: 0); of the weights one per projection, uniform (a
   // wavefront's rows of one projection lie in one block of 128)
   const int c0 = n0 + wn * (G ? 8 * TN : 16 * TN);   // the wavefront's first output column
   const int rb = min(c0 / kBlock, a.row_blocks - 1);
-  const auto scale_row = [&](int row) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.ws + (size_t)row * a.KB), (short)0, a.KB * 4, 0x00020000);
-  };
-  const __amdgpu_buffer_rsrc_t sr0 = scale_row(rb), sr1 = scale_row((G ? a.row_blocks : 0) + rb);
-  const int first_token = 4 * (m0 + 16 * wm * TM + col);
-  const auto as_float = [](unsigned v) { return __builtin_bit_cast(float, v); };
+  const const_floats swp0 = constant(a.ws + (size_t)rb * a.KB), swp1 = constant(a.ws + (size_t)((G ? a.row_blocks : 0) + rb) * a.KB);
 
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -128,24 +109,23 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     return chunk(As + aoff + i * 16 * kBlock + (c ? off1 : off0));
   };
   // a step's scales: sa of the tokens, times the weights' of either projection
-  // With two stages the scales of the next step are loaded as it comes near (the 256-token tile has no registers for
-  // two sets), with more together with the step's data: loads return in order, and one waited for late would wait for all.
-  constexpr int SETS = ST > 2 ? ST : 1;
-  float sa[SETS][TM], sw0[SETS], sw1[SETS], s0[TM], s1[TM];
-  const auto load_scales = [&](int kb, int j) {
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
+  float sa[TM], s0[TM], s1[TM], sw0, sw1 = 0.f;
+  const auto read_scales = [&](int kb, int j) {
+    const int c = anew(lane) & 15;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[j][i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, first_token + 64 * i, 0, 0));
-    sw0[j] = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr0, 0, 4 * kb, 0));
-    sw1[j] = G ? as_float(__builtin_amdgcn_raw_buffer_load_b32(sr1, 0, 4 * kb, 0)) : 0.f;
+    for (int i = 0; i < TM; ++i) sa[i] = ts(j)[wave][16 * i + c];
+    sw0 = swp0[kb];
+    if (G) sw1 = swp1[kb];
   };
   // The loads of a step stay between two barriers (both are fences to the compiler): the waits count them.
-  constexpr int LOADS = LA + LW + (SETS > 1 ? TM + (G ? 2 : 1) : 0), PEND = (ST - 2) * LOADS;
+  constexpr int LOADS = LA + LW + 1, PEND = (ST - 2) * LOADS;
   static_assert((ST - 1) * LOADS <= 63, "vmcnt counts at most 63");
   constexpr auto vmcnt = [](int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); };      // and no LDS read pending
   const auto load_step = [&](int kb, int j) {
-    if constexpr (SETS > 1) load_scales(kb, j);
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)ts(j)[wave], 4,
+                                             4 * (m0 + 16 * wm * TM + (anew(lane) & (16 * TM - 1))), 0, 0, 0);
     load(kb, as(j), ws(j));
   };
   f32x4 p[TM];                                       // block sums that are not yet in acc
@@ -160,9 +140,9 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     for (int r = 0; r < 4; ++r) acc[t][i][r] = __builtin_fmaf(p[i][r], s, acc[t][i][r]);
   };
   // The scales of a step take effect once the last block of the step before is in acc.
-  const auto next_scales = [&](int i, int j) {
-    s0[i] = sa[j % SETS][i] * sw0[j % SETS];
-    s1[i] = sa[j % SETS][i] * sw1[j % SETS];
+  const auto next_scales = [&](int i) {
+    s0[i] = sa[i] * sw0;
+    s1[i] = sa[i] * sw1;
   };
 
   constexpr int RING = FP16 ? 2 : 4;                 // weight chunks in registers
@@ -201,7 +181,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
       if (last) {
         __builtin_amdgcn_s_waitcnt(vmcnt(PEND));
         barrier();
-        if constexpr (SETS == 1) load_scales(kb_next, 0);
+        read_scales(kb_next, (J + 1) % ST);
       }
       if constexpr (FP16) {
 #pragma unroll
@@ -209,7 +189,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
           const int j = e / (2 * TM), b = e / TM % 2, i = e % TM;
           __builtin_amdgcn_sched_barrier(0);
           if (e < TM) accumulate((t + TN - 1) % TN, i);
-          if (e < TM && t == 0) next_scales(i, J);
+          if (e < TM && t == 0) next_scales(i);
           p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[b], xh[i][j].v[b], e < TM ? f32x4{0.f, 0.f, 0.f, 0.f} : p[i], 0, 0, 0);
           const int c = 2 * t + j;
           if (b == 1 && i == 0) w[c % RING] = last ? wchunk(Wn, j) : wchunk(Ws, c + 2);
@@ -227,7 +207,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
         for (int i = 0; i < TM; ++i) {
           __builtin_amdgcn_sched_barrier(0);
           accumulate((t + TN - 1) % TN, i);
-          if (t == 0) next_scales(i, J);
+          if (t == 0) next_scales(i);
           p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
           if (i < 2) w[(2 * t + 2 + i) % RING] = last ? wchunk(Wn, i) : wchunk(Ws, 2 * t + 2 + i);
           if (last) read_x(An, i);
@@ -239,7 +219,6 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   };
 
   const int kl = kb1 - 1;                            // loads past the end read the last k block again, unused
-  if constexpr (SETS == 1) load_scales(kb0, 0);
 #pragma unroll
   for (int j = 0; j < ST; ++j) {
     asm volatile("" ::: "memory");
@@ -247,6 +226,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   }
   __builtin_amdgcn_s_waitcnt(vmcnt((ST - 1) * LOADS));
   barrier();
+  read_scales(kb0, 0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) read_x(A0, i);
 #pragma unroll
@@ -284,74 +264,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
   __syncthreads();                                   // and no wavefront reads it: what follows uses it otherwise
 
-  // ---- splits along K: partial tiles, summed in order by the workgroup that comes last
-  if (a.splits > 1) {
-    constexpr int SLOT = BM * kTileRows * 4;
-    const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
-        a.partials + (size_t)tile * a.splits * (SLOT / 4), (short)0, a.splits * SLOT, 0x00020000);
-    const int at = 16 * threadIdx.x;                 // block f of a slot: 16 bytes per thread
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-      for (int i = 0; i < TM; ++i) store_partial(part, split * SLOT + (t * TM + i) * (64 * NW * 16) + at, acc[t][i]);
-    if (!last_arrival(a.tickets + tile, a.splits, reinterpret_cast<int*>(W0))) return;
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-      for (int i = 0; i < TM; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.splits; ++s)
-#pragma unroll
-      for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int i = 0; i < TM; ++i) acc[t][i] += load_partial(part, s * SLOT + (t * TM + i) * (64 * NW * 16) + at);
-  }
-
-  // ---- outputs: lane l holds token l & 15 and weight rows 4 (l >> 4) .. + 3 of each block
-  constexpr int OT = G ? TN / 2 : TN;
-  if constexpr (!Q) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int m = m0 + 16 * (wm * TM + i) + col;
-      if (m >= a.M) continue;
-#pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        const int n = c0 + 16 * t + 4 * g;
-        if (n < a.N) store4(a, (size_t)m * a.N + n, gated<GATE>(acc[t][i], acc[t + TN - OT][i]));
-      }
-    }
-  } else {
-    auto& top = *reinterpret_cast<unsigned(*)[WN][BM]>(A0);   // largest magnitude of a token in each wavefront's columns
-    unsigned m[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      m[i] = 0;
-#pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        acc[t][i] = gated<GATE>(acc[t][i], acc[t + OT][i]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[i] = max(m[i], magnitude(acc[t][i][r]));
-      }
-      m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 16));
-      m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 32));
-      if (g == 0) top[wn][16 * (wm * TM + i) + col] = m[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-#pragma unroll
-      for (int w = 0; w < WN; ++w) m[i] = max(m[i], top[w][16 * (wm * TM + i) + col]);
-      const BlockScale b = block_scale(m[i], 1.0f);
-      const int token = m0 + 16 * (wm * TM + i) + col;
-      if (token >= a.M) continue;
-      if (wn == 0 && g == 0) a.os[(size_t)tn * a.M + token] = b.scale;
-#pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        const f32x4 v = acc[t][i];
-        *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)token * a.N + c0 + 16 * t + 4 * g) =
-            codes4(v[0] * b.to_code, v[1] * b.to_code, v[2] * b.to_code, v[3] * b.to_code);
-      }
-    }
-  }
+  finish_tile<WN, NW, GATE, Q>(a, acc, A0, W0, tile, split, tn, m0, wm * TM, wn, c0);
 }
 
 template <int WM, int TM, int ST>
@@ -374,8 +287,8 @@ void launch_tile(const W8Plan& pl, const W8Args& a, hipStream_t s) {
 
 hipError_t launch_tiles(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
   switch (pl.tile) {
-    case 64: launch_tile<2, 2, 4>(pl, a, stream); break;
-    case 128: launch_tile<4, 2, 3>(pl, a, stream); break;
+    case 64: launch_tile<2, 2, 3>(pl, a, stream); break;
+    case 128: launch_tile<2, 4, 3>(pl, a, stream); break;
     default: launch_tile<4, 4, 2>(pl, a, stream); break;
   }
   return hipGetLastError();
