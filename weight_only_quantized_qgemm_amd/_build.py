@@ -27,7 +27,7 @@ N_FORMATS = 6
 N_ATTN_UNITS = 6
 UNITS = ([("qgemm_host.cpp", []), ("qgemm_run.hip", []), ("qgemm_attention_host.cpp", []), ("qgemm_heads.hip", []),
           ("qgemm_cache.hip", []), ("qgemm_attention.hip", []), ("qgemm_w8a8_host.cpp", []), ("qgemm_w8a8.hip", []),
-          ("qgemm_add_norm.hip", []), ("qgemm_w8a8_rows.hip", []), ("qgemm_w8a8_stream.hip", []), ("qgemm_w8a8_tiles.hip", [])]
+          ("qgemm_add_norm.hip", []), ("qgemm_w8a8_rows.hip", []), ("qgemm_w8a8_tiles.hip", [])]
          + [(k, [f"-DQGEMM_ATTN_UNIT={u}"]) for k in ("qgemm_attention_rows.hip", "qgemm_attention_tiles.hip")
             for u in range(N_ATTN_UNITS)]
          + [(k, [f"-DQGEMM_FMT_UNIT={f}"]) for k in ("qgemm_decode.hip", "qgemm_prefill.hip", "qgemm_prefill_tw.hip")

@@ -49,12 +49,12 @@ extern "C" qgemm_status_t qgemm_w8a8_run(const qgemm_w8a8_t* p, const void* A, c
   a.gate = p->gate;
   a.splits = pl.splits;
   a.kb_per_split = pl.kb_per_split;
+  a.tiles = pl.tiles;
+  a.whole = pl.whole;
   a.tiles_n = pl.tiles_n;
   a.row_blocks = (a.N + kBlock - 1) / kBlock;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = pl.kind == W8_ROWS     ? w8::launch_rows(pl, a, s)
-                       : pl.kind == W8_STREAM ? w8::launch_stream(pl, a, s)
-                                              : w8::launch_tiles(pl, a, s);
+  const hipError_t e = pl.kind == W8_ROWS ? w8::launch_rows(pl, a, s) : w8::launch_tiles(pl, a, s);
   if (e != hipSuccess) return fail(QGEMM_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return QGEMM_OK;
 }

@@ -18,10 +18,6 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
-// What no kernel writes while it is read, at a uniform address: read by scalar loads.  (A vector load whose value
-// crosses a loop's back edge makes the compiler wait there for every load, those into LDS among them.)
-typedef const float __attribute__((address_space(4)))* const_floats;
-__device__ __forceinline__ const_floats constant(const float* p) { return (const_floats)(uintptr_t)p; }
 
 // Largest magnitude of the 16 lanes of a row (the lanes of one scale block), as the bits of a float:
 // compared as whole numbers, a NaN is larger than infinity and infinity larger than any number, so neither
@@ -83,7 +79,6 @@ __device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
 }
 
 hipError_t launch_rows(const W8Plan& pl, const W8Args& a, hipStream_t stream);
-hipError_t launch_stream(const W8Plan& pl, const W8Args& a, hipStream_t stream);
 hipError_t launch_tiles(const W8Plan& pl, const W8Args& a, hipStream_t stream);
 
 }  // namespace w8

@@ -89,29 +89,29 @@ __device__ __forceinline__ void store4(const W8Args& a, size_t at, f32x4 v) {
 // The end of a workgroup's tile: lane l of a wavefront holds token m0 + 16 (i0 + i) + (l & 15) and weight rows
 // 4 (l >> 4) .. + 3 of each block acc[t][i].  `top` and `flag` are LDS that nothing else uses any more.
 //
-// Workgroups that share a tile (splits along K) leave partial tiles in the workspace, and the one that comes last
+// Workgroups that share tile `group` of the split ones leave partial tiles in the workspace, and the one that comes last
 // sums them in order.
 template <int WN, int NW, int GATE, bool Q, int TN, int TM>
 __device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM], unsigned char* top_lds, unsigned char* flag,
-                                            int tile, int split, int tn, int m0, int i0, int wn, int c0) {
+                                            int group, int splits, int split, int tn, int m0, int i0, int wn, int c0) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int BM = 16 * TM * NW / WN;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
-  if (a.splits > 1) {
+  if (splits > 1) {
     constexpr int SLOT = TN * TM * 64 * NW * 16;     // bytes of a partial tile: 16 per thread and block
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
-        a.partials + (size_t)tile * a.splits * (SLOT / 4), (short)0, a.splits * SLOT, 0x00020000);
+        a.partials + (size_t)group * splits * (SLOT / 4), (short)0, splits * SLOT, 0x00020000);
     const int at = 16 * threadIdx.x;
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
       for (int i = 0; i < TM; ++i) store_partial(part, split * SLOT + (t * TM + i) * (64 * NW * 16) + at, acc[t][i]);
-    if (!last_arrival(a.tickets + tile, a.splits, reinterpret_cast<int*>(flag))) return;
+    if (!last_arrival(a.tickets + group, splits, reinterpret_cast<int*>(flag))) return;
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
       for (int i = 0; i < TM; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.splits; ++s)
+    for (int s = 0; s < splits; ++s)
 #pragma unroll
       for (int t = 0; t < TN; ++t)
 #pragma unroll

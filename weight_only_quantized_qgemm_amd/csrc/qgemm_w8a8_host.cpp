@@ -2,7 +2,6 @@
 // Nothing in this file touches the GPU.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <cstdio>
 #include <cstring>
 
@@ -84,17 +83,26 @@ qgemm_status_t validate_w8a8(const qgemm_w8a8_t* p) {
 // A launch holds less than 2^32 work-items.
 static bool launchable(int64_t workgroups) { return workgroups <= 0xffffffffLL / (64 * kW8Waves); }
 
-static qgemm_status_t finish_plan(W8Plan* pl, int64_t groups, int members_n, int splits, int KB, size_t slot_bytes) {
+// `whole` workgroups on their own and `groups` sets of members_n * splits.
+static qgemm_status_t finish_plan(W8Plan* pl, int64_t whole, int64_t groups, int members_n, int splits, int KB,
+                                  size_t slot_bytes) {
   pl->kb_per_split = (KB + splits - 1) / splits;
   pl->splits = (KB + pl->kb_per_split - 1) / pl->kb_per_split;       // none of them empty
   pl->groups = groups;
   pl->members = members_n * pl->splits;
-  const int64_t workgroups = groups * pl->members;
+  const int64_t sets = groups * pl->members, workgroups = whole + sets;
   if (!launchable(workgroups))
     return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows", (long long)workgroups);
   pl->grid = (unsigned)workgroups;
-  pl->ws_bytes = pl->members > 1 ? (size_t)kW8Tickets * 4 + (size_t)workgroups * slot_bytes : 0;
+  pl->ws_bytes = pl->members > 1 ? (size_t)kW8Tickets * 4 + (size_t)sets * slot_bytes : 0;
   return QGEMM_OK;
+}
+
+// Microseconds that a workgroup of the tiles kernel takes for a k block and besides, while every compute unit has one
+// (e4m3 and fp16 operands), and that sharing a tile costs each more.
+struct TileCost { double step[2], fixed, share; };
+static TileCost tile_cost(int tile) {
+  return tile == 256 ? TileCost{{1.57, 2.95}, 9.0, 2.6} : tile == 128 ? TileCost{{0.93, 1.60}, 5.5, 1.5} : TileCost{{0.60, 1.0}, 4.5, 1.0};
 }
 
 qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
@@ -102,7 +110,6 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   const bool gated = p->gate != QGEMM_GATE_NONE, quantized = p->out_dtype == QGEMM_DT_FP8_E4M3;
   const int KB = (int)(p->K / kBlock);
   const int64_t M = std::max<int64_t>(p->M, 1);
-  const int hint = std::min(p->split_hint, KB);
   if (p->kernel_hint == QGEMM_W8A8_ROWS || (p->kernel_hint == QGEMM_W8A8_AUTO && M <= kRowsMaxM)) {
     pl->kind = W8_ROWS;
     pl->tile = (int)((M + 15) / 16) * 16;
@@ -110,26 +117,46 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
     const int column_blocks = gated ? pl->blocks / 2 : pl->blocks;   // of a workgroup
     const int members = quantized ? kBlock / 16 / column_blocks : 1;
     const int64_t columns = (p->N / 16 + column_blocks - 1) / column_blocks, groups = columns / members;
-    int splits = hint;
+    int splits = std::min(p->split_hint, KB);
     if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, 2 * kCUs / columns), std::max(1, KB / kW8Waves));
     splits = std::min(splits, kMaxSplits);
     if (groups > kW8Tickets) splits = 1;
-    return finish_plan(pl, groups, members, splits, KB, (size_t)pl->blocks * pl->tile * 16 * 4);
+    return finish_plan(pl, 0, groups, members, splits, KB, (size_t)pl->blocks * pl->tile * 16 * 4);
   }
-  const auto tiles_n = [&](int rows) { return (p->N * (gated ? 2 : 1) + rows - 1) / rows; };
-  const auto tiles_of = [&](int t, int rows) { return (M + t - 1) / t * tiles_n(rows); };
-  pl->tile = p->tile_hint;
-  if (!pl->tile) pl->tile = tiles_of(256, kTileRows) >= kCUs ? 256 : tiles_of(128, kTileRows) >= kCUs / 2 ? 128 : 64;
-  pl->kind = getenv("STREAM") && pl->tile < 256 ? W8_STREAM : W8_TILES;
-  pl->blocks = gated || pl->kind == W8_TILES || tiles_of(pl->tile, kTileRows) >= kCUs / 2 ? 2 : 1;
-  const int rows = pl->blocks * kTileRows / 2;
-  pl->tiles_n = (int)tiles_n(rows);
-  const int64_t tiles = tiles_of(pl->tile, rows);
-  int splits = hint;
-  if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / tiles), std::max(1, KB / 4));
-  splits = std::min(splits, kMaxSplits);
-  if (tiles > kW8Tickets) splits = 1;
-  return finish_plan(pl, tiles, 1, splits, KB, (size_t)pl->tile * rows * 4);
+  pl->kind = W8_TILES;
+  const int columns = gated ? kTileRows / 2 : kTileRows;
+  pl->tiles_n = (int)((p->N + columns - 1) / columns);
+  const bool fp16 = quantized || p->out_dtype == QGEMM_DT_F32;
+  // The tiles of whole rounds over the compute units run on their own; those of the last round are split along K as far
+  // as that shortens it (all tiles, where there are fewer than compute units).
+  double best = 0.0;
+  int best_splits = 1;
+  for (int tile : {64, 128, 256}) {
+    if (p->tile_hint && p->tile_hint != tile) continue;
+    const int64_t tiles = (M + tile - 1) / tile * pl->tiles_n, tail = tiles % kCUs, rounds = tiles / kCUs;
+    const TileCost c = tile_cost(tile);
+    for (int s = 1; s <= (p->split_hint ? 1 : std::min(kMaxSplits, KB)); ++s) {
+      const int kb = (KB + s - 1) / s;
+      if (s > 1 && (!tail || (KB + kb - 1) / kb != s)) continue;
+      const double step = c.step[fp16], tail_rounds = (double)((tail * s + kCUs - 1) / kCUs);
+      const double us = (double)rounds * (KB * step + c.fixed) + tail_rounds * (kb * step + c.fixed) + (s > 1 ? 3.0 + s * c.share : 0.0);
+      if (pl->tile == 0 || us < best) {
+        best = us;
+        pl->tile = tile;
+        best_splits = s;
+      }
+    }
+  }
+  const int64_t tiles = (M + pl->tile - 1) / pl->tile * pl->tiles_n;
+  if (!launchable(tiles))
+    return fail(QGEMM_ERR_UNSUPPORTED, "the problem needs %lld workgroups, more than one launch allows", (long long)tiles);
+  pl->tiles = (int)tiles;
+  int splits = p->split_hint ? std::min(p->split_hint, KB) : best_splits;
+  int64_t whole = splits == 1 ? tiles : p->split_hint ? 0 : tiles - tiles % kCUs;
+  if (tiles - whole > kW8Tickets) whole = tiles;                     // a hint, on very many tiles
+  if (whole == tiles) splits = 1;
+  pl->whole = (int)whole;
+  return finish_plan(pl, whole, tiles - whole, 1, splits, KB, (size_t)pl->tile * kTileRows * 4);
 }
 
 // RNE to e4m3, |v| <= 448.
@@ -203,8 +230,8 @@ qgemm_status_t qgemm_w8a8_describe(const qgemm_w8a8_t* p, char* buf, size_t len)
   const int n = p->M == 0 ? std::snprintf(buf, len, "empty")
                 : pl.kind == W8_ROWS ? std::snprintf(buf, len, "rows grid=%u tokens=%d blocks=%d splits=%d members=%d", pl.grid,
                                                      pl.tile, pl.blocks, pl.splits, pl.members)
-                                     : std::snprintf(buf, len, "%s grid=%u tokens=%d blocks=%d splits=%d",
-                                                     pl.kind == W8_STREAM ? "stream" : "tiles", pl.grid, pl.tile, pl.blocks, pl.splits);
+                                     : std::snprintf(buf, len, "tiles grid=%u tokens=%d whole=%d splits=%d", pl.grid, pl.tile, pl.whole,
+                                                     pl.splits);
   if (n < 0 || (size_t)n >= len)
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
   return QGEMM_OK;

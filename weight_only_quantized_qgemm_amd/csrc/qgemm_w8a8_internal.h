@@ -22,14 +22,14 @@ constexpr int rows_blocks(int tokens, bool gated) { return tokens <= 16 ? (gated
 // Wavefronts of a workgroup (both kernels).
 constexpr int kW8Waves = 8;
 
-enum W8Kind : int { W8_ROWS = 1, W8_STREAM = 2, W8_TILES = 3 };
+enum W8Kind : int { W8_ROWS = 1, W8_TILES = 2 };
 
 // Launch plan of qgemm_w8a8_run, a pure function of the descriptor.
 struct W8Plan {
   W8Kind kind;
   int tile;            // tokens: of a tile, or (rows kernel) of the whole problem rounded up to 16
-  int blocks;          // 16-row weight blocks of a workgroup (rows kernel) or wavefront (stream kernel)
-  int tiles_n;         // tiles along the weight rows
+  int blocks;          // rows kernel: 16-row weight blocks of a workgroup
+  int tiles, whole, tiles_n;   // tiles kernel: all tiles, those that are not split, those along the weight rows
   int splits;          // workgroups along K
   int kb_per_split;
   int64_t groups;      // tickets: sets of workgroups whose last one finishes the output
@@ -55,7 +55,7 @@ struct W8Args {
   int M, N, K, KB;
   int out_dtype, gate;
   int splits, kb_per_split;
-  int tiles_n;                      // tiles along the weight rows
+  int tiles, whole, tiles_n;        // tiles kernel: all tiles, those that are not split, those along the weight rows
   int row_blocks;                   // scale blocks of one projection's rows
 };
 

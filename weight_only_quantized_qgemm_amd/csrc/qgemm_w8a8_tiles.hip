@@ -35,27 +35,23 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   __shared__ __attribute__((aligned(1024))) unsigned char W0[kTileRows * kBlock], W1[kTileRows * kBlock];
   __shared__ __attribute__((aligned(1024))) unsigned char A2[ST > 2 ? BM * kBlock : 16], W2[ST > 2 ? kTileRows * kBlock : 16];
   __shared__ __attribute__((aligned(1024))) unsigned char A3[ST > 3 ? BM * kBlock : 16], W3[ST > 3 ? kTileRows * kBlock : 16];
-  __shared__ float T0[NW][64], T1[NW][64], T2[ST > 2 ? NW : 1][64], T3[ST > 3 ? NW : 1][64];   // the tokens' scales
-  static_assert(ST >= 2 && ST <= 4 && TM <= 4, "two to four stages, a lane for each token of a wavefront");
+  static_assert(ST >= 2 && ST <= 4, "two to four stages");
   const auto as = [&](int j) -> unsigned char* { return j == 0 ? A0 : j == 1 ? A1 : j == 2 ? A2 : A3; };
   const auto ws = [&](int j) -> unsigned char* { return j == 0 ? W0 : j == 1 ? W1 : j == 2 ? W2 : W3; };
-  const auto ts = [&](int j) -> float(*)[64] { return j == 0 ? T0 : j == 1 ? T1 : j == 2 ? T2 : T3; };
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int tiles = gridDim.x / a.splits, split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+  // whole tiles first, then those that are split along K
+  const int tail = a.tiles - a.whole, at = blockIdx.x - a.whole;
+  const int splits = at < 0 ? 1 : a.splits, split = at < 0 ? 0 : at / tail;
+  const int tile = at < 0 ? (int)blockIdx.x : a.whole + at - split * tail;
   int tm, tn;
-  tile_of(tile, tiles, a.tiles_n, tm, tn);
+  tile_of(tile, a.tiles, a.tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * COLS;
-  const int kb0 = split * a.kb_per_split, kb1 = min(a.KB, kb0 + a.kb_per_split);
-
-  // What each step needs once is worked out from the lane's number anew: kept in registers, it would not fit beside the sums.
-  const auto anew = [](int l) {
-    asm volatile("" : "+v"(l));
-    return l;
-  };
+  const int kb0 = split * a.kb_per_split, kb1 = splits > 1 ? min(a.KB, kb0 + a.kb_per_split) : a.KB;
 
   // ---- loads into LDS: 1 KiB each, eight rows
+  const int drow = lane >> 3, dchunk = (lane & 7) ^ drow;
   const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.a + (size_t)m0 * a.K), (short)0, min(a.M - m0, BM) * a.K, 0x00020000);
   const int wrows = min(a.N - n0, COLS);
@@ -64,7 +60,8 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   const __amdgpu_buffer_rsrc_t wr1 = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.w + (size_t)(G ? a.N + n0 : n0) * a.K), (short)0, wrows * a.K, 0x00020000);
   const auto load = [&](int kb, unsigned char* As, unsigned char* Ws) {
-    const int l = anew(lane), drow = l >> 3, lane_off = drow * a.K + 16 * ((l & 7) ^ drow);
+    int lane_off = drow * a.K + 16 * dchunk;
+    asm volatile("" : "+v"(lane_off));               // the loads' offsets are added up anew each step, not kept in registers
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       const int r = 8 * (NW * i + wave);             // first row of the load
@@ -84,12 +81,16 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     }
   };
 
-  // ---- scales: of the tokens through LDS, one load a step and wavefront for its 16 TM tokens (a load instruction
-  // costs the same however little it carries; past the last token: 0); of the weights one per projection, uniform (a
+  // ---- scales: one per token block and lane (past the last token: 0); of the weights one per projection (a
   // wavefront's rows of one projection lie in one block of 128)
   const int c0 = n0 + wn * (G ? 8 * TN : 16 * TN);   // the wavefront's first output column
   const int rb = min(c0 / kBlock, a.row_blocks - 1);
-  const const_floats swp0 = constant(a.ws + (size_t)rb * a.KB), swp1 = constant(a.ws + (size_t)((G ? a.row_blocks : 0) + rb) * a.KB);
+  const auto scale_row = [&](int row) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.ws + (size_t)row * a.KB), (short)0, a.KB * 4, 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t sr0 = scale_row(rb), sr1 = scale_row((G ? a.row_blocks : 0) + rb);
+  const int first_token = 4 * (m0 + 16 * wm * TM + col);
+  const auto as_float = [](unsigned v) { return __builtin_bit_cast(float, v); };
 
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -109,23 +110,24 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     return chunk(As + aoff + i * 16 * kBlock + (c ? off1 : off0));
   };
   // a step's scales: sa of the tokens, times the weights' of either projection
-  float sa[TM], s0[TM], s1[TM], sw0, sw1 = 0.f;
-  const auto read_scales = [&](int kb, int j) {
-    const int c = anew(lane) & 15;
+  // With two stages the scales of the next step are loaded as it comes near (the 256-token tile has no registers for
+  // two sets), with more together with the step's data: loads return in order, and one waited for late would wait for all.
+  constexpr int SETS = ST > 2 ? ST : 1;
+  float sa[SETS][TM], sw0[SETS], sw1[SETS], s0[TM], s1[TM];
+  const auto load_scales = [&](int kb, int j) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = ts(j)[wave][16 * i + c];
-    sw0 = swp0[kb];
-    if (G) sw1 = swp1[kb];
+    for (int i = 0; i < TM; ++i) sa[j][i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, first_token + 64 * i, 0, 0));
+    sw0[j] = as_float(__builtin_amdgcn_raw_buffer_load_b32(sr0, 0, 4 * kb, 0));
+    sw1[j] = G ? as_float(__builtin_amdgcn_raw_buffer_load_b32(sr1, 0, 4 * kb, 0)) : 0.f;
   };
   // The loads of a step stay between two barriers (both are fences to the compiler): the waits count them.
-  constexpr int LOADS = LA + LW + 1, PEND = (ST - 2) * LOADS;
+  constexpr int LOADS = LA + LW + (SETS > 1 ? TM + (G ? 2 : 1) : 0), PEND = (ST - 2) * LOADS;
   static_assert((ST - 1) * LOADS <= 63, "vmcnt counts at most 63");
   constexpr auto vmcnt = [](int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); };      // and no LDS read pending
   const auto load_step = [&](int kb, int j) {
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)ts(j)[wave], 4,
-                                             4 * (m0 + 16 * wm * TM + (anew(lane) & (16 * TM - 1))), 0, 0, 0);
+    if constexpr (SETS > 1) load_scales(kb, j);
     load(kb, as(j), ws(j));
   };
   f32x4 p[TM];                                       // block sums that are not yet in acc
@@ -140,9 +142,9 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     for (int r = 0; r < 4; ++r) acc[t][i][r] = __builtin_fmaf(p[i][r], s, acc[t][i][r]);
   };
   // The scales of a step take effect once the last block of the step before is in acc.
-  const auto next_scales = [&](int i) {
-    s0[i] = sa[i] * sw0;
-    s1[i] = sa[i] * sw1;
+  const auto next_scales = [&](int i, int j) {
+    s0[i] = sa[j % SETS][i] * sw0[j % SETS];
+    s1[i] = sa[j % SETS][i] * sw1[j % SETS];
   };
 
   constexpr int RING = FP16 ? 2 : 4;                 // weight chunks in registers
@@ -166,6 +168,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
       x8[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   };
+  const int kl = kb1 - 1;                            // loads past the end read the last k block again, unused
   // One k block: its data lie in stage j, x and the first weight block are in registers.  Block t - 1 enters acc between
   // the MFMAs of block t, so that a wavefront's MFMAs and FMAs overlap (kept apart, the two wavefronts of a SIMD run in step
   // and wait for each other).  Before the last block everything of this step has been read, and the next one's data
@@ -181,7 +184,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
       if (last) {
         __builtin_amdgcn_s_waitcnt(vmcnt(PEND));
         barrier();
-        read_scales(kb_next, (J + 1) % ST);
+        if constexpr (SETS == 1) load_scales(kb_next, 0);
       }
       if constexpr (FP16) {
 #pragma unroll
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
           const int j = e / (2 * TM), b = e / TM % 2, i = e % TM;
           __builtin_amdgcn_sched_barrier(0);
           if (e < TM) accumulate((t + TN - 1) % TN, i);
-          if (e < TM && t == 0) next_scales(i);
+          if (e < TM && t == 0) next_scales(i, J);
           p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[b], xh[i][j].v[b], e < TM ? f32x4{0.f, 0.f, 0.f, 0.f} : p[i], 0, 0, 0);
           const int c = 2 * t + j;
           if (b == 1 && i == 0) w[c % RING] = last ? wchunk(Wn, j) : wchunk(Ws, c + 2);
@@ -207,7 +210,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
         for (int i = 0; i < TM; ++i) {
           __builtin_amdgcn_sched_barrier(0);
           accumulate((t + TN - 1) % TN, i);
-          if (t == 0) next_scales(i);
+          if (t == 0) next_scales(i, J);
           p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
           if (i < 2) w[(2 * t + 2 + i) % RING] = last ? wchunk(Wn, i) : wchunk(Ws, 2 * t + 2 + i);
           if (last) read_x(An, i);
@@ -218,7 +221,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  const int kl = kb1 - 1;                            // loads past the end read the last k block again, unused
+  if constexpr (SETS == 1) load_scales(kb0, 0);
 #pragma unroll
   for (int j = 0; j < ST; ++j) {
     asm volatile("" ::: "memory");
@@ -226,7 +229,6 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   }
   __builtin_amdgcn_s_waitcnt(vmcnt((ST - 1) * LOADS));
   barrier();
-  read_scales(kb0, 0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) read_x(A0, i);
 #pragma unroll
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
   __syncthreads();                                   // and no wavefront reads it: what follows uses it otherwise
 
-  finish_tile<WN, NW, GATE, Q>(a, acc, A0, W0, tile, split, tn, m0, wm * TM, wn, c0);
+  finish_tile<WN, NW, GATE, Q>(a, acc, A0, W0, tile - a.whole, splits, split, tn, m0, wm * TM, wn, c0);
 }
 
 template <int WM, int TM, int ST>
@@ -287,7 +289,7 @@ void launch_tile(const W8Plan& pl, const W8Args& a, hipStream_t s) {
 
 hipError_t launch_tiles(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
   switch (pl.tile) {
-    case 64: launch_tile<2, 2, 3>(pl, a, stream); break;
+    case 64: launch_tile<2, 2, 4>(pl, a, stream); break;
     case 128: launch_tile<2, 4, 3>(pl, a, stream); break;
     default: launch_tile<4, 4, 2>(pl, a, stream); break;
   }
