@@ -240,7 +240,7 @@ def product_check(y, scales, want, tol, out):
     assert np.all((top == 448) | (gs.T <= 2.0 ** -100))
 
 
-SIZES = [(1, 16, 128), (1, 272, 1152), (2, 128, 256), (5, 640, 4096), (16, 256, 2048), (17, 400, 384), (33, 144, 1024),
+SIZES = [(1, 16, 128), (1, 272, 1152), (3, 256, 5120), (9, 128, 1920), (2, 128, 256), (5, 640, 4096), (16, 256, 2048), (17, 400, 384), (33, 144, 1024),
          (48, 512, 640), (64, 1040, 512), (65, 256, 128), (66, 272, 384), (129, 640, 256), (255, 528, 640), (300, 1296, 512),
          (520, 256, 1280)]
 
@@ -258,7 +258,8 @@ def test_products(q, m, n, k, gate):
         product_check(y, scales, want, tol, out)
 
 
-@pytest.mark.parametrize("m,n,k,gate,out", [(7, 256, 1792, "none", "f32"), (40, 256, 1792, "silu", "e4m3"), (64, 144, 1280, "gelu", "f16"),
+@pytest.mark.parametrize("m,n,k,gate,out", [(7, 256, 1792, "none", "f32"), (1, 144, 5120, "none", "f16"),
+                                            (13, 384, 2688, "silu", "e4m3"), (16, 256, 4992, "gelu", "bf16"), (40, 256, 1792, "silu", "e4m3"), (64, 144, 1280, "gelu", "f16"),
                                             (20, 384, 640, "gelu", "e4m3"), (130, 528, 1152, "none", "bf16"),
                                             (270, 384, 1152, "silu", "e4m3"), (61, 272, 1024, "silu", "f32")])
 def test_kernels_splits_and_tiles(q, m, n, k, gate, out):
@@ -268,7 +269,7 @@ def test_kernels_splits_and_tiles(q, m, n, k, gate, out):
     want, tol = product_want(*host, gate, parts)
     ins = on_gpu(*host)
     hints = [dict(kernel_hint=q.W8A8_TILES, tile_hint=t, split_hint=s) for t in (64, 128, 256) for s in (1, 2, 5, 32)]
-    if m <= 64:
+    if m <= 16:
         hints += [dict(kernel_hint=q.W8A8_ROWS, split_hint=s) for s in (1, 2, 3, 32)]
     for h in hints:
         y, scales, p, ws = run_product(q, ins, n, gate, out, **h)
@@ -281,6 +282,23 @@ def test_kernels_splits_and_tiles(q, m, n, k, gate, out):
             assert torch.equal(y.view(torch.uint8), first), h
         if ws is not None:
             assert bool((ws[:4 << 17] == 0).all()), "tickets"
+
+
+def test_last_round_split_along_k(q):
+    """More tiles than compute units: whole ones first, those of the last round shared."""
+    m, n, k = 130, 22000, 1280
+    host = product_inputs(m, n, k, 1, 17)
+    want, tol = product_want(*host, "none", 1)
+    ins = on_gpu(*host)
+    for tile in (64, 128):
+        y, _, p, ws = run_product(q, ins, n, "none", "bf16", tile_hint=tile)
+        product_check(y, None, want, tol, "bf16")
+        first = y.clone()
+        for _ in range(3):
+            q.w8a8_run(p, *ins, y, None, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(y, first)
+    assert any("whole=256" in d and "splits=1" not in d for d in (q.w8a8_describe(q.w8a8_problem(m, n, k, tile_hint=t)) for t in (64, 128)))
 
 
 def test_nan_codes_stay_in_their_rows_and_columns(q):

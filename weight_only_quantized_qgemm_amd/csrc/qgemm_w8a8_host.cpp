@@ -102,7 +102,7 @@ static qgemm_status_t finish_plan(W8Plan* pl, int64_t whole, int64_t groups, int
 // (e4m3 and fp16 operands), and that sharing a tile costs each more.
 struct TileCost { double step[2], fixed, share; };
 static TileCost tile_cost(int tile) {
-  return tile == 256 ? TileCost{{1.57, 2.95}, 9.0, 2.6} : tile == 128 ? TileCost{{0.93, 1.60}, 5.5, 1.5} : TileCost{{0.60, 1.0}, 4.5, 1.0};
+  return tile == 256 ? TileCost{{1.57, 2.95}, 9.0, 4.0} : tile == 128 ? TileCost{{0.93, 1.60}, 5.5, 2.4} : TileCost{{0.60, 1.0}, 4.5, 1.2};
 }
 
 qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
@@ -112,16 +112,20 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   const int64_t M = std::max<int64_t>(p->M, 1);
   if (p->kernel_hint == QGEMM_W8A8_ROWS || (p->kernel_hint == QGEMM_W8A8_AUTO && M <= kRowsMaxM)) {
     pl->kind = W8_ROWS;
-    pl->tile = (int)((M + 15) / 16) * 16;
-    pl->blocks = rows_blocks(pl->tile, gated);
-    const int column_blocks = gated ? pl->blocks / 2 : pl->blocks;   // of a workgroup
-    const int members = quantized ? kBlock / 16 / column_blocks : 1;
-    const int64_t columns = (p->N / 16 + column_blocks - 1) / column_blocks, groups = columns / members;
+    const int members = quantized ? kBlock / 16 : 1;
+    const int64_t columns = p->N / 16, groups = columns / members;   // workgroups without a split
     int splits = std::min(p->split_hint, KB);
-    if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, 2 * kCUs / columns), std::max(1, KB / kW8Waves));
+    // As many as give every compute unit a workgroup, of two k blocks a wavefront at least: sharing an output takes three
+    // dependent trips to memory (4 x 1024 x 2048: 3.3 us alone, 4.3 shared by two; 4 x 1024 x 8192: 7.4, 6.6, by four 6.4).
+    if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / columns), std::max(1, KB / (2 * kW8Waves)));
     splits = std::min(splits, kMaxSplits);
     if (groups > kW8Tickets) splits = 1;
-    return finish_plan(pl, 0, groups, members, splits, KB, (size_t)pl->blocks * pl->tile * 16 * 4);
+    // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
+    // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 4096, 32: 5.25 and 5.68).
+    const int per = (KB + splits - 1) / splits;
+    const auto places = [&](int waves) { return (per + 2 * waves - 1) / (2 * waves) * 2 * waves; };
+    pl->waves = places(4) * 10 <= places(8) * 9 ? 4 : 8;
+    return finish_plan(pl, 0, groups, members, splits, KB, (size_t)(gated ? 2 : 1) * 1024);
   }
   pl->kind = W8_TILES;
   const int columns = gated ? kTileRows / 2 : kTileRows;
@@ -228,8 +232,7 @@ qgemm_status_t qgemm_w8a8_describe(const qgemm_w8a8_t* p, char* buf, size_t len)
   st = make_w8a8_plan(p, &pl);
   if (st != QGEMM_OK) return st;
   const int n = p->M == 0 ? std::snprintf(buf, len, "empty")
-                : pl.kind == W8_ROWS ? std::snprintf(buf, len, "rows grid=%u tokens=%d blocks=%d splits=%d members=%d", pl.grid,
-                                                     pl.tile, pl.blocks, pl.splits, pl.members)
+                : pl.kind == W8_ROWS ? std::snprintf(buf, len, "rows grid=%u waves=%d splits=%d members=%d", pl.grid, pl.waves, pl.splits, pl.members)
                                      : std::snprintf(buf, len, "tiles grid=%u tokens=%d whole=%d splits=%d", pl.grid, pl.tile, pl.whole,
                                                      pl.splits);
   if (n < 0 || (size_t)n >= len)

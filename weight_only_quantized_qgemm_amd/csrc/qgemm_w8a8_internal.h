@@ -15,11 +15,9 @@ constexpr int kBlock = 128;
 // Weight rows of a workgroup's tile (tiles kernel); with a gate half of them belong to each projection,
 // so that a tile's outputs are one scale block wide.
 constexpr int kTileRows = 256;
-// The rows kernel takes up to this many tokens, in column tiles of 16.
-constexpr int kRowsMaxM = 64;
-// Weight blocks of 16 rows that a workgroup of the rows kernel owns.
-constexpr int rows_blocks(int tokens, bool gated) { return tokens <= 16 ? (gated ? 2 : 1) : tokens == 48 ? 4 : 2; }
-// Wavefronts of a workgroup (both kernels).
+// The rows kernel takes up to this many tokens.
+constexpr int kRowsMaxM = 16;
+// Wavefronts of a workgroup (at most: the rows kernel may take 4).
 constexpr int kW8Waves = 8;
 
 enum W8Kind : int { W8_ROWS = 1, W8_TILES = 2 };
@@ -27,8 +25,8 @@ enum W8Kind : int { W8_ROWS = 1, W8_TILES = 2 };
 // Launch plan of qgemm_w8a8_run, a pure function of the descriptor.
 struct W8Plan {
   W8Kind kind;
-  int tile;            // tokens: of a tile, or (rows kernel) of the whole problem rounded up to 16
-  int blocks;          // rows kernel: 16-row weight blocks of a workgroup
+  int tile;            // tiles kernel: tokens of a tile
+  int waves;           // rows kernel: wavefronts of a workgroup
   int tiles, whole, tiles_n;   // tiles kernel: all tiles, those that are not split, those along the weight rows
   int splits;          // workgroups along K
   int kb_per_split;

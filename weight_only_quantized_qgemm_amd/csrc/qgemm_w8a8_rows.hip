@@ -1,4 +1,4 @@
-// The rows kernel of the 8-bit products: a few tokens (M <= 64), the weights streamed once.
+// The rows kernel of the 8-bit products: up to 16 tokens, the weights streamed once.
 //
 //   p_r[m] = sum_b as[b][m] ws[r / 128][b] (sum_{k in block b} a[m][k] w[r][k])
 //
@@ -9,90 +9,83 @@
 // the same for both, which is all that a dot product asks of its order.  The result has token l & 15 and weight rows
 // 4 (l >> 4) .. + 3 in lane l, so both scales are one factor per lane, applied to the fp32 block sum.
 //
+// Bound by the weights' way from memory: 4096 x 11008, one token 10.3 us, 4.4 TB/s, 16 tokens 13.1 us; 11008 x 4096 gated
+// to 16 bits 17.8 and 19.7 us (5.1 and 4.6 TB/s).  Bringing the tokens into LDS first, for fewer load instructions, delays
+// the first product by more than it saves (4096 x 4096, one token: 5.7 us against 5.2).
+//
 // The wavefronts' sums meet in LDS, in wavefront order.  Where several workgroups make one output (splits along
 // K; the eight column blocks of an output scale block) each leaves its fp32 sums in the workspace and takes a
 // ticket, and the one that draws the last ticket adds them in order and finishes: no workgroup waits for another.
+#include <type_traits>
+
 #include "qgemm_w8a8_fixup.h"
 
 namespace qgemm {
 namespace w8 {
 namespace {
 
-template <int MB, int U, int NW, int D, int OCC, int GATE, bool Q>
-__global__ __launch_bounds__(64 * NW, OCC) void rows_kernel(W8Args a) {
+template <int NW, int GATE, bool Q>
+__global__ __launch_bounds__(64 * NW, 4) void rows_kernel(W8Args a) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
-  constexpr int CB = G ? U / 2 : U;                  // column blocks of a workgroup
-  constexpr int F = Q ? kBlock / 16 / CB : 1;        // workgroups along the columns of one output scale block
-  __shared__ f32x4 sums[NW / 2][U][MB][64];
+  constexpr int U = G ? 2 : 1;                       // weight blocks: one of either projection
+  constexpr int F = Q ? kBlock / 16 : 1;             // workgroups along the columns of one output scale block
+  __shared__ f32x4 sums[NW / 2][U][64];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // workgroup = (group, F columns in it, split)
+  // workgroup = (group, column block in it, split)
   const int members = F * a.splits;
   const int member = blockIdx.x % members, group = blockIdx.x / members;
-  const int cg = member / a.splits, split = member - cg * a.splits;
-  const int cb0 = (group * F + cg) * CB;             // first column block
+  const int cb = member / a.splits, split = member - cb * a.splits;
+  const int n0 = (group * F + cb) * 16;              // first output column
   const int kb0 = split * a.kb_per_split, kb1 = min(a.KB, kb0 + a.kb_per_split);
+  const int token = min(col, a.M - 1);               // tokens past the last repeat it and are not stored
 
-  // weight block u: column block u % CB of projection u / CB; blocks past the last repeat it and are not stored
-  // (addresses: a uniform base and a 32-bit offset per lane; 64 rows of K <= 2^22 stay below 2^28)
+  // (addresses: a uniform base and a 32-bit offset per lane; 16 rows of K <= 2^22 stay below 2^26)
   const uint8_t* wp[U];
   const float* sp[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int n = min(cb0 + u % CB, (a.N >> 4) - 1) * 16;
-    wp[u] = a.w + ((size_t)(u / CB) * a.N + n) * a.K;
-    sp[u] = a.ws + ((size_t)(u / CB) * a.row_blocks + n / kBlock) * a.KB;
+    wp[u] = a.w + ((size_t)u * a.N + n0) * a.K;
+    sp[u] = a.ws + ((size_t)u * a.row_blocks + n0 / kBlock) * a.KB;
   }
-  const unsigned woff = col * a.K + 16 * g;
-  unsigned token[MB], aoff[MB];
+  const unsigned woff = col * a.K + 16 * g, aoff = token * a.K + 16 * g;
+  f32x4 acc[U];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    token[i] = min(16 * i + col, a.M - 1);           // likewise
-    aoff[i] = token[i] * a.K + 16 * g;
-  }
-  f32x4 acc[U][MB];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < MB; ++i) acc[u][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int u = 0; u < U; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // D k blocks in flight per wavefront, each in registers of its own
+  // two k blocks in flight per wavefront (four leave registers for half as many workgroups: gated 16 x 11008 x 4096 21.9 us
+  // against 19.7)
+  constexpr int D = 2;
   struct Chunks { i32x4 v[2]; };
-  Chunks w[D][U], x[D][MB];
-  float sw[D][U], sa[D][MB];
+  Chunks w[D][U], x[D];
+  float sw[D][U], sa[D];
+  bool in[D];                                        // whether the block in set d is one of this wavefront's
   const auto chunks = [](const uint8_t* p, unsigned off) {
     return Chunks{{*reinterpret_cast<const i32x4*>(p + off), *reinterpret_cast<const i32x4*>(p + 64 + off)}};
   };
-  bool in[D];                                        // whether the block in set d is one of this wavefront's
   const auto load = [&](int d, int at) {
     in[d] = at < kb1;
     const int kb = min(at, kb1 - 1);
 #pragma unroll
     for (int u = 0; u < U; ++u) w[d][u] = chunks(wp[u] + (size_t)kb * kBlock, woff);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) x[d][i] = chunks(a.a + (size_t)kb * kBlock, aoff[i]);
-#pragma unroll
     for (int u = 0; u < U; ++u) sw[d][u] = sp[u][kb];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) sa[d][i] = (a.as + (size_t)kb * a.M)[token[i]];
+    x[d] = chunks(a.a + (size_t)kb * kBlock, aoff);
+    sa[d] = (a.as + (size_t)kb * a.M)[token];
   };
   const auto compute = [&](int d) {
+    const Halves x0 = halves(x[d].v[0]), x1 = halves(x[d].v[1]);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const Halves x0 = halves(x[d][i].v[0]), x1 = halves(x[d][i].v[1]);
+    for (int u = 0; u < U; ++u) {
+      const Halves w0 = halves(w[d][u].v[0]), w1 = halves(w[d][u].v[1]);
+      f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[0], x0.v[0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[1], x0.v[1], p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[0], x1.v[0], p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[1], x1.v[1], p, 0, 0, 0);
+      const float s = in[d] ? sa[d] * sw[d][u] : 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const Halves w0 = halves(w[d][u].v[0]), w1 = halves(w[d][u].v[1]);
-        f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[0], x0.v[0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[1], x0.v[1], p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[0], x1.v[0], p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[1], x1.v[1], p, 0, 0, 0);
-        const float s = in[d] ? sa[d][i] * sw[d][u] : 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[u][i][r] = __builtin_fmaf(p[r], s, acc[u][i][r]);
-        if (U * MB > 4) __builtin_amdgcn_sched_barrier(0);   // the weights are converted for each token tile: held, they would not fit
-      }
+      for (int r = 0; r < 4; ++r) acc[u][r] = __builtin_fmaf(p[r], s, acc[u][r]);
     }
   };
   // The last round is as long as the others: blocks past the end are the last one again, with factor 0 (branches
@@ -110,121 +103,94 @@ __global__ __launch_bounds__(64 * NW, OCC) void rows_kernel(W8Args a) {
 #pragma unroll
   for (int d = 0; d < D; ++d) compute(d);
 
-  // the wavefronts' sums: 4 .. 7 into 0 .. 3, then those four in order
+  // the wavefronts' sums: the second half into the first, then those in order
   if (wave >= NW / 2) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < MB; ++i) sums[wave - NW / 2][u][i][lane] = acc[u][i];
+    for (int u = 0; u < U; ++u) sums[wave - NW / 2][u][lane] = acc[u];
   }
   __syncthreads();
   if (wave < NW / 2) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < MB; ++i) sums[wave][u][i][lane] += acc[u][i];
+    for (int u = 0; u < U; ++u) sums[wave][u][lane] += acc[u];
   }
   __syncthreads();
-  const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
-      a.partials + (size_t)group * members * (U * MB * 256), (short)0, members * (U * MB * 1024), 0x00020000);
-  const auto slot = [&](int m, int u, int i) { return ((m * U + u) * MB + i) * 1024 + 16 * lane; };
-  const auto joined = [&](int u, int i) {
-    f32x4 v = sums[0][u][i][lane];
+  const __amdgpu_buffer_rsrc_t part =
+      __builtin_amdgcn_make_buffer_rsrc(a.partials + (size_t)group * members * (U * 256), (short)0, members * (U * 1024), 0x00020000);
+  const auto slot = [&](int m, int u) { return (m * U + u) * 1024 + 16 * lane; };
+  const auto joined = [&](int u) {
+    f32x4 v = sums[0][u][lane];
 #pragma unroll
-    for (int w = 1; w < NW / 2; ++w) v += sums[w][u][i][lane];
+    for (int w = 1; w < NW / 2; ++w) v += sums[w][u][lane];
     return v;
   };
   if (members > 1) {
-    for (int f = wave; f < U * MB; f += NW) store_partial(part, slot(member, f / MB, f % MB), joined(f / MB, f % MB));
+    if (wave < U) store_partial(part, slot(member, wave), joined(wave));
     if (!last_arrival(a.tickets + group, members, &s_last)) return;
   }
   if constexpr (!Q) {
-    // one (column block, token tile) after the other, by the wavefronts in turn
-    for (int f = wave; f < CB * MB; f += NW) {
-      const int c = f / MB, i = f % MB;
-      f32x4 v[2];
+    if (wave > 0) return;
+    f32x4 v[2];
 #pragma unroll
-      for (int part_of = 0; part_of < (G ? 2 : 1); ++part_of) {
-        const int u = part_of * CB + c;
-        if (members > 1) {
-          v[part_of] = load_partial(part, slot(0, u, i));
-          for (int s = 1; s < a.splits; ++s) v[part_of] += load_partial(part, slot(s, u, i));
-        } else {
-          v[part_of] = joined(u, i);
-        }
+    for (int u = 0; u < U; ++u) {
+      if (members > 1) {
+        v[u] = load_partial(part, slot(0, u));
+        for (int s = 1; s < a.splits; ++s) v[u] += load_partial(part, slot(s, u));
+      } else {
+        v[u] = joined(u);
       }
-      const int m = 16 * i + col, n = (cb0 + c) * 16 + 4 * g;
-      if (m < a.M && n < a.N) store4(a, (size_t)m * a.N + n, gated<GATE>(v[0], v[G ? 1 : 0]));
     }
+    if (col < a.M) store4(a, (size_t)col * a.N + n0 + 4 * g, gated<GATE>(v[0], v[U - 1]));
   } else {
-    // first every column block's outputs and largest magnitudes, then the codes
-    constexpr int NB = kBlock / 16;
-    __shared__ f32x4 outs[NB * MB][64];
-    __shared__ unsigned top[NB * MB][16];
-    for (int f = wave; f < NB * MB; f += NW) {
-      const int c = f % NB, i = f / NB;
+    // every column block's outputs and largest magnitudes, then the codes
+    constexpr int PER = kBlock / 16 / NW > 0 ? kBlock / 16 / NW : 1;     // column blocks of a wavefront
+    __shared__ unsigned top[kBlock / 16][16];
+    f32x4 y[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int c = wave * PER + j;
       f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
       for (int s = 0; s < a.splits; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) v[h] += load_partial(part, slot(c / CB * a.splits + s, h * CB + c % CB, i));
-      const f32x4 y = gated<GATE>(v[0], v[1]);
-      unsigned m = max(max(magnitude(y[0]), magnitude(y[1])), max(magnitude(y[2]), magnitude(y[3])));
+        for (int u = 0; u < 2; ++u) v[u] += load_partial(part, slot(c * a.splits + s, u));
+      y[j] = gated<GATE>(v[0], v[1]);
+      unsigned m = max(max(magnitude(y[j][0]), magnitude(y[j][1])), max(magnitude(y[j][2]), magnitude(y[j][3])));
       m = max(m, (unsigned)__shfl_xor((int)m, 16));
       m = max(m, (unsigned)__shfl_xor((int)m, 32));
-      outs[f][lane] = y;
-      if (lane < 16) top[f][lane] = m;
+      if (g == 0) top[c][col] = m;
     }
     __syncthreads();
-    for (int f = wave; f < NB * MB; f += NW) {
-      const int c = f % NB, i = f / NB, t = 16 * i + col;
-      unsigned m = 0;
+    unsigned m = 0;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) m = max(m, top[NB * i + b][col]);
-      const BlockScale b = block_scale(m, 1.0f);
-      const f32x4 y = outs[f][lane];
-      if (t < a.M) {
-        *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)t * a.N + group * kBlock + 16 * c + 4 * g) =
-            codes4(y[0] * b.to_code, y[1] * b.to_code, y[2] * b.to_code, y[3] * b.to_code);
-        if (c == 0 && g == 0) a.os[(size_t)group * a.M + t] = b.scale;
-      }
-    }
+    for (int c = 0; c < kBlock / 16; ++c) m = max(m, top[c][col]);
+    const BlockScale b = block_scale(m, 1.0f);
+    if (col >= a.M) return;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)col * a.N + group * kBlock + 16 * (wave * PER + j) + 4 * g) =
+          codes4(y[j][0] * b.to_code, y[j][1] * b.to_code, y[j][2] * b.to_code, y[j][3] * b.to_code);
+    if (wave == 0 && g == 0) a.os[(size_t)group * a.M + col] = b.scale;
   }
 }
 
-#ifndef R1
-#define R1 8, 2, 4
-#define R1G 8, 2, 4
-#define R2 8, 2, 2
-#define R3 8, 2, 2
-#define R4 8, 2, 2
-#endif
-template <int MB, int U, int NW, int D, int OCC>
-void launch_mb(const W8Plan& pl, const W8Args& a, hipStream_t s) {
+template <int NW>
+void launch_waves(const W8Plan& pl, const W8Args& a, hipStream_t s) {
   const dim3 grid(pl.grid), block(64 * NW);
-  const bool q = a.out_dtype == QGEMM_DT_FP8_E4M3;
-  if (a.gate == QGEMM_GATE_NONE) rows_kernel<MB, U, NW, D, OCC, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a);
-  else if constexpr (U > 1) {
-  if (a.gate == QGEMM_GATE_SILU)
-    q ? rows_kernel<MB, U, NW, D, OCC, QGEMM_GATE_SILU, true><<<grid, block, 0, s>>>(a)
-      : rows_kernel<MB, U, NW, D, OCC, QGEMM_GATE_SILU, false><<<grid, block, 0, s>>>(a);
-  else
-    q ? rows_kernel<MB, U, NW, D, OCC, QGEMM_GATE_GELU_TANH, true><<<grid, block, 0, s>>>(a)
-      : rows_kernel<MB, U, NW, D, OCC, QGEMM_GATE_GELU_TANH, false><<<grid, block, 0, s>>>(a);
+  const auto gate = [&](auto g) {
+    constexpr int GATE = decltype(g)::value;
+    if (a.out_dtype != QGEMM_DT_FP8_E4M3) rows_kernel<NW, GATE, false><<<grid, block, 0, s>>>(a);
+    else if constexpr (GATE != QGEMM_GATE_NONE) rows_kernel<NW, GATE, true><<<grid, block, 0, s>>>(a);
+  };
+  switch (a.gate) {
+    case QGEMM_GATE_NONE: gate(std::integral_constant<int, QGEMM_GATE_NONE>{}); break;
+    case QGEMM_GATE_SILU: gate(std::integral_constant<int, QGEMM_GATE_SILU>{}); break;
+    default: gate(std::integral_constant<int, QGEMM_GATE_GELU_TANH>{}); break;
   }
 }
 
 }  // namespace
 
 hipError_t launch_rows(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
-  switch (pl.tile) {
-    case 16:
-      if (pl.blocks == 1) launch_mb<1, 1, R1>(pl, a, stream);
-      else launch_mb<1, 2, R1G>(pl, a, stream);
-      break;
-    case 32: launch_mb<2, rows_blocks(32, false), R2>(pl, a, stream); break;
-    case 48: launch_mb<3, rows_blocks(48, false), R3>(pl, a, stream); break;
-    default: launch_mb<4, rows_blocks(64, false), R4>(pl, a, stream); break;
-  }
+  pl.waves == 8 ? launch_waves<8>(pl, a, stream) : launch_waves<4>(pl, a, stream);
   return hipGetLastError();
 }
 
