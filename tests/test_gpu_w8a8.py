@@ -286,7 +286,7 @@ def test_kernels_splits_and_tiles(q, m, n, k, gate, out):
 
 def test_last_round_split_along_k(q):
     """More tiles than compute units: whole ones first, those of the last round shared."""
-    m, n, k = 130, 22000, 1280
+    m, n, k = 130, 22000, 2560
     host = product_inputs(m, n, k, 1, 17)
     want, tol = product_want(*host, "none", 1)
     ins = on_gpu(*host)

@@ -71,29 +71,57 @@ __device__ __forceinline__ f32x4 gated(f32x4 g, f32x4 u) {
   return y;
 }
 
-// Four consecutive outputs, each rounded once.
-__device__ __forceinline__ void store4(const W8Args& a, size_t at, f32x4 v) {
-  if (a.out_dtype == QGEMM_DT_F32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
-  } else if (a.out_dtype == QGEMM_DT_F16) {
+// Four consecutive outputs rounded to 16 bits.
+__device__ __forceinline__ u32x2 pack16(const W8Args& a, f32x4 v) {
+  if (a.out_dtype == QGEMM_DT_F16) {
     const f16x2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
-        u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
-  } else {
-    const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
-        u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+    return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
   }
+  const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+  return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
 }
 
+// Four consecutive outputs, each rounded once.
+__device__ __forceinline__ void store4(const W8Args& a, size_t at, f32x4 v) {
+  if (a.out_dtype == QGEMM_DT_F32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
+  else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) = pack16(a, v);
+}
+
+// A wavefront's outputs of 16 tokens on their way to memory: rows of RB bytes in LDS of its own, read back so that each store
+// instruction writes whole runs of a row (stored from the MFMA's layout, 32 bytes of sixteen rows at a time, 8192 x 8192 bf16 outputs
+// take 24 us).  Chunk c of 16 bytes of row r lies at c ^ r, so that neither side meets itself in the banks.
+template <int RB>
+struct OutRows {
+  static constexpr int CH = RB / 16;
+  unsigned char* lds;
+  __device__ __forceinline__ unsigned char* at(int row, int byte) const {
+    return lds + row * RB + 16 * ((byte >> 4) ^ (row & (CH - 1))) + (byte & 15);
+  }
+  // out: the first row's first byte; rows and chunks from `rows` and `chunks` on are not stored
+  __device__ __forceinline__ void store(unsigned char* out, size_t stride, int rows, int chunks) const {
+    asm volatile("" ::: "memory");                   // the wavefront's other lanes wrote what a lane reads here
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int r = 0; r < (16 * CH + 63) / 64; ++r) {
+      const int e = 64 * r + lane, row = e / CH, c = e % CH;
+      if (16 * CH < 64 && row >= 16) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(at(row, 16 * c));
+      if (row < rows && c < chunks) *reinterpret_cast<u32x4*>(out + row * stride + 16 * c) = v;
+    }
+    asm volatile("" ::: "memory");
+  }
+};
+
 // The end of a workgroup's tile: lane l of a wavefront holds token m0 + 16 (i0 + i) + (l & 15) and weight rows
-// 4 (l >> 4) .. + 3 of each block acc[t][i].  `top` and `flag` are LDS that nothing else uses any more.
+// 4 (l >> 4) .. + 3 of each block acc[t][i].  `top_lds`, `flag` and out_lds (8 KiB of the wavefront's own) are LDS that
+// nothing else uses any more.
 //
 // Workgroups that share tile `group` of the split ones leave partial tiles in the workspace, and the one that comes last
 // sums them in order.
-template <int WN, int NW, int GATE, bool Q, int TN, int TM>
+template <int WN, int NW, int GATE, bool Q, bool F32, int TN, int TM>
 __device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM], unsigned char* top_lds, unsigned char* flag,
-                                            int group, int splits, int split, int tn, int m0, int i0, int wn, int c0) {
+                                            unsigned char* out_lds, int group, int splits, int split, int tn, int m0, int i0,
+                                            int wn, int c0) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int BM = 16 * TM * NW / WN;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
@@ -117,17 +145,24 @@ __device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[t][i] += load_partial(part, s * SLOT + (t * TM + i) * (64 * NW * 16) + at);
   }
-  constexpr int OT = G ? TN / 2 : TN;
+  constexpr int OT = G ? TN / 2 : TN, ES = Q ? 1 : F32 ? 4 : 2;
+  const OutRows<OT * 16 * ES> rows{out_lds};
+  const size_t stride = (size_t)a.N * ES;
+  const auto store = [&](int i) {
+    const int m = m0 + 16 * (i0 + i);
+    rows.store(static_cast<unsigned char*>(a.out) + (size_t)m * stride + (size_t)c0 * ES, stride, a.M - m, (a.N - c0) * ES / 16);
+  };
   if constexpr (!Q) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int m = m0 + 16 * (i0 + i) + col;
-      if (m >= a.M) continue;
 #pragma unroll
       for (int t = 0; t < OT; ++t) {
-        const int n = c0 + 16 * t + 4 * g;
-        if (n < a.N) store4(a, (size_t)m * a.N + n, gated<GATE>(acc[t][i], acc[t + TN - OT][i]));
+        const f32x4 v = gated<GATE>(acc[t][i], acc[t + TN - OT][i]);
+        unsigned char* const to = rows.at(col, (16 * t + 4 * g) * ES);
+        if constexpr (F32) *reinterpret_cast<f32x4*>(to) = v;
+        else *reinterpret_cast<u32x2*>(to) = pack16(a, v);
       }
+      store(i);
     }
   } else {
     auto& top = *reinterpret_cast<unsigned(*)[WN][BM]>(top_lds);   // largest magnitude of a token in each wavefront's columns
@@ -152,14 +187,14 @@ __device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM
       for (int w = 0; w < WN; ++w) m[i] = max(m[i], top[w][16 * (i0 + i) + col]);
       const BlockScale b = block_scale(m[i], 1.0f);
       const int token = m0 + 16 * (i0 + i) + col;
-      if (token >= a.M) continue;
-      if (wn == 0 && g == 0) a.os[(size_t)tn * a.M + token] = b.scale;
+      if (token < a.M && wn == 0 && g == 0) a.os[(size_t)tn * a.M + token] = b.scale;
 #pragma unroll
       for (int t = 0; t < OT; ++t) {
         const f32x4 v = acc[t][i];
-        *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)token * a.N + c0 + 16 * t + 4 * g) =
+        *reinterpret_cast<unsigned*>(rows.at(col, 16 * t + 4 * g)) =
             codes4(v[0] * b.to_code, v[1] * b.to_code, v[2] * b.to_code, v[3] * b.to_code);
       }
+      store(i);
     }
   }
 }
