@@ -121,10 +121,11 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
     splits = std::min(splits, kMaxSplits);
     if (groups > kW8Tickets) splits = 1;
     // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
-    // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 4096, 32: 5.25 and 5.68).
+    // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
+    // with a gate, where the LDS of eight is for one workgroup a compute unit (11008 x 4096: 22.8 and 20.0).
     const int per = (KB + splits - 1) / splits;
     const auto places = [&](int waves) { return (per + 2 * waves - 1) / (2 * waves) * 2 * waves; };
-    pl->waves = places(4) * 10 <= places(8) * 9 ? 4 : 8;
+    pl->waves = gated || places(4) * 10 <= places(8) * 9 ? 4 : 8;
     return finish_plan(pl, 0, groups, members, splits, KB, (size_t)(gated ? 2 : 1) * 1024);
   }
   pl->kind = W8_TILES;

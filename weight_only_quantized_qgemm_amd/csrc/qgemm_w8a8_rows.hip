@@ -3,15 +3,18 @@
 //   p_r[m] = sum_b as[b][m] ws[r / 128][b] (sum_{k in block b} a[m][k] w[r][k])
 //
 // A workgroup owns one 16-row weight block (with a gate that of both projections); its wavefronts take the k
-// blocks of 128 in turn, so that together they read 1 KiB of every weight row side by side.  The weights go
-// from memory straight into registers, as fp16 into the first operand of v_mfma_f32_16x16x32_f16 and the tokens'
-// codes into the second: lane l holds row (token) l & 15 and the 16-byte chunks l >> 4 and 4 + (l >> 4) of the k block,
-// the same for both, which is all that a dot product asks of its order.  The result has token l & 15 and weight rows
-// 4 (l >> 4) .. + 3 in lane l, so both scales are one factor per lane, applied to the fp32 block sum.
+// blocks of 128 in turn, so that together they read 1 KiB of every weight row side by side.  The weights are, as fp16, the
+// first operand of v_mfma_f32_16x16x32_f16 and the tokens' codes the second: lane l holds row (token) l & 15 and the
+// 16-byte chunks l >> 4 and 4 + (l >> 4) of the k block, the same for both, which is all that a dot product asks of its
+// order.  The result has token l & 15 and weight rows 4 (l >> 4) .. + 3 in lane l, so both scales are one factor per lane, applied
+// to the fp32 block sum.
 //
-// Bound by the weights' way from memory: 4096 x 11008, one token 10.3 us, 4.4 TB/s, 16 tokens 13.1 us; 11008 x 4096 gated
-// to 16 bits 17.8 and 19.7 us (5.1 and 4.6 TB/s).  Bringing the tokens into LDS first, for fewer load instructions, delays
-// the first product by more than it saves (4096 x 4096, one token: 5.7 us against 5.2).
+// Each wavefront brings its k blocks into LDS of its own (buffer loads with the LDS destination, eight rows of 128 bytes
+// each, chunk c of row r at c ^ (r & 7)) and reads the operands from there; nothing is shared, so there is no barrier.  Loaded
+// straight into the operands' registers, sixteen consecutive lanes address sixteen rows, and the address unit takes them one by
+// one: 10240 x 5120, 16 tokens 18.1 us that way and 14.8 this, one token 12.8 and 12.1; 11008 x 4096 gated, 21.8 and 20.2, 19.9 and
+// 19.4.  What is left is the weights' way from memory: 4.6 TB/s for the latter, 5.2 for 10240 x 5120 at one token less 2 us for the
+// launch and the last block's latency.
 //
 // The wavefronts' sums meet in LDS, in wavefront order.  Where several workgroups make one output (splits along
 // K; the eight column blocks of an output scale block) each leaves its fp32 sums in the workspace and takes a
@@ -24,12 +27,17 @@ namespace qgemm {
 namespace w8 {
 namespace {
 
-template <int NW, int GATE, bool Q>
-__global__ __launch_bounds__(64 * NW, 4) void rows_kernel(W8Args a) {
+// (With no second launch bound the compiler orders the loop so that 11008 x 4096 gated takes 20.1 us instead of 19.4.)
+template <int NW, int XH, int GATE, bool Q>
+__global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int U = G ? 2 : 1;                       // weight blocks: one of either projection
   constexpr int F = Q ? kBlock / 16 : 1;             // workgroups along the columns of one output scale block
-  __shared__ f32x4 sums[NW / 2][U][64];
+  // two stages per wavefront: 64 KiB for eight, 48 for four with a gate, so that two or three workgroups share a compute unit (one
+  // stage more and 11008 x 4096 gated takes 21.0 us instead of 20.0, 4096 x 4096 6.3 instead of 5.6)
+  constexpr int SLOT = (U + 1) * 16 * kBlock;
+  __shared__ __attribute__((aligned(1024))) unsigned char S0[NW * SLOT], S1[NW * SLOT];
+  auto& sums = *reinterpret_cast<f32x4(*)[NW / 2][U][64]>(S0);   // after the last k block
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -39,69 +47,90 @@ __global__ __launch_bounds__(64 * NW, 4) void rows_kernel(W8Args a) {
   const int cb = member / a.splits, split = member - cb * a.splits;
   const int n0 = (group * F + cb) * 16;              // first output column
   const int kb0 = split * a.kb_per_split, kb1 = min(a.KB, kb0 + a.kb_per_split);
-  const int token = min(col, a.M - 1);               // tokens past the last repeat it and are not stored
+  const int token = min(col, a.M - 1);               // the scale of tokens past the last, which are not stored
 
-  // (addresses: a uniform base and a 32-bit offset per lane; 16 rows of K <= 2^22 stay below 2^26)
-  const uint8_t* wp[U];
-  const float* sp[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    wp[u] = a.w + ((size_t)u * a.N + n0) * a.K;
-    sp[u] = a.ws + ((size_t)u * a.row_blocks + n0 / kBlock) * a.KB;
-  }
-  const unsigned woff = col * a.K + 16 * g, aoff = token * a.K + 16 * g;
+  // ---- loads; tokens past the last read as zero
+  const int drow = lane >> 3, lane_off = drow * a.K + 16 * ((lane & 7) ^ drow);
+  const auto rows = [&](const uint8_t* p, int n) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, n * a.K, 0x00020000);
+  };
+  const auto scales = [&](int u) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.ws + ((size_t)u * a.row_blocks + n0 / kBlock) * a.KB), (short)0,
+                                             a.KB * 4, 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t xr = rows(a.a, a.M), wr0 = rows(a.w + (size_t)n0 * a.K, 16),
+                               wr1 = rows(a.w + ((size_t)(U - 1) * a.N + n0) * a.K, 16), sr0 = scales(0), sr1 = scales(U - 1);
   f32x4 acc[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // two k blocks in flight per wavefront (four leave registers for half as many workgroups: gated 16 x 11008 x 4096 21.9 us
-  // against 19.7)
-  constexpr int D = 2;
-  struct Chunks { i32x4 v[2]; };
-  Chunks w[D][U], x[D];
-  float sw[D][U], sa[D];
-  bool in[D];                                        // whether the block in set d is one of this wavefront's
-  const auto chunks = [](const uint8_t* p, unsigned off) {
-    return Chunks{{*reinterpret_cast<const i32x4*>(p + off), *reinterpret_cast<const i32x4*>(p + 64 + off)}};
-  };
+  float sw[2][U], sa[2];
+  bool in[2];                                        // whether the block in stage d is one of this wavefront's
+  const auto stage = [&](int d) { return (d ? S1 : S0) + wave * SLOT; };
+  const auto as_float = [](unsigned v) { return __builtin_bit_cast(float, v); };
   const auto load = [&](int d, int at) {
     in[d] = at < kb1;
     const int kb = min(at, kb1 - 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[d][u] = chunks(wp[u] + (size_t)kb * kBlock, woff);
+    for (int u = 0; u <= U; ++u)                     // the weights' blocks, then the tokens'
 #pragma unroll
-    for (int u = 0; u < U; ++u) sw[d][u] = sp[u][kb];
-    x[d] = chunks(a.a + (size_t)kb * kBlock, aoff);
-    sa[d] = (a.as + (size_t)kb * a.M)[token];
+      for (int h = 0; h < (u == U ? XH : 2); ++h)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(u == U ? xr : u ? wr1 : wr0, (lds_ptr_t)(stage(d) + (2 * u + h) * 1024), 16,
+                                                 lane_off + 8 * h * a.K, kb * kBlock, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) sw[d][u] = as_float(__builtin_amdgcn_raw_buffer_load_b32(u ? sr1 : sr0, 0, 4 * kb, 0));
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
+    sa[d] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4 * token, 0, 0));
   };
-  const auto compute = [&](int d) {
-    const Halves x0 = halves(x[d].v[0]), x1 = halves(x[d].v[1]);
+  constexpr int LOADS = 3 * U + 1 + XH;              // vector loads of a stage
+  constexpr auto vmcnt = [](int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); };
+  constexpr int lds_read = 15 | (7 << 4) | (3 << 14);       // no LDS read pending
+  const int off0 = col * kBlock + 16 * (g ^ (col & 7)), off1 = off0 ^ 64;
+  struct Chunks { i32x4 v[2]; };
+  Chunks w[U], x;
+  float f[U];
+  const auto read = [&](int d) {
+    __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));        // this stage has landed, the other may be on its way
+    asm volatile("" ::: "memory");
+    const auto chunks = [&](const unsigned char* p) {
+      return Chunks{{*reinterpret_cast<const i32x4*>(p + off0), *reinterpret_cast<const i32x4*>(p + off1)}};
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = chunks(stage(d) + u * 2048);
+    x = chunks(stage(d) + U * 2048);
+#pragma unroll
+    for (int u = 0; u < U; ++u) f[u] = in[d] ? sa[d] * sw[d][u] : 0.f;
+    __builtin_amdgcn_s_waitcnt(lds_read);            // before the next load writes the stage
+    asm volatile("" ::: "memory");
+  };
+  const auto compute = [&] {
+    const Halves x0 = halves(x.v[0]), x1 = halves(x.v[1]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Halves w0 = halves(w[d][u].v[0]), w1 = halves(w[d][u].v[1]);
+      const Halves w0 = halves(w[u].v[0]), w1 = halves(w[u].v[1]);
       f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[0], x0.v[0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
       p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[1], x0.v[1], p, 0, 0, 0);
       p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[0], x1.v[0], p, 0, 0, 0);
       p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[1], x1.v[1], p, 0, 0, 0);
-      const float s = in[d] ? sa[d] * sw[d][u] : 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[u][r] = __builtin_fmaf(p[r], s, acc[u][r]);
+      for (int r = 0; r < 4; ++r) acc[u][r] = __builtin_fmaf(p[r], f[u], acc[u][r]);
     }
   };
   // The last round is as long as the others: blocks past the end are the last one again, with factor 0 (branches
   // around them would copy the sums from register to register).
-  int kb = kb0 + wave;
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(d, kb + d * NW);
-  for (; kb + D * NW < kb1; kb += D * NW) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      compute(d);
-      load(d, kb + (D + d) * NW);
-    }
+  load(0, kb0 + wave);
+  load(1, kb0 + wave + NW);
+  for (int kb = kb0 + wave; kb < kb1; kb += 2 * NW) {
+    read(0);
+    load(0, kb + 2 * NW);
+    compute();
+    read(1);
+    load(1, kb + 3 * NW);
+    compute();
   }
-#pragma unroll
-  for (int d = 0; d < D; ++d) compute(d);
+  __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
+  __syncthreads();
 
   // the wavefronts' sums: the second half into the first, then those in order
   if (wave >= NW / 2) {
@@ -172,25 +201,26 @@ __global__ __launch_bounds__(64 * NW, 4) void rows_kernel(W8Args a) {
   }
 }
 
-template <int NW>
-void launch_waves(const W8Plan& pl, const W8Args& a, hipStream_t s) {
-  const dim3 grid(pl.grid), block(64 * NW);
-  const auto gate = [&](auto g) {
-    constexpr int GATE = decltype(g)::value;
-    if (a.out_dtype != QGEMM_DT_FP8_E4M3) rows_kernel<NW, GATE, false><<<grid, block, 0, s>>>(a);
-    else if constexpr (GATE != QGEMM_GATE_NONE) rows_kernel<NW, GATE, true><<<grid, block, 0, s>>>(a);
-  };
-  switch (a.gate) {
-    case QGEMM_GATE_NONE: gate(std::integral_constant<int, QGEMM_GATE_NONE>{}); break;
-    case QGEMM_GATE_SILU: gate(std::integral_constant<int, QGEMM_GATE_SILU>{}); break;
-    default: gate(std::integral_constant<int, QGEMM_GATE_GELU_TANH>{}); break;
-  }
+template <int XH>
+void launch_tokens(const W8Plan& pl, const W8Args& a, hipStream_t s) {
+  const dim3 grid(pl.grid), block(64 * pl.waves);
+  const bool q = a.out_dtype == QGEMM_DT_FP8_E4M3;
+  if (a.gate == QGEMM_GATE_NONE)
+    pl.waves == 8 ? rows_kernel<8, XH, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a)
+                  : rows_kernel<4, XH, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a);
+  else if (a.gate == QGEMM_GATE_SILU)
+    q ? rows_kernel<4, XH, QGEMM_GATE_SILU, true><<<grid, block, 0, s>>>(a)
+      : rows_kernel<4, XH, QGEMM_GATE_SILU, false><<<grid, block, 0, s>>>(a);
+  else
+    q ? rows_kernel<4, XH, QGEMM_GATE_GELU_TANH, true><<<grid, block, 0, s>>>(a)
+      : rows_kernel<4, XH, QGEMM_GATE_GELU_TANH, false><<<grid, block, 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_rows(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
-  pl.waves == 8 ? launch_waves<8>(pl, a, stream) : launch_waves<4>(pl, a, stream);
+  // up to eight tokens are one load of a k block, not two (10240 x 5120: 12.1 and 12.7 us)
+  a.M <= 8 ? launch_tokens<1>(pl, a, stream) : launch_tokens<2>(pl, a, stream);
   return hipGetLastError();
 }
 
