@@ -58,7 +58,7 @@ qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* problem, const void* x, in
 
 /* kernel_hint values (testing and tuning; 0 is the right choice for applications) */
 #define QGEMM_W8A8_AUTO 0
-#define QGEMM_W8A8_ROWS 1           /* the weights stream past a few tokens: M <= 16             */
+#define QGEMM_W8A8_ROWS 1           /* the weights stream past a few tokens: M <= 64             */
 #define QGEMM_W8A8_TILES 2          /* tiles of tokens x weight rows, any M                      */
 
 /*

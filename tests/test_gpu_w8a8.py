@@ -260,7 +260,7 @@ def test_products(q, m, n, k, gate):
 
 @pytest.mark.parametrize("m,n,k,gate,out", [(7, 256, 1792, "none", "f32"), (1, 144, 5120, "none", "f16"),
                                             (13, 384, 2688, "silu", "e4m3"), (16, 256, 4992, "gelu", "bf16"), (40, 256, 1792, "silu", "e4m3"), (64, 144, 1280, "gelu", "f16"),
-                                            (20, 384, 640, "gelu", "e4m3"), (130, 528, 1152, "none", "bf16"),
+                                            (20, 384, 640, "gelu", "e4m3"), (48, 128, 2304, "silu", "e4m3"), (37, 272, 2304, "none", "f32"), (130, 528, 1152, "none", "bf16"),
                                             (270, 384, 1152, "silu", "e4m3"), (61, 272, 1024, "silu", "f32")])
 def test_kernels_splits_and_tiles(q, m, n, k, gate, out):
     """Every kernel, tile and number of splits gives results within the same bound, and the same call the same bits."""
@@ -269,7 +269,7 @@ def test_kernels_splits_and_tiles(q, m, n, k, gate, out):
     want, tol = product_want(*host, gate, parts)
     ins = on_gpu(*host)
     hints = [dict(kernel_hint=q.W8A8_TILES, tile_hint=t, split_hint=s) for t in (64, 128, 256) for s in (1, 2, 5, 32)]
-    if m <= 16:
+    if m <= 64:
         hints += [dict(kernel_hint=q.W8A8_ROWS, split_hint=s) for s in (1, 2, 3, 32)]
     for h in hints:
         y, scales, p, ws = run_product(q, ins, n, gate, out, **h)

@@ -67,7 +67,7 @@ BAD = [(dict(M=-1), INV, "M must"), (dict(M=(1 << 24) + 1), INV, "M must"), (dic
        (dict(K=(1 << 22) + 128), INV, "K must"), (dict(gate=3), INV, "gate"), (dict(gate=-1), INV, "gate"),
        (dict(out_dtype=99), INV, "out_dtype"), (dict(out_dtype=q.DT_INT4), UNS, "out_dtype"),
        (dict(out_dtype=q.DT_FP8_E4M3), UNS, "needs a gate"), (dict(out_dtype=q.DT_FP8_E4M3, gate=1, N=272), INV, "N must"),
-       (dict(kernel_hint=3), INV, "kernel_hint"), (dict(kernel_hint=q.W8A8_ROWS, M=17), UNS, "rows kernel"),
+       (dict(kernel_hint=3), INV, "kernel_hint"), (dict(kernel_hint=q.W8A8_ROWS, M=65), UNS, "rows kernel"),
        (dict(split_hint=33), INV, "split_hint"), (dict(split_hint=-1), INV, "split_hint"), (dict(tile_hint=32), INV, "tile_hint"),
        (dict(reserved=5), INV, "reserved"), (dict(M=1 << 24, N=1 << 24), UNS, "launch"),
        (dict(M=16, N=1 << 24, split_hint=32, K=8192, kernel_hint=q.W8A8_ROWS, out_dtype=q.DT_FP8_E4M3, gate=1), UNS, "launch")]
@@ -126,7 +126,7 @@ def test_plans_cover_every_size():
         out = q.DT_F16
         if gate and g.random() < 0.5:
             n, out = -(-n // 128) * 128, q.DT_FP8_E4M3
-        p = q.w8a8_problem(m, n, k, out, gate=gate, kernel_hint=int(g.choice([0, 0, 1, 2])) if m <= 16 else int(g.choice([0, 2])),
+        p = q.w8a8_problem(m, n, k, out, gate=gate, kernel_hint=int(g.choice([0, 0, 1, 2])) if m <= 64 else int(g.choice([0, 2])),
                            split_hint=int(g.choice([0, 0, 1, 2, 7, 32])), tile_hint=int(g.choice([0, 0, 64, 128, 256])))
         head, *rest = q.w8a8_describe(p).split()
         f = {a: int(b) for a, b in (x.split("=") for x in rest)}
@@ -135,8 +135,8 @@ def test_plans_cover_every_size():
         assert 1 <= f["splits"] <= 32 and per * (f["splits"] - 1) < kb <= per * f["splits"]
         if head == "rows":
             members = f["splits"] * (8 if out == q.DT_FP8_E4M3 else 1)
-            assert f["members"] == members and f["grid"] == n // 16 * f["splits"] and m <= 16
-            assert ws == (0 if members == 1 else (4 << 17) + f["grid"] * (2 if gate else 1) * 1024)
+            assert f["members"] == members and f["grid"] == n // 16 * f["splits"] and m <= 64
+            assert ws == (0 if members == 1 else (4 << 17) + f["grid"] * (2 if gate else 1) * 1024 * -(-m // 16))
         else:
             cols = 128 if gate else 256
             tiles = -(-m // f["tokens"]) * -(-n // cols)

@@ -98,6 +98,28 @@ static qgemm_status_t finish_plan(W8Plan* pl, int64_t whole, int64_t groups, int
   return QGEMM_OK;
 }
 
+static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
+  const bool gated = p->gate != QGEMM_GATE_NONE, quantized = p->out_dtype == QGEMM_DT_FP8_E4M3;
+  const int KB = (int)(p->K / kBlock);
+  const int64_t M = std::max<int64_t>(p->M, 1);
+  pl->kind = W8_ROWS;
+  const int members = quantized ? kBlock / 16 : 1;
+  const int64_t columns = p->N / 16, groups = columns / members;   // workgroups without a split
+  int splits = std::min(p->split_hint, KB);
+  // As many as give every compute unit a workgroup, of two k blocks a wavefront at least: sharing an output takes three
+  // dependent trips to memory (4 x 1024 x 2048: 3.3 us alone, 4.3 shared by two; 4 x 1024 x 8192: 7.4, 6.6, by four 6.4).
+  if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / columns), std::max(1, KB / (2 * kW8Waves)));
+  splits = std::min(splits, kMaxSplits);
+  if (groups > kW8Tickets) splits = 1;
+  // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
+  // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
+  // with a gate, where the LDS of eight is for one workgroup a compute unit (11008 x 4096: 22.8 and 20.0).
+  const int per = (KB + splits - 1) / splits;
+  const auto places = [&](int waves) { return (per + 2 * waves - 1) / (2 * waves) * 2 * waves; };
+  pl->waves = gated || M > 32 || places(4) * 10 <= places(8) * 9 ? 4 : 8;
+  return finish_plan(pl, 0, groups, members, splits, KB, (size_t)(gated ? 2 : 1) * 1024 * ((M + 15) / 16));
+}
+
 // Microseconds that a workgroup of the tiles kernel takes for a k block and besides, while every compute unit has one
 // (e4m3 and fp16 operands), and that sharing a tile costs each more.
 struct TileCost { double step[2], fixed, share; };
@@ -105,29 +127,22 @@ static TileCost tile_cost(int tile) {
   return tile == 256 ? TileCost{{1.57, 2.95}, 9.0, 4.0} : tile == 128 ? TileCost{{0.93, 1.60}, 5.5, 2.4} : TileCost{{0.60, 1.0}, 4.5, 1.2};
 }
 
+// Microseconds of the rows kernel for more than 16 tokens: what a compute unit takes for 16 weight rows' k block, with a gate for
+// those of either projection, times its share of them, half of the way from the average to the unit with the most workgroups (they
+// overlap).  Within a tenth of the times at 4096 x 4096 to 28672 x 8192, a fifth with e4m3 outputs.
+static double rows_cost(const qgemm_w8a8_t* p) {
+  const int64_t workgroups = p->N / 16, rounds = (workgroups + kCUs - 1) / kCUs;
+  const double blocks = 0.5 * ((double)workgroups / kCUs + (double)rounds) * (double)(p->K / kBlock);
+  const double one = 0.10 + 0.0021 * (double)p->M;
+  return p->out_dtype == QGEMM_DT_FP8_E4M3 ? 5.0 + 2.6 * one * blocks : p->gate != QGEMM_GATE_NONE ? 3.0 + 1.5 * one * blocks : 2.0 + one * blocks;
+}
+
 qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   *pl = W8Plan{};
+  if (p->kernel_hint == QGEMM_W8A8_ROWS || (p->kernel_hint == QGEMM_W8A8_AUTO && p->M <= 16)) return make_rows_plan(p, pl);
   const bool gated = p->gate != QGEMM_GATE_NONE, quantized = p->out_dtype == QGEMM_DT_FP8_E4M3;
   const int KB = (int)(p->K / kBlock);
   const int64_t M = std::max<int64_t>(p->M, 1);
-  if (p->kernel_hint == QGEMM_W8A8_ROWS || (p->kernel_hint == QGEMM_W8A8_AUTO && M <= kRowsMaxM)) {
-    pl->kind = W8_ROWS;
-    const int members = quantized ? kBlock / 16 : 1;
-    const int64_t columns = p->N / 16, groups = columns / members;   // workgroups without a split
-    int splits = std::min(p->split_hint, KB);
-    // As many as give every compute unit a workgroup, of two k blocks a wavefront at least: sharing an output takes three
-    // dependent trips to memory (4 x 1024 x 2048: 3.3 us alone, 4.3 shared by two; 4 x 1024 x 8192: 7.4, 6.6, by four 6.4).
-    if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / columns), std::max(1, KB / (2 * kW8Waves)));
-    splits = std::min(splits, kMaxSplits);
-    if (groups > kW8Tickets) splits = 1;
-    // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
-    // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
-    // with a gate, where the LDS of eight is for one workgroup a compute unit (11008 x 4096: 22.8 and 20.0).
-    const int per = (KB + splits - 1) / splits;
-    const auto places = [&](int waves) { return (per + 2 * waves - 1) / (2 * waves) * 2 * waves; };
-    pl->waves = gated || places(4) * 10 <= places(8) * 9 ? 4 : 8;
-    return finish_plan(pl, 0, groups, members, splits, KB, (size_t)(gated ? 2 : 1) * 1024);
-  }
   pl->kind = W8_TILES;
   const int columns = gated ? kTileRows / 2 : kTileRows;
   pl->tiles_n = (int)((p->N + columns - 1) / columns);
@@ -150,6 +165,16 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
         pl->tile = tile;
         best_splits = s;
       }
+    }
+  }
+  // Up to 64 tokens either kernel may be the faster: the rows kernel reads the tokens again for every 16 weight rows, the tiles
+  // kernel has few tiles and joins their splits (4096 x 4096, 17 tokens: 6.4 and 13.0 us, 64 tokens 9.3 and 13.4;
+  // 10240 x 5120: 16.6 and 19.1, 31.8 and 20.4; 11008 x 4096 gated to e4m3: 29.1 and 26.6, 48 and 27.7).
+  if (p->kernel_hint == QGEMM_W8A8_AUTO && !p->tile_hint && p->M <= kRowsMaxM) {
+    const double memory = 3.0 + (double)(p->N * p->K) * (gated ? 2 : 1) / 3.7e6;
+    if (rows_cost(p) < std::max(best, memory)) {
+      *pl = W8Plan{};
+      return make_rows_plan(p, pl);
     }
   }
   const int64_t tiles = (M + pl->tile - 1) / pl->tile * pl->tiles_n;

@@ -16,7 +16,7 @@ constexpr int kBlock = 128;
 // so that a tile's outputs are one scale block wide.
 constexpr int kTileRows = 256;
 // The rows kernel takes up to this many tokens.
-constexpr int kRowsMaxM = 16;
+constexpr int kRowsMaxM = 64;
 // Wavefronts of a workgroup (at most: the rows kernel may take 4).
 constexpr int kW8Waves = 8;
 

@@ -1,4 +1,4 @@
-// The rows kernel of the 8-bit products: up to 16 tokens, the weights streamed once.
+// The rows kernel of the 8-bit products: up to 64 tokens, the weights streamed once.
 //
 //   p_r[m] = sum_b as[b][m] ws[r / 128][b] (sum_{k in block b} a[m][k] w[r][k])
 //
@@ -35,9 +35,10 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   constexpr int F = Q ? kBlock / 16 : 1;             // workgroups along the columns of one output scale block
   // two stages per wavefront: 64 KiB for eight, 48 for four with a gate, so that two or three workgroups share a compute unit (one
   // stage more and 11008 x 4096 gated takes 21.0 us instead of 20.0, 4096 x 4096 6.3 instead of 5.6)
-  constexpr int SLOT = (U + 1) * 16 * kBlock;
+  constexpr int MB = (XH + 1) / 2;                   // token blocks
+  constexpr int SLOT = (U + MB) * 16 * kBlock;
   __shared__ __attribute__((aligned(1024))) unsigned char S0[NW * SLOT], S1[NW * SLOT];
-  auto& sums = *reinterpret_cast<f32x4(*)[NW / 2][U][64]>(S0);   // after the last k block
+  auto& sums = *reinterpret_cast<f32x4(*)[NW / 2][U * MB][64]>(S0);   // after the last k block
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -47,7 +48,6 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   const int cb = member / a.splits, split = member - cb * a.splits;
   const int n0 = (group * F + cb) * 16;              // first output column
   const int kb0 = split * a.kb_per_split, kb1 = min(a.KB, kb0 + a.kb_per_split);
-  const int token = min(col, a.M - 1);               // the scale of tokens past the last, which are not stored
 
   // ---- loads; tokens past the last read as zero
   const int drow = lane >> 3, lane_off = drow * a.K + 16 * ((lane & 7) ^ drow);
@@ -60,11 +60,11 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   };
   const __amdgpu_buffer_rsrc_t xr = rows(a.a, a.M), wr0 = rows(a.w + (size_t)n0 * a.K, 16),
                                wr1 = rows(a.w + ((size_t)(U - 1) * a.N + n0) * a.K, 16), sr0 = scales(0), sr1 = scales(U - 1);
-  f32x4 acc[U];
+  f32x4 acc[U * MB];
 #pragma unroll
-  for (int u = 0; u < U; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int u = 0; u < U * MB; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  float sw[2][U], sa[2];
+  float sw[2][U], sa[2][MB];
   bool in[2];                                        // whether the block in stage d is one of this wavefront's
   const auto stage = [&](int d) { return (d ? S1 : S0) + wave * SLOT; };
   const auto as_float = [](unsigned v) { return __builtin_bit_cast(float, v); };
@@ -81,15 +81,16 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
     for (int u = 0; u < U; ++u) sw[d][u] = as_float(__builtin_amdgcn_raw_buffer_load_b32(u ? sr1 : sr0, 0, 4 * kb, 0));
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.as + (size_t)kb * a.M), (short)0, a.M * 4, 0x00020000);
-    sa[d] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4 * token, 0, 0));
+#pragma unroll
+    for (int i = 0; i < MB; ++i) sa[d][i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4 * (16 * i + col), 0, 0));
   };
-  constexpr int LOADS = 3 * U + 1 + XH;              // vector loads of a stage
+  constexpr int LOADS = 3 * U + MB + XH;              // vector loads of a stage
   constexpr auto vmcnt = [](int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); };
   constexpr int lds_read = 15 | (7 << 4) | (3 << 14);       // no LDS read pending
   const int off0 = col * kBlock + 16 * (g ^ (col & 7)), off1 = off0 ^ 64;
   struct Chunks { i32x4 v[2]; };
-  Chunks w[U], x;
-  float f[U];
+  Chunks w[U], x[MB];
+  float f[U * MB];
   const auto read = [&](int d) {
     __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));        // this stage has landed, the other may be on its way
     asm volatile("" ::: "memory");
@@ -98,23 +99,34 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
     };
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = chunks(stage(d) + u * 2048);
-    x = chunks(stage(d) + U * 2048);
 #pragma unroll
-    for (int u = 0; u < U; ++u) f[u] = in[d] ? sa[d] * sw[d][u] : 0.f;
+    for (int i = 0; i < MB; ++i) x[i] = chunks(stage(d) + (U + i) * 2048);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MB; ++i) f[u * MB + i] = in[d] ? sa[d][i] * sw[d][u] : 0.f;
     __builtin_amdgcn_s_waitcnt(lds_read);            // before the next load writes the stage
     asm volatile("" ::: "memory");
   };
   const auto compute = [&] {
-    const Halves x0 = halves(x.v[0]), x1 = halves(x.v[1]);
+    Halves wh[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Halves w0 = halves(w[u].v[0]), w1 = halves(w[u].v[1]);
-      f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[0], x0.v[0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0.v[1], x0.v[1], p, 0, 0, 0);
-      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[0], x1.v[0], p, 0, 0, 0);
-      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1.v[1], x1.v[1], p, 0, 0, 0);
+      wh[u][0] = halves(w[u].v[0]);
+      wh[u][1] = halves(w[u].v[1]);
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[u][r] = __builtin_fmaf(p[r], f[u], acc[u][r]);
+    for (int i = 0; i < MB; ++i) {
+      const Halves x0 = halves(x[i].v[0]), x1 = halves(x[i].v[1]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[u][0].v[0], x0.v[0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[u][0].v[1], x0.v[1], p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[u][1].v[0], x1.v[0], p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[u][1].v[1], x1.v[1], p, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[u * MB + i][r] = __builtin_fmaf(p[r], f[u * MB + i], acc[u * MB + i][r]);
+      }
     }
   };
   // The last round is as long as the others: blocks past the end are the last one again, with factor 0 (branches
@@ -132,72 +144,82 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
   __syncthreads();
 
-  // the wavefronts' sums: the second half into the first, then those in order
+  // the wavefronts' sums: the second half into the first, then those in order; block b is token block b % MB of projection b / MB
+  constexpr int B = U * MB;
   if (wave >= NW / 2) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) sums[wave - NW / 2][u][lane] = acc[u];
+    for (int b = 0; b < B; ++b) sums[wave - NW / 2][b][lane] = acc[b];
   }
   __syncthreads();
   if (wave < NW / 2) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) sums[wave][u][lane] += acc[u];
+    for (int b = 0; b < B; ++b) sums[wave][b][lane] += acc[b];
   }
   __syncthreads();
   const __amdgpu_buffer_rsrc_t part =
-      __builtin_amdgcn_make_buffer_rsrc(a.partials + (size_t)group * members * (U * 256), (short)0, members * (U * 1024), 0x00020000);
-  const auto slot = [&](int m, int u) { return (m * U + u) * 1024 + 16 * lane; };
-  const auto joined = [&](int u) {
-    f32x4 v = sums[0][u][lane];
+      __builtin_amdgcn_make_buffer_rsrc(a.partials + (size_t)group * members * (B * 256), (short)0, members * (B * 1024), 0x00020000);
+  const auto slot = [&](int m, int b) { return (m * B + b) * 1024 + 16 * lane; };
+  const auto joined = [&](int b) {
+    f32x4 v = sums[0][b][lane];
 #pragma unroll
-    for (int w = 1; w < NW / 2; ++w) v += sums[w][u][lane];
+    for (int w = 1; w < NW / 2; ++w) v += sums[w][b][lane];
     return v;
   };
   if (members > 1) {
-    if (wave < U) store_partial(part, slot(member, wave), joined(wave));
+    for (int b = wave; b < B; b += NW) store_partial(part, slot(member, b), joined(b));
     if (!last_arrival(a.tickets + group, members, &s_last)) return;
   }
   if constexpr (!Q) {
-    if (wave > 0) return;
+    const int i = wave;                              // a wavefront finishes a token block
+    if (i >= MB) return;
     f32x4 v[2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (members > 1) {
-        v[u] = load_partial(part, slot(0, u));
-        for (int s = 1; s < a.splits; ++s) v[u] += load_partial(part, slot(s, u));
+        v[u] = load_partial(part, slot(0, u * MB + i));
+        for (int s = 1; s < a.splits; ++s) v[u] += load_partial(part, slot(s, u * MB + i));
       } else {
-        v[u] = joined(u);
+        v[u] = joined(u * MB + i);
       }
     }
-    if (col < a.M) store4(a, (size_t)col * a.N + n0 + 4 * g, gated<GATE>(v[0], v[U - 1]));
+    const int token = 16 * i + col;
+    if (token < a.M) store4(a, (size_t)token * a.N + n0 + 4 * g, gated<GATE>(v[0], v[U - 1]));
   } else {
     // every column block's outputs and largest magnitudes, then the codes
     constexpr int PER = kBlock / 16 / NW > 0 ? kBlock / 16 / NW : 1;     // column blocks of a wavefront
-    __shared__ unsigned top[kBlock / 16][16];
-    f32x4 y[PER];
+    __shared__ unsigned top[kBlock / 16][16 * MB];
+    f32x4 y[PER][MB];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int c = wave * PER + j;
-      f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-      for (int s = 0; s < a.splits; ++s)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) v[u] += load_partial(part, slot(c * a.splits + s, u));
-      y[j] = gated<GATE>(v[0], v[1]);
-      unsigned m = max(max(magnitude(y[j][0]), magnitude(y[j][1])), max(magnitude(y[j][2]), magnitude(y[j][3])));
-      m = max(m, (unsigned)__shfl_xor((int)m, 16));
-      m = max(m, (unsigned)__shfl_xor((int)m, 32));
-      if (g == 0) top[c][col] = m;
+      for (int i = 0; i < MB; ++i) {
+        f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+        for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) v[u] += load_partial(part, slot(c * a.splits + s, u * MB + i));
+        y[j][i] = gated<GATE>(v[0], v[1]);
+        unsigned m = max(max(magnitude(y[j][i][0]), magnitude(y[j][i][1])), max(magnitude(y[j][i][2]), magnitude(y[j][i][3])));
+        m = max(m, (unsigned)__shfl_xor((int)m, 16));
+        m = max(m, (unsigned)__shfl_xor((int)m, 32));
+        if (g == 0) top[c][16 * i + col] = m;
+      }
     }
     __syncthreads();
-    unsigned m = 0;
 #pragma unroll
-    for (int c = 0; c < kBlock / 16; ++c) m = max(m, top[c][col]);
-    const BlockScale b = block_scale(m, 1.0f);
-    if (col >= a.M) return;
+    for (int i = 0; i < MB; ++i) {
+      const int token = 16 * i + col;
+      unsigned m = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)col * a.N + group * kBlock + 16 * (wave * PER + j) + 4 * g) =
-          codes4(y[j][0] * b.to_code, y[j][1] * b.to_code, y[j][2] * b.to_code, y[j][3] * b.to_code);
-    if (wave == 0 && g == 0) a.os[(size_t)group * a.M + col] = b.scale;
+      for (int c = 0; c < kBlock / 16; ++c) m = max(m, top[c][token]);
+      const BlockScale b = block_scale(m, 1.0f);
+      if (token >= a.M) return;
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.out) + (size_t)token * a.N + group * kBlock + 16 * (wave * PER + j) + 4 * g) =
+            codes4(y[j][i][0] * b.to_code, y[j][i][1] * b.to_code, y[j][i][2] * b.to_code, y[j][i][3] * b.to_code);
+      if (wave == 0 && g == 0) a.os[(size_t)group * a.M + token] = b.scale;
+    }
   }
 }
 
@@ -206,7 +228,7 @@ void launch_tokens(const W8Plan& pl, const W8Args& a, hipStream_t s) {
   const dim3 grid(pl.grid), block(64 * pl.waves);
   const bool q = a.out_dtype == QGEMM_DT_FP8_E4M3;
   if (a.gate == QGEMM_GATE_NONE)
-    pl.waves == 8 ? rows_kernel<8, XH, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a)
+    pl.waves == 8 ? rows_kernel<XH <= 4 ? 8 : 4, XH, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a)
                   : rows_kernel<4, XH, QGEMM_GATE_NONE, false><<<grid, block, 0, s>>>(a);
   else if (a.gate == QGEMM_GATE_SILU)
     q ? rows_kernel<4, XH, QGEMM_GATE_SILU, true><<<grid, block, 0, s>>>(a)
@@ -220,7 +242,11 @@ void launch_tokens(const W8Plan& pl, const W8Args& a, hipStream_t s) {
 
 hipError_t launch_rows(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
   // up to eight tokens are one load of a k block, not two (10240 x 5120: 12.1 and 12.7 us)
-  a.M <= 8 ? launch_tokens<1>(pl, a, stream) : launch_tokens<2>(pl, a, stream);
+  if (a.M <= 8) launch_tokens<1>(pl, a, stream);
+  else if (a.M <= 16) launch_tokens<2>(pl, a, stream);
+  else if (a.M <= 32) launch_tokens<4>(pl, a, stream);
+  else if (a.M <= 48) launch_tokens<6>(pl, a, stream);
+  else launch_tokens<8>(pl, a, stream);
   return hipGetLastError();
 }
 
