@@ -2,6 +2,8 @@
 // share an output, the gate, and the stores.
 #pragma once
 
+#include <type_traits>
+
 #include "qgemm_w8a8_device.h"
 
 namespace qgemm {
@@ -115,26 +117,94 @@ struct OutRows {
 // The end of a workgroup's tile: lane l of a wavefront holds token m0 + 16 (i0 + i) + (l & 15) and weight rows
 // 4 (l >> 4) .. + 3 of each block acc[t][i].  `top_lds`, `flag` and out_lds (8 KiB of the wavefront's own) are LDS that
 // nothing else uses any more.
-//
-// Workgroups that share tile `group` of the split ones leave partial tiles in the workspace, and the one that comes last
-// sums them in order.
 template <int WN, int NW, int GATE, bool Q, bool F32, int TN, int TM>
-__device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM], unsigned char* top_lds, unsigned char* flag,
-                                            unsigned char* out_lds, int group, int splits, int split, int tn, int m0, int i0,
-                                            int wn, int c0) {
-  constexpr bool G = GATE != QGEMM_GATE_NONE;
-  constexpr int BM = 16 * TM * NW / WN;
-  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
-  if (splits > 1) {
-    constexpr int SLOT = TN * TM * 64 * NW * 16;     // bytes of a partial tile: 16 per thread and block
-    const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
-        a.partials + (size_t)group * splits * (SLOT / 4), (short)0, splits * SLOT, 0x00020000);
+struct TileEnd {
+  static constexpr bool G = GATE != QGEMM_GATE_NONE;
+  static constexpr int BM = 16 * TM * NW / WN, OT = G ? TN / 2 : TN, ES = Q ? 1 : F32 ? 4 : 2;
+  const W8Args& a;
+  unsigned char *top_lds, *flag, *out_lds;
+  int tn, m0, i0, wn, c0;
+
+  // Blocks O of the outputs of token block i, from column block o on.
+  template <int O>
+  __device__ __forceinline__ OutRows<O * 16 * ES> rows() const { return OutRows<O * 16 * ES>{out_lds}; }
+  template <int O>
+  __device__ __forceinline__ void leave(int i, int o) const {
+    const int m = m0 + 16 * (i0 + i), c = c0 + 16 * o;
+    const size_t stride = (size_t)a.N * ES;
+    rows<O>().store(static_cast<unsigned char*>(a.out) + (size_t)m * stride + (size_t)c * ES, stride, a.M - m, (a.N - c) * ES / 16);
+  }
+  template <int O>
+  __device__ __forceinline__ void put(int t, f32x4 v) const {
+    const int lane = threadIdx.x & 63;
+    unsigned char* const to = rows<O>().at(lane & 15, (16 * t + 4 * (lane >> 4)) * ES);
+    if constexpr (F32) *reinterpret_cast<f32x4*>(to) = v;
+    else *reinterpret_cast<u32x2*>(to) = pack16(a, v);
+  }
+  // e4m3: the largest magnitude of a token in each wavefront's columns
+  __device__ __forceinline__ unsigned& top(int w, int i) const {
+    return reinterpret_cast<unsigned*>(top_lds)[w * BM + 16 * (i0 + i) + (threadIdx.x & 15)];
+  }
+  __device__ __forceinline__ void note(int i, const f32x4 (&y)[OT]) const {
+    unsigned m = 0;
+#pragma unroll
+    for (int t = 0; t < OT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m = max(m, magnitude(y[t][r]));
+    m = max(m, (unsigned)__shfl_xor((int)m, 16));
+    m = max(m, (unsigned)__shfl_xor((int)m, 32));
+    if ((threadIdx.x & 48) == 0) top(wn, i) = m;
+  }
+  __device__ __forceinline__ void code(int i, const f32x4 (&y)[OT]) const {
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15, token = m0 + 16 * (i0 + i) + col;
+    unsigned m = 0;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) m = max(m, top(w, i));
+    const BlockScale b = block_scale(m, 1.0f);
+    if (token < a.M && wn == 0 && g == 0) a.os[(size_t)tn * a.M + token] = b.scale;
+#pragma unroll
+    for (int t = 0; t < OT; ++t)
+      *reinterpret_cast<unsigned*>(rows<OT>().at(col, 16 * t + 4 * g)) =
+          codes4(y[t][0] * b.to_code, y[t][1] * b.to_code, y[t][2] * b.to_code, y[t][3] * b.to_code);
+    leave<OT>(i, 0);
+  }
+
+  __device__ __forceinline__ void whole(f32x4 (&acc)[TN][TM]) const {
+    f32x4 y[TM][OT];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int t = 0; t < OT; ++t) y[i][t] = gated<GATE>(acc[t][i], acc[t + TN - OT][i]);
+      if constexpr (Q) {
+        note(i, y[i]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < OT; ++t) put<OT>(t, y[i][t]);
+        leave<OT>(i, 0);
+      }
+    }
+    if constexpr (Q) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < TM; ++i) code(i, y[i]);
+    }
+  }
+
+  // Workgroups that share tile `group` of the split ones leave partial tiles in the workspace, in the order of the wavefronts' blocks.
+  static constexpr int BLOCK = 64 * NW * 16, SLOT = TN * TM * BLOCK;      // bytes of a block of every wavefront, of a partial tile
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t partials(int group, int splits) const {
+    return __builtin_amdgcn_make_buffer_rsrc(a.partials + (size_t)group * splits * (SLOT / 4), (short)0, splits * SLOT, 0x00020000);
+  }
+
+  // The one that comes last sums them in order.
+  __device__ __forceinline__ void shared_at_once(f32x4 (&acc)[TN][TM], int group, int splits, int split) const {
+    const __amdgpu_buffer_rsrc_t part = partials(group, splits);
     const int at = 16 * threadIdx.x;
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
-      for (int i = 0; i < TM; ++i) store_partial(part, split * SLOT + (t * TM + i) * (64 * NW * 16) + at, acc[t][i]);
-    if (!last_arrival(a.tickets + group, splits, reinterpret_cast<int*>(flag))) return;
+      for (int i = 0; i < TM; ++i) store_partial(part, split * SLOT + (t * TM + i) * BLOCK + at, acc[t][i]);
+    if (!last_arrival(a.tickets + (size_t)group * kTileParts, splits, reinterpret_cast<int*>(flag))) return;
 #pragma unroll
     for (int t = 0; t < TN; ++t)
 #pragma unroll
@@ -143,61 +213,101 @@ __device__ __forceinline__ void finish_tile(const W8Args& a, f32x4 (&acc)[TN][TM
 #pragma unroll
       for (int t = 0; t < TN; ++t)
 #pragma unroll
-        for (int i = 0; i < TM; ++i) acc[t][i] += load_partial(part, s * SLOT + (t * TM + i) * (64 * NW * 16) + at);
+        for (int i = 0; i < TM; ++i) acc[t][i] += load_partial(part, s * SLOT + (t * TM + i) * BLOCK + at);
+    whole(acc);
   }
-  constexpr int OT = G ? TN / 2 : TN, ES = Q ? 1 : F32 ? 4 : 2;
-  const OutRows<OT * 16 * ES> rows{out_lds};
-  const size_t stride = (size_t)a.N * ES;
-  const auto store = [&](int i) {
-    const int m = m0 + 16 * (i0 + i);
-    rows.store(static_cast<unsigned char*>(a.out) + (size_t)m * stride + (size_t)c0 * ES, stride, a.M - m, (a.N - c0) * ES / 16);
-  };
-  if constexpr (!Q) {
+
+  // The same part by part (a token block of every wavefront, or half of its columns), with a ticket for each part, and each
+  // workgroup starting with another part; whoever comes last to a part sums it in order.  So the parts have different last
+  // ones and none reads all partial tiles (300 x 4096 x 4096 by two, 128 tokens: 20.8 us, with one last workgroup 22.0, by four
+  // 18.4 and 20.4; 128 x 1024 x 28672, 64 tokens: 21.4 and 25.5.  64 tokens by two or three are too little for four tickets:
+  // 300 x 4096 x 4096 by three 18.6 and 16.9).
+  __device__ __forceinline__ void shared_in_parts(f32x4 (&acc)[TN][TM], int group, int splits, int split) const {
+    constexpr int H = TM == 2 && !Q ? 2 : 1, PARTS = TM * H, PT = TN / H, PO = OT / H;
+    static_assert((PARTS == 2 || PARTS == 4) && PARTS <= kTileParts && PARTS * PT <= 63, "tickets of a tile; vmcnt counts at most 63");
+    const __amdgpu_buffer_rsrc_t part = partials(group, splits);
+    const int at = 16 * threadIdx.x, first = split * PARTS / splits;
+    const auto part_at = [&](int x) { return (first + x) % PARTS; };
+    const auto hand_over = [&](int which, auto part_q) {
+      constexpr int q = decltype(part_q)::value;
+      if (which != q) return;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+      for (int b = 0; b < PT; ++b)
+        store_partial(part, split * SLOT + (q * PT + b) * BLOCK + at, acc[b < PO ? q % H * PO + b : OT + q % H * PO + b - PO][q / H]);
+      asm volatile("; part %0" ::"i"(q));            // or the compiler makes one store of the four and keeps acc in memory to index it
+    };
 #pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        const f32x4 v = gated<GATE>(acc[t][i], acc[t + TN - OT][i]);
-        unsigned char* const to = rows.at(col, (16 * t + 4 * g) * ES);
-        if constexpr (F32) *reinterpret_cast<f32x4*>(to) = v;
-        else *reinterpret_cast<u32x2*>(to) = pack16(a, v);
+    for (int x = 0; x < PARTS; ++x) {
+      hand_over(part_at(x), std::integral_constant<int, 0>{});
+      hand_over(part_at(x), std::integral_constant<int, 1>{});
+      if constexpr (PARTS > 2) {
+        hand_over(part_at(x), std::integral_constant<int, 2>{});
+        hand_over(part_at(x), std::integral_constant<int, 3>{});
       }
-      store(i);
     }
-  } else {
-    auto& top = *reinterpret_cast<unsigned(*)[WN][BM]>(top_lds);   // largest magnitude of a token in each wavefront's columns
-    unsigned m[TM];
+    unsigned* const tickets = a.tickets + (size_t)group * kTileParts;
+    int* const last = reinterpret_cast<int*>(flag);
+    unsigned ticket[PARTS];
+    const auto arrive = [&](auto at) {
+      constexpr int x = decltype(at)::value, pending = (PARTS - 1 - x) * PT;      // stores complete in order
+      __builtin_amdgcn_s_waitcnt((pending & 15) | (7 << 4) | (15 << 8) | ((pending >> 4) << 14));
+      barrier();
+      if (threadIdx.x == 0)
+        ticket[x] = __hip_atomic_fetch_add(tickets + part_at(x), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    };
+    arrive(std::integral_constant<int, 0>{});
+    arrive(std::integral_constant<int, 1>{});
+    if constexpr (PARTS > 2) {
+      arrive(std::integral_constant<int, 2>{});
+      arrive(std::integral_constant<int, 3>{});
+    }
+    if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      m[i] = 0;
-#pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        acc[t][i] = gated<GATE>(acc[t][i], acc[t + OT][i]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[i] = max(m[i], magnitude(acc[t][i][r]));
+      for (int x = 0; x < PARTS; ++x) {
+        last[x] = ticket[x] == (unsigned)(splits - 1);
+        if (last[x]) __hip_atomic_store(tickets + part_at(x), 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-      m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 16));
-      m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], 32));
-      if (g == 0) top[wn][16 * (i0 + i) + col] = m[i];
     }
     __syncthreads();
+    for (int x = 0; x < PARTS; ++x) {
+      if (!last[x]) continue;
+      const int q = part_at(x), i = q / H;
+      f32x4 v[PT];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+      for (int b = 0; b < PT; ++b) v[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      int from = 0;
+      const auto add = [&](auto ahead) {             // partial tiles whose loads are on their way together
+        constexpr int AHEAD = decltype(ahead)::value;
+        f32x4 p[AHEAD][PT];
 #pragma unroll
-      for (int w = 0; w < WN; ++w) m[i] = max(m[i], top[w][16 * (i0 + i) + col]);
-      const BlockScale b = block_scale(m[i], 1.0f);
-      const int token = m0 + 16 * (i0 + i) + col;
-      if (token < a.M && wn == 0 && g == 0) a.os[(size_t)tn * a.M + token] = b.scale;
+        for (int s = 0; s < AHEAD; ++s)
 #pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        const f32x4 v = acc[t][i];
-        *reinterpret_cast<unsigned*>(rows.at(col, 16 * t + 4 * g)) =
-            codes4(v[0] * b.to_code, v[1] * b.to_code, v[2] * b.to_code, v[3] * b.to_code);
+          for (int b = 0; b < PT; ++b) p[s][b] = load_partial(part, (from + s) * SLOT + (q * PT + b) * BLOCK + at);
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s)
+#pragma unroll
+          for (int b = 0; b < PT; ++b) v[b] += p[s][b];
+        from += AHEAD;
+      };
+      if constexpr (PT < 8)                          // of eight blocks there are registers for two
+        while (from + 4 <= splits) add(std::integral_constant<int, 4>{});
+      while (from + 2 <= splits) add(std::integral_constant<int, 2>{});
+      if (from < splits) add(std::integral_constant<int, 1>{});
+      f32x4 y[PO];
+#pragma unroll
+      for (int t = 0; t < PO; ++t) y[t] = gated<GATE>(v[t], v[t + PT - PO]);
+      if constexpr (Q) {
+        note(i, y);
+        __syncthreads();
+        code(i, y);
+      } else {
+#pragma unroll
+        for (int t = 0; t < PO; ++t) put<PO>(t, y[t]);
+        leave<PO>(i, q % H * PO);
       }
-      store(i);
     }
   }
-}
+};
 
 }  // namespace w8
 }  // namespace qgemm

@@ -121,10 +121,14 @@ static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
 }
 
 // Microseconds that a workgroup of the tiles kernel takes for a k block and besides, while every compute unit has one
-// (e4m3 and fp16 operands), and that sharing a tile costs each more.
-struct TileCost { double step[2], fixed, share; };
+// (e4m3 and fp16 operands).
+struct TileCost { double step[2], fixed; };
 static TileCost tile_cost(int tile) {
-  return tile == 256 ? TileCost{{1.57, 2.95}, 9.0, 4.0} : tile == 128 ? TileCost{{0.93, 1.60}, 5.5, 2.4} : TileCost{{0.60, 1.0}, 4.5, 1.2};
+  return tile == 256 ? TileCost{{1.57, 2.95}, 9.0} : tile == 128 ? TileCost{{0.93, 1.60}, 5.5} : TileCost{{0.60, 1.0}, 4.5};
+}
+// That sharing `tiles` tiles between `splits` workgroups each costs: tickets, and the partial tiles' way to memory and back.
+static double share_cost(int tile, int64_t tiles, int splits) {
+  return splits > 1 ? 3.0 + 0.3 * splits + (double)(tiles * splits) * (tile * kTileRows * 4) * 2 / 10.0e6 : 0.0;
 }
 
 // Microseconds of the rows kernel for more than 16 tokens: what a compute unit takes for 16 weight rows' k block, with a gate for
@@ -159,7 +163,7 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
       const int kb = (KB + s - 1) / s;
       if (s > 1 && (!tail || (KB + kb - 1) / kb != s)) continue;
       const double step = c.step[fp16], tail_rounds = (double)((tail * s + kCUs - 1) / kCUs);
-      const double us = (double)rounds * (KB * step + c.fixed) + tail_rounds * (kb * step + c.fixed) + (s > 1 ? 3.0 + s * c.share : 0.0);
+      const double us = (double)rounds * (KB * step + c.fixed) + tail_rounds * (kb * step + c.fixed) + share_cost(tile, tail, s);
       if (pl->tile == 0 || us < best) {
         best = us;
         pl->tile = tile;
@@ -183,7 +187,7 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   pl->tiles = (int)tiles;
   int splits = p->split_hint ? std::min(p->split_hint, KB) : best_splits;
   int64_t whole = splits == 1 ? tiles : p->split_hint ? 0 : tiles - tiles % kCUs;
-  if (tiles - whole > kW8Tickets) whole = tiles;                     // a hint, on very many tiles
+  if (tiles - whole > kW8Tickets / kTileParts) whole = tiles;        // a hint, on very many tiles
   if (whole == tiles) splits = 1;
   pl->whole = (int)whole;
   return finish_plan(pl, whole, tiles - whole, 1, splits, KB, (size_t)pl->tile * kTileRows * 4);

@@ -40,6 +40,7 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl);
 // The workspace begins with a ticket region of one size, whatever the plan, so that partial results of one
 // problem never lie where another counts and one workspace serves them all.
 constexpr int64_t kW8Tickets = 1 << 17;
+constexpr int kTileParts = 4;          // tickets of a shared tile
 
 namespace w8 {
 

@@ -266,7 +266,15 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
   __syncthreads();                                   // and no wavefront reads it: what follows uses it otherwise
 
-  finish_tile<WN, NW, GATE, Q, FP16 && !Q>(a, acc, A0, A1, (wave < 4 ? W0 : W1) + (wave & 3) * 8192, tile - a.whole, splits, split, tn, m0, wm * TM, wn, c0);
+  const TileEnd<WN, NW, GATE, Q, FP16 && !Q, TN, TM> end{a, A0, A1, (wave < 4 ? W0 : W1) + (wave & 3) * 8192, tn, m0, wm * TM, wn, c0};
+  if (splits == 1) {
+    end.whole(acc);
+  } else {
+    if constexpr (BM == 64) {
+      if (splits < 4) return end.shared_at_once(acc, tile - a.whole, splits, split);
+    }
+    end.shared_in_parts(acc, tile - a.whole, splits, split);
+  }
 }
 
 template <int WM, int TM, int ST>
