@@ -3,8 +3,9 @@
 //   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * w,  16 bits: RNE(y);  8 bits: per block of 128
 //   scale = max|y| / 448, code = e4m3(y / scale) = e4m3(s w 448 / max|s w|)
 //
-// Bound by memory.  T threads hold a row in registers (C chunks of eight values each), so it is read once:
-// the sum of squares is reduced over the threads, and a scale block is the sixteen lanes of one DPP row.
+// Bound by memory, for few tokens by one trip to it.  A workgroup (or a wavefront) holds a row in registers, C chunks of eight
+// values per thread, so it is read once: the sum of squares is reduced over the threads, and a scale block is the sixteen
+// lanes of one DPP row.  8192 x 5120: 61.5 us to 16 bits (5.5 TB/s), 58.3 to 8 (5.0 TB/s); 16 x 4096: 2.4 and 2.7 us.
 #include "qgemm_w8a8_device.h"
 
 namespace {
@@ -53,13 +54,13 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
   return v;
 }
 
-template <bool BF, bool Q, int T, int C>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void add_norm(NormArgs a) {
-  constexpr int R = T < 256 ? 256 / T : 1;           // rows of a workgroup
-  __shared__ float part[T < 256 ? 1 : T / 64];
-  const int t = threadIdx.x % T;
-  const int row = blockIdx.x * R + threadIdx.x / T;
-  if (T < 256 && row >= a.tokens) return;            // whole wavefronts; with T >= 256 the grid is exact
+// WAVE: a row to each of a workgroup's four wavefronts; otherwise one to the workgroup.
+template <bool BF, bool Q, bool WAVE, int C>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void add_norm(NormArgs a) {
+  __shared__ float part[WAVE ? 1 : 16];
+  const int T = WAVE ? 64 : blockDim.x, t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int row = WAVE ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (WAVE && row >= a.tokens) return;
   const uint16_t* x = a.x + row * a.xs;
   const uint16_t* r = a.r ? a.r + row * a.rs : nullptr;
   u32x4 xv[C], rv[C], wv[C];
@@ -92,11 +93,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void add_norm(NormArgs a) {
   if (a.norm) {
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-    if constexpr (T >= 256) {
+    if constexpr (!WAVE) {
       if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
       __syncthreads();
       sum = 0.f;
-#pragma unroll
       for (int i = 0; i < T / 64; ++i) sum += part[i];
     }
     scale = 1.0f / __builtin_sqrtf(sum / (float)a.dim + a.eps);
@@ -128,14 +128,13 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void add_norm(NormArgs a) {
   }
 }
 
-template <int T, int C>
-void launch(bool bf, bool quantized, hipStream_t s, const NormArgs& a) {
-  constexpr int R = T < 256 ? 256 / T : 1, threads = T < 256 ? 256 : T;
-  const dim3 grid((unsigned)((a.tokens + R - 1) / R)), block(threads);
+template <bool WAVE, int C>
+void launch(bool bf, bool quantized, int threads, hipStream_t s, const NormArgs& a) {
+  const dim3 grid((unsigned)(WAVE ? (a.tokens + 3) / 4 : a.tokens)), block(threads);
   if (bf)
-    quantized ? add_norm<true, true, T, C><<<grid, block, 0, s>>>(a) : add_norm<true, false, T, C><<<grid, block, 0, s>>>(a);
+    quantized ? add_norm<true, true, WAVE, C><<<grid, block, 0, s>>>(a) : add_norm<true, false, WAVE, C><<<grid, block, 0, s>>>(a);
   else
-    quantized ? add_norm<false, true, T, C><<<grid, block, 0, s>>>(a) : add_norm<false, false, T, C><<<grid, block, 0, s>>>(a);
+    quantized ? add_norm<false, true, WAVE, C><<<grid, block, 0, s>>>(a) : add_norm<false, false, WAVE, C><<<grid, block, 0, s>>>(a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -186,16 +185,18 @@ extern "C" qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* p, const void* 
   a.eps = p->eps;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf = p->dtype == QGEMM_DT_BF16;
-  const int threads = p->dim <= 1024 ? 64 : p->dim <= 8192 ? 256 : 1024;
+  // As many threads as the row has groups of eight values (up to 1024, then two or four groups each): more values per
+  // thread wait longer for the first (16 x 4096 to 16 bits: 512 threads 2.36 us, 256 with two groups 2.71; 16 x 8192: 1024
+  // 2.94, 256 with four 3.56; 8192 x 8192: 91.9 and 98.1).  Rows up to 512 have one wavefront and no barrier.
+  const bool wave = p->dim <= 512;
+  const int chunks = wave || p->dim <= 8192 ? 1 : p->dim <= 16384 ? 2 : 4;
+  const int threads = wave ? 256 : 64 * ((p->dim + 512 * chunks - 1) / (512 * chunks));
   if (p->tokens > 0xffffff00LL / threads)
     return fail(QGEMM_ERR_UNSUPPORTED, "%lld rows of %d threads are more than one launch allows", (long long)p->tokens, threads);
-  if (p->dim <= 512) launch<64, 1>(bf, quantized, s, a);
-  else if (p->dim <= 1024) launch<64, 2>(bf, quantized, s, a);
-  else if (p->dim <= 2048) launch<256, 1>(bf, quantized, s, a);
-  else if (p->dim <= 4096) launch<256, 2>(bf, quantized, s, a);
-  else if (p->dim <= 8192) launch<256, 4>(bf, quantized, s, a);
-  else if (p->dim <= 16384) launch<1024, 2>(bf, quantized, s, a);
-  else launch<1024, 4>(bf, quantized, s, a);
+  if (wave) launch<true, 1>(bf, quantized, threads, s, a);
+  else if (chunks == 1) launch<false, 1>(bf, quantized, threads, s, a);
+  else if (chunks == 2) launch<false, 2>(bf, quantized, threads, s, a);
+  else launch<false, 4>(bf, quantized, threads, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(QGEMM_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return QGEMM_OK;
