@@ -138,7 +138,9 @@ static double rows_cost(const qgemm_w8a8_t* p) {
   const int64_t workgroups = p->N / 16, rounds = (workgroups + kCUs - 1) / kCUs;
   const double blocks = 0.5 * ((double)workgroups / kCUs + (double)rounds) * (double)(p->K / kBlock);
   const double one = 0.10 + 0.0021 * (double)p->M;
-  return p->out_dtype == QGEMM_DT_FP8_E4M3 ? 5.0 + 2.6 * one * blocks : p->gate != QGEMM_GATE_NONE ? 3.0 + 1.5 * one * blocks : 2.0 + one * blocks;
+  if (p->gate == QGEMM_GATE_NONE) return 2.0 + one * blocks;
+  if (p->out_dtype != QGEMM_DT_FP8_E4M3) return 3.0 + 1.5 * one * blocks;
+  return 5.0 + (p->M > 48 ? 2.6 : 2.0) * one * blocks;              // above 48 tokens a compute unit holds one workgroup, not two
 }
 
 qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
@@ -173,7 +175,7 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   }
   // Up to 64 tokens either kernel may be the faster: the rows kernel reads the tokens again for every 16 weight rows, the tiles
   // kernel has few tiles and joins their splits (4096 x 4096, 17 tokens: 6.4 and 13.0 us, 64 tokens 9.3 and 13.4;
-  // 10240 x 5120: 16.6 and 19.1, 31.8 and 20.4; 11008 x 4096 gated to e4m3: 29.1 and 26.6, 48 and 27.7).
+  // 10240 x 5120: 16.6 and 19.1, 28.5 and 20.4; 11008 x 4096 gated to e4m3: 29.0 and 26.6, 47.6 and 27.7; 5632 x 2048, 40 tokens 14.5 and 16.3).
   if (p->kernel_hint == QGEMM_W8A8_AUTO && !p->tile_hint && p->M <= kRowsMaxM) {
     const double memory = 3.0 + (double)(p->N * p->K) * (gated ? 2 : 1) / 3.7e6;
     if (rows_cost(p) < std::max(best, memory)) {

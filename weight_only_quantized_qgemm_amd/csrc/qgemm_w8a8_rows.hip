@@ -29,7 +29,7 @@ namespace {
 
 // (With no second launch bound the compiler orders the loop so that 11008 x 4096 gated takes 20.1 us instead of 19.4.)
 template <int NW, int XH, int GATE, bool Q>
-__global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
+__global__ __launch_bounds__(64 * NW, XH <= 4 ? 2 : 1) void rows_kernel(W8Args a) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int U = G ? 2 : 1;                       // weight blocks: one of either projection
   constexpr int F = Q ? kBlock / 16 : 1;             // workgroups along the columns of one output scale block
@@ -38,8 +38,9 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   constexpr int MB = (XH + 1) / 2;                   // token blocks
   constexpr int SLOT = (U + MB) * 16 * kBlock;
   __shared__ __attribute__((aligned(1024))) unsigned char S0[NW * SLOT], S1[NW * SLOT];
-  auto& sums = *reinterpret_cast<f32x4(*)[NW / 2][U * MB][64]>(S0);   // after the last k block
-  __shared__ int s_last;
+  auto& sums = *reinterpret_cast<f32x4(*)[NW / 2][U * MB][64]>(S0);   // after the last k block, as the next two
+  int* const s_last = reinterpret_cast<int*>(S1);
+  auto& top = *reinterpret_cast<unsigned(*)[kBlock / 16][16 * MB]>(S1 + 16);   // largest magnitude of a token in each column block
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroup = (group, column block in it, split)
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   };
   if (members > 1) {
     for (int b = wave; b < B; b += NW) store_partial(part, slot(member, b), joined(b));
-    if (!last_arrival(a.tickets + group, members, &s_last)) return;
+    if (!last_arrival(a.tickets + group, members, s_last)) return;
   }
   if constexpr (!Q) {
     const int i = wave;                              // a wavefront finishes a token block
@@ -187,7 +188,6 @@ __global__ __launch_bounds__(64 * NW, 2) void rows_kernel(W8Args a) {
   } else {
     // every column block's outputs and largest magnitudes, then the codes
     constexpr int PER = kBlock / 16 / NW > 0 ? kBlock / 16 / NW : 1;     // column blocks of a wavefront
-    __shared__ unsigned top[kBlock / 16][16 * MB];
     f32x4 y[PER][MB];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {

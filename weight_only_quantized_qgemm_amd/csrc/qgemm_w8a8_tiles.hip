@@ -115,8 +115,9 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   const auto achunk = [&](const unsigned char* As, int i, int c) {
     return chunk(As + aoff + i * 16 * kBlock + (c ? off1 : off0));
   };
-  // A step's scales: sa of the tokens, times the weights' of either projection.  With two stages the scales of the next step are loaded as it comes near (the 256-token tile has no registers for
-  // two sets), with more together with the step's data: loads return in order, and one waited for late would wait for all.
+  // A step's scales: sa of the tokens, times the weights' of either projection.  With two stages the scales of the next step
+  // are loaded as it comes near (the 256-token tile has no registers for two sets), with more together with the step's data:
+  // loads return in order, and one waited for late would wait for all.
   constexpr int SETS = ST > 2 ? ST : 1;
   float sa[SETS][TM], sw0[SETS], sw1[SETS], s0[TM], s1[TM];
   const auto load_scales = [&](int kb, int j) {
