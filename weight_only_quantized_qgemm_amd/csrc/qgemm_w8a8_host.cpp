@@ -98,6 +98,13 @@ static qgemm_status_t finish_plan(W8Plan* pl, int64_t whole, int64_t groups, int
   return QGEMM_OK;
 }
 
+// The rows kernel's workgroups along K: as many as give every compute unit one, of two k blocks a wavefront at least: sharing
+// an output takes three dependent trips to memory (4 x 1024 x 2048: 3.3 us alone, 4.3 shared by two; 4 x 1024 x 8192: 7.4, 6.6,
+// by four 6.4).
+static int rows_splits(int64_t columns, int KB) {
+  return (int)std::min<int64_t>({std::max<int64_t>(1, kCUs / columns), std::max(1, KB / (2 * kW8Waves)), kMaxSplits});
+}
+
 static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   const bool gated = p->gate != QGEMM_GATE_NONE, quantized = p->out_dtype == QGEMM_DT_FP8_E4M3;
   const int KB = (int)(p->K / kBlock);
@@ -105,11 +112,7 @@ static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   pl->kind = W8_ROWS;
   const int members = quantized ? kBlock / 16 : 1;
   const int64_t columns = p->N / 16, groups = columns / members;   // workgroups without a split
-  int splits = std::min(p->split_hint, KB);
-  // As many as give every compute unit a workgroup, of two k blocks a wavefront at least: sharing an output takes three
-  // dependent trips to memory (4 x 1024 x 2048: 3.3 us alone, 4.3 shared by two; 4 x 1024 x 8192: 7.4, 6.6, by four 6.4).
-  if (!splits) splits = (int)std::min<int64_t>(std::max<int64_t>(1, kCUs / columns), std::max(1, KB / (2 * kW8Waves)));
-  splits = std::min(splits, kMaxSplits);
+  int splits = p->split_hint ? std::min(p->split_hint, KB) : rows_splits(columns, KB);
   if (groups > kW8Tickets) splits = 1;
   // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
   // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
@@ -135,8 +138,9 @@ static double share_cost(int tile, int64_t tiles, int splits) {
 // those of either projection, times its share of them, half of the way from the average to the unit with the most workgroups (they
 // overlap).  Within a tenth of the times at 4096 x 4096 to 28672 x 8192, a fifth with e4m3 outputs.
 static double rows_cost(const qgemm_w8a8_t* p) {
-  const int64_t workgroups = p->N / 16, rounds = (workgroups + kCUs - 1) / kCUs;
-  const double blocks = 0.5 * ((double)workgroups / kCUs + (double)rounds) * (double)(p->K / kBlock);
+  const int KB = (int)(p->K / kBlock), splits = rows_splits(p->N / 16, KB);
+  const int64_t workgroups = p->N / 16 * splits, rounds = (workgroups + kCUs - 1) / kCUs;
+  const double blocks = 0.5 * ((double)workgroups / kCUs + (double)rounds) * KB / splits;
   const double one = 0.10 + 0.0021 * (double)p->M;
   if (p->gate == QGEMM_GATE_NONE) return 2.0 + one * blocks;
   if (p->out_dtype != QGEMM_DT_FP8_E4M3) return 3.0 + 1.5 * one * blocks;
@@ -177,8 +181,9 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   // kernel has few tiles and joins their splits (4096 x 4096, 17 tokens: 6.4 and 13.0 us, 64 tokens 9.3 and 13.4;
   // 10240 x 5120: 16.6 and 19.1, 28.5 and 20.4; 11008 x 4096 gated to e4m3: 29.0 and 26.6, 47.6 and 27.7; 5632 x 2048, 40 tokens 14.5 and 16.3).
   if (p->kernel_hint == QGEMM_W8A8_AUTO && !p->tile_hint && p->M <= kRowsMaxM) {
+    // With so few tokens the weights come from memory: split tiles take about 3 us more than the fit, and no less than that reading.
     const double memory = 3.0 + (double)(p->N * p->K) * (gated ? 2 : 1) / 3.7e6;
-    if (rows_cost(p) < std::max(best, memory)) {
+    if (rows_cost(p) < std::max(best + (best_splits > 1 ? 3.0 : 0.0), memory)) {
       *pl = W8Plan{};
       return make_rows_plan(p, pl);
     }
