@@ -116,10 +116,12 @@ static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   if (groups > kW8Tickets) splits = 1;
   // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
   // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
-  // with a gate, where the LDS of eight is for one workgroup a compute unit (11008 x 4096: 22.8 and 20.0).
+  // where the LDS of eight leaves room for one workgroup a compute unit and more are waiting: with a gate (11008 x 4096: 22.8
+  // and 20.0) and from 17 tokens on (17 x 8192 x 4096: 11.6 and 10.4; 17 x 4096 x 4096, one each, 6.4 and 6.7), above 32 always.
   const int per = (KB + splits - 1) / splits;
   const auto places = [&](int waves) { return (per + 2 * waves - 1) / (2 * waves) * 2 * waves; };
-  pl->waves = gated || M > 32 || places(4) * 10 <= places(8) * 9 ? 4 : 8;
+  const bool crowded = M > 32 || (M > 16 && columns * splits > kCUs);
+  pl->waves = gated || crowded || places(4) * 10 <= places(8) * 9 ? 4 : 8;
   return finish_plan(pl, 0, groups, members, splits, KB, (size_t)(gated ? 2 : 1) * 1024 * ((M + 15) / 16));
 }
 

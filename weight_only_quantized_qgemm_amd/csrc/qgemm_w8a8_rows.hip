@@ -27,14 +27,14 @@ namespace qgemm {
 namespace w8 {
 namespace {
 
-// (With no second launch bound the compiler orders the loop so that 11008 x 4096 gated takes 20.1 us instead of 19.4.)
+// XH: loads of eight tokens each.  (With no second launch bound the compiler orders the loop so that 11008 x 4096 gated takes 20.1 us instead of 19.4.)
 template <int NW, int XH, int GATE, bool Q>
 __global__ __launch_bounds__(64 * NW, XH <= 4 ? 2 : 1) void rows_kernel(W8Args a) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int U = G ? 2 : 1;                       // weight blocks: one of either projection
   constexpr int F = Q ? kBlock / 16 : 1;             // workgroups along the columns of one output scale block
-  // two stages per wavefront: 64 KiB for eight, 48 for four with a gate, so that two or three workgroups share a compute unit (one
-  // stage more and 11008 x 4096 gated takes 21.0 us instead of 20.0, 4096 x 4096 6.3 instead of 5.6)
+  // Two stages per wavefront: to 16 tokens 64 KiB for eight, 48 for four with a gate, so that two or three workgroups share a
+  // compute unit (one stage more and 11008 x 4096 gated takes 21.0 us instead of 20.0, 4096 x 4096 6.3 instead of 5.6).
   constexpr int MB = (XH + 1) / 2;                   // token blocks
   constexpr int SLOT = (U + MB) * 16 * kBlock;
   __shared__ __attribute__((aligned(1024))) unsigned char S0[NW * SLOT], S1[NW * SLOT];
