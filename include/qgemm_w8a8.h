@@ -46,7 +46,9 @@ typedef struct qgemm_add_norm {
  *   weight    dim 16-bit values, or NULL (ones); ignored for norm = 0.
  *   y         [tokens][dim] contiguous, of out_dtype; overlaps no other argument.
  *   y_scales  fp32 [dim / 128][tokens] for FP8_E4M3, otherwise NULL.
- * Pointers are 16-byte aligned (y_scales: 4).  |s| up to 2^56 is covered: beyond it the sum of squares overflows.
+ * Pointers are 16-byte aligned (y_scales: 4).  |s| up to 2^56 is covered: beyond it the sum of squares overflows.  So is any
+ * eps, but with eps below 2^-126 a row whose root mean square is below 2^-56: its squares underflow.  With eps = 0 a row
+ * of zeros is NaN, as 0 / 0 is.
  */
 qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* problem, const void* x, int64_t x_stride, const void* residual,
                               int64_t residual_stride, const void* weight, void* sum_out, int64_t sum_stride, void* y,

@@ -101,6 +101,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void add_norm(NormArgs a) {
     }
     scale = 1.0f / __builtin_sqrtf(sum / (float)a.dim + a.eps);
   }
+  // 8 bits: the root's power of two goes to the values before the weight does, its rest in [1, 2) to the blocks' scales, so that
+  // neither a small eps nor a small weight takes s w or a factor out of range.  (Infinite for a row of zeros and eps = 0,
+  // whose codes are NaN as 0 / 0 is; 0 where the sum of squares is infinite.)
+  const unsigned bits = __builtin_bit_cast(unsigned, scale);
+  const float power = __builtin_bit_cast(float, bits & 0x7f800000u), rest = __builtin_bit_cast(float, (bits & 0x007fffffu) | 0x3f800000u);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int d = 8 * (c * T + t);
@@ -110,10 +115,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void add_norm(NormArgs a) {
       unsigned m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        s[c][i] *= power;
         if (a.w) s[c][i] *= w[i];
         m = max(m, magnitude(s[c][i]));
       }
-      const BlockScale b = block_scale(max_row16(m), scale);   // a block is past the row's end as a whole
+      const BlockScale b = block_scale(max_row16(m), rest);   // a block is past the row's end as a whole
       if (d < a.dim) {
         const u32x2 v = {codes4(s[c][0] * b.to_code, s[c][1] * b.to_code, s[c][2] * b.to_code, s[c][3] * b.to_code),
                          codes4(s[c][4] * b.to_code, s[c][5] * b.to_code, s[c][6] * b.to_code, s[c][7] * b.to_code)};

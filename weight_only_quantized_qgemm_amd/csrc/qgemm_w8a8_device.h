@@ -32,7 +32,8 @@ __device__ __forceinline__ unsigned max_row16(unsigned m) {
 __device__ __forceinline__ unsigned magnitude(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
 
 // Scale of a block whose largest |value| is `amax` (bits), and the factor from `unit` times its values to
-// codes: values y are held as y = t * r, with t at hand, and amax that of t.
+// codes: values y are held as y = t * r, with t at hand, and amax that of t.  r lies in [1, 2): then t is as large as y, and
+// neither factor leaves fp32's range, however small the block.
 struct BlockScale { float scale, to_code; };
 __device__ __forceinline__ BlockScale block_scale(unsigned amax_bits, float r) {
   constexpr float kLeast = 0x1p-100f;
