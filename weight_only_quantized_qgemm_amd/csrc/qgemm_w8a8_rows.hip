@@ -133,6 +133,7 @@ __global__ __launch_bounds__(64 * NW, XH <= 4 ? 2 : 1) void rows_kernel(W8Args a
   // The last round is as long as the others: blocks past the end are the last one again, with factor 0 (branches
   // around them would copy the sums from register to register).
   load(0, kb0 + wave);
+  asm volatile("" ::: "memory");                     // the first wait counts the second load
   load(1, kb0 + wave + NW);
   for (int kb = kb0 + wave; kb < kb1; kb += 2 * NW) {
     read(0);
