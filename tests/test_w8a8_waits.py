@@ -70,3 +70,13 @@ def test_first_loads_come_stage_by_stage(kernels):
         first, second = order[:into_lds + scales], order[into_lds + scales:]
         assert len(order) == 2 * (into_lds + scales), (k, order)
         assert first.count("L") == second.count("L") == into_lds, (k, order)
+
+
+def test_each_stage_waits_for_itself_alone(kernels):
+    """In a round of the loop one wait for each stage, while all loads of the other are on their way: nothing else waits for loads
+    (as it did where the scales' product was moved up to the other stage's)."""
+    for k, lines in kernels.items():
+        each, loop = sum(stage_loads(k)), prologue_and_loop(lines)[1]
+        waits = [i for i, l in enumerate(loop) if l.startswith("s_waitcnt") and "vmcnt" in l]
+        assert [re.search(r"vmcnt\((\d+)\)", loop[i])[1] for i in waits] == [str(each)] * 2, k
+        assert not loads(loop[:waits[0]]) and len(loads(loop[waits[0]:waits[1]])) == each, k

@@ -94,6 +94,11 @@ __global__ __launch_bounds__(64 * NW, XH <= 4 ? 2 : 1) void rows_kernel(W8Args a
   float f[U * MB];
   const auto read = [&](int d) {
     __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));        // this stage has landed, the other may be on its way
+    // the scales are used from here on: moved up to the other stage's, their product would wait for everything
+#pragma unroll
+    for (int u = 0; u < U; ++u) asm volatile("" : "+v"(sw[d][u]));
+#pragma unroll
+    for (int i = 0; i < MB; ++i) asm volatile("" : "+v"(sa[d][i]));
     asm volatile("" ::: "memory");
     const auto chunks = [&](const unsigned char* p) {
       return Chunks{{*reinterpret_cast<const i32x4*>(p + off0), *reinterpret_cast<const i32x4*>(p + off1)}};
