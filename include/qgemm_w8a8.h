@@ -107,6 +107,7 @@ qgemm_status_t qgemm_w8a8_workspace_bytes(const qgemm_w8a8_t* problem, size_t* b
  *   out         [M][N] of out_dtype, contiguous, 16-byte aligned;  out_scales fp32 [N / 128][M] for FP8_E4M3,
  *               otherwise NULL.
  *   workspace   see qgemm_w8a8_workspace_bytes; 256-byte aligned; may be NULL when 0 bytes are needed.
+ * out, out_scales and the needed part of workspace overlap each other and the inputs nowhere (refused: INVALID_ARGUMENT).
  * M = 0 enqueues nothing.  Results are bitwise deterministic.
  */
 qgemm_status_t qgemm_w8a8_run(const qgemm_w8a8_t* problem, const void* A, const float* a_scales, const void* W,

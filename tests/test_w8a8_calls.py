@@ -1,0 +1,37 @@
+"""Calls of the 8-bit operators that the C ABI refuses beside those of a single argument (nothing is launched)."""
+import ctypes
+
+import pytest
+
+import weight_only_quantized_qgemm_amd as q
+
+# M = 4, N = K = 256: where each argument of a gated call to e4m3 lies, and its bytes
+AT = dict(A=0x100000, sa=0x200000, W=0x300000, sw=0x400000, out=0x500000, so=0x600000, ws=0x700000)
+BYTES = dict(A=4 * 256, sa=4 * 2 * 4, W=512 * 256, sw=4 * 2 * 4, out=4 * 256, so=4 * 2 * 4, ws=0)
+NAMES = dict(A="A", sa="a_scales", W="W", sw="w_scales", out="out", so="out_scales", ws="workspace")
+
+
+def call(p, **at):
+    c = dict(AT, **at)
+    return q.lib.qgemm_w8a8_run(ctypes.byref(p), c["A"], c["sa"], c["W"], c["sw"], c["out"], c["so"], c["ws"], 1 << 24, None)
+
+
+@pytest.mark.parametrize("written", ["out", "so", "ws"])
+@pytest.mark.parametrize("other", list(AT))
+def test_outputs_on_other_arguments_are_refused(written, other):
+    """A gated product to e4m3 with N = K has outputs of its activations' shape and type."""
+    if written == other:
+        return
+    p = q.w8a8_problem(4, 256, 256, q.DT_FP8_E4M3, gate=q.GATE_SILU)
+    size = dict(BYTES, ws=q.w8a8_workspace_bytes(p))
+    align = dict(out=16, so=4, ws=256)[written]
+    last = (size[other] - 1) // align * align                                 # begins on the other's last bytes, or ends on its first
+    before = -((size[written] - 1) // align * align)
+    for distance in {0, last, before}:
+        assert call(p, **{written: AT[other] + distance}) == q.ERR_INVALID_ARGUMENT, (written, other, distance)
+        assert "overlaps" in q.last_error() and NAMES[written] in q.last_error() and NAMES[other] in q.last_error()
+
+
+def test_a_16_bit_output_on_its_activations_is_refused():
+    p = q.w8a8_problem(4, 128, 256, q.DT_BF16)
+    assert call(p, out=AT["A"], so=None) == q.ERR_INVALID_ARGUMENT and "out overlaps A" in q.last_error()

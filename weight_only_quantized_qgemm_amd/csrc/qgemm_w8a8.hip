@@ -32,6 +32,20 @@ extern "C" qgemm_status_t qgemm_w8a8_run(const qgemm_w8a8_t* p, const void* A, c
                   workspace ? workspace_bytes : (size_t)0, workspace ? "" : " (NULL)");
     if (!aligned(workspace, 256)) return fail(QGEMM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
   }
+  // What is written must be apart from everything else: other workgroups still read A when the first outputs are stored.
+  const uint64_t M = p->M, N = p->N, K = p->K, KB = K / kBlock, parts = p->gate != QGEMM_GATE_NONE ? 2 : 1;
+  const struct { const char* name; const void* p; uint64_t bytes; } all[] = {
+      {"out", out, M * N * (quantized ? 1 : p->out_dtype == QGEMM_DT_F32 ? 4 : 2)},
+      {"out_scales", out_scales, quantized ? M * (N / kBlock) * 4 : 0},
+      {"workspace", workspace, pl.ws_bytes},                           // the first three are written
+      {"A", A, M * K}, {"a_scales", a_scales, M * KB * 4}, {"W", W, parts * N * K},
+      {"w_scales", w_scales, parts * ((N + kBlock - 1) / kBlock) * KB * 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 7; ++j) {
+      const uint64_t x = reinterpret_cast<uintptr_t>(all[i].p), y = reinterpret_cast<uintptr_t>(all[j].p);
+      if (all[i].bytes && all[j].bytes && x < y + all[j].bytes && y < x + all[i].bytes)
+        return fail(QGEMM_ERR_INVALID_ARGUMENT, "%s overlaps %s", all[i].name, all[j].name);
+    }
   w8::W8Args a{};
   a.a = static_cast<const uint8_t*>(A);
   a.w = static_cast<const uint8_t*>(W);
