@@ -63,6 +63,10 @@ qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* problem, const void* x, in
 #define QGEMM_W8A8_ROWS 1           /* the weights stream past a few tokens: M <= 64             */
 #define QGEMM_W8A8_TILES 2          /* tiles of tokens x weight rows, any M                      */
 
+/* sums values: how products enter their sums (qgemm_w8a8_run) */
+#define QGEMM_W8A8_SUMS_AUTO 0      /* as fine as the outputs show in ordinary data              */
+#define QGEMM_W8A8_SUMS_WHOLE 1     /* every product whole, whatever the outputs and the kernel  */
+
 /*
  * qgemm_w8a8_t -- out [M][N] from activations A [M][K] and weights W.
  *   M in [0, 2^24]; N a multiple of 16 in [16, 2^24]; K a multiple of 128 in [128, 2^22] (more workgroups than one
@@ -72,13 +76,13 @@ qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* problem, const void* x, in
  *   its own, the last one short where N is no multiple of 128);
  *   out_dtype F16, BF16 or F32, or with a gate FP8_E4M3 (N then a multiple of 128): the activations of the next product;
  *   kernel_hint QGEMM_W8A8_*; split_hint 0 = automatic, else the workgroups (1 to 32) that share the K axis of
- *   one tile; tile_hint 0 = automatic, else the tokens of a tile of the tiles kernel (64, 128 or 256).
+ *   one tile; tile_hint 0 = automatic, else the tokens of a tile of the tiles kernel (64, 128 or 256);
+ *   sums QGEMM_W8A8_SUMS_* (other values are reserved).
  *   The launch depends on the descriptor only.
  */
 typedef struct qgemm_w8a8 {
   int64_t M, N, K;
-  int32_t out_dtype, gate, kernel_hint, split_hint, tile_hint;
-  int32_t reserved;                 /* 0 */
+  int32_t out_dtype, gate, kernel_hint, split_hint, tile_hint, sums;
 } qgemm_w8a8_t;
 
 /*
@@ -99,10 +103,12 @@ qgemm_status_t qgemm_w8a8_workspace_bytes(const qgemm_w8a8_t* problem, size_t* b
  * qgemm_w8a8_run -- enqueue
  *   p_r[m] = sum_b a_scale[b][m] w_scale[r / 128][b] (sum_{k in block b} a[m][k] w[r][k])
  *   out[m][n] = p_n[m],  or act(p_n[m]) p_{N + n}[m] with a gate,
- * the sums in fp32, one rounding to out_dtype.  With F32 and FP8_E4M3 outputs every product enters its sum whole.  With F16
- * and BF16 outputs of more than 16 tokens the products of eight consecutive k may be added first, cut off at 2^-13 of the
- * largest one's power of two: an error of at most 7 * 2^-13 times the sum of the groups' largest products (of normally
- * distributed values 1.4e-5 of an output's standard deviation).
+ * the sums in fp32, one rounding to out_dtype.  With F32 and FP8_E4M3 outputs, in the rows kernel and with sums =
+ * QGEMM_W8A8_SUMS_WHOLE every product enters its sum whole.  Otherwise, with F16 and BF16 outputs, the tiles kernel (without a
+ * hint from 17 tokens on, always above 64) adds the products of eight consecutive k first, cut off at 2^-13 of the largest
+ * one's power of two: an error of at most 7 * 2^-13 times the sum of the groups' largest products (of normally distributed
+ * values 1.4e-5 of an output's standard deviation).  Whole sums take the tiles kernel up to twice as
+ * long; ask for them where large products may cancel, or where one token and a prompt must agree beyond the cut.
  *   A, W        e4m3 codes, contiguous, 16-byte aligned;  a_scales, w_scales fp32, contiguous, 4-byte aligned.
  *   out         [M][N] of out_dtype, contiguous, 16-byte aligned;  out_scales fp32 [N / 128][M] for FP8_E4M3,
  *               otherwise NULL.

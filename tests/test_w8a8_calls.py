@@ -35,3 +35,13 @@ def test_outputs_on_other_arguments_are_refused(written, other):
 def test_a_16_bit_output_on_its_activations_is_refused():
     p = q.w8a8_problem(4, 128, 256, q.DT_BF16)
     assert call(p, out=AT["A"], so=None) == q.ERR_INVALID_ARGUMENT and "out overlaps A" in q.last_error()
+
+
+def test_sums_are_checked():
+    for bad in (-1, 2):
+        p = q.w8a8_problem(4, 256, 256, sums=bad)
+        assert call(p, so=None) == q.ERR_INVALID_ARGUMENT and "sums" in q.last_error()
+        with pytest.raises(q.QgemmError, match="sums"):
+            q.w8a8_describe(p)
+    whole = q.w8a8_problem(200, 256, 256, sums=q.W8A8_SUMS_WHOLE)
+    assert "operands=16" in q.w8a8_describe(whole) and "operands=8" in q.w8a8_describe(q.w8a8_problem(200, 256, 256))

@@ -43,6 +43,7 @@ KERNEL_AUTO, KERNEL_DECODE, KERNEL_PREFILL, KERNEL_PREFILL_STREAMK, KERNEL_PREFI
 ATTENTION_AUTO, ATTENTION_ROWS, ATTENTION_TILES = range(3)
 GATE_NONE, GATE_SILU, GATE_GELU_TANH = range(3)
 W8A8_AUTO, W8A8_ROWS, W8A8_TILES = range(3)
+W8A8_SUMS_AUTO, W8A8_SUMS_WHOLE = range(2)
 
 
 class Problem(ctypes.Structure):
@@ -85,7 +86,7 @@ class AddNorm(ctypes.Structure):
 class W8A8(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
                 ("gate", ctypes.c_int32), ("kernel_hint", ctypes.c_int32), ("split_hint", ctypes.c_int32),
-                ("tile_hint", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("tile_hint", ctypes.c_int32), ("sums", ctypes.c_int32)]
 
 
 assert (ctypes.sizeof(NormRope), ctypes.sizeof(Cache), ctypes.sizeof(Attention)) == (48, 32, 80)
@@ -442,9 +443,11 @@ def add_norm(p, x, residual, weight, sum_out, y, y_scales=None, stream=None):
         _check(st)
 
 
-def w8a8_problem(M, N, K, out_dtype=DT_BF16, gate=GATE_NONE, kernel_hint=W8A8_AUTO, split_hint=0, tile_hint=0):
-    """Descriptor of a product of 8-bit activations and weights, or with a gate of a pair of them."""
-    return W8A8(M, N, K, out_dtype, gate, kernel_hint, split_hint, tile_hint, 0)
+def w8a8_problem(M, N, K, out_dtype=DT_BF16, gate=GATE_NONE, kernel_hint=W8A8_AUTO, split_hint=0, tile_hint=0,
+                 sums=W8A8_SUMS_AUTO):
+    """Descriptor of a product of 8-bit activations and weights, or with a gate of a pair of them.  W8A8_SUMS_WHOLE has every
+    product enter its sum whole where the default leaves 16-bit outputs to the faster e4m3 matrix instruction."""
+    return W8A8(M, N, K, out_dtype, gate, kernel_hint, split_hint, tile_hint, sums)
 
 
 def w8a8_quantize(p, w):

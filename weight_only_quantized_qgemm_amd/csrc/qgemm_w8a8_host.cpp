@@ -76,7 +76,8 @@ qgemm_status_t validate_w8a8(const qgemm_w8a8_t* p) {
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "split_hint must be in [0, %d], got %d", kMaxSplits, p->split_hint);
   if (p->tile_hint != 0 && p->tile_hint != 64 && p->tile_hint != 128 && p->tile_hint != 256)
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "tile_hint must be 0, 64, 128 or 256, got %d", p->tile_hint);
-  if (p->reserved != 0) return fail(QGEMM_ERR_INVALID_ARGUMENT, "reserved must be 0, got %d", p->reserved);
+  if (p->sums != QGEMM_W8A8_SUMS_AUTO && p->sums != QGEMM_W8A8_SUMS_WHOLE)
+    return fail(QGEMM_ERR_INVALID_ARGUMENT, "sums must be 0 or 1 (other values are reserved), got %d", p->sums);
   return QGEMM_OK;
 }
 
@@ -158,7 +159,7 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   pl->kind = W8_TILES;
   const int columns = gated ? kTileRows / 2 : kTileRows;
   pl->tiles_n = (int)((p->N + columns - 1) / columns);
-  const bool fp16 = quantized || p->out_dtype == QGEMM_DT_F32;
+  pl->fp16 = quantized || p->out_dtype == QGEMM_DT_F32 || p->sums == QGEMM_W8A8_SUMS_WHOLE;
   // The tiles of whole rounds over the compute units run on their own; those of the last round are split along K as far
   // as that shortens it (all tiles, where there are fewer than compute units).
   double best = 0.0;
@@ -170,7 +171,7 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
     for (int s = 1; s <= (p->split_hint ? 1 : std::min(kMaxSplits, KB)); ++s) {
       const int kb = (KB + s - 1) / s;
       if (s > 1 && (!tail || (KB + kb - 1) / kb != s)) continue;
-      const double step = c.step[fp16], tail_rounds = (double)((tail * s + kCUs - 1) / kCUs);
+      const double step = c.step[pl->fp16], tail_rounds = (double)((tail * s + kCUs - 1) / kCUs);
       const double us = (double)rounds * (KB * step + c.fixed) + tail_rounds * (kb * step + c.fixed) + share_cost(tile, tail, s);
       if (pl->tile == 0 || us < best) {
         best = us;
@@ -272,8 +273,8 @@ qgemm_status_t qgemm_w8a8_describe(const qgemm_w8a8_t* p, char* buf, size_t len)
   if (st != QGEMM_OK) return st;
   const int n = p->M == 0 ? std::snprintf(buf, len, "empty")
                 : pl.kind == W8_ROWS ? std::snprintf(buf, len, "rows grid=%u waves=%d splits=%d members=%d", pl.grid, pl.waves, pl.splits, pl.members)
-                                     : std::snprintf(buf, len, "tiles grid=%u tokens=%d whole=%d splits=%d", pl.grid, pl.tile, pl.whole,
-                                                     pl.splits);
+                                     : std::snprintf(buf, len, "tiles grid=%u tokens=%d whole=%d splits=%d operands=%d", pl.grid, pl.tile, pl.whole,
+                                                     pl.splits, pl.fp16 ? 16 : 8);
   if (n < 0 || (size_t)n >= len)
     return fail(QGEMM_ERR_INVALID_ARGUMENT, "the line needs %d bytes, buf holds %zu", n + 1, len);
   return QGEMM_OK;

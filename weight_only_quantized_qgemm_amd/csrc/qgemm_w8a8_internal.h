@@ -26,6 +26,7 @@ enum W8Kind : int { W8_ROWS = 1, W8_TILES = 2 };
 struct W8Plan {
   W8Kind kind;
   int tile;            // tiles kernel: tokens of a tile
+  bool fp16;           // tiles kernel: operands are converted to fp16, so that sums are whole
   int waves;           // rows kernel: wavefronts of a workgroup
   int tiles, whole, tiles_n;   // tiles kernel: all tiles, those that are not split, those along the weight rows
   int splits;          // workgroups along K

@@ -29,10 +29,12 @@ namespace qgemm {
 namespace w8 {
 namespace {
 
-template <int WM, int TM, int ST, int GATE, bool Q, bool FP16>
+// OUT: outputs in 16 bits, fp32 or e4m3.  FP16: operands converted to fp16, whole sums; fp32 and e4m3 outputs have no other form.
+enum Out { OUT_16, OUT_F32, OUT_E4M3 };
+template <int WM, int TM, int ST, int GATE, Out OUT, bool FP16>
 __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   constexpr int NW = kW8Waves, WN = NW / WM, TN = kTileRows / (16 * WN), BM = 16 * WM * TM;
-  constexpr bool G = GATE != QGEMM_GATE_NONE;
+  constexpr bool G = GATE != QGEMM_GATE_NONE, Q = OUT == OUT_E4M3;
   constexpr int COLS = G ? kTileRows / 2 : kTileRows;          // output columns of a tile
   constexpr int LA = BM / (8 * NW), LW = kTileRows / (8 * NW); // loads of a wavefront per step
   static_assert(!G || TN % 2 == 0, "both projections' rows lie in one wavefront");
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void tiles_kernel(W8Args a) {
   __builtin_amdgcn_s_waitcnt(0);                     // no load is still writing LDS
   __syncthreads();                                   // and no wavefront reads it: what follows uses it otherwise
 
-  const TileEnd<WN, NW, GATE, Q, FP16 && !Q, TN, TM> end{a, A0, A1, (wave < 4 ? W0 : W1) + (wave & 3) * 8192, tn, m0, wm * TM, wn, c0};
+  const TileEnd<WN, NW, GATE, Q, OUT == OUT_F32, TN, TM> end{a, A0, A1, (wave < 4 ? W0 : W1) + (wave & 3) * 8192, tn, m0, wm * TM, wn, c0};
   if (splits == 1) {
     end.whole(acc);
   } else {
@@ -288,9 +290,11 @@ void launch_tile(const W8Plan& pl, const W8Args& a, hipStream_t s) {
   const dim3 grid(pl.grid), block(64 * kW8Waves);
   const auto gate = [&](auto g) {
     constexpr int GATE = decltype(g)::value;
-    if (a.out_dtype == QGEMM_DT_F32) tiles_kernel<WM, TM, ST, GATE, false, true><<<grid, block, 0, s>>>(a);
-    else if (a.out_dtype != QGEMM_DT_FP8_E4M3) tiles_kernel<WM, TM, ST, GATE, false, false><<<grid, block, 0, s>>>(a);
-    else if constexpr (GATE != QGEMM_GATE_NONE) tiles_kernel<WM, TM, ST, GATE, true, true><<<grid, block, 0, s>>>(a);
+    if (a.out_dtype == QGEMM_DT_F32) tiles_kernel<WM, TM, ST, GATE, OUT_F32, true><<<grid, block, 0, s>>>(a);
+    else if (a.out_dtype != QGEMM_DT_FP8_E4M3)
+      pl.fp16 ? tiles_kernel<WM, TM, ST, GATE, OUT_16, true><<<grid, block, 0, s>>>(a)
+              : tiles_kernel<WM, TM, ST, GATE, OUT_16, false><<<grid, block, 0, s>>>(a);
+    else if constexpr (GATE != QGEMM_GATE_NONE) tiles_kernel<WM, TM, ST, GATE, OUT_E4M3, true><<<grid, block, 0, s>>>(a);
   };
   switch (a.gate) {
     case QGEMM_GATE_NONE: gate(std::integral_constant<int, QGEMM_GATE_NONE>{}); break;
