@@ -66,11 +66,16 @@ def call(q, ins, m, gate, out, **hints):
                                           ("gelu", (True, False)), ("gelu", (False, True))])
 def test_every_product_enters_whole(q, m, gate, cancels):
     ins, (y64, tol) = inputs(m, cancels), want(m, cancels, gate)
-    for out in ("f16", "bf16"):
-        sums = q.W8A8_SUMS_WHOLE
+    for out in ["f32", "f16", "bf16"] + (["e4m3"] if gate != "none" else []):
+        sums = q.W8A8_SUMS_WHOLE if out in T16 else q.W8A8_SUMS_AUTO
         for h in launches(q, m):
             y, scales = call(q, ins, m, gate, out, sums=sums, **h)
-            assert np.all(np.abs(y - y64) <= tol + STEP[out] * (np.abs(y64) + tol)), (out, h, np.abs(y / y64 - 1).max())
+            if out == "e4m3":                                                 # all outputs of a token are alike: the largest, code 448
+                assert (y == 448).all(), h
+                s = scales.double().cpu().numpy()
+                assert np.all(np.abs(s * 448 - y64.T) <= tol.T + 3 * U24 * (y64 + tol).T), h
+            else:
+                assert np.all(np.abs(y - y64) <= tol + STEP[out] * (np.abs(y64) + tol)), (out, h, np.abs(y / y64 - 1).max())
 
 
 @pytest.mark.parametrize("gate", ["none", "silu"])
