@@ -76,7 +76,7 @@ qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* problem, const void* x, in
  *   its own, the last one short where N is no multiple of 128);
  *   out_dtype F16, BF16 or F32, or with a gate FP8_E4M3 (N then a multiple of 128): the activations of the next product;
  *   kernel_hint QGEMM_W8A8_*; split_hint 0 = automatic, else the workgroups (1 to 32) that share the K axis of
- *   one tile; tile_hint 0 = automatic, else the tokens of a tile of the tiles kernel (64, 128 or 256);
+ *   one tile, in the kernel and with the tile that are taken without it; tile_hint 0 = automatic, else the tokens of a tile of the tiles kernel (64, 128 or 256);
  *   sums QGEMM_W8A8_SUMS_* (other values are reserved).
  *   The launch depends on the descriptor only.
  */

@@ -45,3 +45,15 @@ def test_sums_are_checked():
             q.w8a8_describe(p)
     whole = q.w8a8_problem(200, 256, 256, sums=q.W8A8_SUMS_WHOLE)
     assert "operands=16" in q.w8a8_describe(whole) and "operands=8" in q.w8a8_describe(q.w8a8_problem(200, 256, 256))
+
+
+def test_a_split_hint_leaves_the_kernel_and_its_tile():
+    """The launch that is taken without the hint is the one that the hint splits."""
+    for m in (1, 16, 17, 24, 40, 64, 65, 200, 333, 1000):
+        for n, k in ((4096, 4096), (10240, 5120), (1024, 28672), (22016, 4096), (2048, 512)):
+            for gate, out in ((q.GATE_NONE, q.DT_BF16), (q.GATE_NONE, q.DT_F32), (q.GATE_SILU, q.DT_FP8_E4M3)):
+                def launch(split):
+                    head, *f = q.w8a8_describe(q.w8a8_problem(m, n, k, out, gate=gate, split_hint=split)).split()
+                    return head, [x for x in f if x.startswith("tokens=")]
+                for split in (1, 2, 5, 32):
+                    assert launch(split) == launch(0), (m, n, k, gate, out, split)

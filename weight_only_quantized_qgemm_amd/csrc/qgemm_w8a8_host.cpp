@@ -161,14 +161,15 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   pl->tiles_n = (int)((p->N + columns - 1) / columns);
   pl->fp16 = quantized || p->out_dtype == QGEMM_DT_F32 || p->sums == QGEMM_W8A8_SUMS_WHOLE;
   // The tiles of whole rounds over the compute units run on their own; those of the last round are split along K as far
-  // as that shortens it (all tiles, where there are fewer than compute units).
+  // as that shortens it (all tiles, where there are fewer than compute units).  A split hint takes no part in the choice of tile
+  // and kernel, on either side: it splits the launch that is taken without it.
   double best = 0.0;
   int best_splits = 1;
   for (int tile : {64, 128, 256}) {
     if (p->tile_hint && p->tile_hint != tile) continue;
     const int64_t tiles = (M + tile - 1) / tile * pl->tiles_n, tail = tiles % kCUs, rounds = tiles / kCUs;
     const TileCost c = tile_cost(tile);
-    for (int s = 1; s <= (p->split_hint ? 1 : std::min(kMaxSplits, KB)); ++s) {
+    for (int s = 1; s <= std::min(kMaxSplits, KB); ++s) {
       const int kb = (KB + s - 1) / s;
       if (s > 1 && (!tail || (KB + kb - 1) / kb != s)) continue;
       const double step = c.step[pl->fp16], tail_rounds = (double)((tail * s + kCUs - 1) / kCUs);
