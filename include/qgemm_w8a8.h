@@ -95,8 +95,9 @@ typedef struct qgemm_w8a8 {
 qgemm_status_t qgemm_w8a8_quantize(const qgemm_w8a8_t* problem, const float* w, uint8_t* codes, float* scales);
 
 /* qgemm_w8a8_workspace_bytes -- device workspace of qgemm_w8a8_run (0 when none): zero-filled once by the caller,
- * then reusable by later calls in stream order.  One workspace of the largest size asked for serves any descriptors;
- * calls that overlap in time need different ones. */
+ * then reusable by later calls in stream order.  One workspace of the largest size asked for serves all the descriptors it
+ * was asked for; calls that overlap in time need different ones.  The size does not grow with M (11008 x 4096 gated to
+ * e4m3: 1.9 MB for 16 tokens, 11.8 for 40, 0 for 200, 50.9 for 4096, 0 for 8192): a program that runs several M asks for each. */
 qgemm_status_t qgemm_w8a8_workspace_bytes(const qgemm_w8a8_t* problem, size_t* bytes);
 
 /*

@@ -57,3 +57,14 @@ def test_a_split_hint_leaves_the_kernel_and_its_tile():
                     return head, [x for x in f if x.startswith("tokens=")]
                 for split in (1, 2, 5, 32):
                     assert launch(split) == launch(0), (m, n, k, gate, out, split)
+
+
+def test_one_workspace_for_every_number_of_tokens():
+    """The largest number of tokens needs no workspace, smaller ones do: a workspace is allocated for all of them."""
+    ps = [q.w8a8_problem(m, 11008, 4096, q.DT_FP8_E4M3, gate=q.GATE_SILU) for m in (1, 16, 40, 200, 333, 4096, 8192)]
+    sizes = [q.w8a8_workspace_bytes(p) for p in ps]
+    assert sizes[-1] == 0 and max(sizes) > 0 and sizes != sorted(sizes)
+    ws = q.alloc_w8a8_workspace(ps, device="cpu")
+    assert ws.numel() == max(sizes) and not ws.any()
+    assert q.alloc_w8a8_workspace(ps[-1:], device="cpu") is None and q.alloc_w8a8_workspace([], device="cpu") is None
+    assert q.alloc_w8a8_workspace(ps[1], device="cpu").numel() == sizes[1]

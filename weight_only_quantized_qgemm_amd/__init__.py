@@ -463,14 +463,15 @@ def w8a8_quantize(p, w):
 
 
 def w8a8_workspace_bytes(p):
+    """Bytes of workspace of one problem.  They do not grow with M: a program that runs several M needs the largest of theirs."""
     n = _sz(0)
     _check(_lib.qgemm_w8a8_workspace_bytes(ctypes.byref(p), ctypes.byref(n)))
     return n.value
 
 
 def alloc_w8a8_workspace(p, device="cuda"):
-    """A zero-filled workspace of the size qgemm_w8a8_workspace_bytes reports (or None)."""
-    n = w8a8_workspace_bytes(p)
+    """A zero-filled workspace of the size qgemm_w8a8_workspace_bytes reports (or None); of several problems, one that serves them all."""
+    n = w8a8_workspace_bytes(p) if isinstance(p, W8A8) else max(map(w8a8_workspace_bytes, p), default=0)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
