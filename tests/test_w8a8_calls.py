@@ -68,3 +68,15 @@ def test_one_workspace_for_every_number_of_tokens():
     assert ws.numel() == max(sizes) and not ws.any()
     assert q.alloc_w8a8_workspace(ps[-1:], device="cpu") is None and q.alloc_w8a8_workspace([], device="cpu") is None
     assert q.alloc_w8a8_workspace(ps[1], device="cpu").numel() == sizes[1]
+
+
+def test_the_faster_kernel_is_taken_up_to_64_tokens():
+    """Where one kernel takes at least a tenth longer than the other (measured with weights from memory, us)."""
+    silu = q.GATE_SILU
+    for m, n, k, gate, out, rows, tiles in (
+            (17, 4096, 4096, 0, q.DT_F16, 6.1, 12.2), (64, 4096, 11008, 0, q.DT_BF16, 20.2, 23.4), (32, 6144, 8192, 0, q.DT_BF16, 17.7, 19.6),
+            (24, 28672, 8192, 0, q.DT_BF16, 58.4, 66.2), (48, 16384, 2048, 0, q.DT_F16, 13.3, 16.1), (64, 2816, 4096, silu, q.DT_FP8_E4M3, 16.1, 19.3),
+            (40, 10240, 5120, 0, q.DT_BF16, 22.2, 19.8), (64, 28672, 8192, 0, q.DT_BF16, 86.5, 67.9), (64, 6144, 8192, 0, q.DT_BF16, 25.5, 20.2),
+            (40, 11008, 4096, silu, q.DT_FP8_E4M3, 32.2, 26.8), (64, 11008, 4096, silu, q.DT_BF16, 32.4, 23.8), (47, 14336, 4096, 0, q.DT_F16, 23.3, 20.2)):
+        taken = q.w8a8_describe(q.w8a8_problem(m, n, k, out, gate=gate)).split()[0]
+        assert taken == ("rows" if rows < tiles else "tiles"), (m, n, k, gate, out)

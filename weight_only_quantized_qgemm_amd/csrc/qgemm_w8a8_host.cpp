@@ -139,15 +139,16 @@ static double share_cost(int tile, int64_t tiles, int splits) {
 
 // Microseconds of the rows kernel for more than 16 tokens: what a compute unit takes for 16 weight rows' k block, with a gate for
 // those of either projection, times its share of them, half of the way from the average to the unit with the most workgroups (they
-// overlap).  Within a tenth of the times at 4096 x 4096 to 28672 x 8192, a fifth with e4m3 outputs.
+// overlap).  Fitted to 96 times at 1024 x 28672 to 28672 x 8192, 17 to 64 tokens, with weights from memory: within 7% on average, 28% at
+// most (2048 x 8192); the faster kernel is missed by more than 5% on 3 of the 96, by 8% at most.
 static double rows_cost(const qgemm_w8a8_t* p) {
   const int KB = (int)(p->K / kBlock), splits = rows_splits(p->N / 16, KB);
   const int64_t workgroups = p->N / 16 * splits, rounds = (workgroups + kCUs - 1) / kCUs;
   const double blocks = 0.5 * ((double)workgroups / kCUs + (double)rounds) * KB / splits;
-  const double one = 0.10 + 0.0021 * (double)p->M;
+  const double one = 0.091 + 0.0018 * (double)p->M;
   if (p->gate == QGEMM_GATE_NONE) return 2.0 + one * blocks;
-  if (p->out_dtype != QGEMM_DT_FP8_E4M3) return 3.0 + 1.5 * one * blocks;
-  return 5.0 + (p->M > 48 ? 2.6 : 2.0) * one * blocks;              // above 48 tokens a compute unit holds one workgroup, not two
+  if (p->out_dtype != QGEMM_DT_FP8_E4M3) return 2.4 + 1.57 * one * blocks;
+  return 6.4 + (p->M > 48 ? 2.16 : 1.65) * one * blocks;            // above 48 tokens a compute unit holds one workgroup, not two
 }
 
 qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
@@ -182,8 +183,8 @@ qgemm_status_t make_w8a8_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
     }
   }
   // Up to 64 tokens either kernel may be the faster: the rows kernel reads the tokens again for every 16 weight rows, the tiles
-  // kernel has few tiles and joins their splits (4096 x 4096, 17 tokens: 6.4 and 13.0 us, 64 tokens 9.3 and 13.4;
-  // 10240 x 5120: 16.6 and 19.1, 28.5 and 20.4; 11008 x 4096 gated to e4m3: 29.0 and 26.6, 47.6 and 27.7; 5632 x 2048, 40 tokens 14.5 and 16.3).
+  // kernel has few tiles and joins their splits (4096 x 4096, 17 tokens: 6.1 and 12.2 us, 64 tokens 8.1 and 12.8;
+  // 10240 x 5120: 16.2 and 19.3, 28.0 and 20.5; 11008 x 4096 gated to e4m3: 27.0 and 26.5, 46.1 and 27.3; 5632 x 2048, 40 tokens 14.5 and 17.0).
   if (p->kernel_hint == QGEMM_W8A8_AUTO && !p->tile_hint && p->M <= kRowsMaxM) {
     // With so few tokens the weights come from memory: split tiles take about 3 us more than the fit, and no less than that reading.
     const double memory = 3.0 + (double)(p->N * p->K) * (gated ? 2 : 1) / 3.7e6;
