@@ -80,3 +80,10 @@ def test_the_faster_kernel_is_taken_up_to_64_tokens():
             (40, 11008, 4096, silu, q.DT_FP8_E4M3, 32.2, 26.8), (64, 11008, 4096, silu, q.DT_BF16, 32.4, 23.8), (47, 14336, 4096, 0, q.DT_F16, 23.3, 20.2)):
         taken = q.w8a8_describe(q.w8a8_problem(m, n, k, out, gate=gate)).split()[0]
         assert taken == ("rows" if rows < tiles else "tiles"), (m, n, k, gate, out)
+
+
+def test_few_tokens_split_along_k_only_where_it_pays():
+    """The rows kernel's splits: as measured with weights from memory, the fastest of 1, 2, 4 and 8 but for a tenth."""
+    for m, n, k, splits in ((4, 1024, 2048, 1), (16, 512, 4096, 1), (1, 2048, 4096, 1), (4, 1024, 8192, 2), (16, 1024, 8192, 2),
+                            (16, 2048, 8192, 2), (40, 1024, 8192, 4), (16, 1024, 28672, 4), (64, 1024, 28672, 4), (1, 2048, 28672, 2), (1, 4096, 28672, 1)):
+        assert f"rows grid={n // 16 * splits} " in q.w8a8_describe(q.w8a8_problem(m, n, k)), (m, n, k)

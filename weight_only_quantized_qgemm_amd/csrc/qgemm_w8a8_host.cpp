@@ -99,11 +99,13 @@ static qgemm_status_t finish_plan(W8Plan* pl, int64_t whole, int64_t groups, int
   return QGEMM_OK;
 }
 
-// The rows kernel's workgroups along K: as many as give every compute unit one, of two k blocks a wavefront at least: sharing
-// an output takes three dependent trips to memory (4 x 1024 x 2048: 3.3 us alone, 4.3 shared by two; 4 x 1024 x 8192: 7.4, 6.6,
-// by four 6.4).
-static int rows_splits(int64_t columns, int KB) {
-  return (int)std::min<int64_t>({std::max<int64_t>(1, kCUs / columns), std::max(1, KB / (2 * kW8Waves)), kMaxSplits});
+// The rows kernel's workgroups along K: as many as give every compute unit one, of four k blocks a wavefront at least, from 17 tokens on
+// two: sharing an output takes three dependent trips to memory (unsplit, by two and by four, weights from memory: 4 x 1024 x 2048 3.7, 4.8,
+// 6.0 us; 16 x 512 x 4096 5.2, 5.5, 5.6; 4 x 1024 x 8192 6.0, 6.2, 6.9; 16 x 1024 x 8192 7.7, 7.0, 7.2; 40 x 1024 x 8192 10.9, 8.7, 8.0;
+// 16 x 1024 x 28672 20.7, 13.6, 10.7).
+static int rows_splits(int64_t M, int64_t columns, int KB) {
+  const int least = (M <= 16 ? 4 : 2) * kW8Waves;
+  return (int)std::min<int64_t>({std::max<int64_t>(1, kCUs / columns), std::max(1, KB / least), kMaxSplits});
 }
 
 static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
@@ -113,7 +115,7 @@ static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   pl->kind = W8_ROWS;
   const int members = quantized ? kBlock / 16 : 1;
   const int64_t columns = p->N / 16, groups = columns / members;   // workgroups without a split
-  int splits = p->split_hint ? std::min(p->split_hint, KB) : rows_splits(columns, KB);
+  int splits = p->split_hint ? std::min(p->split_hint, KB) : rows_splits(M, columns, KB);
   if (groups > kW8Tickets) splits = 1;
   // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
   // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
@@ -142,7 +144,7 @@ static double share_cost(int tile, int64_t tiles, int splits) {
 // overlap).  Fitted to 96 times at 1024 x 28672 to 28672 x 8192, 17 to 64 tokens, with weights from memory: within 7% on average, 28% at
 // most (2048 x 8192); the faster kernel is missed by more than 5% on 3 of the 96, by 8% at most.
 static double rows_cost(const qgemm_w8a8_t* p) {
-  const int KB = (int)(p->K / kBlock), splits = rows_splits(p->N / 16, KB);
+  const int KB = (int)(p->K / kBlock), splits = rows_splits(p->M, p->N / 16, KB);
   const int64_t workgroups = p->N / 16 * splits, rounds = (workgroups + kCUs - 1) / kCUs;
   const double blocks = 0.5 * ((double)workgroups / kCUs + (double)rounds) * KB / splits;
   const double one = 0.091 + 0.0018 * (double)p->M;
