@@ -118,9 +118,10 @@ static qgemm_status_t make_rows_plan(const qgemm_w8a8_t* p, W8Plan* pl) {
   int splits = p->split_hint ? std::min(p->split_hint, KB) : rows_splits(M, columns, KB);
   if (groups > kW8Tickets) splits = 1;
   // A wavefront takes its k blocks in pairs; four wavefronts where eight would leave a tenth or more of the pairs' places
-  // empty (10240 x 5120, 40 k blocks: one token 13.2 us with eight, 11.3 with four; 4096 x 11008, 86: 13.0 and 13.7), and
-  // where the LDS of eight leaves room for one workgroup a compute unit and more are waiting: with a gate (11008 x 4096: 22.8
-  // and 20.0) and from 17 tokens on (17 x 8192 x 4096: 11.6 and 10.4; 17 x 4096 x 4096, one each, 6.4 and 6.7), above 32 always.
+  // empty (10240 x 5120, 40 k blocks: one token 12.7 us with eight, 12.2 with four, 16 tokens 16.1 and 14.9; 4096 x 11008, 86: one token
+  // 12.7 and 13.2, 16 tokens 14.1 and 13.6), and where the LDS of eight leaves room for one workgroup a compute unit and more are
+  // waiting: with a gate (11008 x 4096: 22.8 and 20.0) and from 17 tokens on (17 x 8192 x 4096: 11.2 and 9.9; 17 x 4096 x 4096, one
+  // each, 6.05 and 6.05), above 32 always.
   const int per = (KB + splits - 1) / splits;
   const auto places = [&](int waves) { return (per + 2 * waves - 1) / (2 * waves) * 2 * waves; };
   const bool crowded = M > 32 || (M > 16 && columns * splits > kCUs);

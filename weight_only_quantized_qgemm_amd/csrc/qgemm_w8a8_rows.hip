@@ -12,9 +12,9 @@
 // Each wavefront brings its k blocks into LDS of its own (buffer loads with the LDS destination, eight rows of 128 bytes
 // each, chunk c of row r at c ^ (r & 7)) and reads the operands from there; nothing is shared, so there is no barrier.  Loaded
 // straight into the operands' registers, sixteen consecutive lanes address sixteen rows, and the address unit takes them one by
-// one: 10240 x 5120, 16 tokens 18.1 us that way and 14.8 this, one token 12.8 and 12.1; 11008 x 4096 gated, 21.8 and 20.2, 19.9 and
-// 19.4.  What is left is the weights' way from memory: 4.6 TB/s for the latter, 5.2 for 10240 x 5120 at one token less 2 us for the
-// launch and the last block's latency.
+// one: 10240 x 5120, 16 tokens 18.1 us that way and 14.9 this, one token 12.8 and 12.2; 11008 x 4096 gated, 21.8 and 20.2, 19.9 and
+// 19.1 (weights from memory).  One token reads at 4.7 TB/s for the latter, at 5.1 for 10240 x 5120 less 2 us for the launch and the
+// last block's latency.  With one workgroup a compute unit 4096 x 11008 reads at 3.5 TB/s (12.7 us), with two 8192 x 28672 at 5.1.
 //
 // The wavefronts' sums meet in LDS, in wavefront order.  Where several workgroups make one output (splits along
 // K; the eight column blocks of an output scale block) each leaves its fp32 sums in the workspace and takes a
@@ -27,14 +27,15 @@ namespace qgemm {
 namespace w8 {
 namespace {
 
-// XH: loads of eight tokens each.  (With no second launch bound the compiler orders the loop so that 11008 x 4096 gated takes 20.1 us instead of 19.4.)
+// XH: loads of eight tokens each.
 template <int NW, int XH, int GATE, bool Q>
-__global__ __launch_bounds__(64 * NW, XH <= 4 ? 2 : 1) void rows_kernel(W8Args a) {
+__global__ __launch_bounds__(64 * NW) void rows_kernel(W8Args a) {
   constexpr bool G = GATE != QGEMM_GATE_NONE;
   constexpr int U = G ? 2 : 1;                       // weight blocks: one of either projection
   constexpr int F = Q ? kBlock / 16 : 1;             // workgroups along the columns of one output scale block
   // Two stages per wavefront: to 16 tokens 64 KiB for eight, 48 for four with a gate, so that two or three workgroups share a
-  // compute unit (one stage more and 11008 x 4096 gated takes 21.0 us instead of 20.0, 4096 x 4096 6.3 instead of 5.6).
+  // compute unit (one stage more and 11008 x 4096 gated to e4m3 takes 24.7 us instead of 21.6, 4096 x 4096 6.0 instead of 5.4;
+  // only 16 x 4096 x 11008 gains, 13.9 and 14.1).
   constexpr int MB = (XH + 1) / 2;                   // token blocks
   constexpr int SLOT = (U + MB) * 16 * kBlock;
   __shared__ __attribute__((aligned(1024))) unsigned char S0[NW * SLOT], S1[NW * SLOT];
