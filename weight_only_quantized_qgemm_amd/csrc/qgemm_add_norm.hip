@@ -197,8 +197,9 @@ extern "C" qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* p, const void* 
   const bool wave = p->dim <= 512;
   const int chunks = wave || p->dim <= 8192 ? 1 : p->dim <= 16384 ? 2 : 4;
   const int threads = wave ? 256 : 64 * ((p->dim + 512 * chunks - 1) / (512 * chunks));
-  if (p->tokens > 0xffffff00LL / threads)
-    return fail(QGEMM_ERR_UNSUPPORTED, "%lld rows of %d threads are more than one launch allows", (long long)p->tokens, threads);
+  const int row_threads = wave ? 64 : threads;
+  if (p->tokens > 0xffffff00LL / row_threads)
+    return fail(QGEMM_ERR_UNSUPPORTED, "%lld rows of %d threads are more than one launch allows", (long long)p->tokens, row_threads);
   if (wave) launch<true, 1>(bf, quantized, threads, s, a);
   else if (chunks == 1) launch<false, 1>(bf, quantized, threads, s, a);
   else if (chunks == 2) launch<false, 2>(bf, quantized, threads, s, a);
