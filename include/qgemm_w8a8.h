@@ -55,7 +55,7 @@ qgemm_status_t qgemm_add_norm(const qgemm_add_norm_t* problem, const void* x, in
                               float* y_scales, void* stream);
 
 #define QGEMM_GATE_NONE 0
-#define QGEMM_GATE_SILU 1           /* act(g) = g / (1 + exp(-g))                                              */
+#define QGEMM_GATE_SILU 1           /* act(g) = g / (1 + exp(-g))  (either act: 0 where it lies below 2^-119)  */
 #define QGEMM_GATE_GELU_TANH 2      /* act(g) = g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))              */
 
 /* kernel_hint values (testing and tuning; 0 is the right choice for applications) */

@@ -248,7 +248,7 @@ void launch_tokens(const W8Plan& pl, const W8Args& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rows(const W8Plan& pl, const W8Args& a, hipStream_t stream) {
-  // up to eight tokens are one load of a k block, not two (10240 x 5120: 12.1 and 12.7 us)
+  // up to eight tokens are one load of a k block, not two (10240 x 5120: eight 12.9 us, nine 13.4)
   if (a.M <= 8) launch_tokens<1>(pl, a, stream);
   else if (a.M <= 16) launch_tokens<2>(pl, a, stream);
   else if (a.M <= 32) launch_tokens<4>(pl, a, stream);

@@ -16,11 +16,17 @@
 // scales of a k block are one factor per lane and MFMA block, and a step costs one fp32 FMA per 128 products beside the
 // MFMA (16 issue cycles beside 32 MFMA cycles, or 64 with fp16 operands).
 //
-// 256 tokens: bound by LDS (a step reads 192 KiB and receives 64) beside the MFMAs: 8192 x 10240 x 5120 to bf16 374 us, 2.3
-// PFLOP/s; with fp16 operands by the issue of MFMAs, conversions and FMAs: 8192 x 11008 x 4096 gated to e4m3 1106 us,
-// 1.34 PFLOP/s.  64 and 128 tokens: by the way from L2 into LDS, 60 to 67 KiB a microsecond and compute unit whatever the tile
-// (40 KiB a step of 64 tokens x 256 rows, 0.6 us): 200 x 10240 x 5120 26 us.  Weights straight into registers instead: 50 us, since
-// sixteen lanes would address sixteen rows.  More stages hide more of a load's 1.4 us: 64 tokens with two 35.1 us, with four 27.3.
+// What a step takes (us, 160 tiles at once over 4096 weight rows; its loads and barrier alone, its products and operand reads alone):
+//                      e4m3 operands            fp16 operands
+//   64 tokens          0.50 (0.39, 0.32)        0.93 (0.39, 0.80)
+//   128 tokens         0.70 (0.46, 0.49)        1.45 (0.46, 1.25)
+//   256 tokens         1.16 (0.82, 0.99)        2.60 (-, 2.35)
+// So neither side bounds the smaller tiles by itself: they overlap in part, and a load's latency and the barrier show.  With fp16
+// operands the issue of MFMAs, conversions and FMAs does (8192 x 11008 x 4096 gated to e4m3 1103 us, 1.34 PFLOP/s), with e4m3
+// operands and 256 tokens LDS beside the MFMAs (a step reads 192 KiB and receives 64; 8192 x 10240 x 5120 to bf16 374 us, 2.3 PFLOP/s).
+// 200 x 10240 x 5120: 26 us with the weights in the 256 MB cache (21 and 18), 35 from memory (34 and 18): the reading, by 160 of 256
+// compute units.  Weights straight into registers instead: 50 us, since sixteen lanes would address sixteen rows.  More stages
+// hide more of a load's 1.4 us: 64 tokens with two 35.1 us, with four 27.3.
 #include <type_traits>
 
 #include "qgemm_w8a8_fixup.h"
