@@ -1,6 +1,7 @@
 """Calls of the 8-bit operators that the C ABI refuses beside those of a single argument (nothing is launched)."""
 import ctypes
 
+import numpy as np
 import pytest
 
 import weight_only_quantized_qgemm_amd as q
@@ -87,3 +88,10 @@ def test_few_tokens_split_along_k_only_where_it_pays():
     for m, n, k, splits in ((4, 1024, 2048, 1), (16, 512, 4096, 1), (1, 2048, 4096, 1), (4, 1024, 8192, 2), (16, 1024, 8192, 2),
                             (16, 2048, 8192, 2), (40, 1024, 8192, 4), (16, 1024, 28672, 4), (64, 1024, 28672, 4), (1, 2048, 28672, 2), (1, 4096, 28672, 1)):
         assert f"rows grid={n // 16 * splits} " in q.w8a8_describe(q.w8a8_problem(m, n, k)), (m, n, k)
+
+
+def test_quantize_refuses_weights_of_another_shape():
+    """With an exception that optimized Python keeps: the library reads as many weights as the problem has."""
+    for gate, shape in ((q.GATE_NONE, (32, 128)), (q.GATE_SILU, (16, 128)), (q.GATE_SILU, (32, 64)), (q.GATE_NONE, (16 * 128,))):
+        with pytest.raises(ValueError, match="w must be"):
+            q.w8a8_quantize(q.w8a8_problem(1, 16, 128, gate=gate), np.zeros(shape, np.float32))

@@ -455,7 +455,8 @@ def w8a8_quantize(p, w):
     [row blocks, K / 128]), host numpy.  On the GPU the codes are viewed as torch.float8_e4m3fn."""
     w = np.ascontiguousarray(w, dtype=np.float32)
     parts = 1 if p.gate == GATE_NONE else 2
-    assert w.shape == (parts * p.N, p.K)
+    if w.shape != (parts * p.N, p.K):
+        raise ValueError(f"w must be [{parts * p.N}, {p.K}], got {list(w.shape)}")
     codes = np.empty(w.shape, np.uint8)
     scales = np.empty((parts * -(-int(p.N) // 128), p.K // 128), np.float32)
     _check(_lib.qgemm_w8a8_quantize(ctypes.byref(p), w.ctypes.data, codes.ctypes.data, scales.ctypes.data))
