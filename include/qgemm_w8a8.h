@@ -108,9 +108,10 @@ qgemm_status_t qgemm_w8a8_workspace_bytes(const qgemm_w8a8_t* problem, size_t* b
  * QGEMM_W8A8_SUMS_WHOLE every product enters its sum whole.  Otherwise, with F16 and BF16 outputs, the tiles kernel (without a
  * hint from 17 tokens on, always above 64) adds the products of eight consecutive k first, cut off at 2^-13 of the largest
  * one's power of two: an error of at most 7 * 2^-13 times the sum of the groups' largest products (of normally distributed
- * values 1.4e-5 of an output's standard deviation).  Whole sums take the tiles kernel up to twice as
- * long; ask for them where large products may cancel, or where one token and a prompt must agree beyond the cut.
- *   A, W        e4m3 codes, contiguous, 16-byte aligned;  a_scales, w_scales fp32, contiguous, 4-byte aligned.
+ * values 1.4e-5 of an output's standard deviation).  Whole sums take the tiles kernel up to twice as long; ask for them where
+ * large products may cancel, or where one token and a prompt must agree beyond the cut.
+ *   A, W        e4m3 codes, contiguous, 16-byte aligned;  a_scales, w_scales fp32, contiguous, 4-byte aligned.  The two scales of
+ *               a block sum are multiplied first: their product is covered from 2^-126 to 2^127, and 0.
  *   out         [M][N] of out_dtype, contiguous, 16-byte aligned;  out_scales fp32 [N / 128][M] for FP8_E4M3,
  *               otherwise NULL.
  *   workspace   see qgemm_w8a8_workspace_bytes; 256-byte aligned; may be NULL when 0 bytes are needed.
